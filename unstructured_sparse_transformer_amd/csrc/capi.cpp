@@ -6,14 +6,11 @@
 
 #include <hip/hip_runtime.h>
 
+#include "checks.h"
 #include "decode2.h"
 #include "launch.h"
 
 namespace {
-
-bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-int elem_size(int32_t vdtype) { return vdtype == TWELL_BF16 ? 2 : 4; }
 
 // Shape / type rules shared by every call.
 int check_layout(const twell_t *h, int32_t d)
@@ -53,13 +50,6 @@ int check_ptrs(const twell_t *h)
     return TWELL_OK;
 }
 
-int check_mat(const void *p)
-{
-    if (!p)
-        return TWELL_E_NULL;
-    return aligned16(p) ? TWELL_OK : TWELL_E_ALIGN;
-}
-
 int check_hybrid(const twell_hybrid_t *hy)
 {
     if (!hy)
@@ -79,17 +69,6 @@ int check_hybrid(const twell_hybrid_t *hy)
         return TWELL_E_ALIGN;
     return TWELL_OK;
 }
-
-int hip_status(hipError_t e) { return e == hipSuccess ? TWELL_OK : TWELL_E_HIP; }
-
-#define TWELL_TRY(expr)                  \
-    do {                                 \
-        const int _st = (expr);          \
-        if (_st != TWELL_OK)             \
-            return _st;                  \
-    } while (0)
-
-size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // Workspace of the calls that take one (the fused step and the overflow FFN),
 // 256-byte aligned sections: the fused step's (twell::fused_ws_layout: packed
@@ -116,18 +95,6 @@ Ws ws_layout(const twell_hybrid_t *hy, int32_t d)
 {
     const twell_t *h = &hy->ell;
     return ws_layout(h->T, h->F, h->tile_w, h->cap, hy->max_ovf, d, h->vdtype);
-}
-
-// The workspace argument against a layout's size.
-int check_ws(const void *workspace, size_t workspace_bytes, size_t need)
-{
-    if (need == 0)
-        return TWELL_OK;
-    if (!workspace || workspace_bytes < need)
-        return TWELL_E_WORKSPACE;
-    if ((reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
-        return TWELL_E_ALIGN;
-    return TWELL_OK;
 }
 
 // Checks shared by twell_ffn_from_gate and twell_ffn_forward (T > 0).
