@@ -18,6 +18,7 @@
  *   statistics  twell_pack_gate_stats
  *   training    twell_dense_to_hybrid, twell_hybrid_to_dense,
  *               twell_compact_hybrid, twell_compact_to_dense, twell_ffn_backward
+ *   optimizer   twell_adamw_step, twell_adamw_unpack
  *
  * Notation: T tokens (rows), d model width, F hidden width (d_ff), w tile
  * width, n_b = F / w tiles per row, cap = slots per (row, tile).
@@ -391,6 +392,57 @@ TWELL_API int twell_ffn_backward(const twell_hybrid_t *hy, const void *x, const 
                                  const void *wd, int32_t d, const float *dy, float *dx, float *dwg, float *dwu,
                                  float *dwd, int32_t max_entries, void *workspace, size_t workspace_bytes,
                                  void *stream);
+
+/* ---- Optimizer -------------------------------------------------------------
+ * One AdamW step over many tensors at once: for every element
+ *   g = grad * *grad_scale,  m = beta1 m + (1 - beta1) g,
+ *   v = beta2 v + (1 - beta2) g^2,
+ *   p = (1 - lr weight_decay) p
+ *       - lr / (1 - beta1^step) * m / (sqrt(v) / sqrt(1 - beta2^step) + eps)
+ * in fp32, each operation rounded by itself.  The tensors of one call have the
+ * same state format and may differ in everything else.  p is float, or bf16
+ * (then rounded to nearest, which loses updates below 2^-9 of the value: train
+ * with float p and a bf16 `copy` for the layers).  States:
+ *   state_bits 32   m, v : float [n]
+ *   state_bits 8    m, v : uint8 [n], m_scale, v_scale : float [ceil(n / 256)].
+ *                   m holds sign and 7 bits, v the root sqrt(v) in 8 bits, as
+ *                   floating codes relative to the largest magnitude of the
+ *                   256 elements that share a scale; written back with
+ *                   stochastic rounding whose noise is a hash of (seed, the
+ *                   tensor's place in the list, the element), so equal calls
+ *                   give equal bits.  All zeros is the state before the first
+ *                   step.  A block that meets an infinity or a NaN reads back
+ *                   as NaN as a whole.
+ * The descriptor array is HOST memory, read during the call only; what it
+ * points to is device memory.  Pointers need the alignment of their elements;
+ * where all of a tensor's pointers are 16-byte aligned (8-bit codes: 8) its
+ * accesses are wide. */
+typedef struct twell_adamw_tensor_t {
+    int64_t n;          /* elements, >= 0 */
+    void *p;            /* device [n], pdtype: parameters, updated in place */
+    void *copy;         /* device [n] bf16, written with the updated p, or NULL */
+    const void *grad;   /* device [n], gdtype */
+    void *m, *v;        /* device states, updated in place */
+    float *m_scale, *v_scale;   /* 8-bit states: device scales; else NULL */
+    float *m_values, *v_values; /* twell_adamw_unpack only: device [n] float */
+    double weight_decay;
+    int32_t pdtype;     /* enum twell_dtype of p */
+    int32_t gdtype;     /* enum twell_dtype of grad */
+} twell_adamw_tensor_t;
+
+/* The step.  step >= 1 counts the steps of this state, 0 <= beta < 1, eps > 0.
+ * grad_scale : device float, or NULL for 1: multiplies every gradient (the
+ *     inverse of a loss scale, a clip coefficient).  Where it is 0, infinite or
+ *     NaN the call changes nothing.
+ * lr, the betas and step are read by the call: a captured graph repeats the
+ * captured step's values.  Returns TWELL_OK or a negative twell_status. */
+TWELL_API int twell_adamw_step(const twell_adamw_tensor_t *tensors, int32_t count, int32_t state_bits, double lr,
+                               double beta1, double beta2, double eps, int64_t step, uint32_t seed,
+                               const float *grad_scale, void *stream);
+
+/* The values of 8-bit states, for a checkpoint or a look at them: m_values =
+ * m, v_values = v (the square of the stored root). */
+TWELL_API int twell_adamw_unpack(const twell_adamw_tensor_t *tensors, int32_t count, void *stream);
 
 /* Static text for a status code. */
 TWELL_API const char *twell_status_str(int status);

@@ -13,7 +13,7 @@ The functions carry the C names (``include/twell.h``):
 ``twell_ffn_decode_workspace_bytes``, ``twell_ffn_decode_noalloc``, ``twell_dense_to_hybrid``,
 ``twell_hybrid_to_dense``, ``twell_compact_min_bytes``, ``twell_compact_hybrid``,
 ``twell_compact_to_dense``, ``twell_ffn_backward``,
-``twell_ffn_backward_workspace_bytes``.
+``twell_ffn_backward_workspace_bytes``, ``twell_adamw_step``, ``twell_adamw_unpack``.
 
 One layer's forward pass, bf16 (x [T][d], W_g^T and W_u^T [F][d], W_d [F][d],
 all contiguous on the GPU; y [T][d] fp32)::
@@ -46,7 +46,8 @@ EXPORTS = ("twell_ffn_forward", "twell_ffn_from_gate", "twell_pack_gate", "twell
            "twell_ffn_fused", "twell_workspace_bytes", "twell_ffn_overflow", "twell_ffn_hybrid",
            "twell_ffn_decode_workspace_bytes", "twell_ffn_decode", "twell_ffn_decode_noalloc", "twell_dense_to_hybrid", "twell_hybrid_to_dense",
            "twell_compact_min_bytes", "twell_compact_hybrid", "twell_compact_to_dense",
-           "twell_ffn_backward_workspace_bytes", "twell_ffn_backward", "twell_status_str", "twell_version")
+           "twell_ffn_backward_workspace_bytes", "twell_ffn_backward", "twell_adamw_step", "twell_adamw_unpack",
+           "twell_status_str", "twell_version")
 
 
 class TwellT(ctypes.Structure):
@@ -59,6 +60,13 @@ class TwellHybridT(ctypes.Structure):
     _fields_ = [("ell", TwellT), ("max_ovf", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("row_ovf", ctypes.c_void_p), ("ovf_rows", ctypes.c_void_p), ("n_ovf", ctypes.c_void_p),
                 ("dense", ctypes.c_void_p), ("order", ctypes.c_void_p)]
+
+
+class TwellAdamWTensorT(ctypes.Structure):
+    _fields_ = [("n", ctypes.c_int64), ("p", ctypes.c_void_p), ("copy", ctypes.c_void_p), ("grad", ctypes.c_void_p),
+                ("m", ctypes.c_void_p), ("v", ctypes.c_void_p), ("m_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("m_values", ctypes.c_void_p), ("v_values", ctypes.c_void_p),
+                ("weight_decay", ctypes.c_double), ("pdtype", ctypes.c_int32), ("gdtype", ctypes.c_int32)]
 
 
 class TwellError(RuntimeError):
@@ -107,6 +115,9 @@ def load(path: str = LIB_PATH):
     lib.twell_ffn_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.twell_ffn_backward.argtypes = [ctypes.POINTER(TwellHybridT), P, P, P, P, I32, P, P, P, P, P, I32, P,
                                        ctypes.c_size_t, P]
+    F64 = ctypes.c_double
+    lib.twell_adamw_step.argtypes = [P, I32, I32, F64, F64, F64, F64, ctypes.c_int64, ctypes.c_uint32, P, P]
+    lib.twell_adamw_unpack.argtypes = [P, I32, P]
     lib.twell_status_str.argtypes = [ctypes.c_int]
     lib.twell_status_str.restype = ctypes.c_char_p
     lib.twell_version.restype = ctypes.c_int
@@ -114,7 +125,7 @@ def load(path: str = LIB_PATH):
                lib.twell_ffn_fused, lib.twell_ffn_hybrid, lib.twell_ffn_overflow, lib.twell_ffn_forward,
                lib.twell_ffn_from_gate, lib.twell_ffn_decode, lib.twell_ffn_decode_noalloc,
                lib.twell_dense_to_hybrid, lib.twell_hybrid_to_dense, lib.twell_compact_hybrid,
-               lib.twell_compact_to_dense, lib.twell_ffn_backward):
+               lib.twell_compact_to_dense, lib.twell_ffn_backward, lib.twell_adamw_step, lib.twell_adamw_unpack):
         fn.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -386,3 +397,73 @@ def hybrid_workspace(hy: "Hybrid", d: int, device="cuda"):
     """The workspace for the calls on hybrid `hy` with model width d."""
     e = hy.ell
     return workspace(e.T, e.F, e.tile_w, e.cap, hy.max_ovf, d, e.dtype, device)
+
+
+# ---------------------------------------------------------------- the optimizer
+ADAMW_BLOCK = 256  # elements that share a scale of the 8-bit states
+
+
+class AdamWTensors:
+    """The tensors of one AdamW step, with their C descriptors.
+
+    ``tensors`` is a list of dicts: ``p`` (float32 or bfloat16), ``grad``, ``m``,
+    ``v``, and as needed ``copy`` (bfloat16, written with the updated p),
+    ``weight_decay``, and for 8-bit states (``m``, ``v`` uint8) ``m_scale``,
+    ``v_scale`` (float32, one per 256 elements) and, for ``twell_adamw_unpack``,
+    ``m_values``, ``v_values`` (float32).  The tensors are contiguous and stay
+    where they are while this object is in use (it keeps references to them);
+    build another one when a gradient moves.  All have the same state format.
+    """
+
+    def __init__(self, tensors):
+        import torch
+        self.tensors = [dict(t) for t in tensors]
+        for i, t in enumerate(self.tensors):
+            for k in ("p", "grad", "m", "v"):
+                if t.get(k) is None:
+                    raise ValueError(f"AdamWTensors: tensor {i} has no {k!r}")
+        self.desc = (TwellAdamWTensorT * max(len(self.tensors), 1))()
+        self.state_bits = 8 if self.tensors and self.tensors[0]["m"].dtype == torch.uint8 else 32
+        self.device = self.tensors[0]["p"].device if self.tensors else None
+        self.can_unpack = self.state_bits == 8 and all(t.get("m_values") is not None and t.get("v_values") is not None
+                                                       for t in self.tensors)
+        state = torch.uint8 if self.state_bits == 8 else torch.float32
+        for i, (o, t) in enumerate(zip(self.desc, self.tensors)):
+            n = t["p"].numel()
+            blocks = -(-n // ADAMW_BLOCK)
+            want = {"p": (None, n), "grad": (None, n), "copy": (torch.bfloat16, n), "m": (state, n), "v": (state, n),
+                    "m_scale": (torch.float32, blocks), "v_scale": (torch.float32, blocks),
+                    "m_values": (torch.float32, n), "v_values": (torch.float32, n)}
+            for k in ("m_scale", "v_scale") if self.state_bits == 8 else ():
+                if t.get(k) is None:
+                    raise ValueError(f"AdamWTensors: tensor {i} has no {k!r}")
+            for k, (dtype, size) in want.items():
+                x = t.get(k)
+                if x is None:
+                    continue
+                if x.device != self.device:
+                    raise ValueError(f"AdamWTensors: {k!r} of tensor {i} is on {x.device}, not on {self.device}")
+                if not x.is_contiguous() or x.numel() != size:
+                    raise ValueError(f"AdamWTensors: {k!r} of tensor {i} must be contiguous with {size} elements")
+                if dtype is not None and x.dtype != dtype:
+                    raise TypeError(f"AdamWTensors: {k!r} of tensor {i} must be {dtype}, not {x.dtype}")
+                setattr(o, k, x.data_ptr())
+            o.n = n
+            o.weight_decay = float(t.get("weight_decay", 0.0))
+            o.pdtype, o.gdtype = vdtype_of(t["p"].dtype), vdtype_of(t["grad"].dtype)
+
+
+def twell_adamw_step(params: AdamWTensors, lr: float, beta1: float, beta2: float, eps: float, step: int, seed: int = 0,
+                     grad_scale=None, stream=None):
+    """One step; step counts from 1; grad_scale: a float32 tensor of one element on the GPU (0, inf or NaN in it:
+    nothing changes); seed: of the 8-bit states' rounding, another one each step."""
+    _check("twell_adamw_step",
+           load().twell_adamw_step(params.desc, len(params.tensors), params.state_bits, lr, beta1, beta2, eps, step,
+                                   seed & 0xFFFFFFFF, _ptr(grad_scale), _stream(stream)))
+
+
+def twell_adamw_unpack(params: AdamWTensors, stream=None):
+    """Writes the values of 8-bit states to m_values and v_values."""
+    if not params.can_unpack:
+        raise ValueError("twell_adamw_unpack: 8-bit states with m_values and v_values are needed")
+    _check("twell_adamw_unpack", load().twell_adamw_unpack(params.desc, len(params.tensors), _stream(stream)))

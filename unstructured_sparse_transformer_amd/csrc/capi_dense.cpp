@@ -1,0 +1,154 @@
+// capi_dense.cpp -- the C ABI of the dense layer's operators (include/twell.h):
+// argument checks on the host, then launches on the caller's stream.
+#include "twell.h"
+
+#include <cmath>
+
+#include <hip/hip_runtime.h>
+
+#include "adamw.h"
+#include "checks.h"
+
+namespace {
+
+bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+bool known_dtype(int32_t dt) { return dt == TWELL_F32 || dt == TWELL_BF16; }
+
+// A vector of elements of size es: NULL and alignment.
+int check_vec(const void *p, size_t es)
+{
+    if (!p)
+        return TWELL_E_NULL;
+    return aligned_to(p, es) ? TWELL_OK : TWELL_E_ALIGN;
+}
+
+// One descriptor of twell_adamw_step (grads) or twell_adamw_unpack (values).
+int check_adamw(const twell_adamw_tensor_t &t, bool coded, bool unpack)
+{
+    if (t.n < 0 || t.n > ((int64_t)1 << 40))
+        return TWELL_E_SHAPE;
+    if (!unpack && (!known_dtype(t.pdtype) || !known_dtype(t.gdtype)))
+        return TWELL_E_UNSUPPORTED;
+    if (t.n == 0)
+        return TWELL_OK;
+    TWELL_TRY(check_vec(t.m, coded ? 1 : 4));
+    TWELL_TRY(check_vec(t.v, coded ? 1 : 4));
+    if (coded) {
+        TWELL_TRY(check_vec(t.m_scale, 4));
+        TWELL_TRY(check_vec(t.v_scale, 4));
+    }
+    if (unpack) {
+        TWELL_TRY(check_vec(t.m_values, 4));
+        return check_vec(t.v_values, 4);
+    }
+    TWELL_TRY(check_vec(t.p, elem_size(t.pdtype)));
+    TWELL_TRY(check_vec(t.grad, elem_size(t.gdtype)));
+    return t.copy ? check_vec(t.copy, 2) : TWELL_OK;
+}
+
+// Chunks of AW_CHUNK elements; a launch's total fits a grid.
+constexpr int64_t AW_MOST_CHUNKS = (int64_t)1 << 30;
+int64_t aw_chunks(int64_t n) { return (n + twell::AW_CHUNK - 1) / twell::AW_CHUNK; }
+
+}  // namespace
+
+extern "C" {
+
+int twell_adamw_step(const twell_adamw_tensor_t *tensors, int32_t count, int32_t state_bits, double lr, double beta1,
+                     double beta2, double eps, int64_t step, uint32_t seed, const float *grad_scale, void *stream)
+{
+    if (count < 0 || step < 1 || !(lr >= 0) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps > 0))
+        return TWELL_E_SHAPE;
+    if (state_bits != 8 && state_bits != 32)
+        return TWELL_E_UNSUPPORTED;
+    if (count == 0)
+        return TWELL_OK;
+    if (!tensors)
+        return TWELL_E_NULL;
+    const bool coded = state_bits == 8;
+    for (int32_t i = 0; i < count; ++i)
+        TWELL_TRY(check_adamw(tensors[i], coded, false));
+    if (grad_scale && !aligned_to(grad_scale, 4))
+        return TWELL_E_ALIGN;
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    twell::AwBatch b{};
+    b.beta1 = (float)beta1;
+    b.omb1 = (float)(1 - beta1);
+    b.beta2 = (float)beta2;
+    b.omb2 = (float)(1 - beta2);
+    b.eps = (float)eps;
+    b.size = (float)(lr / (1 - std::pow(beta1, (double)step)));
+    b.root = (float)(1 / std::sqrt(1 - std::pow(beta2, (double)step)));
+    b.grad_scale = grad_scale;
+    int64_t chunks = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const twell_adamw_tensor_t &t = tensors[i];
+        const int64_t c = aw_chunks(t.n);
+        if (c == 0)
+            continue;
+        if (b.count == twell::AW_BATCH || chunks + c > AW_MOST_CHUNKS) {
+            TWELL_TRY(hip_status(twell::launch_adamw(b, coded, (int)chunks, s)));
+            b.count = 0;
+            chunks = 0;
+        }
+        const bool vec = aligned16(t.p) && aligned16(t.grad) && aligned16(t.copy) &&
+                         aligned_to(t.m, coded ? 8 : 16) && aligned_to(t.v, coded ? 8 : 16);
+        twell::AwTensor &o = b.t[b.count++];
+        o.n = t.n;
+        o.p = t.p;
+        o.copy = static_cast<__bf16 *>(t.copy);
+        o.grad = t.grad;
+        o.m = t.m;
+        o.v = t.v;
+        o.m_scale = t.m_scale;
+        o.v_scale = t.v_scale;
+        o.decay = (float)(1 - lr * t.weight_decay);
+        o.flags = (t.pdtype == TWELL_BF16 ? twell::AW_P_BF16 : 0) | (t.gdtype == TWELL_BF16 ? twell::AW_G_BF16 : 0) |
+                  (vec ? twell::AW_VEC : 0);
+        o.key = seed * 0x9E3779B9u + (uint32_t)i * 0x632BE5ABu;
+        o.chunk0 = (int32_t)chunks;
+        chunks += c;
+    }
+    return b.count ? hip_status(twell::launch_adamw(b, coded, (int)chunks, s)) : TWELL_OK;
+}
+
+int twell_adamw_unpack(const twell_adamw_tensor_t *tensors, int32_t count, void *stream)
+{
+    if (count < 0)
+        return TWELL_E_SHAPE;
+    if (count == 0)
+        return TWELL_OK;
+    if (!tensors)
+        return TWELL_E_NULL;
+    for (int32_t i = 0; i < count; ++i)
+        TWELL_TRY(check_adamw(tensors[i], true, true));
+    hipStream_t s = static_cast<hipStream_t>(stream);
+    twell::AwUnpack b{};
+    int64_t chunks = 0;
+    for (int32_t i = 0; i < count; ++i) {
+        const twell_adamw_tensor_t &t = tensors[i];
+        const int64_t c = aw_chunks(t.n);
+        if (c == 0)
+            continue;
+        if (b.count == twell::AW_BATCH || chunks + c > AW_MOST_CHUNKS) {
+            TWELL_TRY(hip_status(twell::launch_adamw_unpack(b, (int)chunks, s)));
+            b.count = 0;
+            chunks = 0;
+        }
+        auto &o = b.t[b.count++];
+        o.n = t.n;
+        o.m = static_cast<const uint8_t *>(t.m);
+        o.v = static_cast<const uint8_t *>(t.v);
+        o.m_scale = t.m_scale;
+        o.v_scale = t.v_scale;
+        o.m_values = t.m_values;
+        o.v_values = t.v_values;
+        o.chunk0 = (int32_t)chunks;
+        o.vec = aligned_to(t.m, 8) && aligned_to(t.v, 8) && aligned16(t.m_values) && aligned16(t.v_values);
+        chunks += c;
+    }
+    return b.count ? hip_status(twell::launch_adamw_unpack(b, (int)chunks, s)) : TWELL_OK;
+}
+
+}  // extern "C"
