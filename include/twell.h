@@ -18,6 +18,7 @@
  *   statistics  twell_pack_gate_stats
  *   training    twell_dense_to_hybrid, twell_hybrid_to_dense,
  *               twell_compact_hybrid, twell_compact_to_dense, twell_ffn_backward
+ *   norms       twell_block_norm_forward, twell_block_norm_backward
  *   optimizer   twell_adamw_step, twell_adamw_unpack
  *
  * Notation: T tokens (rows), d model width, F hidden width (d_ff), w tile
@@ -392,6 +393,60 @@ TWELL_API int twell_ffn_backward(const twell_hybrid_t *hy, const void *x, const 
                                  const void *wd, int32_t d, const float *dy, float *dx, float *dwg, float *dwu,
                                  float *dwd, int32_t max_entries, void *workspace, size_t workspace_bytes,
                                  void *stream);
+
+/* ---- Block norms -----------------------------------------------------------
+ * The norms before and after a block with the block's gate, residual scale and
+ * residual sum, for T rows of d:
+ *   p = norm(y; w_post, b_post)  when post, else y
+ *   r = res + alpha * gate * p   (r = res when y is NULL)
+ *   out = r,  n = norm(r; w_pre, b_pre)
+ * TWELL_NORM_RMS: norm(v) = v / sqrt(mean(v^2) + eps) * w + b;
+ * TWELL_NORM_LAYER: v - mean(v) in the place of v.  A weight that is NULL is 1,
+ * a bias 0.  n comes from r before it is rounded to out's type.  Sums are fp32
+ * in a fixed order: repeated calls give the same bits.
+ * A gate row of d values serves gate_span consecutive rows: 1 = a gate per
+ * token, a sequence's length = one per sequence, >= T = one for all. */
+enum twell_norm { TWELL_NORM_RMS = 0, TWELL_NORM_LAYER = 1 };
+
+typedef struct twell_block_norm_t {
+    int32_t T, d;       /* rows >= 0, 1 <= d <= 8192 */
+    int32_t kind;       /* enum twell_norm */
+    int32_t post;       /* 1: a norm after the block */
+    float eps, alpha;   /* eps > 0 */
+    int32_t gate_span;  /* rows that share a gate row; 0: no gate */
+    int32_t rdtype;     /* enum twell_dtype of res, out, gate and their gradients */
+    int32_t ydtype;     /* of y and dy (twell_ffn_forward's y is float) */
+    int32_t ndtype;     /* of n, the next block's input */
+    int32_t wdtype;     /* of the weights and biases */
+    int32_t reserved;
+    const void *gate;   /* device [ceil(T / gate_span)][d] */
+    const void *w_post, *b_post, *w_pre, *b_pre; /* device [d] or NULL */
+} twell_block_norm_t;
+
+/* res, y, out, n : device [T][d].  y NULL: no block before this norm (out is
+ * not written).  n NULL: no norm after the sum; out NULL: the sum is not
+ * wanted (one of the two is).  out may be res.  Pointers need the alignment of
+ * their elements; with 16-byte aligned pointers and d a multiple of 8 the
+ * accesses are wide. */
+TWELL_API int twell_block_norm_forward(const twell_block_norm_t *bn, const void *res, const void *y, void *out,
+                                       void *n, void *stream);
+
+/* Bytes of device workspace of the backward pass (0 for invalid sizes). */
+TWELL_API size_t twell_block_norm_workspace_bytes(int32_t T, int32_t d);
+
+/* Gradients of twell_block_norm_forward.  out : the forward's out (its res,
+ * when y is NULL), needed with dn; y : the forward's y or NULL; dout : gradient
+ * of out, rdtype, or NULL for 0; dn : gradient of n, dndtype, or NULL without
+ * a norm after the sum (one of the two is given).  Writes dres [T][d] (rdtype,
+ * may be dout), with y dy [T][d] (ydtype), with a gate dgate (rdtype, the
+ * gate's shape), and those of dw_post, db_post, dw_pre, db_pre (device float
+ * [d], overwritten) that are not NULL.
+ * workspace : device, >= twell_block_norm_workspace_bytes(T, d), 256-byte
+ * aligned, content ignored on entry. */
+TWELL_API int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, const void *y,
+                                        const void *dout, const void *dn, int32_t dndtype, void *dres, void *dy,
+                                        void *dgate, float *dw_post, float *db_post, float *dw_pre, float *db_pre,
+                                        void *workspace, size_t workspace_bytes, void *stream);
 
 /* ---- Optimizer -------------------------------------------------------------
  * One AdamW step over many tensors at once: for every element

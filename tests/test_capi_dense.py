@@ -49,3 +49,45 @@ def test_adamw_validation():
     assert lib.twell_adamw_unpack(ctypes.byref(t), 1, None) == NULL      # v_values
     t.v_values = GOOD + 2
     assert lib.twell_adamw_unpack(ctypes.byref(t), 1, None) == ALIGN
+
+
+def _bn(**kw):
+    t = tw.TwellBlockNormT(T=8, d=64, kind=0, post=1, eps=1e-6, alpha=1.0, gate_span=0)
+    for k, v in kw.items():
+        setattr(t, k, v)
+    return ctypes.byref(t)
+
+
+def test_block_norm_validation():
+    lib = tw.load()
+    f = lib.twell_block_norm_forward
+    assert f(None, GOOD, GOOD, GOOD, GOOD, None) == NULL
+    assert f(_bn(T=0), None, None, None, None, None) == 0
+    assert f(_bn(), None, GOOD, GOOD, GOOD, None) == NULL              # res
+    assert f(_bn(), GOOD, GOOD, None, None, None) == NULL              # neither out nor n
+    assert f(_bn(), GOOD, None, GOOD, None, None) == NULL              # out without a block is not written
+    assert f(_bn(gate_span=2), GOOD, GOOD, GOOD, GOOD, None) == NULL   # gate
+    assert f(_bn(), GOOD + 2, GOOD, GOOD, GOOD, None) == ALIGN
+    assert f(_bn(w_pre=GOOD + 2), GOOD, GOOD, GOOD, GOOD, None) == ALIGN
+    assert f(_bn(rdtype=1, ydtype=1, ndtype=1), GOOD, GOOD, GOOD + 1, GOOD, None) == ALIGN
+    for kw in (dict(kind=2), dict(d=8193), dict(rdtype=2), dict(ydtype=-1), dict(ndtype=5), dict(wdtype=2)):
+        assert f(_bn(**kw), GOOD, GOOD, GOOD, GOOD, None) == UNSUPPORTED, kw
+    for kw in (dict(T=-1), dict(d=0), dict(gate_span=-1), dict(eps=0.0), dict(eps=float("nan"))):
+        assert f(_bn(**kw), GOOD, GOOD, GOOD, GOOD, None) == SHAPE, kw
+    size = lib.twell_block_norm_workspace_bytes
+    assert size(-1, 64) == 0 and size(8, 0) == 0 and size(8, 8193) == 0 and size(0, 64) == 0
+    need = size(8, 64)
+    assert need > 0
+
+    def b(bn=None, out=GOOD, y=GOOD, dout=GOOD, dn=GOOD, dndtype=0, dres=GOOD, dy=GOOD, dgate=None, dw=None, ws=GOOD,
+          nbytes=need):
+        return lib.twell_block_norm_backward(bn or _bn(), out, y, dout, dn, dndtype, dres, dy, dgate, dw, None, None, None,
+                                             ws, nbytes, None)
+    assert b(dout=None, dn=None) == NULL
+    assert b(out=None) == NULL
+    assert b(dres=None) == NULL
+    assert b(dy=None) == NULL
+    assert b(bn=_bn(gate_span=2, gate=GOOD)) == NULL                    # dgate
+    assert b(dw=GOOD + 2) == ALIGN
+    assert b(dndtype=3) == UNSUPPORTED
+    assert b(ws=None) == WORKSPACE and b(nbytes=need - 1) == WORKSPACE and b(ws=GOOD + 128) == ALIGN

@@ -13,7 +13,8 @@ The functions carry the C names (``include/twell.h``):
 ``twell_ffn_decode_workspace_bytes``, ``twell_ffn_decode_noalloc``, ``twell_dense_to_hybrid``,
 ``twell_hybrid_to_dense``, ``twell_compact_min_bytes``, ``twell_compact_hybrid``,
 ``twell_compact_to_dense``, ``twell_ffn_backward``,
-``twell_ffn_backward_workspace_bytes``, ``twell_adamw_step``, ``twell_adamw_unpack``.
+``twell_ffn_backward_workspace_bytes``, ``twell_block_norm_forward``,
+``twell_block_norm_workspace_bytes``, ``twell_block_norm_backward``, ``twell_adamw_step``, ``twell_adamw_unpack``.
 
 One layer's forward pass, bf16 (x [T][d], W_g^T and W_u^T [F][d], W_d [F][d],
 all contiguous on the GPU; y [T][d] fp32)::
@@ -46,7 +47,8 @@ EXPORTS = ("twell_ffn_forward", "twell_ffn_from_gate", "twell_pack_gate", "twell
            "twell_ffn_fused", "twell_workspace_bytes", "twell_ffn_overflow", "twell_ffn_hybrid",
            "twell_ffn_decode_workspace_bytes", "twell_ffn_decode", "twell_ffn_decode_noalloc", "twell_dense_to_hybrid", "twell_hybrid_to_dense",
            "twell_compact_min_bytes", "twell_compact_hybrid", "twell_compact_to_dense",
-           "twell_ffn_backward_workspace_bytes", "twell_ffn_backward", "twell_adamw_step", "twell_adamw_unpack",
+           "twell_ffn_backward_workspace_bytes", "twell_ffn_backward", "twell_block_norm_forward",
+           "twell_block_norm_workspace_bytes", "twell_block_norm_backward", "twell_adamw_step", "twell_adamw_unpack",
            "twell_status_str", "twell_version")
 
 
@@ -60,6 +62,15 @@ class TwellHybridT(ctypes.Structure):
     _fields_ = [("ell", TwellT), ("max_ovf", ctypes.c_int32), ("reserved", ctypes.c_int32),
                 ("row_ovf", ctypes.c_void_p), ("ovf_rows", ctypes.c_void_p), ("n_ovf", ctypes.c_void_p),
                 ("dense", ctypes.c_void_p), ("order", ctypes.c_void_p)]
+
+
+class TwellBlockNormT(ctypes.Structure):
+    _fields_ = [("T", ctypes.c_int32), ("d", ctypes.c_int32), ("kind", ctypes.c_int32), ("post", ctypes.c_int32),
+                ("eps", ctypes.c_float), ("alpha", ctypes.c_float), ("gate_span", ctypes.c_int32),
+                ("rdtype", ctypes.c_int32), ("ydtype", ctypes.c_int32), ("ndtype", ctypes.c_int32),
+                ("wdtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("gate", ctypes.c_void_p),
+                ("w_post", ctypes.c_void_p), ("b_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
+                ("b_pre", ctypes.c_void_p)]
 
 
 class TwellAdamWTensorT(ctypes.Structure):
@@ -115,6 +126,11 @@ def load(path: str = LIB_PATH):
     lib.twell_ffn_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.twell_ffn_backward.argtypes = [ctypes.POINTER(TwellHybridT), P, P, P, P, I32, P, P, P, P, P, I32, P,
                                        ctypes.c_size_t, P]
+    BN = ctypes.POINTER(TwellBlockNormT)
+    lib.twell_block_norm_forward.argtypes = [BN, P, P, P, P, P]
+    lib.twell_block_norm_workspace_bytes.argtypes = [I32, I32]
+    lib.twell_block_norm_workspace_bytes.restype = ctypes.c_size_t
+    lib.twell_block_norm_backward.argtypes = [BN, P, P, P, P, I32, P, P, P, P, P, P, P, P, ctypes.c_size_t, P]
     F64 = ctypes.c_double
     lib.twell_adamw_step.argtypes = [P, I32, I32, F64, F64, F64, F64, ctypes.c_int64, ctypes.c_uint32, P, P]
     lib.twell_adamw_unpack.argtypes = [P, I32, P]
@@ -125,7 +141,8 @@ def load(path: str = LIB_PATH):
                lib.twell_ffn_fused, lib.twell_ffn_hybrid, lib.twell_ffn_overflow, lib.twell_ffn_forward,
                lib.twell_ffn_from_gate, lib.twell_ffn_decode, lib.twell_ffn_decode_noalloc,
                lib.twell_dense_to_hybrid, lib.twell_hybrid_to_dense, lib.twell_compact_hybrid,
-               lib.twell_compact_to_dense, lib.twell_ffn_backward, lib.twell_adamw_step, lib.twell_adamw_unpack):
+               lib.twell_compact_to_dense, lib.twell_ffn_backward, lib.twell_block_norm_forward,
+               lib.twell_block_norm_backward, lib.twell_adamw_step, lib.twell_adamw_unpack):
         fn.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -397,6 +414,104 @@ def hybrid_workspace(hy: "Hybrid", d: int, device="cuda"):
     """The workspace for the calls on hybrid `hy` with model width d."""
     e = hy.ell
     return workspace(e.T, e.F, e.tile_w, e.cap, hy.max_ovf, d, e.dtype, device)
+
+
+# ---------------------------------------------------------------- block norms
+NORM_KINDS = {"rms": 0, "layer": 1}
+
+
+def _tensor(fn: str, name: str, t, shape, like, dtype=None):
+    """Checks an argument: contiguous, on `like`'s device, of this shape and (if given) element type."""
+    if t is None:
+        raise ValueError(f"{fn}: {name} is missing")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    if not t.is_contiguous():
+        raise ValueError(f"{fn}: {name} must be contiguous")
+    if t.device != like.device:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on {like.device}")
+    if dtype is not None and t.dtype != dtype:
+        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
+    return t.data_ptr()
+
+
+class BlockNorm:
+    """The norms around a block and their weights ([d] tensors of one type, or None for 1 and 0): the norm after the
+    block (``post``; ``w_post``, ``b_post``), the residual scale ``alpha``, the norm before the next (``w_pre``,
+    ``b_pre``).  ``kind``: "rms" or "layer"."""
+
+    def __init__(self, kind="rms", eps=1e-6, alpha=1.0, post=False, w_post=None, b_post=None, w_pre=None, b_pre=None):
+        if kind not in NORM_KINDS:
+            raise ValueError(f"BlockNorm: kind {kind!r}: one of {', '.join(NORM_KINDS)}")
+        self.kind, self.eps, self.alpha, self.post = kind, eps, alpha, post
+        self.weights = {"w_post": w_post, "b_post": b_post, "w_pre": w_pre, "b_pre": b_pre}
+        given = [w for w in self.weights.values() if w is not None]
+        self._desc = TwellBlockNormT(kind=NORM_KINDS[kind], eps=eps, alpha=alpha, post=int(bool(post)),
+                                     wdtype=vdtype_of(given[0].dtype) if given else TWELL_F32)
+        for k, w in self.weights.items():
+            if w is not None:
+                setattr(self._desc, k, _tensor("BlockNorm", k, w, given[0].shape, given[0], given[0].dtype))
+        self.d = given[0].numel() if given else None
+
+    def desc(self, fn, rows, y, gate, gate_span) -> TwellBlockNormT:
+        T, d = rows.shape
+        if self.d is not None and d != self.d:
+            raise ValueError(f"{fn}: rows of {d}, weights of {self.d}")
+        o = TwellBlockNormT.from_buffer_copy(self._desc)
+        o.T, o.d, o.rdtype = T, d, vdtype_of(rows.dtype)
+        if y is not None:
+            _tensor(fn, "y", y, (T, d), rows)
+            o.ydtype = vdtype_of(y.dtype)
+        if gate is not None:
+            if gate_span < 1:
+                raise ValueError(f"{fn}: gate_span {gate_span}: a gate row serves at least one row")
+            o.gate_span = gate_span
+            o.gate = _tensor(fn, "gate", gate, (-(-T // gate_span), d), rows, rows.dtype)
+        return o
+
+
+def twell_block_norm_forward(bn: BlockNorm, res, y, out, n, gate=None, gate_span: int = 0, stream=None):
+    """out = res + alpha * gate * norm(y), n = norm(out); y, out, n may be None (see include/twell.h)."""
+    fn = "twell_block_norm_forward"
+    o = bn.desc(fn, res, y, gate, gate_span)
+    p_res = _tensor(fn, "res", res, res.shape, res)
+    p_out = None if out is None else _tensor(fn, "out", out, res.shape, res, res.dtype)
+    p_n = None
+    if n is not None:
+        p_n = _tensor(fn, "n", n, res.shape, res)
+        o.ndtype = vdtype_of(n.dtype)
+    _check(fn, load().twell_block_norm_forward(o, p_res, _ptr(y), p_out, p_n, _stream(stream)))
+
+
+def twell_block_norm_workspace_bytes(T: int, d: int) -> int:
+    return int(load().twell_block_norm_workspace_bytes(T, d))
+
+
+def block_norm_workspace(T: int, d: int, device="cuda"):
+    """A workspace tensor for twell_block_norm_backward."""
+    import torch
+    return torch.empty(max(twell_block_norm_workspace_bytes(T, d), 256), dtype=torch.uint8, device=device)
+
+
+def twell_block_norm_backward(bn: BlockNorm, out, y, dout, dn, dres, dy, workspace, gate=None, gate_span: int = 0,
+                              dgate=None, dw_post=None, db_post=None, dw_pre=None, db_pre=None, stream=None):
+    """The forward's gradients; out is the forward's out (its res without a block); y, dout, dn, dy and the weight
+    gradients (float32 [d]) may be None (see include/twell.h)."""
+    import torch
+    fn = "twell_block_norm_backward"
+    o = bn.desc(fn, dres, y, gate, gate_span)
+    shape, dt = dres.shape, dres.dtype
+    p = {"out": out, "dout": dout, "dn": dn, "dy": dy}
+    want = {"out": dt, "dout": dt, "dn": None, "dy": None if y is None else y.dtype}
+    p = {k: None if t is None else _tensor(fn, k, t, shape, dres, want[k]) for k, t in p.items()}
+    p_dres = _tensor(fn, "dres", dres, shape, dres)
+    p_dgate = None if dgate is None else _tensor(fn, "dgate", dgate, gate.shape if gate is not None else (), dres, dt)
+    dw = [None if t is None else _tensor(fn, k, t, (shape[1],), dres, torch.float32)
+          for k, t in (("dw_post", dw_post), ("db_post", db_post), ("dw_pre", dw_pre), ("db_pre", db_pre))]
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(fn, load().twell_block_norm_backward(o, p["out"], _ptr(y), p["dout"], p["dn"],
+                                                TWELL_F32 if dn is None else vdtype_of(dn.dtype), p_dres, p["dy"],
+                                                p_dgate, *dw, _ptr(workspace), nbytes, _stream(stream)))
 
 
 # ---------------------------------------------------------------- the optimizer

@@ -1,0 +1,37 @@
+// block_norm.h -- arguments of the block norms (host and device side).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+namespace twell {
+
+constexpr int BN_MAX_D = 8192;   // 1024 threads of 8 elements hold a row
+constexpr int BN_BWD_WGS = 512;  // workgroups of the backward pass: each adds its rows' weight gradients
+
+// A tensor whose element type is known at run time.
+struct BnTensor {
+    void *p;
+    int bf16;
+};
+
+struct BnArgs {
+    int T, d;
+    int post;            // a norm after the block
+    float eps, alpha;
+    int gate_span;       // rows that share a gate row; 0 without a gate
+    BnTensor res, y, gate, out, n;   // forward: out, n written; backward: out read as `res`
+    BnTensor w_post, b_post, w_pre, b_pre;
+    // backward
+    BnTensor dout, dn, dres, dy, dgate;
+    float *dw[4];        // dw_post, db_post, dw_pre, db_pre (or NULL)
+    float *part;         // [6][wgs][d]: the four vectors, then the gate rows cut at a workgroup's first and last row
+    int wgs;
+    int rows;            // rows of a workgroup
+};
+
+hipError_t launch_block_norm(const BnArgs &a, bool layer, bool vec, hipStream_t s);
+hipError_t launch_block_norm_backward(const BnArgs &a, bool layer, bool vec, hipStream_t s);
+int block_norm_wgs(int T);
+
+}  // namespace twell

@@ -7,6 +7,7 @@
 #include <hip/hip_runtime.h>
 
 #include "adamw.h"
+#include "block_norm.h"
 #include "checks.h"
 
 namespace {
@@ -21,6 +22,52 @@ int check_vec(const void *p, size_t es)
     if (!p)
         return TWELL_E_NULL;
     return aligned_to(p, es) ? TWELL_OK : TWELL_E_ALIGN;
+}
+
+// The descriptor of the block norms, and with `gated` its gate pointer.
+int check_block_norm(const twell_block_norm_t *bn, bool gated)
+{
+    if (!bn)
+        return TWELL_E_NULL;
+    if ((bn->kind != TWELL_NORM_RMS && bn->kind != TWELL_NORM_LAYER) || !known_dtype(bn->rdtype) ||
+        !known_dtype(bn->ydtype) || !known_dtype(bn->ndtype) || !known_dtype(bn->wdtype) ||
+        bn->d > twell::BN_MAX_D)
+        return TWELL_E_UNSUPPORTED;
+    if (bn->T < 0 || bn->d < 1 || bn->gate_span < 0 || !(bn->eps > 0))
+        return TWELL_E_SHAPE;
+    for (const void *w : {bn->w_post, bn->b_post, bn->w_pre, bn->b_pre})
+        if (w)
+            TWELL_TRY(check_vec(w, elem_size(bn->wdtype)));
+    return gated && bn->T > 0 ? check_vec(bn->gate, elem_size(bn->rdtype)) : TWELL_OK;
+}
+
+twell::BnTensor bn_tensor(const void *p, int32_t dt) { return twell::BnTensor{const_cast<void *>(p), dt == TWELL_BF16}; }
+
+twell::BnArgs bn_args(const twell_block_norm_t *bn, bool block)
+{
+    twell::BnArgs a{};
+    a.T = bn->T;
+    a.d = bn->d;
+    a.post = block && bn->post;
+    a.eps = bn->eps;
+    a.alpha = bn->alpha;
+    a.gate_span = block ? bn->gate_span : 0;
+    a.gate = bn_tensor(a.gate_span ? bn->gate : nullptr, bn->rdtype);
+    a.w_post = bn_tensor(a.post ? bn->w_post : nullptr, bn->wdtype);
+    a.b_post = bn_tensor(a.post ? bn->b_post : nullptr, bn->wdtype);
+    a.w_pre = bn_tensor(bn->w_pre, bn->wdtype);
+    a.b_pre = bn_tensor(bn->b_pre, bn->wdtype);
+    return a;
+}
+
+// Whether every row of every tensor starts at a 16-byte boundary.
+bool bn_wide(const twell::BnArgs &a)
+{
+    bool ok = a.d % 8 == 0;
+    for (const twell::BnTensor *t : {&a.res, &a.y, &a.gate, &a.out, &a.n, &a.w_post, &a.b_post, &a.w_pre, &a.b_pre,
+                                     &a.dout, &a.dn, &a.dres, &a.dy, &a.dgate})
+        ok = ok && aligned16(t->p);
+    return ok;
 }
 
 // One descriptor of twell_adamw_step (grads) or twell_adamw_unpack (values).
@@ -54,6 +101,90 @@ int64_t aw_chunks(int64_t n) { return (n + twell::AW_CHUNK - 1) / twell::AW_CHUN
 }  // namespace
 
 extern "C" {
+
+int twell_block_norm_forward(const twell_block_norm_t *bn, const void *res, const void *y, void *out, void *n,
+                             void *stream)
+{
+    TWELL_TRY(check_block_norm(bn, bn && y && bn->gate_span));
+    if (bn->T == 0)
+        return TWELL_OK;
+    const int rs = elem_size(bn->rdtype);
+    TWELL_TRY(check_vec(res, rs));
+    if (y)
+        TWELL_TRY(check_vec(y, elem_size(bn->ydtype)));
+    else
+        out = nullptr;
+    if (!out && !n)
+        return TWELL_E_NULL;
+    if (out)
+        TWELL_TRY(check_vec(out, rs));
+    if (n)
+        TWELL_TRY(check_vec(n, elem_size(bn->ndtype)));
+    twell::BnArgs a = bn_args(bn, y != nullptr);
+    a.res = bn_tensor(res, bn->rdtype);
+    a.y = bn_tensor(y, bn->ydtype);
+    a.out = bn_tensor(out, bn->rdtype);
+    a.n = bn_tensor(n, bn->ndtype);
+    return hip_status(twell::launch_block_norm(a, bn->kind == TWELL_NORM_LAYER, bn_wide(a),
+                                               static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_block_norm_workspace_bytes(int32_t T, int32_t d)
+{
+    if (T < 0 || d < 1 || d > twell::BN_MAX_D)
+        return 0;
+    return (size_t)6 * twell::block_norm_wgs(T) * d * sizeof(float);
+}
+
+int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, const void *y, const void *dout,
+                              const void *dn, int32_t dndtype, void *dres, void *dy, void *dgate, float *dw_post,
+                              float *db_post, float *dw_pre, float *db_pre, void *workspace, size_t workspace_bytes,
+                              void *stream)
+{
+    const bool gated = bn && y && bn->gate_span;
+    TWELL_TRY(check_block_norm(bn, gated));
+    if (!known_dtype(dndtype))
+        return TWELL_E_UNSUPPORTED;
+    const int rs = elem_size(bn->rdtype), ys = elem_size(bn->ydtype);
+    for (const float *w : {dw_post, db_post, dw_pre, db_pre})
+        if (w)
+            TWELL_TRY(check_vec(w, 4));
+    if (bn->T > 0) {
+        if (!dout && !dn)
+            return TWELL_E_NULL;
+        if (dout)
+            TWELL_TRY(check_vec(dout, rs));
+        if (dn) {
+            TWELL_TRY(check_vec(dn, elem_size(dndtype)));
+            TWELL_TRY(check_vec(out, rs));
+        }
+        TWELL_TRY(check_vec(dres, rs));
+        if (y) {
+            TWELL_TRY(check_vec(y, ys));
+            TWELL_TRY(check_vec(dy, ys));
+        }
+        if (gated)
+            TWELL_TRY(check_vec(dgate, rs));
+        TWELL_TRY(check_ws(workspace, workspace_bytes, twell_block_norm_workspace_bytes(bn->T, bn->d)));
+    }
+    twell::BnArgs a = bn_args(bn, y != nullptr);
+    a.res = bn_tensor(dn ? out : nullptr, bn->rdtype);
+    a.y = bn_tensor(y, bn->ydtype);
+    a.dout = bn_tensor(dout, bn->rdtype);
+    a.dn = bn_tensor(dn, dndtype);
+    a.dres = bn_tensor(dres, bn->rdtype);
+    a.dy = bn_tensor(dy, bn->ydtype);
+    a.dgate = bn_tensor(gated ? dgate : nullptr, bn->rdtype);
+    a.dw[0] = dw_post;
+    a.dw[1] = db_post;
+    a.dw[2] = dw_pre;
+    a.dw[3] = db_pre;
+    a.part = static_cast<float *>(workspace);
+    a.wgs = twell::block_norm_wgs(bn->T);
+    a.rows = a.wgs ? (bn->T + a.wgs - 1) / a.wgs : 0;
+    return hip_status(twell::launch_block_norm_backward(a, bn->kind == TWELL_NORM_LAYER, bn_wide(a),
+                                                        static_cast<hipStream_t>(stream)));
+}
 
 int twell_adamw_step(const twell_adamw_tensor_t *tensors, int32_t count, int32_t state_bits, double lr, double beta1,
                      double beta2, double eps, int64_t step, uint32_t seed, const float *grad_scale, void *stream)
