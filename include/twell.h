@@ -18,6 +18,7 @@
  *   statistics  twell_pack_gate_stats
  *   training    twell_dense_to_hybrid, twell_hybrid_to_dense,
  *               twell_compact_hybrid, twell_compact_to_dense, twell_ffn_backward
+ *   dense       twell_glu_forward, twell_glu_backward
  *   norms       twell_block_norm_forward, twell_block_norm_backward
  *   optimizer   twell_adamw_step, twell_adamw_unpack
  *
@@ -393,6 +394,45 @@ TWELL_API int twell_ffn_backward(const twell_hybrid_t *hy, const void *x, const 
                                  const void *wd, int32_t d, const float *dy, float *dx, float *dwg, float *dwu,
                                  float *dwd, int32_t max_entries, void *workspace, size_t workspace_bytes,
                                  void *stream);
+
+/* ---- Dense gated product ---------------------------------------------------
+ * h = act(x . W_g) * (x . W_u): the gated FFN's hidden activation without
+ * sparsity, for layers or models whose activation is not sparse (or not ReLU).
+ * x [T][d], W_g^T and W_u^T [F][d], h [T][F], all vdtype (TWELL_BF16 with fp32
+ * accumulation, or TWELL_F32), 16-byte aligned; d and F multiples of 64, d <=
+ * 2^20, F <= 2^19. */
+enum twell_act {
+    TWELL_ACT_RELU = 0,
+    TWELL_ACT_SILU = 1,     /* g / (1 + exp(-g)) */
+    TWELL_ACT_GELU = 2,     /* g / 2 (1 + erf(g / sqrt 2)) */
+    TWELL_ACT_GELU_TANH = 3 /* g / 2 (1 + tanh(sqrt(2 / pi) (g + 0.044715 g^3))) */
+};
+
+/* g = x . W_g and u = x . W_u are written too where their pointers (device
+ * [T][F] vdtype) are not NULL: the backward pass takes them.  h comes from g
+ * and u before they are rounded.  For T <= 64 (bf16) the kernels are organised
+ * for few tokens.  Inputs are finite; a NaN or an infinity spoils at most its
+ * own row (of x) or column (of a weight).
+ * workspace : device, >= twell_glu_workspace_bytes(T, d, F, vdtype) (0 bytes:
+ * may be NULL), 256-byte aligned, content ignored on entry. */
+TWELL_API int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
+                                int32_t vdtype, int32_t act, void *h, void *g, void *u, void *workspace,
+                                size_t workspace_bytes, void *stream);
+TWELL_API size_t twell_glu_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype);
+
+/* Gradients of twell_glu_forward from the stored g and u and dh = dL/dh
+ * ([T][F] vdtype): with dg = dh u act'(g) and du = dh act(g) (rounded to
+ * vdtype for the products; act'(0) = 0 for ReLU),
+ *   dx = dg . W_g^T + du . W_u^T [T][d],  dwg = dg^T . x,  dwu = du^T . x [F][d],
+ * vdtype, overwritten, sums in fp32 in a fixed order.  dx NULL: not computed;
+ * dwg and dwu NULL: not computed (both or neither).
+ * workspace : device, >= twell_glu_backward_workspace_bytes(T, d, F, vdtype),
+ * 256-byte aligned, content ignored on entry (it holds dg and du). */
+TWELL_API int twell_glu_backward(const void *x, const void *wg_t, const void *wu_t, const void *g, const void *u,
+                                 const void *dh, int32_t T, int32_t d, int32_t F, int32_t vdtype, int32_t act,
+                                 void *dx, void *dwg, void *dwu, void *workspace, size_t workspace_bytes,
+                                 void *stream);
+TWELL_API size_t twell_glu_backward_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype);
 
 /* ---- Block norms -----------------------------------------------------------
  * The norms before and after a block with the block's gate, residual scale and

@@ -142,3 +142,29 @@ def act_grad(g, name):
     c = math.sqrt(2 / math.pi)
     t = torch.tanh(c * (g + 0.044715 * g ** 3))
     return 0.5 * (1 + t) + 0.5 * g * (1 - t * t) * c * (1 + 3 * 0.044715 * g * g)
+
+
+def glu_forward(x, wg, wu, name):
+    """{name: (value, bound)} of g, u and h; an fp32 sum of K products is off by at most K u of their magnitudes."""
+    x, wg, wu = x.double(), wg.double(), wu.double()
+    g, u = x @ wg.T, x @ wu.T
+    k = x.shape[1] * U
+    eg, eu = k * (x.abs() @ wg.abs().T), k * (x.abs() @ wu.abs().T)
+    a = act(g, name)
+    # the activations' own 32-bit evaluation, and slopes of at most 1.13
+    ea = 1.13 * eg + 4e-6 * (1 + g.abs())
+    return {"g": (g, eg), "u": (u, eu), "h": (a * u, ea * u.abs() + a.abs() * eu + ea * eu)}
+
+
+def glu_backward(x, wg, wu, g, u, dh, name, dtype):
+    """{name: (value, bound)} of dx, dwg, dwu; dg and du are rounded to dtype before the products."""
+    x, wg, wu, g, u, dh = (t.double() for t in (x, wg, wu, g, u, dh))
+    dg, du = dh * u * act_grad(g, name), dh * act(g, name)
+    slack = 4e-6 * (1 + g.abs()) ** 2
+    eg = half_step(dg, dtype) * 1.01 + slack * (dh * u).abs()
+    eu = half_step(du, dtype) * 1.01 + slack * dh.abs()
+    k, t = 2 * wg.shape[0] * U, x.shape[0] * U
+    ag, au = dg.abs() + eg, du.abs() + eu
+    return {"dx": (dg @ wg + du @ wu, eg @ wg.abs() + eu @ wu.abs() + k * (ag @ wg.abs() + au @ wu.abs())),
+            "dwg": (dg.T @ x, eg.T @ x.abs() + t * (ag.T @ x.abs())),
+            "dwu": (du.T @ x, eu.T @ x.abs() + t * (au.T @ x.abs()))}

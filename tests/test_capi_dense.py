@@ -91,3 +91,34 @@ def test_block_norm_validation():
     assert b(dw=GOOD + 2) == ALIGN
     assert b(dndtype=3) == UNSUPPORTED
     assert b(ws=None) == WORKSPACE and b(nbytes=need - 1) == WORKSPACE and b(ws=GOOD + 128) == ALIGN
+
+
+def test_glu_validation():
+    lib = tw.load()
+
+    def f(x=GOOD, wg=GOOD, wu=GOOD, T=8, d=64, F=128, vd=1, act=1, h=GOOD, g=None, u=None):
+        return lib.twell_glu_forward(x, wg, wu, T, d, F, vd, act, h, g, u, None, 0, None)
+
+    for k in ("x", "wg", "wu", "h"):
+        assert f(**{k: None}) == NULL and f(**{k: GOOD + 8}) == ALIGN, k
+    assert f(g=GOOD + 2) == ALIGN and f(u=GOOD + 8) == ALIGN
+    assert f(T=0, x=None, h=None) == 0
+    for kw in (dict(T=-1), dict(d=0), dict(d=96), dict(F=100), dict(F=0), dict(d=-64)):
+        assert f(**kw) == SHAPE, kw
+    for kw in (dict(vd=2), dict(act=-1), dict(act=4), dict(d=(1 << 20) + 64), dict(F=(1 << 19) + 64)):
+        assert f(**kw) == UNSUPPORTED, kw
+    assert f(T=(1 << 31) - 1, F=1 << 19) == SHAPE
+    size = lib.twell_glu_backward_workspace_bytes
+    assert size(8, 60, 128, 1) == 0 and size(-1, 64, 128, 1) == 0 and size(8, 64, 128, 3) == 0
+    need = size(8, 64, 128, 1)
+    assert need >= 64 * 256 * 2
+
+    def b(x=GOOD, wg=GOOD, wu=GOOD, g=GOOD, u=GOOD, dh=GOOD, dx=GOOD, dwg=GOOD, dwu=GOOD, ws=GOOD, nbytes=need):
+        return lib.twell_glu_backward(x, wg, wu, g, u, dh, 8, 64, 128, 1, 1, dx, dwg, dwu, ws, nbytes, None)
+
+    for k in ("x", "wg", "wu", "g", "u", "dh"):
+        assert b(**{k: None}) == NULL and b(**{k: GOOD + 4}) == ALIGN, k
+    assert b(dx=None, dwg=None, dwu=None) == NULL and b(dwg=None) == NULL and b(dwu=None) == NULL
+    for k in ("dx", "dwg", "dwu"):
+        assert b(**{k: GOOD + 8}) == ALIGN, k
+    assert b(ws=None) == WORKSPACE and b(nbytes=need - 1) == WORKSPACE and b(ws=GOOD + 16) == ALIGN

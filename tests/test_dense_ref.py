@@ -50,3 +50,17 @@ def test_act(name):
     theirs = {"relu": torch.relu, "silu": torch.nn.functional.silu, "gelu": torch.nn.functional.gelu,
               "gelu_tanh": lambda x: torch.nn.functional.gelu(x, approximate="tanh")}[name](g)
     assert torch.allclose(dense_ref.act(g, name), theirs, atol=1e-12)
+
+
+@pytest.mark.parametrize("name", ["relu", "silu", "gelu", "gelu_tanh"])
+def test_glu_backward_against_differences(name):
+    gen = torch.Generator().manual_seed(8)
+    rnd = lambda *s: torch.randn(s, generator=gen, dtype=torch.float64)  # noqa: E731
+    val = dict(x=rnd(3, 4), wg=rnd(5, 4), wu=rnd(5, 4))
+    dh = rnd(3, 5)
+    fwd = dense_ref.glu_forward(**val, name=name)
+    got = dense_ref.glu_backward(val["x"], val["wg"], val["wu"], fwd["g"][0], fwd["u"][0], dh, name, torch.float32)
+    for k in val:
+        want = _difference(lambda x: float((dense_ref.glu_forward(**dict(val, **{k: x}), name=name)["h"][0] * dh).sum()),
+                           val[k])
+        assert torch.allclose(got["d" + k][0], want, rtol=1e-6, atol=1e-7), k

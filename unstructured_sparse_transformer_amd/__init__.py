@@ -13,7 +13,8 @@ The functions carry the C names (``include/twell.h``):
 ``twell_ffn_decode_workspace_bytes``, ``twell_ffn_decode_noalloc``, ``twell_dense_to_hybrid``,
 ``twell_hybrid_to_dense``, ``twell_compact_min_bytes``, ``twell_compact_hybrid``,
 ``twell_compact_to_dense``, ``twell_ffn_backward``,
-``twell_ffn_backward_workspace_bytes``, ``twell_block_norm_forward``,
+``twell_ffn_backward_workspace_bytes``, ``twell_glu_forward``, ``twell_glu_workspace_bytes``,
+``twell_glu_backward``, ``twell_glu_backward_workspace_bytes``, ``twell_block_norm_forward``,
 ``twell_block_norm_workspace_bytes``, ``twell_block_norm_backward``, ``twell_adamw_step``, ``twell_adamw_unpack``.
 
 One layer's forward pass, bf16 (x [T][d], W_g^T and W_u^T [F][d], W_d [F][d],
@@ -47,7 +48,8 @@ EXPORTS = ("twell_ffn_forward", "twell_ffn_from_gate", "twell_pack_gate", "twell
            "twell_ffn_fused", "twell_workspace_bytes", "twell_ffn_overflow", "twell_ffn_hybrid",
            "twell_ffn_decode_workspace_bytes", "twell_ffn_decode", "twell_ffn_decode_noalloc", "twell_dense_to_hybrid", "twell_hybrid_to_dense",
            "twell_compact_min_bytes", "twell_compact_hybrid", "twell_compact_to_dense",
-           "twell_ffn_backward_workspace_bytes", "twell_ffn_backward", "twell_block_norm_forward",
+           "twell_ffn_backward_workspace_bytes", "twell_ffn_backward", "twell_glu_workspace_bytes",
+           "twell_glu_forward", "twell_glu_backward_workspace_bytes", "twell_glu_backward", "twell_block_norm_forward",
            "twell_block_norm_workspace_bytes", "twell_block_norm_backward", "twell_adamw_step", "twell_adamw_unpack",
            "twell_status_str", "twell_version")
 
@@ -126,6 +128,11 @@ def load(path: str = LIB_PATH):
     lib.twell_ffn_backward_workspace_bytes.restype = ctypes.c_size_t
     lib.twell_ffn_backward.argtypes = [ctypes.POINTER(TwellHybridT), P, P, P, P, I32, P, P, P, P, P, I32, P,
                                        ctypes.c_size_t, P]
+    for fn in (lib.twell_glu_workspace_bytes, lib.twell_glu_backward_workspace_bytes):
+        fn.argtypes = [I32, I32, I32, I32]
+        fn.restype = ctypes.c_size_t
+    lib.twell_glu_forward.argtypes = [P, P, P, I32, I32, I32, I32, I32, P, P, P, P, ctypes.c_size_t, P]
+    lib.twell_glu_backward.argtypes = [P, P, P, P, P, P, I32, I32, I32, I32, I32, P, P, P, P, ctypes.c_size_t, P]
     BN = ctypes.POINTER(TwellBlockNormT)
     lib.twell_block_norm_forward.argtypes = [BN, P, P, P, P, P]
     lib.twell_block_norm_workspace_bytes.argtypes = [I32, I32]
@@ -141,7 +148,8 @@ def load(path: str = LIB_PATH):
                lib.twell_ffn_fused, lib.twell_ffn_hybrid, lib.twell_ffn_overflow, lib.twell_ffn_forward,
                lib.twell_ffn_from_gate, lib.twell_ffn_decode, lib.twell_ffn_decode_noalloc,
                lib.twell_dense_to_hybrid, lib.twell_hybrid_to_dense, lib.twell_compact_hybrid,
-               lib.twell_compact_to_dense, lib.twell_ffn_backward, lib.twell_block_norm_forward,
+               lib.twell_compact_to_dense, lib.twell_ffn_backward, lib.twell_glu_forward,
+               lib.twell_glu_backward, lib.twell_block_norm_forward,
                lib.twell_block_norm_backward, lib.twell_adamw_step, lib.twell_adamw_unpack):
         fn.restype = ctypes.c_int
     _lib = lib
@@ -416,10 +424,7 @@ def hybrid_workspace(hy: "Hybrid", d: int, device="cuda"):
     return workspace(e.T, e.F, e.tile_w, e.cap, hy.max_ovf, d, e.dtype, device)
 
 
-# ---------------------------------------------------------------- block norms
-NORM_KINDS = {"rms": 0, "layer": 1}
-
-
+# ---------------------------------------------------------------- the dense gated product
 def _tensor(fn: str, name: str, t, shape, like, dtype=None):
     """Checks an argument: contiguous, on `like`'s device, of this shape and (if given) element type."""
     if t is None:
@@ -433,6 +438,65 @@ def _tensor(fn: str, name: str, t, shape, like, dtype=None):
     if dtype is not None and t.dtype != dtype:
         raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
     return t.data_ptr()
+
+
+ACTS = {"relu": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
+
+
+def _act(fn: str, act: str) -> int:
+    if act not in ACTS:
+        raise ValueError(f"{fn}: act {act!r}: one of {', '.join(ACTS)}")
+    return ACTS[act]
+
+
+def twell_glu_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
+    return int(load().twell_glu_workspace_bytes(T, d, F, vdtype_of(dtype)))
+
+
+def glu_workspace(T: int, d: int, F: int, dtype, device="cuda"):
+    """A workspace tensor for twell_glu_forward, or None when it needs none."""
+    import torch
+    n = twell_glu_workspace_bytes(T, d, F, dtype)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def twell_glu_forward(x, wg_t, wu_t, act: str, h, workspace=None, g=None, u=None, stream=None):
+    """h = act(x W_g) * (x W_u); g and u (optional, h's shape) receive the two products for the backward pass."""
+    fn = "twell_glu_forward"
+    (T, d), (F, _), dt = x.shape, wg_t.shape, x.dtype
+    p = [_tensor(fn, k, t, s, x, dt) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)), ("wu_t", wu_t, (F, d)),
+                                                     ("h", h, (T, F)))]
+    pg, pu = (None if t is None else _tensor(fn, k, t, (T, F), x, dt) for k, t in (("g", g), ("u", u)))
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(fn, load().twell_glu_forward(p[0], p[1], p[2], T, d, F, vdtype_of(dt), _act(fn, act), p[3], pg, pu,
+                                        _ptr(workspace), nbytes, _stream(stream)))
+
+
+def twell_glu_backward_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
+    return int(load().twell_glu_backward_workspace_bytes(T, d, F, vdtype_of(dtype)))
+
+
+def glu_backward_workspace(T: int, d: int, F: int, dtype, device="cuda"):
+    """A workspace tensor for twell_glu_backward."""
+    import torch
+    return torch.empty(max(twell_glu_backward_workspace_bytes(T, d, F, dtype), 256), dtype=torch.uint8, device=device)
+
+
+def twell_glu_backward(x, wg_t, wu_t, g, u, dh, act: str, dx, dwg, dwu, workspace, stream=None):
+    """dx [T][d], dwg and dwu [F][d] (dx, or both of the others, may be None) from the forward's g and u and dh."""
+    fn = "twell_glu_backward"
+    (T, d), (F, _), dt = x.shape, wg_t.shape, x.dtype
+    p = [_tensor(fn, k, t, s, x, dt) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)), ("wu_t", wu_t, (F, d)),
+                                                     ("g", g, (T, F)), ("u", u, (T, F)), ("dh", dh, (T, F)))]
+    o = [None if t is None else _tensor(fn, k, t, s, x, dt)
+         for k, t, s in (("dx", dx, (T, d)), ("dwg", dwg, (F, d)), ("dwu", dwu, (F, d)))]
+    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
+    _check(fn, load().twell_glu_backward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *o, _ptr(workspace), nbytes,
+                                         _stream(stream)))
+
+
+# ---------------------------------------------------------------- block norms
+NORM_KINDS = {"rms": 0, "layer": 1}
 
 
 class BlockNorm:

@@ -9,6 +9,7 @@
 #include "adamw.h"
 #include "block_norm.h"
 #include "checks.h"
+#include "glu.h"
 
 namespace {
 
@@ -22,6 +23,20 @@ int check_vec(const void *p, size_t es)
     if (!p)
         return TWELL_E_NULL;
     return aligned_to(p, es) ? TWELL_OK : TWELL_E_ALIGN;
+}
+
+// Sizes and types of the gated product.
+int check_glu(int32_t T, int32_t d, int32_t F, int32_t vdtype, int32_t act)
+{
+    if (!known_dtype(vdtype) || act < TWELL_ACT_RELU || act > TWELL_ACT_GELU_TANH)
+        return TWELL_E_UNSUPPORTED;
+    if (T < 0 || d <= 0 || F <= 0 || d % 64 != 0 || F % 64 != 0)
+        return TWELL_E_SHAPE;
+    // a tile's rows are addressed with 32-bit offsets
+    if (d > (1 << 20) || F > (1 << 19))
+        return TWELL_E_UNSUPPORTED;
+    // workgroups of 64 x 64 results, split up to 16 times
+    return ((int64_t)T + 63) / 64 * (F / 64 > d / 64 ? F / 64 : d / 64) * 16 < ((int64_t)1 << 31) ? TWELL_OK : TWELL_E_SHAPE;
 }
 
 // The descriptor of the block norms, and with `gated` its gate pointer.
@@ -101,6 +116,81 @@ int64_t aw_chunks(int64_t n) { return (n + twell::AW_CHUNK - 1) / twell::AW_CHUN
 }  // namespace
 
 extern "C" {
+
+size_t twell_glu_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype)
+{
+    (void)T, (void)d, (void)F, (void)vdtype;
+    return 0;
+}
+
+int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
+                      int32_t vdtype, int32_t act, void *h, void *g, void *u, void *workspace, size_t workspace_bytes,
+                      void *stream)
+{
+    TWELL_TRY(check_glu(T, d, F, vdtype, act));
+    if (T == 0)
+        return TWELL_OK;
+    TWELL_TRY(check_mat(x));
+    TWELL_TRY(check_mat(wg_t));
+    TWELL_TRY(check_mat(wu_t));
+    TWELL_TRY(check_mat(h));
+    if (!aligned16(g) || !aligned16(u))
+        return TWELL_E_ALIGN;
+    TWELL_TRY(check_ws(workspace, workspace_bytes, twell_glu_workspace_bytes(T, d, F, vdtype)));
+    twell::GluFwd a{};
+    a.T = T;
+    a.d = d;
+    a.F = F;
+    a.act = act;
+    a.x = x;
+    a.wg = wg_t;
+    a.wu = wu_t;
+    a.h = h;
+    a.g = g;
+    a.u = u;
+    return hip_status(twell::launch_glu(vdtype, a, static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_glu_backward_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype)
+{
+    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_backward_ws(T, d, F, vdtype).bytes : 0;
+}
+
+int twell_glu_backward(const void *x, const void *wg_t, const void *wu_t, const void *g, const void *u, const void *dh,
+                       int32_t T, int32_t d, int32_t F, int32_t vdtype, int32_t act, void *dx, void *dwg, void *dwu,
+                       void *workspace, size_t workspace_bytes, void *stream)
+{
+    TWELL_TRY(check_glu(T, d, F, vdtype, act));
+    if (T > 0) {
+        for (const void *p : {x, wg_t, wu_t, g, u, dh})
+            TWELL_TRY(check_mat(p));
+        if (!dx && !dwg)
+            return TWELL_E_NULL;
+    }
+    if (!dwg != !dwu)
+        return TWELL_E_NULL;
+    if (!aligned16(dx) || !aligned16(dwg) || !aligned16(dwu))
+        return TWELL_E_ALIGN;
+    const twell::GluWs w = twell::glu_backward_ws(T, d, F, vdtype);
+    TWELL_TRY(check_ws(workspace, workspace_bytes, w.bytes));
+    twell::GluBwd a{};
+    a.T = T;
+    a.d = d;
+    a.F = F;
+    a.act = act;
+    a.x = x;
+    a.wg = wg_t;
+    a.wu = wu_t;
+    a.g = g;
+    a.u = u;
+    a.dh = dh;
+    a.dx = dx;
+    a.dwg = dwg;
+    a.dwu = dwu;
+    a.dgu = static_cast<char *>(workspace) + w.dgu;
+    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.part);
+    return hip_status(twell::launch_glu_backward(vdtype, a, static_cast<hipStream_t>(stream)));
+}
 
 int twell_block_norm_forward(const twell_block_norm_t *bn, const void *res, const void *y, void *out, void *n,
                              void *stream)

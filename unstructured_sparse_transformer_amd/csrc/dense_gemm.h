@@ -1,0 +1,265 @@
+// dense_gemm.h -- the matrix-product core of the gated product (gfx950).
+//
+// C[m][n] = sum_k A(m, k) B(k, n) on workgroup tiles of BM x BN, K in stages of
+// 64 bf16 elements, fp32 accumulators (v_mfma_f32_32x32x16_bf16).  Each operand
+// is read as it lies in memory:
+//   KC  rows of its M (or N) index, K contiguous:   x and W of the forward pass
+//   KS  rows of K, its M (or N) index contiguous:   W in dx, x and dg in dW
+// A stage of either is 128 bytes per M (or N) index, copied by global->LDS
+// instructions of 1 KiB per wave.  KC stages keep 128-byte rows with XORed
+// 16-byte chunks (lds_off); KS stages keep the raw rows, their chunks XORed so
+// that a transposing LDS read (ds_read_b64_tr_b16) of 4 rows meets every bank
+// once.
+#pragma once
+
+#include "twell_device.h"
+
+namespace twell {
+
+// Tiles' 64-bit base addresses with 32-bit offsets inside a tile: the matrices
+// themselves have no size limit.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t dg_rsrc(const void *base)
+{
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, -1, 0x00020000);
+}
+
+// One operand of a workgroup: IDX tile indices, NW waves.  DB > 0 (KC only):
+// the tile's rows alternate between two matrices in blocks of DB (row 2 DB q +
+// r, r < DB, is column DB q + r of the first, row 2 DB q + DB + r of the second).
+template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
+    static constexpr int BYTES = IDX * 128;
+    static constexpr int LD = IDX / 8 / NW;          // 1 KiB copies per wave and stage
+    static constexpr int RAW = IDX * 2;              // KS: bytes of a raw row
+    static constexpr int RPI = KC ? 8 : 1024 / RAW;  // rows per copy
+    static_assert(IDX % (8 * NW) == 0, "copies split over the waves");
+    static_assert(KC || (RAW >= 256 && RAW <= 1024), "raw rows span whole 256-byte bank windows");
+    static_assert(DB == 0 || (KC && DB % 8 == 0), "a copy's rows belong to one matrix");
+
+    const char *base;  // at the workgroup's first index and stage 0
+    int64_t other;     // bytes from there to the same place of the second matrix (DB; KS: from stage `turn` on)
+    int64_t step;      // bytes from one stage to the next
+    int turn;          // KS: first stage of the second matrix
+    int last, voff[LD], vlast[LD];
+
+    __device__ __forceinline__ static int raw_slot(int r, int c) { return c ^ ((r & 3) << 2); }
+
+    // idx0: the workgroup's first index, n: indices there are, ld: bytes between rows, k: K elements there are (KS:
+    // the last stage's rows past k repeat row k - 1; the other operand holds zeros there).
+    __device__ __forceinline__ void setup(const void *p, const void *p2, int64_t ld, int idx0, int n, int k, int turn_,
+                                          int wave, int lane)
+    {
+        turn = turn_;
+        last = (k - 1) >> 6;
+        if constexpr (KC) {
+            const int first = DB > 0 ? idx0 / 2 : idx0;  // DB: idx0 counts the rows of both
+            base = (const char *)p + (int64_t)first * ld;
+            other = (const char *)p2 - (const char *)p;
+            step = 128;
+#pragma unroll
+            for (int j = 0; j < LD; ++j) {
+                const int r = (j * NW + wave) * 8 + (lane >> 3);
+                const int c = (lane & 7) ^ ((r >> 1) & 7);
+                int q = DB > 0 ? r / (2 * DB) * DB + r % DB : r;
+                q = first + q < n ? q : n - 1 - first;  // rows past the end repeat the last; their results are dropped
+                voff[j] = q * (int)ld + c * 16;
+            }
+        } else {
+            base = (const char *)p + (int64_t)idx0 * 2;
+            step = 64 * ld;
+            other = (const char *)p2 - (const char *)p - turn_ * step;
+#pragma unroll
+            for (int j = 0; j < LD; ++j) {
+                const int r = (j * NW + wave) * RPI + lane / (RAW / 16);
+                int c = raw_slot(r, lane % (RAW / 16)) * 8;
+                c = idx0 + c <= n - 8 ? c : n - 8 - idx0;
+                voff[j] = r * (int)ld + c * 2;
+                const int rl = last * 64 + r < k ? r : k - 1 - last * 64;
+                vlast[j] = rl * (int)ld + c * 2;
+            }
+        }
+    }
+
+    // Copy j of stage kt into the operand's LDS area.
+    __device__ __forceinline__ void copy(int kt, int j, char *lds, int wave) const
+    {
+        char *dst = lds + (j * NW + wave) * 1024;
+        if constexpr (KC) {
+            const bool second = DB > 0 && ((((j * NW + wave) * 8) / (DB > 0 ? DB : 1)) & 1);
+            dma16(dg_rsrc(base + (second ? other : 0)), dst, voff[j], kt * 128);
+        } else {
+            dma16(dg_rsrc(base + (kt * step + (kt < turn ? 0 : other))), dst, kt == last ? vlast[j] : voff[j], 0);
+        }
+    }
+
+    // The fragment of 32 indices from i0, K sub-step ss (16 elements): lane l
+    // holds index i0 + l % 32, elements 16 ss + 8 (l / 32) .. + 7.
+    __device__ __forceinline__ static u32x4 fragment(const char *lds, int i0, int ss, int lane)
+    {
+        if constexpr (KC) {
+            return *reinterpret_cast<const u32x4 *>(lds + lds_off<128>(i0 + (lane & 31), ss * 2 + (lane >> 5)));
+        } else {
+            // Within a 16-lane group the transposing read hands lane i element i % 4 of the 8-byte pieces addressed
+            // by lanes i / 4 + 4 j (j < 4) as its values j: lane p addresses row k0 + p / 4 (+ 4 for the second
+            // half), columns 4 (p % 4) .. + 3 of the group's 16.
+            typedef short v4s __attribute__((ext_vector_type(4)));
+            const int grp = lane >> 4, p = lane & 15;
+            const int k0 = ss * 16 + ((grp >> 1) << 3) + (p >> 2);
+            const int i = i0 + ((grp & 1) << 4) + ((p & 3) << 2);
+            uint2 w[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                const int r = k0 + 4 * half;
+                const char *a = lds + r * RAW + (raw_slot(r, i >> 3) << 4) + (((i >> 2) & 1) << 3);
+                w[half] = __builtin_bit_cast(
+                    uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(a)));
+            }
+            return u32x4{w[0].x, w[0].y, w[1].x, w[1].y};
+        }
+    }
+};
+
+template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> struct DgCore {
+    static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, THREADS = NW * 64;
+    static constexpr int FM = WM / 32, FN = WN / 32;
+    using A = DgOperand<BM, A_KC, NW>;
+    using B = DgOperand<BN, B_KC, NW, DB>;
+    static constexpr int STAGE = A::BYTES + B::BYTES;
+    static constexpr int LDS = 2 * STAGE;
+    static constexpr int COPIES = A::LD + B::LD;
+    static_assert(DB == 0 || WN == 2 * DB, "a wave holds both products of its columns");
+
+    A a;
+    B b;
+
+    __device__ __forceinline__ void copy(int kt, int c, char *buf, int wave) const
+    {
+        if (c < A::LD)
+            a.copy(kt, c, buf, wave);
+        else
+            b.copy(kt, c - A::LD, buf + A::BYTES, wave);
+    }
+
+    __device__ __forceinline__ static void fragments(const char *buf, int wm, int wn, int ss, int lane, u32x4 (&af)[FM],
+                                                     u32x4 (&bf)[FN])
+    {
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+            af[f] = A::fragment(buf, wm * WM + f * 32, ss, lane);
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+            bf[f] = B::fragment(buf + A::BYTES, wn * WN + f * 32, ss, lane);
+    }
+
+    // The MFMAs of a sub-step with copies C0..C1-1 of stage kt spread between them.
+    template <int C0, int C1>
+    __device__ __forceinline__ void products(const u32x4 (&af)[FM], const u32x4 (&bf)[FN], f32x16 (&acc)[FM][FN], int kt,
+                                             char *buf, int wave, bool on) const
+    {
+        constexpr int NM = FM * FN, NC = C1 - C0;
+#pragma unroll
+        for (int q = 0; q < NM; ++q) {
+            mfma_chunk(__bf16{}, af[q / FN], bf[q % FN], acc[q / FN][q % FN]);
+#pragma unroll
+            for (int c = C0; c < C1; ++c)
+                if ((c - C0) * NM / (NC > 0 ? NC : 1) == q && on)
+                    copy(kt, c, buf, wave);
+            __builtin_amdgcn_sched_barrier(0);
+        }
+    }
+
+    // Stages [k0, k1): two LDS slots; the copies of stage kt + 2 go into stage
+    // kt's slot once the barrier before stage kt's last sub-step has passed,
+    // half between that sub-step's MFMAs and half between the next one's, and
+    // fragments are read one sub-step ahead.  Ends with a barrier: the caller
+    // may use `smem`.
+    __device__ __forceinline__ void run(int k0, int k1, char *smem, int tid, f32x16 (&acc)[FM][FN]) const
+    {
+        constexpr int H = COPIES / 2;
+        const int lane = tid & 63;
+        const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+        const int wm = wave / NWN, wn = wave % NWN;
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    acc[fm][fn][i] = 0.f;
+        if (k0 < k1) {
+#pragma unroll
+            for (int c = 0; c < COPIES; ++c)
+                copy(k0, c, smem, wave);
+            __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+            wg_barrier();
+            u32x4 af[2][FM], bf[2][FN];
+            fragments(smem, wm, wn, 0, lane, af[0], bf[0]);
+            if (k0 + 1 < k1) {
+#pragma unroll
+                for (int c = 0; c < COPIES; ++c)
+                    copy(k0 + 1, c, smem + STAGE, wave);
+            }
+            int slot = 0;
+#pragma clang loop unroll(disable)
+            for (int kt = k0; kt < k1; ++kt) {
+                char *cur = smem + slot * STAGE, *nxt = smem + (slot ^ 1) * STAGE;
+                const bool pend = kt > k0 && kt + 1 < k1;
+#pragma unroll
+                for (int ss = 0; ss < 4; ++ss) {
+                    const int cb = ss & 1, nb = cb ^ 1;
+                    if (ss < 3) {
+                        fragments(cur, wm, wn, ss + 1, lane, af[nb], bf[nb]);
+                        __builtin_amdgcn_sched_barrier(0);
+                    } else {
+                        __builtin_amdgcn_sched_barrier(0);
+                        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot has been read
+                        if (kt + 1 < k1) {
+                            __builtin_amdgcn_s_waitcnt(0x0070);  // stage kt + 1 has arrived
+                            wg_barrier();
+                            fragments(nxt, wm, wn, 0, lane, af[nb], bf[nb]);
+                            __builtin_amdgcn_sched_barrier(0);
+                        }
+                    }
+                    if (ss == 0)
+                        products<H, COPIES>(af[cb], bf[cb], acc, kt + 1, nxt, wave, pend);
+                    else if (ss == 3)
+                        products<0, H>(af[cb], bf[cb], acc, kt + 2, cur, wave, kt + 2 < k1);
+                    else
+                        products<0, 0>(af[cb], bf[cb], acc, 0, cur, wave, false);
+                }
+                slot ^= 1;
+            }
+        }
+        __syncthreads();
+    }
+};
+
+// A wave's block of 32 rows by 32 NB columns in bf16, from accumulator layout
+// (value(fn, i)) to memory by way of LDS: 16-byte stores of whole row pieces.
+// `lds`: 32 * (64 NB + 16) bytes of the wave's own (the 16 bytes keep the two
+// half-waves' rows, 4 apart, on different banks).
+template <int NB> constexpr int dg_stage_bytes() { return 32 * (64 * NB + 16); }
+template <int NB, typename V>
+__device__ __forceinline__ void dg_store_rows(char *lds, int lane, V value, __bf16 *out, int64_t ld, int m0, int n0,
+                                              int M, int N)
+{
+    constexpr int PITCH = 64 * NB + 16;
+    asm volatile("" ::: "memory");
+#pragma unroll
+    for (int fn = 0; fn < NB; ++fn)
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            *reinterpret_cast<__bf16 *>(lds + acc_row(i, lane) * PITCH + (fn * 32 + (lane & 31)) * 2) =
+                (__bf16)value(fn, i);
+    asm volatile("" ::: "memory");
+    constexpr int CPR = 4 * NB;  // 16-byte chunks of a row
+#pragma unroll
+    for (int c0 = 0; c0 < 32 * CPR; c0 += 64) {
+        const int c = c0 + lane, r = c / CPR, q = c % CPR;
+        const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * PITCH + q * 16);
+        if (m0 + r < M && n0 + q * 8 < N)
+            *reinterpret_cast<u32x4 *>(out + (int64_t)(m0 + r) * ld + n0 + q * 8) = v;
+    }
+    asm volatile("" ::: "memory");
+}
+
+}  // namespace twell

@@ -1,0 +1,36 @@
+// glu.h -- arguments of the dense gated product (host and device side).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace twell {
+
+enum GluAct { GLU_RELU = 0, GLU_SILU = 1, GLU_GELU = 2, GLU_GELU_TANH = 3 };
+
+constexpr int GLU_FEW = 64;  // rows up to which the forward pass streams the weights (bf16)
+
+struct GluFwd {
+    int T, d, F, act, MT, NT;
+    const void *x, *wg, *wu;
+    void *h, *g, *u;  // g, u may be NULL
+};
+
+struct GluBwd {
+    int T, d, F, act;
+    const void *x, *wg, *wu, *g, *u, *dh;
+    void *dx, *dwg, *dwu;  // NULL: not wanted
+    void *dgu;             // [T to a multiple of 64][2 F]: a row's dg, then its du
+    float *part;           // split-K partial sums
+};
+
+struct GluWs {
+    size_t dgu, part, bytes;  // offsets
+};
+GluWs glu_backward_ws(int T, int d, int F, int vdtype);
+
+hipError_t launch_glu(int vdtype, const GluFwd &a, hipStream_t s);
+hipError_t launch_glu_backward(int vdtype, const GluBwd &a, hipStream_t s);
+
+}  // namespace twell
