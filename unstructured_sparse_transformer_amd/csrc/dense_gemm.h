@@ -23,6 +23,58 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dg_rsrc(const void *base)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, -1, 0x00020000);
 }
 
+// Tiles to workgroups.  Workgroup g runs on XCD g % 8, and each XCD has an L2 of
+// its own: the tile grid is cut into 8 rectangles of `rows` x `cols` tiles, xm
+// of them down and 8 / xm across, one per XCD, and a rectangle is walked in
+// bands of 8 tile rows, so that the 32 workgroups an XCD runs at once form a
+// block of 8 x 4 tiles and read 12 operand tiles instead of up to 33.
+struct DgTiles {
+    int MT, NT, xm, rows, cols;
+};
+
+// Tile (mt, nt) of workgroup g; the splits follow one another.  False: a
+// rectangle's place past the grid's edge.
+__device__ __forceinline__ bool dg_tile(const DgTiles &t, int g, int &mt, int &nt, int &split)
+{
+    const int xcd = g & 7, per = t.rows * t.cols;
+    int s = g >> 3;
+    split = s / per;
+    s -= split * per;
+    const int band = s / (8 * t.cols), r = s - band * 8 * t.cols;
+    const int left = t.rows - band * 8, h = left < 8 ? left : 8;
+    mt = xcd % t.xm * t.rows + band * 8 + r % h;
+    nt = xcd / t.xm * t.cols + r / h;
+    return mt < t.MT && nt < t.NT;
+}
+
+// The cut with the fewest workgroups per XCD (places past the edge idle), then
+// the smallest block of operands in flight.
+inline DgTiles dg_tiles(int64_t MT, int64_t NT)
+{
+    DgTiles best{};
+    int64_t best_cost = INT64_MAX;
+    for (int xm = 1; xm <= 8; xm *= 2) {
+        const int64_t xn = 8 / xm, rows = (MT + xm - 1) / xm, cols = (NT + xn - 1) / xn;
+        const int64_t h = rows < 8 ? rows : 8, w = cols < 32 / h ? cols : 32 / h;
+        const int64_t cost = rows * cols * 4096 + (h + w) * 4096 / (h * w);
+        if (cost < best_cost) {
+            best_cost = cost;
+            best = DgTiles{(int)MT, (int)NT, xm, (int)rows, (int)cols};
+        }
+    }
+    return best;
+}
+
+// A transposing LDS read.  `restrict` gives the instruction alias information
+// of its own: without any, the compiler waits for every global->LDS copy in
+// flight before it (vmcnt(0)), which would serialise copies and products.  The
+// waits that are due stand in the K loop.
+typedef short dg_v4s __attribute__((ext_vector_type(4)));
+__device__ __forceinline__ uint2 dg_read_tr(__attribute__((address_space(3))) dg_v4s *__restrict p)
+{
+    return __builtin_bit_cast(uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16(p));
+}
+
 // One operand of a workgroup: IDX tile indices, NW waves.  DB > 0 (KC only):
 // the tile's rows alternate between two matrices in blocks of DB (row 2 DB q +
 // r, r < DB, is column DB q + r of the first, row 2 DB q + DB + r of the second).
@@ -59,7 +111,8 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
             for (int j = 0; j < LD; ++j) {
                 const int r = (j * NW + wave) * 8 + (lane >> 3);
                 const int c = (lane & 7) ^ ((r >> 1) & 7);
-                int q = DB > 0 ? r / (2 * DB) * DB + r % DB : r;
+                constexpr int D = DB > 0 ? DB : 1;
+                int q = DB > 0 ? r / (2 * D) * D + r % D : r;
                 q = first + q < n ? q : n - 1 - first;  // rows past the end repeat the last; their results are dropped
                 voff[j] = q * (int)ld + c * 16;
             }
@@ -101,7 +154,6 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
             // Within a 16-lane group the transposing read hands lane i element i % 4 of the 8-byte pieces addressed
             // by lanes i / 4 + 4 j (j < 4) as its values j: lane p addresses row k0 + p / 4 (+ 4 for the second
             // half), columns 4 (p % 4) .. + 3 of the group's 16.
-            typedef short v4s __attribute__((ext_vector_type(4)));
             const int grp = lane >> 4, p = lane & 15;
             const int k0 = ss * 16 + ((grp >> 1) << 3) + (p >> 2);
             const int i = i0 + ((grp & 1) << 4) + ((p & 3) << 2);
@@ -110,8 +162,7 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
             for (int half = 0; half < 2; ++half) {
                 const int r = k0 + 4 * half;
                 const char *a = lds + r * RAW + (raw_slot(r, i >> 3) << 4) + (((i >> 2) & 1) << 3);
-                w[half] = __builtin_bit_cast(
-                    uint2, __builtin_amdgcn_ds_read_tr16_b64_v4i16((__attribute__((address_space(3))) v4s *)(a)));
+                w[half] = dg_read_tr((__attribute__((address_space(3))) dg_v4s *)(a));
             }
             return u32x4{w[0].x, w[0].y, w[1].x, w[1].y};
         }
@@ -139,30 +190,35 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> stru
             b.copy(kt, c - A::LD, buf + A::BYTES, wave);
     }
 
-    __device__ __forceinline__ static void fragments(const char *buf, int wm, int wn, int ss, int lane, u32x4 (&af)[FM],
-                                                     u32x4 (&bf)[FN])
-    {
-#pragma unroll
-        for (int f = 0; f < FM; ++f)
-            af[f] = A::fragment(buf, wm * WM + f * 32, ss, lane);
-#pragma unroll
-        for (int f = 0; f < FN; ++f)
-            bf[f] = B::fragment(buf + A::BYTES, wn * WN + f * 32, ss, lane);
-    }
-
-    // The MFMAs of a sub-step with copies C0..C1-1 of stage kt spread between them.
+    // One sub-step: the MFMAs of fragments af, bf, and between them, in this
+    // order, the reads of the next sub-step's fragments (one before each of the
+    // first MFMAs) and copies C0..C1-1 of stage kt.  Spread like this neither
+    // queue fills up and the MFMA pipe is not held by either: all reads first
+    // cost 2-3% of a large product, all copies at once 3-4%.  The order of the
+    // products changes one fragment at a time (fewer operand bits toggle; the
+    // clock is set by the power that is drawn).
     template <int C0, int C1>
-    __device__ __forceinline__ void products(const u32x4 (&af)[FM], const u32x4 (&bf)[FN], f32x16 (&acc)[FM][FN], int kt,
-                                             char *buf, int wave, bool on) const
+    __device__ __forceinline__ void step(const char *rbuf, int rss, u32x4 (&an)[FM], u32x4 (&bn)[FN],
+                                         const u32x4 (&af)[FM], const u32x4 (&bf)[FN], f32x16 (&acc)[FM][FN], int wm,
+                                         int wn, int lane, int kt, char *cbuf, int wave, bool on) const
     {
         constexpr int NM = FM * FN, NC = C1 - C0;
+        static_assert(FM + FN <= NM, "a read before each of the first products");
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
-            mfma_chunk(__bf16{}, af[q / FN], bf[q % FN], acc[q / FN][q % FN]);
+            if (q == 0)
+                bn[0] = B::fragment(rbuf + A::BYTES, wn * WN, rss, lane);
+            else if (q <= FM)
+                an[q - 1] = A::fragment(rbuf, wm * WM + (q - 1) * 32, rss, lane);
+            else if (q < FM + FN)
+                bn[q - FM] = B::fragment(rbuf + A::BYTES, wn * WN + (q - FM) * 32, rss, lane);
+            __builtin_amdgcn_sched_barrier(0);
+            const int fn = q / FM, fm = fn & 1 ? FM - 1 - q % FM : q % FM;
+            mfma_chunk(__bf16{}, af[fm], bf[fn], acc[fm][fn]);
 #pragma unroll
             for (int c = C0; c < C1; ++c)
                 if ((c - C0) * NM / (NC > 0 ? NC : 1) == q && on)
-                    copy(kt, c, buf, wave);
+                    copy(kt, c, cbuf, wave);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
@@ -192,7 +248,12 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> stru
             __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
             wg_barrier();
             u32x4 af[2][FM], bf[2][FN];
-            fragments(smem, wm, wn, 0, lane, af[0], bf[0]);
+#pragma unroll
+            for (int f = 0; f < FM; ++f)
+                af[0][f] = A::fragment(smem, wm * WM + f * 32, 0, lane);
+#pragma unroll
+            for (int f = 0; f < FN; ++f)
+                bf[0][f] = B::fragment(smem + A::BYTES, wn * WN + f * 32, 0, lane);
             if (k0 + 1 < k1) {
 #pragma unroll
                 for (int c = 0; c < COPIES; ++c)
@@ -203,29 +264,16 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> stru
             for (int kt = k0; kt < k1; ++kt) {
                 char *cur = smem + slot * STAGE, *nxt = smem + (slot ^ 1) * STAGE;
                 const bool pend = kt > k0 && kt + 1 < k1;
-#pragma unroll
-                for (int ss = 0; ss < 4; ++ss) {
-                    const int cb = ss & 1, nb = cb ^ 1;
-                    if (ss < 3) {
-                        fragments(cur, wm, wn, ss + 1, lane, af[nb], bf[nb]);
-                        __builtin_amdgcn_sched_barrier(0);
-                    } else {
-                        __builtin_amdgcn_sched_barrier(0);
-                        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot has been read
-                        if (kt + 1 < k1) {
-                            __builtin_amdgcn_s_waitcnt(0x0070);  // stage kt + 1 has arrived
-                            wg_barrier();
-                            fragments(nxt, wm, wn, 0, lane, af[nb], bf[nb]);
-                            __builtin_amdgcn_sched_barrier(0);
-                        }
-                    }
-                    if (ss == 0)
-                        products<H, COPIES>(af[cb], bf[cb], acc, kt + 1, nxt, wave, pend);
-                    else if (ss == 3)
-                        products<0, H>(af[cb], bf[cb], acc, kt + 2, cur, wave, kt + 2 < k1);
-                    else
-                        products<0, 0>(af[cb], bf[cb], acc, 0, cur, wave, false);
+                step<H, COPIES>(cur, 1, af[1], bf[1], af[0], bf[0], acc, wm, wn, lane, kt + 1, nxt, wave, pend);
+                step<0, 0>(cur, 2, af[0], bf[0], af[1], bf[1], acc, wm, wn, lane, 0, nxt, wave, false);
+                step<0, 0>(cur, 3, af[1], bf[1], af[0], bf[0], acc, wm, wn, lane, 0, nxt, wave, false);
+                __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot has been read
+                if (kt + 1 < k1) {
+                    __builtin_amdgcn_s_waitcnt(0x0070);  // stage kt + 1 has arrived
+                    wg_barrier();
                 }
+                // (after the last stage this reads the other slot as it is; the values are not used)
+                step<0, H>(nxt, 0, af[0], bf[0], af[1], bf[1], acc, wm, wn, lane, kt + 2, cur, wave, kt + 2 < k1);
                 slot ^= 1;
             }
         }

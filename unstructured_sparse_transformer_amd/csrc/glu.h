@@ -5,6 +5,8 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "dense_gemm.h"
+
 namespace twell {
 
 enum GluAct { GLU_RELU = 0, GLU_SILU = 1, GLU_GELU = 2, GLU_GELU_TANH = 3 };
@@ -12,7 +14,9 @@ enum GluAct { GLU_RELU = 0, GLU_SILU = 1, GLU_GELU = 2, GLU_GELU_TANH = 3 };
 constexpr int GLU_FEW = 64;  // rows up to which the forward pass streams the weights (bf16)
 
 struct GluFwd {
-    int T, d, F, act, MT, NT;
+    int T, d, F, act;
+    int MT, NT;     // fp32 tiles
+    DgTiles tiles;  // bf16 tiles
     const void *x, *wg, *wu;
     void *h, *g, *u;  // g, u may be NULL
 };
@@ -21,9 +25,15 @@ struct GluBwd {
     int T, d, F, act;
     const void *x, *wg, *wu, *g, *u, *dh;
     void *dx, *dwg, *dwu;  // NULL: not wanted
-    void *dgu;             // [T to a multiple of 64][2 F]: a row's dg, then its du
+    void *dgu;             // [T to a multiple of 64] rows of glu_pitch(F): a row's dg, then its du
     float *part;           // split-K partial sums
 };
+
+// Elements from one row of dgu to the next.  64 more than it holds: rows that
+// are a power of two apart meet few of the memory channels when a tile reads
+// the same columns of 256 of them (dx at the 2B-like layer: 425 us with the
+// gap, 437 us without).
+__host__ __device__ inline int64_t glu_pitch(int F) { return 2 * (int64_t)F + 64; }
 
 struct GluWs {
     size_t dgu, part, bytes;  // offsets

@@ -79,8 +79,9 @@ glu_kernel(GluFwd p)
     using Core = DgCore<BM, BN, WM, WN, true, true, DB>;
     __shared__ __attribute__((aligned(16))) char smem[Core::LDS];
     static_assert(Core::NW * dg_stage_bytes<NB>() <= Core::LDS, "the stores' staging fits");
-    int mt, nt;
-    tile_coords(blockIdx.x, p.MT, p.NT, mt, nt);
+    int mt, nt, split;
+    if (!dg_tile(p.tiles, blockIdx.x, mt, nt, split))
+        return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Core core;
@@ -216,7 +217,7 @@ template <typename TI> __global__ __launch_bounds__(256) void glu_dact_kernel(Gl
             __builtin_memcpy(&og, rg, 16);
             __builtin_memcpy(&ou, ru, 16);
         }
-        TI *o = (TI *)p.dgu + t * 2 * p.F + j;
+        TI *o = (TI *)p.dgu + t * glu_pitch(p.F) + j;
         *reinterpret_cast<u32x4 *>(o) = og;
         *reinterpret_cast<u32x4 *>(o + p.F) = ou;
     }
@@ -232,7 +233,9 @@ struct GluMul {
     void *out, *out2;
     int m_turn;
     float *part;
-    int splits, MT, NT;
+    int splits;
+    int MT, NT;     // fp32 tiles
+    DgTiles tiles;  // bf16 tiles
 };
 
 template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC>
@@ -242,10 +245,9 @@ glu_mul_kernel(GluMul p)
     using Core = DgCore<BM, BN, WM, WN, A_KC, B_KC>;
     __shared__ __attribute__((aligned(16))) char smem[Core::LDS];
     static_assert(Core::NW * dg_stage_bytes<Core::FN>() <= Core::LDS, "the stores' staging fits");
-    const int tiles = p.MT * p.NT;
-    const int split = blockIdx.x / tiles;
-    int mt, nt;
-    tile_coords(blockIdx.x - split * tiles, p.MT, p.NT, mt, nt);
+    int mt, nt, split;
+    if (!dg_tile(p.tiles, blockIdx.x, mt, nt, split))
+        return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Core core;
@@ -328,9 +330,10 @@ template <int IDX, bool KC, int DB> struct F32Operand {
             if constexpr (KC) {
                 idx[v] = u >> 2;
                 k[v] = (u & 3) * 4;
-                int q = DB > 0 ? idx0 / 2 + idx[v] / (2 * DB) * DB + idx[v] % DB : idx0 + idx[v];
+                constexpr int D = DB > 0 ? DB : 1;
+                int q = DB > 0 ? idx0 / 2 + idx[v] / (2 * D) * D + idx[v] % D : idx0 + idx[v];
                 q = q < n ? q : n - 1;
-                base[v] = (const float *)(DB > 0 && ((idx[v] / (DB > 0 ? DB : 1)) & 1) ? p2 : p) + q * ld + k[v];
+                base[v] = (const float *)(DB > 0 && ((idx[v] / D) & 1) ? p2 : p) + q * ld + k[v];
                 second[v] = base[v];
             } else {
                 k[v] = u / (IDX / 4);
@@ -496,13 +499,11 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
         return hipGetLastError();
     }
     if (ceil_div(p.T, 256) * ceil_div(p.F, 128) >= 192) {
-        p.MT = (int)ceil_div(p.T, 256);
-        p.NT = (int)ceil_div(p.F, 128);
-        glu_kernel<256, 256, 64, 128><<<dim3(p.MT * p.NT), dim3(512), 0, s>>>(p);
+        p.tiles = dg_tiles(ceil_div(p.T, 256), ceil_div(p.F, 128));
+        glu_kernel<256, 256, 64, 128><<<dim3(8 * p.tiles.rows * p.tiles.cols), dim3(512), 0, s>>>(p);
     } else {
-        p.MT = (int)ceil_div(p.T, 128);
-        p.NT = (int)ceil_div(p.F, 64);
-        glu_kernel<128, 128, 64, 64><<<dim3(p.MT * p.NT), dim3(256), 0, s>>>(p);
+        p.tiles = dg_tiles(ceil_div(p.T, 128), ceil_div(p.F, 64));
+        glu_kernel<128, 128, 64, 64><<<dim3(8 * p.tiles.rows * p.tiles.cols), dim3(256), 0, s>>>(p);
     }
     return hipGetLastError();
 }
@@ -533,7 +534,7 @@ GluWs glu_backward_ws(int T, int d, int F, int vdtype)
 {
     GluWs w{};
     const size_t es = vdtype == 1 ? 2 : 4;
-    w.part = up256_((size_t)ceil_div(T, 64) * 64 * 2 * F * es);
+    w.part = up256_((size_t)ceil_div(T, 64) * 64 * glu_pitch(F) * es);
     const MulPlan dx = mul_plan(vdtype, T, d, 2 * (int64_t)F), dw = mul_plan(vdtype, 2 * (int64_t)F, d, T);
     const size_t a = dx.splits > 1 ? (size_t)dx.splits * T * d * 4 : 0;
     const size_t b = dw.splits > 1 ? (size_t)dw.splits * 2 * F * d * 4 : 0;
@@ -545,16 +546,19 @@ template <bool A_KC, bool B_KC> static hipError_t mul_go(int vdtype, GluMul p, h
 {
     const MulPlan plan = mul_plan(vdtype, p.M, p.N, p.K);
     p.splits = plan.splits;
-    const int bm = vdtype == 0 ? 64 : plan.big ? 256 : 128, bn = plan.big ? 256 : 128;
-    p.MT = (int)ceil_div(p.M, bm);
-    p.NT = (int)ceil_div(p.N, bn);
-    const dim3 grid(p.MT * p.NT * p.splits);
-    if (vdtype == 0)
-        glu_mul_f32_kernel<A_KC, B_KC><<<grid, dim3(256), 0, s>>>(p);
-    else if (plan.big)
-        glu_mul_kernel<256, 256, 64, 128, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
-    else
-        glu_mul_kernel<128, 128, 64, 64, A_KC, B_KC><<<grid, dim3(256), 0, s>>>(p);
+    if (vdtype == 0) {
+        p.MT = (int)ceil_div(p.M, 64);
+        p.NT = (int)ceil_div(p.N, 128);
+        glu_mul_f32_kernel<A_KC, B_KC><<<dim3(p.MT * p.NT * p.splits), dim3(256), 0, s>>>(p);
+    } else {
+        const int tile = plan.big ? 256 : 128;
+        p.tiles = dg_tiles(ceil_div(p.M, tile), ceil_div(p.N, tile));
+        const dim3 grid(8 * p.tiles.rows * p.tiles.cols * p.splits);
+        if (plan.big)
+            glu_mul_kernel<256, 256, 64, 128, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+        else
+            glu_mul_kernel<128, 128, 64, 64, A_KC, B_KC><<<grid, dim3(256), 0, s>>>(p);
+    }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
@@ -584,7 +588,7 @@ hipError_t launch_glu_backward(int vdtype, const GluBwd &p, hipStream_t s)
     }
     GluMul m{};
     m.a = p.dgu;
-    m.lda = (int64_t)2 * p.F * es;
+    m.lda = glu_pitch(p.F) * es;
     m.ldb = (int64_t)p.d * es;
     m.N = p.d;
     m.part = p.part;
@@ -595,7 +599,6 @@ hipError_t launch_glu_backward(int vdtype, const GluBwd &p, hipStream_t s)
         m.b2 = p.wu;
         m.k_turn = p.F;
         m.out = m.out2 = p.dx;
-        m.m_turn = p.T;
         m.m_turn = (int)ceil_div(p.T, 64) * 64;
         if ((e = mul_go<true, false>(vdtype, m, s)) != hipSuccess)
             return e;
