@@ -164,7 +164,8 @@ def _ptr(t) -> int | None:
 def _stream(stream) -> int | None:
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object (2.7 us less)
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -425,19 +426,27 @@ def hybrid_workspace(hy: "Hybrid", d: int, device="cuda"):
 
 
 # ---------------------------------------------------------------- the dense gated product
-def _tensor(fn: str, name: str, t, shape, like, dtype=None):
-    """Checks an argument: contiguous, on `like`'s device, of this shape and (if given) element type."""
+def _device(fn: str, t) -> int:
+    """The GPU a call's tensors have to be on."""
+    dev = t.get_device()
+    if dev < 0:
+        raise ValueError(f"{fn}: tensors on a GPU are needed, got one on {t.device}")
+    return dev
+
+
+def _tensor(fn: str, name: str, t, shape, dev: int, dtype=None) -> int:
+    """The pointer of an argument: contiguous, on GPU `dev`, of this shape and (if given) element type."""
     if t is None:
         raise ValueError(f"{fn}: {name} is missing")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape == shape and t.is_contiguous() and t.get_device() == dev and (dtype is None or t.dtype is dtype):
+        return t.data_ptr()
+    if t.shape != shape:
         raise ValueError(f"{fn}: {name} has shape {tuple(t.shape)}, not {tuple(shape)}")
     if not t.is_contiguous():
         raise ValueError(f"{fn}: {name} must be contiguous")
-    if t.device != like.device:
-        raise ValueError(f"{fn}: {name} is on {t.device}, not on {like.device}")
-    if dtype is not None and t.dtype != dtype:
-        raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
-    return t.data_ptr()
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on cuda:{dev}")
+    raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
 
 
 ACTS = {"relu": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
@@ -463,13 +472,14 @@ def glu_workspace(T: int, d: int, F: int, dtype, device="cuda"):
 def twell_glu_forward(x, wg_t, wu_t, act: str, h, workspace=None, g=None, u=None, stream=None):
     """h = act(x W_g) * (x W_u); g and u (optional, h's shape) receive the two products for the backward pass."""
     fn = "twell_glu_forward"
-    (T, d), (F, _), dt = x.shape, wg_t.shape, x.dtype
-    p = [_tensor(fn, k, t, s, x, dt) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)), ("wu_t", wu_t, (F, d)),
-                                                     ("h", h, (T, F)))]
-    pg, pu = (None if t is None else _tensor(fn, k, t, (T, F), x, dt) for k, t in (("g", g), ("u", u)))
+    dev, dt, (T, d), F = _device(fn, x), x.dtype, x.shape, wg_t.shape[0]
+    p = (_tensor(fn, "x", x, (T, d), dev), _tensor(fn, "wg_t", wg_t, (F, d), dev, dt),
+         _tensor(fn, "wu_t", wu_t, (F, d), dev, dt))
+    out = (_tensor(fn, "h", h, (T, F), dev, dt), None if g is None else _tensor(fn, "g", g, (T, F), dev, dt),
+           None if u is None else _tensor(fn, "u", u, (T, F), dev, dt))
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(fn, load().twell_glu_forward(p[0], p[1], p[2], T, d, F, vdtype_of(dt), _act(fn, act), p[3], pg, pu,
-                                        _ptr(workspace), nbytes, _stream(stream)))
+    _check(fn, load().twell_glu_forward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *out, _ptr(workspace), nbytes,
+                                        _stream(stream)))
 
 
 def twell_glu_backward_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
@@ -485,10 +495,10 @@ def glu_backward_workspace(T: int, d: int, F: int, dtype, device="cuda"):
 def twell_glu_backward(x, wg_t, wu_t, g, u, dh, act: str, dx, dwg, dwu, workspace, stream=None):
     """dx [T][d], dwg and dwu [F][d] (dx, or both of the others, may be None) from the forward's g and u and dh."""
     fn = "twell_glu_backward"
-    (T, d), (F, _), dt = x.shape, wg_t.shape, x.dtype
-    p = [_tensor(fn, k, t, s, x, dt) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)), ("wu_t", wu_t, (F, d)),
-                                                     ("g", g, (T, F)), ("u", u, (T, F)), ("dh", dh, (T, F)))]
-    o = [None if t is None else _tensor(fn, k, t, s, x, dt)
+    dev, dt, (T, d), F = _device(fn, x), x.dtype, x.shape, wg_t.shape[0]
+    p = [_tensor(fn, k, t, s, dev, dt) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)), ("wu_t", wu_t, (F, d)),
+                                                       ("g", g, (T, F)), ("u", u, (T, F)), ("dh", dh, (T, F)))]
+    o = [None if t is None else _tensor(fn, k, t, s, dev, dt)
          for k, t, s in (("dx", dx, (T, d)), ("dwg", dwg, (F, d)), ("dwu", dwu, (F, d)))]
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(fn, load().twell_glu_backward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *o, _ptr(workspace), nbytes,
@@ -510,39 +520,41 @@ class BlockNorm:
         self.kind, self.eps, self.alpha, self.post = kind, eps, alpha, post
         self.weights = {"w_post": w_post, "b_post": b_post, "w_pre": w_pre, "b_pre": b_pre}
         given = [w for w in self.weights.values() if w is not None]
+        dev = _device("BlockNorm", given[0]) if given else None
         self._desc = TwellBlockNormT(kind=NORM_KINDS[kind], eps=eps, alpha=alpha, post=int(bool(post)),
                                      wdtype=vdtype_of(given[0].dtype) if given else TWELL_F32)
         for k, w in self.weights.items():
             if w is not None:
-                setattr(self._desc, k, _tensor("BlockNorm", k, w, given[0].shape, given[0], given[0].dtype))
-        self.d = given[0].numel() if given else None
+                setattr(self._desc, k, _tensor("BlockNorm", k, w, given[0].shape, dev, given[0].dtype))
+        self.d, self.dev = (given[0].numel(), dev) if given else (None, None)
 
-    def desc(self, fn, rows, y, gate, gate_span) -> TwellBlockNormT:
+    def desc(self, fn, dev, rows, y, gate, gate_span) -> TwellBlockNormT:
         T, d = rows.shape
-        if self.d is not None and d != self.d:
-            raise ValueError(f"{fn}: rows of {d}, weights of {self.d}")
+        if self.d is not None and (d != self.d or dev != self.dev):
+            raise ValueError(f"{fn}: rows of {d} on cuda:{dev}, weights of {self.d} on cuda:{self.dev}")
         o = TwellBlockNormT.from_buffer_copy(self._desc)
         o.T, o.d, o.rdtype = T, d, vdtype_of(rows.dtype)
         if y is not None:
-            _tensor(fn, "y", y, (T, d), rows)
+            _tensor(fn, "y", y, (T, d), dev)
             o.ydtype = vdtype_of(y.dtype)
         if gate is not None:
             if gate_span < 1:
                 raise ValueError(f"{fn}: gate_span {gate_span}: a gate row serves at least one row")
             o.gate_span = gate_span
-            o.gate = _tensor(fn, "gate", gate, (-(-T // gate_span), d), rows, rows.dtype)
+            o.gate = _tensor(fn, "gate", gate, (-(-T // gate_span), d), dev, rows.dtype)
         return o
 
 
 def twell_block_norm_forward(bn: BlockNorm, res, y, out, n, gate=None, gate_span: int = 0, stream=None):
     """out = res + alpha * gate * norm(y), n = norm(out); y, out, n may be None (see include/twell.h)."""
     fn = "twell_block_norm_forward"
-    o = bn.desc(fn, res, y, gate, gate_span)
-    p_res = _tensor(fn, "res", res, res.shape, res)
-    p_out = None if out is None else _tensor(fn, "out", out, res.shape, res, res.dtype)
+    dev, shape = _device(fn, res), res.shape
+    o = bn.desc(fn, dev, res, y, gate, gate_span)
+    p_res = _tensor(fn, "res", res, shape, dev)
+    p_out = None if out is None else _tensor(fn, "out", out, shape, dev, res.dtype)
     p_n = None
     if n is not None:
-        p_n = _tensor(fn, "n", n, res.shape, res)
+        p_n = _tensor(fn, "n", n, shape, dev)
         o.ndtype = vdtype_of(n.dtype)
     _check(fn, load().twell_block_norm_forward(o, p_res, _ptr(y), p_out, p_n, _stream(stream)))
 
@@ -563,14 +575,13 @@ def twell_block_norm_backward(bn: BlockNorm, out, y, dout, dn, dres, dy, workspa
     gradients (float32 [d]) may be None (see include/twell.h)."""
     import torch
     fn = "twell_block_norm_backward"
-    o = bn.desc(fn, dres, y, gate, gate_span)
-    shape, dt = dres.shape, dres.dtype
-    p = {"out": out, "dout": dout, "dn": dn, "dy": dy}
-    want = {"out": dt, "dout": dt, "dn": None, "dy": None if y is None else y.dtype}
-    p = {k: None if t is None else _tensor(fn, k, t, shape, dres, want[k]) for k, t in p.items()}
-    p_dres = _tensor(fn, "dres", dres, shape, dres)
-    p_dgate = None if dgate is None else _tensor(fn, "dgate", dgate, gate.shape if gate is not None else (), dres, dt)
-    dw = [None if t is None else _tensor(fn, k, t, (shape[1],), dres, torch.float32)
+    dev, shape, dt = _device(fn, dres), dres.shape, dres.dtype
+    o = bn.desc(fn, dev, dres, y, gate, gate_span)
+    want = {"out": (out, dt), "dout": (dout, dt), "dn": (dn, None), "dy": (dy, None if y is None else y.dtype)}
+    p = {k: None if t is None else _tensor(fn, k, t, shape, dev, w) for k, (t, w) in want.items()}
+    p_dres = _tensor(fn, "dres", dres, shape, dev)
+    p_dgate = None if dgate is None else _tensor(fn, "dgate", dgate, gate.shape if gate is not None else (), dev, dt)
+    dw = [None if t is None else _tensor(fn, k, t, (shape[1],), dev, torch.float32)
           for k, t in (("dw_post", dw_post), ("db_post", db_post), ("dw_pre", dw_pre), ("db_pre", db_pre))]
     nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(fn, load().twell_block_norm_backward(o, p["out"], _ptr(y), p["dout"], p["dn"],
@@ -604,6 +615,8 @@ class AdamWTensors:
         self.desc = (TwellAdamWTensorT * max(len(self.tensors), 1))()
         self.state_bits = 8 if self.tensors and self.tensors[0]["m"].dtype == torch.uint8 else 32
         self.device = self.tensors[0]["p"].device if self.tensors else None
+        if self.tensors:
+            _device("AdamWTensors", self.tensors[0]["p"])
         self.can_unpack = self.state_bits == 8 and all(t.get("m_values") is not None and t.get("v_values") is not None
                                                        for t in self.tensors)
         state = torch.uint8 if self.state_bits == 8 else torch.float32
