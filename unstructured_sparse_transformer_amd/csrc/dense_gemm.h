@@ -23,6 +23,13 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t dg_rsrc(const void *base)
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, -1, 0x00020000);
 }
 
+// Waits until at most N copies of this wave are in flight, and for its LDS reads.
+template <int N> __device__ __forceinline__ void dg_wait()
+{
+    static_assert(N <= 63, "vmcnt range");
+    __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));
+}
+
 // Tiles to workgroups.  Workgroup g runs on XCD g % 8, and each XCD has an L2 of
 // its own: the tile grid is cut into 8 rectangles of `rows` x `cols` tiles, xm
 // of them down and 8 / xm across, one per XCD, and a rectangle is walked in
@@ -85,13 +92,15 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
     static constexpr int RPI = KC ? 8 : 1024 / RAW;  // rows per copy
     static_assert(IDX % (8 * NW) == 0, "copies split over the waves");
     static_assert(KC || (RAW >= 256 && RAW <= 1024), "raw rows span whole 256-byte bank windows");
-    static_assert(DB == 0 || (KC && DB % 8 == 0), "a copy's rows belong to one matrix");
+    // the matrix of a copy goes by its number alone, or by its wave alone
+    static constexpr bool BY_COPY = DB > 0 && DB % (8 * NW) == 0;
+    static_assert(DB == 0 || (KC && (BY_COPY || 8 * NW % (2 * DB) == 0)), "a copy's rows belong to one matrix");
 
-    const char *base;  // at the workgroup's first index and stage 0
-    int64_t other;     // bytes from there to the same place of the second matrix (DB; KS: from stage `turn` on)
-    int64_t step;      // bytes from one stage to the next
-    int turn;          // KS: first stage of the second matrix
-    int last, voff[LD], vlast[LD];
+    const char *ptr;  // at the workgroup's first index and the present stage
+    int64_t other;    // bytes from there to the same place of the second matrix (DB; KS: added at stage `turn`)
+    int64_t step;     // bytes from one stage to the next
+    int turn, last;   // KS: first stage of the second matrix, last stage of all
+    int voff[LD], vlast[LD];
 
     __device__ __forceinline__ static int raw_slot(int r, int c) { return c ^ ((r & 3) << 2); }
 
@@ -104,8 +113,10 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
         last = (k - 1) >> 6;
         if constexpr (KC) {
             const int first = DB > 0 ? idx0 / 2 : idx0;  // DB: idx0 counts the rows of both
-            base = (const char *)p + (int64_t)first * ld;
+            ptr = (const char *)p + (int64_t)first * ld;
             other = (const char *)p2 - (const char *)p;
+            if (DB > 0 && !BY_COPY && ((wave * 8 / (DB > 0 ? DB : 1)) & 1))
+                ptr += other;
             step = 128;
 #pragma unroll
             for (int j = 0; j < LD; ++j) {
@@ -117,7 +128,7 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
                 voff[j] = q * (int)ld + c * 16;
             }
         } else {
-            base = (const char *)p + (int64_t)idx0 * 2;
+            ptr = (const char *)p + (int64_t)idx0 * 2;
             step = 64 * ld;
             other = (const char *)p2 - (const char *)p - turn_ * step;
 #pragma unroll
@@ -132,16 +143,37 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
         }
     }
 
-    // Copy j of stage kt into the operand's LDS area.
-    __device__ __forceinline__ void copy(int kt, int j, char *lds, int wave) const
+    // Goes from stage 0 to stage kt, or from stage kt - 1 on to stage kt: what
+    // changes from stage to stage is done here, once, and not at every copy.
+    __device__ __forceinline__ void start(int kt)
     {
-        char *dst = lds + (j * NW + wave) * 1024;
-        if constexpr (KC) {
-            const bool second = DB > 0 && ((((j * NW + wave) * 8) / (DB > 0 ? DB : 1)) & 1);
-            dma16(dg_rsrc(base + (second ? other : 0)), dst, voff[j], kt * 128);
-        } else {
-            dma16(dg_rsrc(base + (kt * step + (kt < turn ? 0 : other))), dst, kt == last ? vlast[j] : voff[j], 0);
+        ptr += kt * step + (!KC && kt >= turn ? other : 0);
+        tail(kt);
+    }
+    __device__ __forceinline__ void next(int kt)
+    {
+        ptr += step;
+        if (!KC && kt == turn)
+            ptr += other;
+        tail(kt);
+    }
+    __device__ __forceinline__ void tail(int kt)
+    {
+        if constexpr (!KC) {
+            if (kt == last) {
+#pragma unroll
+                for (int j = 0; j < LD; ++j)
+                    voff[j] = vlast[j];
+            }
         }
+    }
+
+    // Copy j of the present stage into the operand's LDS area.
+    __device__ __forceinline__ void copy(int j, char *lds, int wave) const
+    {
+        constexpr int D = DB > 0 ? DB : 1;
+        const bool second = BY_COPY && ((j * NW * 8 / D) & 1);
+        dma16(dg_rsrc(second ? ptr + other : ptr), lds + (j * NW + wave) * 1024, voff[j], 0);
     }
 
     // The fragment of 32 indices from i0, K sub-step ss (16 elements): lane l
@@ -169,30 +201,35 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
     }
 };
 
-template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> struct DgCore {
+template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int S = 2> struct DgCore {
     static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, THREADS = NW * 64;
     static constexpr int FM = WM / 32, FN = WN / 32;
     using A = DgOperand<BM, A_KC, NW>;
     using B = DgOperand<BN, B_KC, NW, DB>;
     static constexpr int STAGE = A::BYTES + B::BYTES;
-    static constexpr int LDS = 2 * STAGE;
+    static constexpr int LDS = S * STAGE;  // S slots
     static constexpr int COPIES = A::LD + B::LD;
     static_assert(DB == 0 || WN == 2 * DB, "a wave holds both products of its columns");
 
     A a;
     B b;
 
-    __device__ __forceinline__ void copy(int kt, int c, char *buf, int wave) const
+    __device__ __forceinline__ void copy(int c, char *buf, int wave) const
     {
         if (c < A::LD)
-            a.copy(kt, c, buf, wave);
+            a.copy(c, buf, wave);
         else
-            b.copy(kt, c - A::LD, buf + A::BYTES, wave);
+            b.copy(c - A::LD, buf + A::BYTES, wave);
+    }
+    __device__ __forceinline__ void next(int kt)
+    {
+        a.next(kt);
+        b.next(kt);
     }
 
     // One sub-step: the MFMAs of fragments af, bf, and between them, in this
     // order, the reads of the next sub-step's fragments (one before each of the
-    // first MFMAs) and copies C0..C1-1 of stage kt.  Spread like this neither
+    // first MFMAs) and copies C0..C1-1 of the operands' present stage.  Spread like this neither
     // queue fills up and the MFMA pipe is not held by either: all reads first
     // cost 2-3% of a large product, all copies at once 3-4%.  The order of the
     // products changes one fragment at a time (fewer operand bits toggle; the
@@ -200,35 +237,38 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> stru
     template <int C0, int C1>
     __device__ __forceinline__ void step(const char *rbuf, int rss, u32x4 (&an)[FM], u32x4 (&bn)[FN],
                                          const u32x4 (&af)[FM], const u32x4 (&bf)[FN], f32x16 (&acc)[FM][FN], int wm,
-                                         int wn, int lane, int kt, char *cbuf, int wave, bool on) const
+                                         int wn, int lane, char *cbuf, int wave, bool on) const
     {
-        constexpr int NM = FM * FN, NC = C1 - C0;
-        static_assert(FM + FN <= NM, "a read before each of the first products");
+        constexpr int NM = FM * FN, NC = C1 - C0, NR = FM + FN;
 #pragma unroll
         for (int q = 0; q < NM; ++q) {
-            if (q == 0)
-                bn[0] = B::fragment(rbuf + A::BYTES, wn * WN, rss, lane);
-            else if (q <= FM)
-                an[q - 1] = A::fragment(rbuf, wm * WM + (q - 1) * 32, rss, lane);
-            else if (q < FM + FN)
-                bn[q - FM] = B::fragment(rbuf + A::BYTES, wn * WN + (q - FM) * 32, rss, lane);
+#pragma unroll
+            for (int r = 0; r < NR; ++r)
+                if ((NR <= NM ? r : r * NM / NR) == q) {
+                    if (r == 0)
+                        bn[0] = B::fragment(rbuf + A::BYTES, wn * WN, rss, lane);
+                    else if (r <= FM)
+                        an[r - 1] = A::fragment(rbuf, wm * WM + (r - 1) * 32, rss, lane);
+                    else
+                        bn[r - FM] = B::fragment(rbuf + A::BYTES, wn * WN + (r - FM) * 32, rss, lane);
+                }
             __builtin_amdgcn_sched_barrier(0);
             const int fn = q / FM, fm = fn & 1 ? FM - 1 - q % FM : q % FM;
             mfma_chunk(__bf16{}, af[fm], bf[fn], acc[fm][fn]);
 #pragma unroll
             for (int c = C0; c < C1; ++c)
                 if ((c - C0) * NM / (NC > 0 ? NC : 1) == q && on)
-                    copy(kt, c, cbuf, wave);
+                    copy(c, cbuf, wave);
             __builtin_amdgcn_sched_barrier(0);
         }
     }
 
-    // Stages [k0, k1): two LDS slots; the copies of stage kt + 2 go into stage
-    // kt's slot once the barrier before stage kt's last sub-step has passed,
-    // half between that sub-step's MFMAs and half between the next one's, and
-    // fragments are read one sub-step ahead.  Ends with a barrier: the caller
-    // may use `smem`.
-    __device__ __forceinline__ void run(int k0, int k1, char *smem, int tid, f32x16 (&acc)[FM][FN]) const
+    // Stages [k0, k1) through S LDS slots: the copies of stage kt + S go into
+    // stage kt's slot once the barrier before stage kt's last sub-step has
+    // passed, half between that sub-step's MFMAs and half between the next
+    // one's, and fragments are read one sub-step ahead.  Ends with a barrier: the
+    // caller may use `smem`.
+    __device__ __forceinline__ void run(int k0, int k1, char *smem, int tid, f32x16 (&acc)[FM][FN])
     {
         constexpr int H = COPIES / 2;
         const int lane = tid & 63;
@@ -242,10 +282,23 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> stru
                 for (int i = 0; i < 16; ++i)
                     acc[fm][fn][i] = 0.f;
         if (k0 < k1) {
+            a.start(k0);
+            b.start(k0);
 #pragma unroll
             for (int c = 0; c < COPIES; ++c)
-                copy(k0, c, smem, wave);
-            __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0) lgkmcnt(0)
+                copy(c, smem, wave);
+#pragma unroll
+            for (int k = 1; k < S; ++k)
+                if (k0 + k < k1) {
+                    next(k0 + k);
+#pragma unroll
+                    for (int c = 0; c < COPIES; ++c)
+                        copy(c, smem + k * STAGE, wave);
+                }
+            if (k0 + S - 1 < k1)
+                dg_wait<(S - 1) * COPIES>();
+            else
+                dg_wait<0>();
             wg_barrier();
             u32x4 af[2][FM], bf[2][FN];
 #pragma unroll
@@ -254,27 +307,29 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0> stru
 #pragma unroll
             for (int f = 0; f < FN; ++f)
                 bf[0][f] = B::fragment(smem + A::BYTES, wn * WN + f * 32, 0, lane);
-            if (k0 + 1 < k1) {
-#pragma unroll
-                for (int c = 0; c < COPIES; ++c)
-                    copy(k0 + 1, c, smem + STAGE, wave);
-            }
             int slot = 0;
 #pragma clang loop unroll(disable)
             for (int kt = k0; kt < k1; ++kt) {
-                char *cur = smem + slot * STAGE, *nxt = smem + (slot ^ 1) * STAGE;
-                const bool pend = kt > k0 && kt + 1 < k1;
-                step<H, COPIES>(cur, 1, af[1], bf[1], af[0], bf[0], acc, wm, wn, lane, kt + 1, nxt, wave, pend);
-                step<0, 0>(cur, 2, af[0], bf[0], af[1], bf[1], acc, wm, wn, lane, 0, nxt, wave, false);
-                step<0, 0>(cur, 3, af[1], bf[1], af[0], bf[0], acc, wm, wn, lane, 0, nxt, wave, false);
+                const int nslot = slot + 1 == S ? 0 : slot + 1, pslot = slot == 0 ? S - 1 : slot - 1;
+                char *cur = smem + slot * STAGE, *nxt = smem + nslot * STAGE, *prv = smem + pslot * STAGE;
+                const bool pend = kt > k0 && kt - 1 + S < k1;  // the second half of the copies begun in stage kt - 1
+                step<H, COPIES>(cur, 1, af[1], bf[1], af[0], bf[0], acc, wm, wn, lane, prv, wave, pend);
+                step<0, 0>(cur, 2, af[0], bf[0], af[1], bf[1], acc, wm, wn, lane, nxt, wave, false);
+                step<0, 0>(cur, 3, af[1], bf[1], af[0], bf[0], acc, wm, wn, lane, nxt, wave, false);
                 __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot has been read
                 if (kt + 1 < k1) {
-                    __builtin_amdgcn_s_waitcnt(0x0070);  // stage kt + 1 has arrived
+                    // stage kt + 1 has arrived; the S - 2 after it may be on their way
+                    if (kt + S - 1 < k1)
+                        dg_wait<(S - 2) * COPIES>();
+                    else
+                        dg_wait<0>();
                     wg_barrier();
                 }
+                if (kt + S < k1)
+                    next(kt + S);
                 // (after the last stage this reads the other slot as it is; the values are not used)
-                step<0, H>(nxt, 0, af[0], bf[0], af[1], bf[1], acc, wm, wn, lane, kt + 2, cur, wave, kt + 2 < k1);
-                slot ^= 1;
+                step<0, H>(nxt, 0, af[0], bf[0], af[1], bf[1], acc, wm, wn, lane, cur, wave, kt + S < k1);
+                slot = nslot;
             }
         }
         __syncthreads();

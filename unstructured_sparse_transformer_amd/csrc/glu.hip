@@ -71,12 +71,12 @@ template <bool FAST> __device__ __forceinline__ float glu_act_grad(float g, int 
 }
 
 // ------------------------------------------------------------------ forward
-template <int BM, int BN, int WM, int WN>
+template <int BM, int BN, int WM, int WN, int S>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 glu_kernel(GluFwd p)
 {
     constexpr int DB = WN / 2, NB = DB / 32;
-    using Core = DgCore<BM, BN, WM, WN, true, true, DB>;
+    using Core = DgCore<BM, BN, WM, WN, true, true, DB, S>;
     __shared__ __attribute__((aligned(16))) char smem[Core::LDS];
     static_assert(Core::NW * dg_stage_bytes<NB>() <= Core::LDS, "the stores' staging fits");
     int mt, nt, split;
@@ -105,83 +105,118 @@ glu_kernel(GluFwd p)
     }
 }
 
-// Few rows (T <= 16 MB <= 64): bound by reading the weights once.  A workgroup
-// takes 8 neurons, i.e. 8 rows of W_g and 8 of W_u as one 16-row operand, and
-// copies up to FEW_KS of their K elements into LDS at a time, all in flight at
-// once; two workgroups per CU, so one's copies run beside the other's
-// products (v_mfma_f32_16x16x32_bf16).  The waves deal out 64-element K chunks
-// and their partial products meet in LDS, added in wave order.
-constexpr int FEW_KS = 2048;
-
-typedef float f32x4 __attribute__((ext_vector_type(4)));
-
-template <int MB> __global__ __launch_bounds__(256) void glu_few_kernel(GluFwd p)
+// Few rows: the weights stream through a ring of S LDS slots, one stage (64 K
+// elements of the workgroup's NB rows of W_g, its NB of W_u, and of x) a slot,
+// with the copies of S - 1 stages in flight, two workgroups per CU.  Bound by
+// reading the weights once: 67 MB of the 2B-like layer in 12.9 us at T = 1
+// (5.2 TB/s) and 13.5 us at T = 64.  Workgroups start at different stages:
+// W's rows are a power of two apart, and all of them at the same columns meet
+// few of the memory channels (17.6 us).  The 4 waves share a stage by K,
+// 16 elements each, and their partial products meet in LDS at the end, added in
+// wave order.
+template <int BM, int NB, int S> __global__ __launch_bounds__(256) void glu_stream_kernel(GluFwd p)
 {
-    constexpr int NW = 4, SB = 16 * FEW_KS * 2;
-    __shared__ __attribute__((aligned(16))) char sb[SB];
-    static_assert(NW * MB * 4 * 64 * 4 <= SB, "the partial products fit");
+    constexpr int R = 2 * NB, FM = BM / 32, FN = R / 32;
+    constexpr int A_BYTES = BM * 128, SLOT = A_BYTES + R * 128, A_LD = BM / 32, B_LD = R / 32;
+    constexpr int RED = 4 * FM * FN * 16 * 64 * 4;
+    __shared__ __attribute__((aligned(16))) char smem[S * SLOT > RED ? S * SLOT : RED];
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
-    const int n0 = blockIdx.x * 8, r = lane & 15, q = lane >> 4;
+    const int n0 = blockIdx.x * NB;
     const int64_t ld = (int64_t)p.d * 2;
-    const __amdgpu_buffer_rsrc_t wg = dg_rsrc((const char *)p.wg + n0 * ld), wu = dg_rsrc((const char *)p.wu + n0 * ld);
-    f32x4 acc[MB];
-    const char *xr[MB];
+    const __amdgpu_buffer_rsrc_t rx = dg_rsrc(p.x), rg = dg_rsrc((const char *)p.wg + n0 * ld),
+                                 ru = dg_rsrc((const char *)p.wu + n0 * ld);
+    // copy j of a wave fills rows (j 4 + wave) 8 .. + 7; x's rows past T stay as they are (their results are dropped)
+    int voff[A_LD + B_LD], na = 0;
 #pragma unroll
-    for (int mb = 0; mb < MB; ++mb) {
-        acc[mb] = f32x4{0.f, 0.f, 0.f, 0.f};
-        const int m = mb * 16 + r;
-        xr[mb] = (const char *)p.x + (int64_t)(m < p.T ? m : p.T - 1) * ld;  // rows past T: their results are dropped
+    for (int j = 0; j < A_LD + B_LD; ++j) {
+        const bool x = j < A_LD;
+        const int r = ((x ? j : j - A_LD) * 4 + wave) * 8 + (lane >> 3);
+        const int c = (lane & 7) ^ ((r >> 1) & 7);
+        const int row = x ? (r < p.T ? r : p.T - 1) : r % NB;
+        voff[j] = row * (int)ld + c * 16;
+        na += x && (j * 4 + wave) * 8 < p.T;
     }
-    for (int k0 = 0; k0 < p.d; k0 += FEW_KS) {
-        const int ks = p.d - k0 < FEW_KS ? p.d - k0 : FEW_KS;  // a multiple of 64
-        const int cpr = ks / 8, spr = (cpr + 15) & ~15;        // 16-byte chunks of a row, and its slots in LDS
-        for (int s0 = wave * 64; s0 < 16 * spr; s0 += NW * 64) {
-            const int slot = s0 + lane, row = slot / spr, sl = slot - row * spr;
-            const int ch = (sl & ~15) | ((sl ^ row) & 15);
-            const int voff = (row & 7) * (int)ld + k0 * 2 + (ch < cpr ? ch : 0) * 16;
-            if (s0 / spr >= 8)  // 8 rows are whole groups of 64 slots
-                dma16(wu, sb + s0 * 16, voff, 0);
-            else
-                dma16(wg, sb + s0 * 16, voff, 0);
-        }
-        __builtin_amdgcn_s_waitcnt(0x0070);
-        wg_barrier();
-        for (int kc = wave; kc < ks / 64; kc += NW) {
+    const int nk = p.d >> 6;
+    const int rot = (int)(blockIdx.x % (unsigned)nk);
+    auto load = [&](int k, char *slot) {
+        const int kt = k + rot < nk ? k + rot : k + rot - nk;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                const int ch = kc * 8 + half * 4 + q;
-                const u32x4 b = *reinterpret_cast<const u32x4 *>(sb + (r * spr + ((ch & ~15) | ((ch ^ r) & 15))) * 16);
+        for (int j = 0; j < A_LD; ++j)
+            if (j < na)
+                dma16(rx, slot + (j * 4 + wave) * 1024, voff[j], kt * 128);
 #pragma unroll
-                for (int mb = 0; mb < MB; ++mb) {
-                    const u32x4 a = ldg16(xr[mb] + (k0 + ch * 8) * 2);
-                    acc[mb] = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
-                                                                      __builtin_bit_cast(bf16x8, b), acc[mb], 0, 0, 0);
-                }
-            }
+        for (int j = 0; j < B_LD; ++j) {
+            const int r = (j * 4 + wave) * 8;
+            dma16(r < NB ? rg : ru, slot + A_BYTES + r * 128, voff[A_LD + j], kt * 128);
         }
-        __syncthreads();
+    };
+    f32x16 acc[FM][FN];
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                acc[fm][fn][i] = 0.f;
+#pragma unroll
+    for (int k = 0; k < S - 1; ++k)
+        if (k < nk)
+            load(k, smem + k * SLOT);
+    int slot = 0;
+    for (int kt = 0; kt < nk; ++kt) {
+        // stage kt has arrived: the S - 2 stages after it may be on their way (fewer at the end: then all are waited for)
+        if (kt + S - 1 > nk)
+            __builtin_amdgcn_s_waitcnt(0x0070);
+        else if (na == 0)
+            dg_wait<(S - 2) * B_LD>();
+        else if (na == 1)
+            dg_wait<(S - 2) * (B_LD + 1)>();
+        else
+            dg_wait<(S - 2) * (B_LD + 2)>();
+        wg_barrier();  // and every wave has read stage kt - 1, whose slot is filled again
+        if (kt + S - 1 < nk)
+            load(kt + S - 1, smem + (slot == 0 ? S - 1 : slot - 1) * SLOT);
+        const char *cur = smem + slot * SLOT;
+        u32x4 a[FM], b[FN];
+#pragma unroll
+        for (int f = 0; f < FM; ++f)
+            a[f] = DgOperand<32, true, 1>::fragment(cur, f * 32, wave, lane);
+#pragma unroll
+        for (int f = 0; f < FN; ++f)
+            b[f] = DgOperand<32, true, 1>::fragment(cur + A_BYTES, f * 32, wave, lane);
+#pragma unroll
+        for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < FN; ++fn)
+                mfma_chunk(__bf16{}, a[fm], b[fn], acc[fm][fn]);
+        __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot has been read
+        slot = slot + 1 == S ? 0 : slot + 1;
     }
-    float *red = reinterpret_cast<float *>(sb);  // [wave][block][register][lane]
-#pragma unroll
-    for (int mb = 0; mb < MB; ++mb)
-#pragma unroll
-        for (int i = 0; i < 4; ++i)
-            red[((wave * MB + mb) * 4 + i) * 64 + lane] = acc[mb][i];
     __syncthreads();
-    // row m, column c of a block: register m % 4 of lane 16 (m / 4) + c
-    for (int e = tid; e < MB * 128; e += 256) {
-        const int mb = e >> 7, m = (e >> 3) & 15, c = e & 7;
-        if (mb * 16 + m >= p.T)
-            continue;
-        const int at = (mb * 4 + (m & 3)) * 64 + (m >> 2) * 16 + c;
+    float *red = reinterpret_cast<float *>(smem);  // [wave][block][register][lane]
+#pragma unroll
+    for (int fm = 0; fm < FM; ++fm)
+#pragma unroll
+        for (int fn = 0; fn < FN; ++fn)
+#pragma unroll
+            for (int i = 0; i < 16; ++i)
+                red[((wave * FM * FN + fm * FN + fn) * 16 + i) * 64 + lane] = acc[fm][fn][i];
+    __syncthreads();
+    for (int e = tid; e < BM * NB; e += 256) {
+        const int m = e / NB, c = e % NB, r = m & 31;
+        if (m >= p.T)
+            break;
+        // row r of a block: register (r / 8) 4 + r % 4 of the lanes of its half; u's columns follow g's NB
+        const int at = ((r >> 3) * 4 + (r & 3)) * 64 + ((r >> 2) & 1) * 32;
+        const int bg = (m >> 5) * FN, bu = bg + (NB >> 5);
         float g = 0.f, u = 0.f;
 #pragma unroll
-        for (int w = 0; w < NW; ++w) {
-            g += red[w * MB * 256 + at];
-            u += red[w * MB * 256 + at + 8];
+        for (int w = 0; w < 4; ++w) {
+            g += red[(w * FM * FN + bg) * 1024 + at + c];
+            u += red[(w * FM * FN + bu) * 1024 + at + (c + NB) % 32];
         }
-        const int64_t o = (int64_t)(mb * 16 + m) * p.F + n0 + c;
+        const int64_t o = (int64_t)m * p.F + n0 + c;
         if (p.g)
             ((__bf16 *)p.g)[o] = (__bf16)g;
         if (p.u)
@@ -238,11 +273,11 @@ struct GluMul {
     DgTiles tiles;  // bf16 tiles
 };
 
-template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC>
+template <int BM, int BN, int WM, int WN, int S, bool A_KC, bool B_KC>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
 glu_mul_kernel(GluMul p)
 {
-    using Core = DgCore<BM, BN, WM, WN, A_KC, B_KC>;
+    using Core = DgCore<BM, BN, WM, WN, A_KC, B_KC, 0, S>;
     __shared__ __attribute__((aligned(16))) char smem[Core::LDS];
     static_assert(Core::NW * dg_stage_bytes<Core::FN>() <= Core::LDS, "the stores' staging fits");
     int mt, nt, split;
@@ -471,6 +506,44 @@ template <bool A_KC, bool B_KC> __global__ __launch_bounds__(256) void glu_mul_f
 // ------------------------------------------------------------------ host
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
+// The workgroup tiles of the bf16 products, and what one stage of 64 K elements
+// and the rest of a tile cost on a CU (us, measured on products of many sizes
+// with one tile per CU): larger tiles move fewer bytes per product, smaller ones
+// give every CU work.
+struct MulTile {
+    int bm, bn;
+    double stage;
+};
+constexpr MulTile MUL_TILES[] = {{256, 256, 1.5}, {256, 128, 0.88}, {128, 128, 0.52}, {128, 64, 0.36}};
+constexpr double MUL_TILE_US = 5, MUL_JOIN_US = 4, MUL_PART_BYTES_PER_US = 4e6;
+constexpr int CUS = 256;
+
+struct MulPlan {
+    int tile, splits;
+};
+
+// The tile and the number of K splits with the least estimated time.
+static MulPlan mul_plan(int64_t M, int64_t N, int64_t K, int tiles, int most_splits)
+{
+    MulPlan best{0, 1};
+    double best_us = 1e300;
+    const int64_t stages = (K + 63) / 64;
+    for (int t = 0; t < tiles; ++t)
+        for (int splits = 1; splits <= most_splits && splits <= stages; splits *= 2) {
+            const int64_t wgs = ((M + MUL_TILES[t].bm - 1) / MUL_TILES[t].bm) *
+                                ((N + MUL_TILES[t].bn - 1) / MUL_TILES[t].bn) * splits;
+            const double rounds = (double)((wgs + CUS - 1) / CUS), per = (double)((stages + splits - 1) / splits);
+            double us = rounds * (per * MUL_TILES[t].stage + MUL_TILE_US);
+            if (splits > 1)
+                us += MUL_JOIN_US + (double)M * N * 8 * splits / MUL_PART_BYTES_PER_US;
+            if (us < best_us) {
+                best_us = us;
+                best = MulPlan{t, splits};
+            }
+        }
+    return best;
+}
+
 hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
 {
     GluFwd p = args;
@@ -481,51 +554,46 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
         return hipGetLastError();
     }
     if (p.T <= GLU_FEW) {
-        const dim3 grid(p.F / 8);
-        switch ((p.T + 15) / 16) {
-        case 1:
-            glu_few_kernel<1><<<grid, dim3(256), 0, s>>>(p);
-            break;
-        case 2:
-            glu_few_kernel<2><<<grid, dim3(256), 0, s>>>(p);
-            break;
-        case 3:
-            glu_few_kernel<3><<<grid, dim3(256), 0, s>>>(p);
-            break;
-        default:
-            glu_few_kernel<4><<<grid, dim3(256), 0, s>>>(p);
-            break;
-        }
+        const dim3 grid(p.F / 16), block(256);
+        if (p.T <= 32)
+            glu_stream_kernel<32, 16, 9><<<grid, block, 0, s>>>(p);
+        else
+            glu_stream_kernel<64, 16, 6><<<grid, block, 0, s>>>(p);
         return hipGetLastError();
     }
-    if (ceil_div(p.T, 256) * ceil_div(p.F, 128) >= 192) {
-        p.tiles = dg_tiles(ceil_div(p.T, 256), ceil_div(p.F, 128));
-        glu_kernel<256, 256, 64, 128><<<dim3(8 * p.tiles.rows * p.tiles.cols), dim3(512), 0, s>>>(p);
-    } else {
-        p.tiles = dg_tiles(ceil_div(p.T, 128), ceil_div(p.F, 64));
-        glu_kernel<128, 128, 64, 64><<<dim3(8 * p.tiles.rows * p.tiles.cols), dim3(256), 0, s>>>(p);
+    const int tile = mul_plan(p.T, 2 * (int64_t)p.F, p.d, 4, 1).tile;
+    p.tiles = dg_tiles(ceil_div(p.T, MUL_TILES[tile].bm), ceil_div(p.F, MUL_TILES[tile].bn / 2));
+    const dim3 grid(8 * p.tiles.rows * p.tiles.cols);
+    switch (tile) {
+    case 0:
+        glu_kernel<256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(p);
+        break;
+    case 1:
+        glu_kernel<256, 128, 64, 64, 3><<<grid, dim3(512), 0, s>>>(p);
+        break;
+    case 2:
+        glu_kernel<128, 128, 32, 64, 4><<<grid, dim3(512), 0, s>>>(p);
+        break;
+    default:
+        glu_kernel<128, 64, 32, 64, 3><<<grid, dim3(256), 0, s>>>(p);
+        break;
     }
     return hipGetLastError();
 }
 
-// Tiles and splits of a product of the backward pass.
-struct MulPlan {
-    bool big;
-    int splits;
-};
-
-static MulPlan mul_plan(int vdtype, int64_t M, int64_t N, int64_t K)
+// Tiles and splits of a product of the backward pass.  fp32 has one tile, 64 x
+// 128, and splits until there are two workgroups per CU.
+static MulPlan backward_plan(int vdtype, int64_t M, int64_t N, int64_t K)
 {
-    if (M == 0 || N == 0)
-        return {false, 1};
-    const int64_t stages = ceil_div(K, 64);
-    if (vdtype == 1 && ceil_div(M, 256) * ceil_div(N, 256) >= 192)
-        return {true, 1};
-    const int64_t tiles = vdtype == 1 ? ceil_div(M, 128) * ceil_div(N, 128) : ceil_div(M, 64) * ceil_div(N, 128);
+    if (M == 0 || N == 0 || K == 0)
+        return {0, 1};
+    if (vdtype == 1)
+        return mul_plan(M, N, K, 3, 16);
+    const int64_t tiles = ceil_div(M, 64) * ceil_div(N, 128), stages = ceil_div(K, 64);
     int splits = 1;
     while (splits < 16 && tiles * splits * 2 <= 512 && stages / (splits * 2) >= 8)
         splits *= 2;
-    return {false, splits};
+    return {0, splits};
 }
 
 static size_t up256_(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -535,7 +603,7 @@ GluWs glu_backward_ws(int T, int d, int F, int vdtype)
     GluWs w{};
     const size_t es = vdtype == 1 ? 2 : 4;
     w.part = up256_((size_t)ceil_div(T, 64) * 64 * glu_pitch(F) * es);
-    const MulPlan dx = mul_plan(vdtype, T, d, 2 * (int64_t)F), dw = mul_plan(vdtype, 2 * (int64_t)F, d, T);
+    const MulPlan dx = backward_plan(vdtype, T, d, 2 * (int64_t)F), dw = backward_plan(vdtype, 2 * (int64_t)F, d, T);
     const size_t a = dx.splits > 1 ? (size_t)dx.splits * T * d * 4 : 0;
     const size_t b = dw.splits > 1 ? (size_t)dw.splits * 2 * F * d * 4 : 0;
     w.bytes = w.part + (a > b ? a : b);
@@ -544,20 +612,22 @@ GluWs glu_backward_ws(int T, int d, int F, int vdtype)
 
 template <bool A_KC, bool B_KC> static hipError_t mul_go(int vdtype, GluMul p, hipStream_t s)
 {
-    const MulPlan plan = mul_plan(vdtype, p.M, p.N, p.K);
+    const MulPlan plan = backward_plan(vdtype, p.M, p.N, p.K);
     p.splits = plan.splits;
     if (vdtype == 0) {
         p.MT = (int)ceil_div(p.M, 64);
         p.NT = (int)ceil_div(p.N, 128);
         glu_mul_f32_kernel<A_KC, B_KC><<<dim3(p.MT * p.NT * p.splits), dim3(256), 0, s>>>(p);
     } else {
-        const int tile = plan.big ? 256 : 128;
-        p.tiles = dg_tiles(ceil_div(p.M, tile), ceil_div(p.N, tile));
+        const MulTile &tile = MUL_TILES[plan.tile];
+        p.tiles = dg_tiles(ceil_div(p.M, tile.bm), ceil_div(p.N, tile.bn));
         const dim3 grid(8 * p.tiles.rows * p.tiles.cols * p.splits);
-        if (plan.big)
-            glu_mul_kernel<256, 256, 64, 128, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+        if (plan.tile == 0)
+            glu_mul_kernel<256, 256, 64, 128, 2, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+        else if (plan.tile == 1)
+            glu_mul_kernel<256, 128, 64, 64, 3, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
         else
-            glu_mul_kernel<128, 128, 64, 64, A_KC, B_KC><<<grid, dim3(256), 0, s>>>(p);
+            glu_mul_kernel<128, 128, 32, 64, 4, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
