@@ -1,8 +1,11 @@
 // dense_gemm.h -- the matrix-product core of the gated product (gfx950).
 //
 // C[m][n] = sum_k A(m, k) B(k, n) on workgroup tiles of BM x BN, K in stages of
-// 64 bf16 elements, fp32 accumulators (v_mfma_f32_32x32x16_bf16).  Each operand
-// is read as it lies in memory:
+// 64 bf16 elements, fp32 accumulators (v_mfma_f32_32x32x16_bf16).  B's fragment
+// is the instruction's first operand: a lane then holds 4 consecutive n of one m
+// (element i of lane l of a block: n = 8 (i / 4) + 4 (l / 32) + i % 4, m = l % 32),
+// which leave as one 8-byte piece of a row.  Each operand is read as it lies in
+// memory:
 //   KC  rows of its M (or N) index, K contiguous:   x and W of the forward pass
 //   KS  rows of K, its M (or N) index contiguous:   W in dx, x and dg in dW
 // A stage of either is 128 bytes per M (or N) index, copied by global->LDS
@@ -254,7 +257,7 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int 
                 }
             __builtin_amdgcn_sched_barrier(0);
             const int fn = q / FM, fm = fn & 1 ? FM - 1 - q % FM : q % FM;
-            mfma_chunk(__bf16{}, af[fm], bf[fn], acc[fm][fn]);
+            mfma_chunk(__bf16{}, bf[fn], af[fm], acc[fm][fn]);
 #pragma unroll
             for (int c = C0; c < C1; ++c)
                 if ((c - C0) * NM / (NC > 0 ? NC : 1) == q && on)
@@ -336,10 +339,10 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int 
     }
 };
 
-// A wave's block of 32 rows by 32 NB columns in bf16, from accumulator layout
+// A wave's block of 32 rows by 32 NB columns in bf16, from accumulators
 // (value(fn, i)) to memory by way of LDS: 16-byte stores of whole row pieces.
-// `lds`: 32 * (64 NB + 16) bytes of the wave's own (the 16 bytes keep the two
-// half-waves' rows, 4 apart, on different banks).
+// `lds`: dg_stage_bytes<NB>() bytes of the wave's own (16 bytes between the rows
+// spread their pieces over the banks).
 template <int NB> constexpr int dg_stage_bytes() { return 32 * (64 * NB + 16); }
 template <int NB, typename V>
 __device__ __forceinline__ void dg_store_rows(char *lds, int lane, V value, __bf16 *out, int64_t ld, int m0, int n0,
@@ -350,9 +353,12 @@ __device__ __forceinline__ void dg_store_rows(char *lds, int lane, V value, __bf
 #pragma unroll
     for (int fn = 0; fn < NB; ++fn)
 #pragma unroll
-        for (int i = 0; i < 16; ++i)
-            *reinterpret_cast<__bf16 *>(lds + acc_row(i, lane) * PITCH + (fn * 32 + (lane & 31)) * 2) =
-                (__bf16)value(fn, i);
+        for (int i = 0; i < 16; i += 4) {
+            const bf16x2 lo = {(__bf16)value(fn, i), (__bf16)value(fn, i + 1)};
+            const bf16x2 hi = {(__bf16)value(fn, i + 2), (__bf16)value(fn, i + 3)};
+            *reinterpret_cast<uint2 *>(lds + (lane & 31) * PITCH + (fn * 32 + acc_row(i, lane)) * 2) =
+                make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
+        }
     asm volatile("" ::: "memory");
     constexpr int CPR = 4 * NB;  // 16-byte chunks of a row
 #pragma unroll

@@ -299,10 +299,12 @@ glu_mul_kernel(GluMul p)
 #pragma unroll
             for (int fn = 0; fn < Core::FN; ++fn)
 #pragma unroll
-                for (int i = 0; i < 16; ++i) {
-                    const int m = m0 + fm * 32 + acc_row(i, lane), n = n0 + fn * 32 + (lane & 31);
+                for (int i = 0; i < 16; i += 4) {
+                    const int m = m0 + fm * 32 + (lane & 31), n = n0 + fn * 32 + acc_row(i, lane);
+                    const f32x16 &v = acc[fm][fn];
                     if (m < p.M && n < p.N)
-                        p.part[((int64_t)split * p.M + m) * p.N + n] = acc[fm][fn][i];
+                        *reinterpret_cast<float4 *>(p.part + ((int64_t)split * p.M + m) * p.N + n) =
+                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
                 }
         return;
     }
