@@ -11,7 +11,7 @@ namespace twell {
 
 enum GluAct { GLU_RELU = 0, GLU_SILU = 1, GLU_GELU = 2, GLU_GELU_TANH = 3 };
 
-constexpr int GLU_FEW = 64;  // rows up to which the forward pass streams the weights (bf16)
+constexpr int GLU_FEW = 64;  // rows up to which the forward pass streams the weights
 
 struct GluFwd {
     int T, d, F, act;

@@ -105,8 +105,8 @@ glu_kernel(GluFwd p)
     }
 }
 
-// Few rows: the weights stream through a ring of S LDS slots, one stage (64 K
-// elements of the workgroup's NB rows of W_g, its NB of W_u, and of x) a slot,
+// Few rows: the weights stream through a ring of S LDS slots, one stage (128
+// bytes, 64 bf16 or 32 fp32 K elements, of the workgroup's NB rows of W_g, its NB of W_u, and of x) a slot,
 // with the copies of S - 1 stages in flight, two workgroups per CU.  Bound by
 // reading the weights once: 67 MB of the 2B-like layer in 12.9 us at T = 1
 // (5.2 TB/s) and 13.5 us at T = 64.  Workgroups start at different stages:
@@ -114,7 +114,7 @@ glu_kernel(GluFwd p)
 // few of the memory channels (17.6 us).  The 4 waves share a stage by K,
 // 16 elements each, and their partial products meet in LDS at the end, added in
 // wave order.
-template <int BM, int NB, int S> __global__ __launch_bounds__(256) void glu_stream_kernel(GluFwd p)
+template <typename TI, int BM, int NB, int S> __global__ __launch_bounds__(256) void glu_stream_kernel(GluFwd p)
 {
     constexpr int R = 2 * NB, FM = BM / 32, FN = R / 32;
     constexpr int A_BYTES = BM * 128, SLOT = A_BYTES + R * 128, A_LD = BM / 32, B_LD = R / 32;
@@ -123,7 +123,7 @@ template <int BM, int NB, int S> __global__ __launch_bounds__(256) void glu_stre
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     const int n0 = blockIdx.x * NB;
-    const int64_t ld = (int64_t)p.d * 2;
+    const int64_t ld = (int64_t)p.d * sizeof(TI);
     const __amdgpu_buffer_rsrc_t rx = dg_rsrc(p.x), rg = dg_rsrc((const char *)p.wg + n0 * ld),
                                  ru = dg_rsrc((const char *)p.wu + n0 * ld);
     // copy j of a wave fills rows (j 4 + wave) 8 .. + 7; x's rows past T stay as they are (their results are dropped)
@@ -137,7 +137,7 @@ template <int BM, int NB, int S> __global__ __launch_bounds__(256) void glu_stre
         voff[j] = row * (int)ld + c * 16;
         na += x && (j * 4 + wave) * 8 < p.T;
     }
-    const int nk = p.d >> 6;
+    const int nk = (int)(ld >> 7);
     const int rot = (int)(blockIdx.x % (unsigned)nk);
     auto load = [&](int k, char *slot) {
         const int kt = k + rot < nk ? k + rot : k + rot - nk;
@@ -189,7 +189,7 @@ template <int BM, int NB, int S> __global__ __launch_bounds__(256) void glu_stre
         for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
             for (int fn = 0; fn < FN; ++fn)
-                mfma_chunk(__bf16{}, a[fm], b[fn], acc[fm][fn]);
+                mfma_chunk(TI{}, a[fm], b[fn], acc[fm][fn]);
         __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0): the slot has been read
         slot = slot + 1 == S ? 0 : slot + 1;
     }
@@ -218,10 +218,10 @@ template <int BM, int NB, int S> __global__ __launch_bounds__(256) void glu_stre
         }
         const int64_t o = (int64_t)m * p.F + n0 + c;
         if (p.g)
-            ((__bf16 *)p.g)[o] = (__bf16)g;
+            store_elem((TI *)p.g + o, g);
         if (p.u)
-            ((__bf16 *)p.u)[o] = (__bf16)u;
-        ((__bf16 *)p.h)[o] = (__bf16)(glu_act<true>(g, p.act) * u);
+            store_elem((TI *)p.u + o, u);
+        store_elem((TI *)p.h + o, glu_act<sizeof(TI) == 2>(g, p.act) * u);
     }
 }
 
@@ -345,7 +345,9 @@ template <typename TI> __global__ __launch_bounds__(256) void glu_join_kernel(Gl
 // 64 x 128 tiles, 4 waves of 32 x 64, v_mfma_f32_32x32x2f32: a lane supplies one
 // element, index l % 32 at K index l / 32, so LDS keeps [K][index] rows for both
 // layouts and is read without conflicts.  K in steps of 16, two LDS slots, the
-// next step's elements on their way in registers meanwhile.
+// next F32_AHEAD steps' elements on their way in registers meanwhile (one step
+// ahead left a load's whole latency to wait for: 59 us at 300 x 1024 x 1024).
+constexpr int F32_AHEAD = 4;
 template <int IDX, bool KC, int DB> struct F32Operand {
     static constexpr int V = IDX / 64;  // float4 a thread
     static constexpr int PITCH = IDX + 4;
@@ -417,28 +419,35 @@ template <bool A_KC, bool B_KC, int DB> struct F32Core {
 #pragma unroll
             for (int i = 0; i < 16; ++i)
                 acc[fn][i] = 0.f;
-        float4 ra[1], rb[2];
-        if (k0 < k1) {
-            a.load(k0, ra);
-            b.load(k0, rb);
-        }
-        for (int kt = k0; kt < k1; ++kt) {
-            float *sa = smem + ((kt - k0) & 1) * SLOT, *sb = sa + 16 * (BM + 4);
-            a.store(sa, ra);
-            b.store(sb, rb);
-            __syncthreads();
-            if (kt + 1 < k1) {
-                a.load(kt + 1, ra);
-                b.load(kt + 1, rb);
+        float4 ra[F32_AHEAD][1], rb[F32_AHEAD][2];
+#pragma unroll
+        for (int j = 0; j < F32_AHEAD; ++j)
+            if (k0 + j < k1) {
+                a.load(k0 + j, ra[j]);
+                b.load(k0 + j, rb[j]);
             }
+        for (int kt = k0; kt < k1; kt += F32_AHEAD) {
 #pragma unroll
-            for (int k = 0; k < 16; k += 2) {
-                const int kk = k + (lane >> 5), col = lane & 31;
-                const float av = sa[kk * (BM + 4) + wm * 32 + col];
+            for (int j = 0; j < F32_AHEAD; ++j) {
+                if (kt + j >= k1)
+                    break;
+                float *sa = smem + (j & 1) * SLOT, *sb = sa + 16 * (BM + 4);
+                a.store(sa, ra[j]);
+                b.store(sb, rb[j]);
+                __syncthreads();  // the other slot's readers have passed the barrier before
+                if (kt + j + F32_AHEAD < k1) {
+                    a.load(kt + j + F32_AHEAD, ra[j]);
+                    b.load(kt + j + F32_AHEAD, rb[j]);
+                }
 #pragma unroll
-                for (int fn = 0; fn < 2; ++fn)
-                    acc[fn] = __builtin_amdgcn_mfma_f32_32x32x2f32(av, sb[kk * (BN + 4) + wn * 64 + fn * 32 + col],
-                                                                   acc[fn], 0, 0, 0);
+                for (int k = 0; k < 16; k += 2) {
+                    const int kk = k + (lane >> 5), col = lane & 31;
+                    const float av = sa[kk * (BM + 4) + wm * 32 + col];
+#pragma unroll
+                    for (int fn = 0; fn < 2; ++fn)
+                        acc[fn] = __builtin_amdgcn_mfma_f32_32x32x2f32(av, sb[kk * (BN + 4) + wn * 64 + fn * 32 + col],
+                                                                       acc[fn], 0, 0, 0);
+                }
             }
         }
     }
@@ -549,18 +558,22 @@ static MulPlan mul_plan(int64_t M, int64_t N, int64_t K, int tiles, int most_spl
 hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
 {
     GluFwd p = args;
+    if (p.T <= GLU_FEW) {
+        const dim3 grid(p.F / 16), block(256);
+        if (vdtype == 1 && p.T <= 32)
+            glu_stream_kernel<__bf16, 32, 16, 9><<<grid, block, 0, s>>>(p);
+        else if (vdtype == 1)
+            glu_stream_kernel<__bf16, 64, 16, 6><<<grid, block, 0, s>>>(p);
+        else if (p.T <= 32)
+            glu_stream_kernel<float, 32, 16, 9><<<grid, block, 0, s>>>(p);
+        else
+            glu_stream_kernel<float, 64, 16, 6><<<grid, block, 0, s>>>(p);
+        return hipGetLastError();
+    }
     if (vdtype == 0) {
         p.MT = (int)ceil_div(p.T, 64);
         p.NT = (int)ceil_div(p.F, 64);
         glu_f32_kernel<<<dim3(p.MT * p.NT), dim3(256), 0, s>>>(p);
-        return hipGetLastError();
-    }
-    if (p.T <= GLU_FEW) {
-        const dim3 grid(p.F / 16), block(256);
-        if (p.T <= 32)
-            glu_stream_kernel<32, 16, 9><<<grid, block, 0, s>>>(p);
-        else
-            glu_stream_kernel<64, 16, 6><<<grid, block, 0, s>>>(p);
         return hipGetLastError();
     }
     const int tile = mul_plan(p.T, 2 * (int64_t)p.F, p.d, 4, 1).tile;
