@@ -14,9 +14,11 @@
 // with 8-bit states.  One launch covers up to AW_BATCH tensors: their table is
 // in the kernel's arguments (no table to build in device memory, and a captured
 // graph keeps it), a workgroup finds its tensor by a binary search over the
-// first-workgroup numbers.  A thread holds 8 consecutive elements: 16-byte
-// accesses throughout, and a block of 256 that shares a scale is 32 lanes, so
-// its largest value needs no LDS.
+// first-workgroup numbers.  A lane holds 4 consecutive elements of each of two
+// blocks of 256: a wave's fp32 accesses are 16 bytes a lane without gaps (8
+// consecutive elements a lane left gaps of 16 bytes between a store's pieces),
+// and the 256 elements that share a scale are one wave, so their largest value
+// needs no LDS.
 //
 // 8-bit states.  m: sign and 7 bits, sqrt(v): 8 bits, both the upper bits of
 // the fp32 pattern of |x| / scale (3 and 4 bits of mantissa) with the exponent
@@ -29,6 +31,8 @@
 #include "adamw.h"
 #include "twell_device.h"
 
+#include <type_traits>
+
 namespace twell {
 
 __device__ __forceinline__ uint32_t aw_noise(uint32_t key, int64_t i)
@@ -39,16 +43,23 @@ __device__ __forceinline__ uint32_t aw_noise(uint32_t key, int64_t i)
     return x ^ (x >> 16);
 }
 
-// Largest of `bits` (non-negative floats' patterns, NaN above all) over the
-// 32 lanes of a half-wave.
-__device__ __forceinline__ uint32_t half_wave_umax(uint32_t b)
+// Largest of `b` (non-negative floats' patterns, NaN above all) over the wave,
+// with DPP row shifts and row broadcasts; lanes without a source count as 0.
+__device__ __forceinline__ uint32_t wave_umax(uint32_t b)
 {
-#pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        const uint32_t o = (uint32_t)__shfl_xor((int)b, m, 64);
+    auto step = [&](auto ctrl, auto rows) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)b, decltype(ctrl)::value, decltype(rows)::value,
+                                                                 0xf, false);
         b = o > b ? o : b;
-    }
-    return b;
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});  // row_shr:2
+    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});  // row_shr:4
+    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});  // row_shr:8
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)b, 63);
 }
 
 constexpr int AW_M_OFF = 889, AW_V_OFF = 1777;  // codes 127 and 255 are 1.0
@@ -83,26 +94,29 @@ __device__ __forceinline__ uint32_t aw_code(float a, float inv, uint32_t noise, 
     return (uint32_t)c;
 }
 
-__device__ __forceinline__ void load8f(const void *p, int64_t i, bool bf16, bool vec, int left, float (&o)[8])
+// 4 elements from index i, `left` of them inside the tensor; WIDE: all 4, and
+// aligned for one access.  The types are the template's: a conversion under a
+// run-time branch would wait for its load there, one load after another.
+template <bool BF16, bool WIDE> __device__ __forceinline__ void load4f(const void *p, int64_t i, int left, float (&o)[4])
 {
-    if (vec && left >= 8) {
-        if (bf16) {
-            const u32x4 c = ldg16((const __bf16 *)p + i);
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                o[e] = chunk_elem<__bf16>(c, e);
+    if constexpr (WIDE) {
+        if constexpr (BF16) {
+            const uint2 c = *reinterpret_cast<const uint2 *>((const __bf16 *)p + i);
+            o[0] = __uint_as_float(c.x << 16);
+            o[1] = __uint_as_float(c.x & 0xFFFF0000u);
+            o[2] = __uint_as_float(c.y << 16);
+            o[3] = __uint_as_float(c.y & 0xFFFF0000u);
         } else {
-            const u32x4 a = ldg16((const float *)p + i), b = ldg16((const float *)p + i + 4);
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                o[e] = __uint_as_float(a[e]);
-                o[e + 4] = __uint_as_float(b[e]);
-            }
+            const float4 c = *reinterpret_cast<const float4 *>((const float *)p + i);
+            o[0] = c.x;
+            o[1] = c.y;
+            o[2] = c.z;
+            o[3] = c.w;
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            o[e] = e >= left ? 0.f : bf16 ? (float)((const __bf16 *)p)[i + e] : ((const float *)p)[i + e];
+        for (int e = 0; e < 4; ++e)
+            o[e] = e >= left ? 0.f : BF16 ? (float)((const __bf16 *)p)[i + e] : ((const float *)p)[i + e];
     }
 }
 
@@ -112,22 +126,19 @@ __device__ __forceinline__ uint32_t pack2(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-__device__ __forceinline__ void store8f(void *p, int64_t i, bool bf16, bool vec, int left, const float (&v)[8])
+template <bool BF16, bool WIDE>
+__device__ __forceinline__ void store4f(void *p, int64_t i, int left, const float (&v)[4])
 {
-    if (vec && left >= 8) {
-        if (bf16) {
-            *reinterpret_cast<u32x4 *>((__bf16 *)p + i) =
-                u32x4{pack2(v[0], v[1]), pack2(v[2], v[3]), pack2(v[4], v[5]), pack2(v[6], v[7])};
-        } else {
-            float *q = (float *)p + i;
-            *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
-            *reinterpret_cast<float4 *>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
-        }
+    if constexpr (WIDE) {
+        if constexpr (BF16)
+            *reinterpret_cast<uint2 *>((__bf16 *)p + i) = make_uint2(pack2(v[0], v[1]), pack2(v[2], v[3]));
+        else
+            *reinterpret_cast<float4 *>((float *)p + i) = make_float4(v[0], v[1], v[2], v[3]);
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
+        for (int e = 0; e < 4; ++e)
             if (e < left) {
-                if (bf16)
+                if constexpr (BF16)
                     ((__bf16 *)p)[i + e] = (__bf16)v[e];
                 else
                     ((float *)p)[i + e] = v[e];
@@ -135,34 +146,31 @@ __device__ __forceinline__ void store8f(void *p, int64_t i, bool bf16, bool vec,
     }
 }
 
-__device__ __forceinline__ void load8c(const uint8_t *p, int64_t i, bool vec, int left, uint32_t (&c)[8])
+template <bool WIDE> __device__ __forceinline__ uint32_t load4c(const uint8_t *p, int64_t i, int left)
 {
-    if (vec && left >= 8) {
-        const uint2 w = *reinterpret_cast<const uint2 *>(p + i);
+    if constexpr (WIDE)
+        return *reinterpret_cast<const uint32_t *>(p + i);
+    uint32_t c = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            c[e] = (w.x >> (8 * e)) & 255u;
-            c[e + 4] = (w.y >> (8 * e)) & 255u;
-        }
+    for (int e = 0; e < 4; ++e)
+        if (e < left)
+            c |= (uint32_t)p[i + e] << (8 * e);
+    return c;
+}
+
+template <bool WIDE> __device__ __forceinline__ void store4c(uint8_t *p, int64_t i, int left, uint32_t c)
+{
+    if constexpr (WIDE) {
+        *reinterpret_cast<uint32_t *>(p + i) = c;
     } else {
 #pragma unroll
-        for (int e = 0; e < 8; ++e)
-            c[e] = e < left ? p[i + e] : 0u;
+        for (int e = 0; e < 4; ++e)
+            if (e < left)
+                p[i + e] = (uint8_t)(c >> (8 * e));
     }
 }
 
-__device__ __forceinline__ void store8c(uint8_t *p, int64_t i, bool vec, int left, const uint32_t (&c)[8])
-{
-    if (vec && left >= 8) {
-        *reinterpret_cast<uint2 *>(p + i) = make_uint2(c[0] | c[1] << 8 | c[2] << 16 | c[3] << 24,
-                                                       c[4] | c[5] << 8 | c[6] << 16 | c[7] << 24);
-    } else {
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            if (e < left)
-                p[i + e] = (uint8_t)c[e];
-    }
-}
+__device__ __forceinline__ int aw_left(int64_t n, int64_t i) { return n - i >= 4 ? 4 : n - i > 0 ? (int)(n - i) : 0; }
 
 // The tensor whose workgroups include `wg`.
 template <typename B> __device__ __forceinline__ int aw_find(const B &b, int wg)
@@ -178,9 +186,99 @@ template <typename B> __device__ __forceinline__ int aw_find(const B &b, int wg)
     return lo;
 }
 
-template <bool CODED> __global__ __launch_bounds__(AW_THREADS) void adamw_kernel(AwBatch b)
+// The step on one workgroup's elements, from c0 on.
+template <bool CODED, bool PB, bool GB, bool WIDE>
+__device__ __forceinline__ void adamw_chunk(const AwBatch &b, const AwTensor &t, int64_t c0, float gs)
 {
 #pragma clang fp contract(off)
+    const int lane = threadIdx.x & 63;
+    const int64_t w0 = c0 + (threadIdx.x >> 6) * (2 * AW_QBLOCK);
+#pragma unroll 1
+    for (int pass = 0; pass < AW_CHUNK / AW_PASS; ++pass) {
+        const int64_t b0 = w0 + pass * AW_PASS;  // the wave's first block
+        if (!WIDE && b0 >= t.n)
+            return;
+        float p[2][4], g[2][4], m[2][4], v[2][4];
+        uint32_t cm[2], cv[2];
+        float sm[2], sv[2];
+        int left[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t i = b0 + h * AW_QBLOCK + lane * 4;
+            left[h] = WIDE ? 4 : aw_left(t.n, i);
+            load4f<PB, WIDE>(t.p, i, left[h], p[h]);
+            load4f<GB, WIDE>(t.grad, i, left[h], g[h]);
+            if constexpr (CODED) {
+                cm[h] = load4c<WIDE>((const uint8_t *)t.m, i, left[h]);
+                cv[h] = load4c<WIDE>((const uint8_t *)t.v, i, left[h]);
+                const int64_t q = (WIDE || b0 + h * AW_QBLOCK < t.n ? b0 + h * AW_QBLOCK : b0) / AW_QBLOCK;
+                sm[h] = t.m_scale[q];
+                sv[h] = t.v_scale[q];
+            } else {
+                load4f<false, WIDE>(t.m, i, left[h], m[h]);
+                load4f<false, WIDE>(t.v, i, left[h], v[h]);
+            }
+        }
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int64_t i = b0 + h * AW_QBLOCK + lane * 4;
+            float r[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if constexpr (CODED) {
+                    m[h][e] = aw_dec_m((cm[h] >> (8 * e)) & 255u, sm[h]);
+                    const float root = aw_dec_r((cv[h] >> (8 * e)) & 255u, sv[h]);
+                    v[h][e] = root * root;
+                }
+                const float ge = g[h][e] * gs;
+                m[h][e] = m[h][e] * b.beta1 + ge * b.omb1;
+                v[h][e] = v[h][e] * b.beta2 + (ge * ge) * b.omb2;
+                r[e] = sqrtf(v[h][e]);
+                p[h][e] = p[h][e] * t.decay - (m[h][e] / (r[e] * b.root + b.eps)) * b.size;
+            }
+            store4f<PB, WIDE>(t.p, i, left[h], p[h]);
+            if (t.copy)
+                store4f<true, WIDE>(t.copy, i, left[h], p[h]);
+            if constexpr (CODED) {
+                if (!WIDE && b0 + h * AW_QBLOCK >= t.n)
+                    return;
+                uint32_t am = 0, ar = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    if (e < left[h]) {
+                        const uint32_t bm = __float_as_uint(m[h][e]) & 0x7FFFFFFFu;
+                        const uint32_t br = __float_as_uint(r[e]) & 0x7FFFFFFFu;
+                        am = bm > am ? bm : am;
+                        ar = br > ar ? br : ar;
+                    }
+                float im, ir;
+                aw_scale(wave_umax(am), sm[h], im);
+                aw_scale(wave_umax(ar), sv[h], ir);
+                uint32_t om = 0, ov = 0;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint32_t x = aw_noise(t.key, i + e);
+                    om |= (aw_code(fabsf(m[h][e]), im, x & 0xFFFFFu, 20, AW_M_OFF, 127) | (m[h][e] < 0.f ? 128u : 0u))
+                          << (8 * e);
+                    const uint32_t c = aw_code(r[e], ir, x >> 13, 19, AW_V_OFF, 255);
+                    ov |= (c == 0 && r[e] * ir > 0.f ? 1u : c) << (8 * e);
+                }
+                store4c<WIDE>((uint8_t *)t.m, i, left[h], om);
+                store4c<WIDE>((uint8_t *)t.v, i, left[h], ov);
+                if (lane == 0) {
+                    t.m_scale[b0 / AW_QBLOCK + h] = sm[h];
+                    t.v_scale[b0 / AW_QBLOCK + h] = sv[h];
+                }
+            } else {
+                store4f<false, WIDE>(t.m, i, left[h], m[h]);
+                store4f<false, WIDE>(t.v, i, left[h], v[h]);
+            }
+        }
+    }
+}
+
+template <bool CODED> __global__ __launch_bounds__(AW_THREADS) void adamw_kernel(AwBatch b)
+{
     float gs = 1.f;
     if (b.grad_scale) {
         gs = *b.grad_scale;
@@ -189,103 +287,60 @@ template <bool CODED> __global__ __launch_bounds__(AW_THREADS) void adamw_kernel
             return;
     }
     const AwTensor &t = b.t[aw_find(b, blockIdx.x)];
-    const bool vec = t.flags & AW_VEC, pb = t.flags & AW_P_BF16, gb = t.flags & AW_G_BF16;
-    const int64_t i0 = (int64_t)((int)blockIdx.x - t.chunk0) * AW_CHUNK + threadIdx.x * 8;
-#pragma unroll 1
-    for (int pass = 0; pass < AW_CHUNK / AW_PASS; ++pass) {
-        const int64_t i = i0 + pass * AW_PASS;
-        // whole blocks of 256 leave together: their 32 lanes share the largest value
-        if ((i & ~(int64_t)(AW_QBLOCK - 1)) >= t.n)
-            return;
-        const int left = t.n - i >= 8 ? 8 : t.n - i > 0 ? (int)(t.n - i) : 0;
-        float p[8], g[8], m[8], v[8];
-        load8f(t.p, i, pb, vec, left, p);
-        load8f(t.grad, i, gb, vec, left, g);
-        if constexpr (CODED) {
-            uint32_t cm[8], cv[8];
-            load8c((const uint8_t *)t.m, i, vec, left, cm);
-            load8c((const uint8_t *)t.v, i, vec, left, cv);
-            const float sm = t.m_scale[i / AW_QBLOCK], sv = t.v_scale[i / AW_QBLOCK];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                m[e] = aw_dec_m(cm[e], sm);
-                const float r = aw_dec_r(cv[e], sv);
-                v[e] = r * r;
-            }
-        } else {
-            load8f(t.m, i, false, vec, left, m);
-            load8f(t.v, i, false, vec, left, v);
-        }
-        float r[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const float ge = g[e] * gs;
-            m[e] = m[e] * b.beta1 + ge * b.omb1;
-            v[e] = v[e] * b.beta2 + (ge * ge) * b.omb2;
-            r[e] = sqrtf(v[e]);
-            p[e] = p[e] * t.decay - (m[e] / (r[e] * b.root + b.eps)) * b.size;
-        }
-        store8f(t.p, i, pb, vec, left, p);
-        if (t.copy)
-            store8f(t.copy, i, true, vec, left, p);
-        if constexpr (CODED) {
-            uint32_t am = 0, ar = 0;
-#pragma unroll
-            for (int e = 0; e < 8; ++e)
-                if (e < left) {
-                    const uint32_t bm = __float_as_uint(m[e]) & 0x7FFFFFFFu, br = __float_as_uint(r[e]) & 0x7FFFFFFFu;
-                    am = bm > am ? bm : am;
-                    ar = br > ar ? br : ar;
-                }
-            float sm, im, sr, ir;
-            aw_scale(half_wave_umax(am), sm, im);
-            aw_scale(half_wave_umax(ar), sr, ir);
-            uint32_t cm[8], cv[8];
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const uint32_t x = aw_noise(t.key, i + e);
-                cm[e] = aw_code(fabsf(m[e]), im, x & 0xFFFFFu, 20, AW_M_OFF, 127) | (m[e] < 0.f ? 128u : 0u);
-                const uint32_t c = aw_code(r[e], ir, x >> 13, 19, AW_V_OFF, 255);
-                cv[e] = c == 0 && r[e] * ir > 0.f ? 1u : c;
-            }
-            store8c((uint8_t *)t.m, i, vec, left, cm);
-            store8c((uint8_t *)t.v, i, vec, left, cv);
-            if ((threadIdx.x & 31) == 0) {
-                t.m_scale[i / AW_QBLOCK] = sm;
-                t.v_scale[i / AW_QBLOCK] = sr;
-            }
-        } else {
-            store8f(t.m, i, false, vec, left, m);
-            store8f(t.v, i, false, vec, left, v);
-        }
+    const int64_t c0 = (int64_t)((int)blockIdx.x - t.chunk0) * AW_CHUNK;
+    const bool pb = t.flags & AW_P_BF16, gb = t.flags & AW_G_BF16;
+    if ((t.flags & AW_VEC) && c0 + AW_CHUNK <= t.n) {
+        if (pb)
+            gb ? adamw_chunk<CODED, true, true, true>(b, t, c0, gs) : adamw_chunk<CODED, true, false, true>(b, t, c0, gs);
+        else
+            gb ? adamw_chunk<CODED, false, true, true>(b, t, c0, gs) : adamw_chunk<CODED, false, false, true>(b, t, c0, gs);
+    } else {
+        if (pb)
+            gb ? adamw_chunk<CODED, true, true, false>(b, t, c0, gs) : adamw_chunk<CODED, true, false, false>(b, t, c0, gs);
+        else
+            gb ? adamw_chunk<CODED, false, true, false>(b, t, c0, gs) : adamw_chunk<CODED, false, false, false>(b, t, c0, gs);
     }
 }
 
 // m_values = m, v_values = sqrt(v)^2 of the codes: 2 + 8 bytes an element.
+template <typename T, bool WIDE> __device__ __forceinline__ void unpack_chunk(T t, int64_t c0)
+{
+    constexpr int N = AW_CHUNK / AW_THREADS / 4;
+    uint32_t cm[N], cv[N];
+    float sm[N], sv[N];
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int64_t i = c0 + k * (AW_THREADS * 4) + threadIdx.x * 4;
+        const int left = WIDE ? 4 : aw_left(t.n, i);
+        cm[k] = load4c<WIDE>(t.m, i, left);
+        cv[k] = load4c<WIDE>(t.v, i, left);
+        sm[k] = left ? t.m_scale[i / AW_QBLOCK] : 0.f;
+        sv[k] = left ? t.v_scale[i / AW_QBLOCK] : 0.f;
+    }
+#pragma unroll
+    for (int k = 0; k < N; ++k) {
+        const int64_t i = c0 + k * (AW_THREADS * 4) + threadIdx.x * 4;
+        const int left = WIDE ? 4 : aw_left(t.n, i);
+        float m[4], v[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            m[e] = aw_dec_m((cm[k] >> (8 * e)) & 255u, sm[k]);
+            const float r = aw_dec_r((cv[k] >> (8 * e)) & 255u, sv[k]);
+            v[e] = r * r;
+        }
+        store4f<false, WIDE>(t.m_values, i, left, m);
+        store4f<false, WIDE>(t.v_values, i, left, v);
+    }
+}
+
 __global__ __launch_bounds__(AW_THREADS) void adamw_unpack_kernel(AwUnpack b)
 {
     const auto &t = b.t[aw_find(b, blockIdx.x)];
-    const int64_t i0 = (int64_t)((int)blockIdx.x - t.chunk0) * AW_CHUNK + threadIdx.x * 8;
-#pragma unroll 1
-    for (int pass = 0; pass < AW_CHUNK / AW_PASS; ++pass) {
-        const int64_t i = i0 + pass * AW_PASS;
-        if (i >= t.n)
-            return;
-        const int left = t.n - i >= 8 ? 8 : (int)(t.n - i);
-        uint32_t cm[8], cv[8];
-        load8c(t.m, i, t.vec, left, cm);
-        load8c(t.v, i, t.vec, left, cv);
-        const float sm = t.m_scale[i / AW_QBLOCK], sv = t.v_scale[i / AW_QBLOCK];
-        float m[8], v[8];
-#pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            m[e] = aw_dec_m(cm[e], sm);
-            const float r = aw_dec_r(cv[e], sv);
-            v[e] = r * r;
-        }
-        store8f(t.m_values, i, false, t.vec, left, m);
-        store8f(t.v_values, i, false, t.vec, left, v);
-    }
+    const int64_t c0 = (int64_t)((int)blockIdx.x - t.chunk0) * AW_CHUNK;
+    if (t.vec && c0 + AW_CHUNK <= t.n)
+        unpack_chunk<decltype(t), true>(t, c0);
+    else
+        unpack_chunk<decltype(t), false>(t, c0);
 }
 
 hipError_t launch_adamw(const AwBatch &b, bool coded, int chunks, hipStream_t s)
