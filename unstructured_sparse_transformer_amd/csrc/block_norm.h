@@ -7,7 +7,7 @@
 namespace twell {
 
 constexpr int BN_MAX_D = 8192;   // 1024 threads of 8 elements hold a row
-constexpr int BN_BWD_WGS = 512;  // workgroups of the backward pass: each adds its rows' weight gradients
+constexpr int BN_BWD_THREADS = 256 * 768;  // threads of the backward pass
 
 // A tensor whose element type is known at run time.
 struct BnTensor {
@@ -25,13 +25,14 @@ struct BnArgs {
     // backward
     BnTensor dout, dn, dres, dy, dgate;
     float *dw[4];        // dw_post, db_post, dw_pre, db_pre (or NULL)
-    float *part;         // [6][wgs][d]: the four vectors, then the gate rows cut at a workgroup's first and last row
-    int wgs;
-    int rows;            // rows of a workgroup
+    float *part;         // [6][groups][d]: the four vectors, then the gate rows cut at a group's first and last row
+    int groups;          // row groups of the backward pass
+    int rows;            // rows of a group
+    int cuts;            // gate rows or group boundaries to look for cut gate rows at
 };
 
 hipError_t launch_block_norm(const BnArgs &a, bool layer, bool vec, hipStream_t s);
 hipError_t launch_block_norm_backward(const BnArgs &a, bool layer, bool vec, hipStream_t s);
-int block_norm_wgs(int T);
+int block_norm_groups(int T, int d);
 
 }  // namespace twell

@@ -27,26 +27,60 @@
 
 namespace twell {
 
+// How a row's columns lie on its NT threads, 8 a thread: BN_ANY one by one, for
+// any width and alignment; BN_8 eight consecutive ones (16 bytes of bf16); BN_4
+// two groups of four, the second 4 NT columns on (16 bytes of fp32, so that a
+// wave's accesses to fp32 have no gaps).
+enum BnLay { BN_ANY, BN_8, BN_4 };
+
+template <BnLay L, int NT> __device__ __forceinline__ int bn_col(int tid, int e)
+{
+    return L == BN_8 ? tid * 8 + e : L == BN_4 ? (e >> 2) * 4 * NT + tid * 4 + (e & 3) : e * NT + tid;
+}
+
 // 8 elements of a row as they lie in memory, requested now and used later.
 struct Raw8 {
     u32x4 a, b;
 };
 
-// Element e of thread `tid` is column tid * 8 + e (VEC) or e * NT + tid.
-template <bool VEC, int NT> __device__ __forceinline__ int bn_col(int tid, int e) { return VEC ? tid * 8 + e : e * NT + tid; }
+template <bool ONCE> __device__ __forceinline__ u32x4 bn_ld16(const void *p)
+{
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+    if constexpr (ONCE)
+        return __builtin_nontemporal_load(q);
+    return *q;
+}
 
-template <bool VEC, int NT> __device__ __forceinline__ Raw8 bn_load(BnTensor t, int64_t row, int d, int tid)
+template <BnLay L, int NT, bool ONCE = false>
+__device__ __forceinline__ Raw8 bn_load(BnTensor t, int64_t row, int d, int tid)
 {
     Raw8 r{};
-    if constexpr (VEC) {
+    if constexpr (L == BN_8) {
         if (tid * 8 < d) {
             if (t.bf16) {
-                r.a = ldg16((const __bf16 *)t.p + row * d + tid * 8);
+                r.a = bn_ld16<ONCE>((const __bf16 *)t.p + row * d + tid * 8);
             } else {
                 const float *q = (const float *)t.p + row * d + tid * 8;
-                r.a = ldg16(q);
-                r.b = ldg16(q + 4);
+                r.a = bn_ld16<ONCE>(q);
+                r.b = bn_ld16<ONCE>(q + 4);
             }
+        }
+    } else if constexpr (L == BN_4) {
+        const int c0 = tid * 4, c1 = 4 * NT + tid * 4;
+        if (t.bf16) {
+            const __bf16 *q = (const __bf16 *)t.p + row * d;
+            uint2 x{}, y{};
+            if (c0 < d)
+                x = *reinterpret_cast<const uint2 *>(q + c0);
+            if (c1 < d)
+                y = *reinterpret_cast<const uint2 *>(q + c1);
+            r.a = u32x4{x.x, x.y, y.x, y.y};
+        } else {
+            const float *q = (const float *)t.p + row * d;
+            if (c0 < d)
+                r.a = bn_ld16<ONCE>(q + c0);
+            if (c1 < d)
+                r.b = bn_ld16<ONCE>(q + c1);
         }
     } else {
 #pragma unroll
@@ -83,10 +117,10 @@ __device__ __forceinline__ uint32_t bn_pack(float a, float b)
     return __builtin_bit_cast(uint32_t, v);
 }
 
-template <bool VEC, int NT>
+template <BnLay L, int NT>
 __device__ __forceinline__ void bn_store(BnTensor t, int64_t row, int d, int tid, const float (&v)[8])
 {
-    if constexpr (VEC) {
+    if constexpr (L == BN_8) {
         if (tid * 8 < d) {
             if (t.bf16) {
                 *reinterpret_cast<u32x4 *>((__bf16 *)t.p + row * d + tid * 8) =
@@ -95,6 +129,19 @@ __device__ __forceinline__ void bn_store(BnTensor t, int64_t row, int d, int tid
                 float *q = (float *)t.p + row * d + tid * 8;
                 *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<float4 *>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
+            }
+        }
+    } else if constexpr (L == BN_4) {
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            const int c = h * 4 * NT + tid * 4;
+            if (c < d) {
+                if (t.bf16)
+                    *reinterpret_cast<uint2 *>((__bf16 *)t.p + row * d + c) =
+                        make_uint2(bn_pack(v[4 * h], v[4 * h + 1]), bn_pack(v[4 * h + 2], v[4 * h + 3]));
+                else
+                    *reinterpret_cast<float4 *>((float *)t.p + row * d + c) =
+                        make_float4(v[4 * h], v[4 * h + 1], v[4 * h + 2], v[4 * h + 3]);
             }
         }
     } else {
@@ -113,11 +160,11 @@ __device__ __forceinline__ void bn_store(BnTensor t, int64_t row, int d, int tid
 
 // Weights of a row's columns, `none` where the pointer is NULL.  Columns past d
 // hold 0 everywhere in a row, weights and biases too, so they add nothing to a sum.
-template <bool VEC, int NT>
+template <BnLay L, int NT>
 __device__ __forceinline__ void bn_weights(BnTensor t, int d, int tid, float none, float (&w)[8])
 {
     if (t.p) {
-        bn_values(bn_load<VEC, NT>(t, 0, d, tid), t.bf16, w);
+        bn_values(bn_load<L, NT>(t, 0, d, tid), t.bf16, w);
     } else {
 #pragma unroll
         for (int e = 0; e < 8; ++e)
@@ -154,7 +201,7 @@ template <int NT, int N> __device__ __forceinline__ void row_sums(float (&v)[N],
 }
 
 // v := vhat; returns rstd.  Columns past d hold 0 on entry and on return.
-template <bool LAYER, bool VEC, int NT>
+template <bool LAYER, BnLay L, int NT>
 __device__ __forceinline__ float bn_hat(float (&v)[8], int d, int tid, float eps, float *red, int &slot)
 {
     const float inv_d = 1.f / (float)d;
@@ -168,7 +215,7 @@ __device__ __forceinline__ float bn_hat(float (&v)[8], int d, int tid, float eps
         const float mean = s[0] * inv_d;
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            v[e] = bn_col<VEC, NT>(tid, e) < d ? v[e] - mean : 0.f;
+            v[e] = bn_col<L, NT>(tid, e) < d ? v[e] - mean : 0.f;
     }
     s[0] = 0.f;
 #pragma unroll
@@ -183,7 +230,7 @@ __device__ __forceinline__ float bn_hat(float (&v)[8], int d, int tid, float eps
 }
 
 // g (gradient times weight, 0 past d) := the norm's input gradient.
-template <bool LAYER, bool VEC, int NT>
+template <bool LAYER, BnLay L, int NT>
 __device__ __forceinline__ void bn_hat_grad(float (&g)[8], const float (&hat)[8], float rstd, int d, int tid,
                                             float *red, int &slot)
 {
@@ -211,78 +258,82 @@ __device__ __forceinline__ void bn_hat_grad(float (&g)[8], const float (&hat)[8]
 // workgroup each.
 template <int NT> constexpr int bn_threads() { return NT == 64 ? 256 : NT; }
 
-template <bool LAYER, bool VEC, int NT>
+template <bool LAYER, BnLay L, int NT>
 __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_kernel(BnArgs a)
 {
     constexpr int RPW = bn_threads<NT>() / NT;
     __shared__ float red[NT > 64 ? 4 * (NT / 64) : 1];
     int slot = 0;
     const int tid = threadIdx.x % NT;
-    const int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / NT;
+    const int64_t step = (int64_t)gridDim.x * RPW;
+    int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / NT;
     if (row >= a.T)  // whole waves: a row is a multiple of 64 threads
         return;
-    const Raw8 rr = bn_load<VEC, NT>(a.res, row, a.d, tid);
-    float r[8];
-    if (a.y.p) {
-        const Raw8 ry = bn_load<VEC, NT>(a.y, row, a.d, tid);
-        Raw8 rg{};
+    const bool block = a.y.p, next = a.n.p;
+    Raw8 rr{}, ry{}, rg{};
+    auto request = [&](int64_t t) {
+        rr = bn_load<L, NT>(a.res, t, a.d, tid);
+        if (block)
+            ry = bn_load<L, NT>(a.y, t, a.d, tid);
         if (a.gate_span)
-            rg = bn_load<VEC, NT>(a.gate, (int)row / a.gate_span, a.d, tid);
-        float p[8];
+            rg = bn_load<L, NT>(a.gate, (int)t / a.gate_span, a.d, tid);
+    };
+    request(row);
+    float wpost[8], bpost[8], wpre[8], bpre[8];
+    bn_weights<L, NT>(a.w_post, a.d, tid, 1.f, wpost);
+    bn_weights<L, NT>(a.b_post, a.d, tid, 0.f, bpost);
+    bn_weights<L, NT>(a.w_pre, a.d, tid, 1.f, wpre);
+    bn_weights<L, NT>(a.b_pre, a.d, tid, 0.f, bpre);
+    for (; row < a.T; row += step) {
+        float r[8], p[8], g[8];
+        bn_values(rr, a.res.bf16, r);
         bn_values(ry, a.y.bf16, p);
-        if (a.post) {
-            float w[8], b[8];
-            bn_weights<VEC, NT>(a.w_post, a.d, tid, 1.f, w);
-            bn_weights<VEC, NT>(a.b_post, a.d, tid, 0.f, b);
-            bn_hat<LAYER, VEC, NT>(p, a.d, tid, a.eps, red, slot);
+        bn_values(rg, a.gate.bf16, g);
+        if (row + step < a.T)  // on its way while this row's sums are taken
+            request(row + step);
+        if (block) {
+            if (a.post) {
+                bn_hat<LAYER, L, NT>(p, a.d, tid, a.eps, red, slot);
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    p[e] = p[e] * wpost[e] + bpost[e];
+            }
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                p[e] = p[e] * w[e] + b[e];
+                r[e] += a.alpha * (a.gate_span ? p[e] * g[e] : p[e]);
+            if (a.out.p)
+                bn_store<L, NT>(a.out, row, a.d, tid, r);
         }
-        if (a.gate_span) {
-            float g[8];
-            bn_values(rg, a.gate.bf16, g);
+        if (next) {
+            bn_hat<LAYER, L, NT>(r, a.d, tid, a.eps, red, slot);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                p[e] *= g[e];
+                r[e] = r[e] * wpre[e] + bpre[e];
+            bn_store<L, NT>(a.n, row, a.d, tid, r);
         }
-        bn_values(rr, a.res.bf16, r);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            r[e] += a.alpha * p[e];
-        if (a.out.p)
-            bn_store<VEC, NT>(a.out, row, a.d, tid, r);
-    } else {
-        bn_values(rr, a.res.bf16, r);
-    }
-    if (a.n.p) {
-        float w[8], b[8];
-        bn_weights<VEC, NT>(a.w_pre, a.d, tid, 1.f, w);
-        bn_weights<VEC, NT>(a.b_pre, a.d, tid, 0.f, b);
-        bn_hat<LAYER, VEC, NT>(r, a.d, tid, a.eps, red, slot);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            r[e] = r[e] * w[e] + b[e];
-        bn_store<VEC, NT>(a.n, row, a.d, tid, r);
     }
 }
 
-// Workgroup b takes the rows [b rows, (b + 1) rows).  Its sums over those rows
-// stay in registers and leave as one partial row per vector.  A gate row whose
-// rows all lie in the workgroup is finished here; one cut at the workgroup's
-// first row leaves in slot 4, one cut at its last row only in slot 5.
-template <bool LAYER, bool VEC, int NT>
-__global__ __launch_bounds__(NT) void block_norm_backward_kernel(BnArgs a)
+// Row group b (the NT threads of a row; 4 of them in a workgroup when NT = 64)
+// takes the rows [b rows, (b + 1) rows).  Its sums over those rows stay in
+// registers and leave as one partial row per vector.  A gate row whose rows all
+// lie in the group is finished here; one cut at the group's first row leaves in
+// slot 4, one cut at its last row only in slot 5.
+template <bool LAYER, bool BIAS, BnLay L, int NT>
+__global__ __launch_bounds__(bn_threads<NT>()) void block_norm_backward_kernel(BnArgs a)
 {
     __shared__ float red[NT > 64 ? 4 * (NT / 64) : 1];
     int slot = 0;
-    const int tid = threadIdx.x;
-    const int64_t r0 = (int64_t)blockIdx.x * a.rows;
+    const int tid = threadIdx.x % NT;
+    const int grp = NT == 64 ? (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : (int)blockIdx.x;
+    if (grp >= a.groups)
+        return;
+    const int64_t r0 = (int64_t)grp * a.rows;
     const int64_t r1 = r0 + a.rows < a.T ? r0 + a.rows : a.T;
     float wpost[8], bpost[8], wpre[8], acc[4][8], ag[8];
-    bn_weights<VEC, NT>(a.w_post, a.d, tid, 1.f, wpost);
-    bn_weights<VEC, NT>(a.b_post, a.d, tid, 0.f, bpost);
-    bn_weights<VEC, NT>(a.w_pre, a.d, tid, 1.f, wpre);
+    bn_weights<L, NT>(a.w_post, a.d, tid, 1.f, wpost);
+    bn_weights<L, NT>(a.b_post, a.d, tid, 0.f, bpost);
+    bn_weights<L, NT>(a.w_pre, a.d, tid, 1.f, wpre);
 #pragma unroll
     for (int e = 0; e < 8; ++e) {
         ag[e] = 0.f;
@@ -294,43 +345,44 @@ __global__ __launch_bounds__(NT) void block_norm_backward_kernel(BnArgs a)
     for (int64_t row = r0; row < r1; ++row) {
         Raw8 ro{}, rd{}, rn{}, ry{}, rg{};
         if (a.dout.p)
-            rd = bn_load<VEC, NT>(a.dout, row, a.d, tid);
+            rd = bn_load<L, NT, true>(a.dout, row, a.d, tid);
         if (a.dn.p) {
-            ro = bn_load<VEC, NT>(a.res, row, a.d, tid);
-            rn = bn_load<VEC, NT>(a.dn, row, a.d, tid);
+            ro = bn_load<L, NT, true>(a.res, row, a.d, tid);
+            rn = bn_load<L, NT, true>(a.dn, row, a.d, tid);
         }
         if (a.y.p)
-            ry = bn_load<VEC, NT>(a.y, row, a.d, tid);
+            ry = bn_load<L, NT, true>(a.y, row, a.d, tid);
         if (a.gate_span)
-            rg = bn_load<VEC, NT>(a.gate, (int)row / a.gate_span, a.d, tid);
+            rg = bn_load<L, NT>(a.gate, (int)row / a.gate_span, a.d, tid);
         float dr[8];
         bn_values(rd, a.dout.bf16, dr);
         if (a.dn.p) {
             float hat[8], dn[8];
             bn_values(ro, a.res.bf16, hat);
             bn_values(rn, a.dn.bf16, dn);
-            const float rstd = bn_hat<LAYER, VEC, NT>(hat, a.d, tid, a.eps, red, slot);
+            const float rstd = bn_hat<LAYER, L, NT>(hat, a.d, tid, a.eps, red, slot);
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 acc[2][e] += dn[e] * hat[e];
-                acc[3][e] += dn[e];
+                if constexpr (BIAS)
+                    acc[3][e] += dn[e];
                 dn[e] *= wpre[e];
             }
-            bn_hat_grad<LAYER, VEC, NT>(dn, hat, rstd, a.d, tid, red, slot);
+            bn_hat_grad<LAYER, L, NT>(dn, hat, rstd, a.d, tid, red, slot);
 #pragma unroll
             for (int e = 0; e < 8; ++e)
                 dr[e] += dn[e];
         }
-        bn_store<VEC, NT>(a.dres, row, a.d, tid, dr);
+        bn_store<L, NT>(a.dres, row, a.d, tid, dr);
         if (!a.y.p)
             continue;
         float hat[8], rstd = 1.f;
         bn_values(ry, a.y.bf16, hat);
         if (a.post)
-            rstd = bn_hat<LAYER, VEC, NT>(hat, a.d, tid, a.eps, red, slot);
+            rstd = bn_hat<LAYER, L, NT>(hat, a.d, tid, a.eps, red, slot);
 #pragma unroll
         for (int e = 0; e < 8; ++e)
-            dr[e] = bn_col<VEC, NT>(tid, e) < a.d ? dr[e] * a.alpha : 0.f;
+            dr[e] = bn_col<L, NT>(tid, e) < a.d ? dr[e] * a.alpha : 0.f;
         if (a.gate_span) {
             float g[8];
             bn_values(rg, a.gate.bf16, g);
@@ -344,10 +396,10 @@ __global__ __launch_bounds__(NT) void block_norm_backward_kernel(BnArgs a)
                 const bool head = group * a.gate_span < r0;
                 const bool tail = (group + 1) * a.gate_span > r1 && r1 < a.T;
                 if (!head && !tail) {
-                    bn_store<VEC, NT>(a.dgate, group, a.d, tid, ag);
+                    bn_store<L, NT>(a.dgate, group, a.d, tid, ag);
                 } else {
-                    const BnTensor t{a.part + ((int64_t)(head ? 4 : 5) * a.wgs + blockIdx.x) * a.d, 0};
-                    bn_store<VEC, NT>(t, 0, a.d, tid, ag);
+                    const BnTensor t{a.part + ((int64_t)(head ? 4 : 5) * a.groups + grp) * a.d, 0};
+                    bn_store<L, NT>(t, 0, a.d, tid, ag);
                 }
                 group = next;
 #pragma unroll
@@ -359,109 +411,165 @@ __global__ __launch_bounds__(NT) void block_norm_backward_kernel(BnArgs a)
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 acc[0][e] += dr[e] * hat[e];
-                acc[1][e] += dr[e];
+                if constexpr (BIAS)
+                    acc[1][e] += dr[e];
                 dr[e] *= wpost[e];
             }
-            bn_hat_grad<LAYER, VEC, NT>(dr, hat, rstd, a.d, tid, red, slot);
+            bn_hat_grad<LAYER, L, NT>(dr, hat, rstd, a.d, tid, red, slot);
         }
-        bn_store<VEC, NT>(a.dy, row, a.d, tid, dr);
+        bn_store<L, NT>(a.dy, row, a.d, tid, dr);
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (a.dw[k]) {
-            const BnTensor t{a.part + ((int64_t)k * a.wgs + blockIdx.x) * a.d, 0};
-            bn_store<VEC, NT>(t, 0, a.d, tid, acc[k]);
+            const BnTensor t{a.part + ((int64_t)k * a.groups + grp) * a.d, 0};
+            bn_store<L, NT>(t, 0, a.d, tid, acc[k]);
         }
 }
 
-// Column sums over the workgroups' partial rows in a fixed order: 32 columns a
-// workgroup, 8 threads a column.  blockIdx.y < 4: a weight gradient.  Above:
-// the gate rows that are cut between workgroups; the boundaries b - 1 | b are
-// dealt out over the rest of grid y, and the first boundary inside a gate row
-// owns it.
+// Column sums over the row groups' partial rows in a fixed order: 32 columns a
+// workgroup, 32 threads of 4 columns each for them (8 of one column where d is no
+// multiple of 4).  blockIdx.y < 4: a weight gradient.  Above: the gate rows that
+// are cut between groups, found from the gate rows or from the groups' boundaries,
+// whichever are fewer (a.cuts of them, dealt out over the rest of grid y).
 __global__ __launch_bounds__(256) void block_norm_reduce_kernel(BnArgs a)
 {
-    __shared__ float red[8][33];
-    const int cl = threadIdx.x & 31, seg = threadIdx.x >> 5;
-    const int c = blockIdx.x * 32 + cl;
+    __shared__ __attribute__((aligned(16))) float red[32][32];
+    const int c = blockIdx.x * 32 + (threadIdx.x & 31), seg = threadIdx.x >> 5;
     auto column = [&](int kind0, int b0, int kind, int b1) {  // partial rows b0 (of kind0), then b0 + 1 .. b1 - 1
         const int n = b1 - b0;
-        float s = 0.f;
-        if (c < a.d) {
-#pragma unroll 4
-            for (int i = seg; i < n; i += 8)
-                s += a.part[((int64_t)(i == 0 ? kind0 : kind) * a.wgs + b0 + i) * a.d + c];
+        __syncthreads();
+        if (a.d % 4 == 0) {
+            const int c4 = (threadIdx.x & 7) * 4, s4 = threadIdx.x >> 3;
+            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (blockIdx.x * 32 + c4 < a.d) {
+#pragma unroll 8
+                for (int i = s4; i < n; i += 32) {
+                    const float4 v = *reinterpret_cast<const float4 *>(
+                        a.part + ((int64_t)(i == 0 ? kind0 : kind) * a.groups + b0 + i) * a.d + blockIdx.x * 32 + c4);
+                    s.x += v.x;
+                    s.y += v.y;
+                    s.z += v.z;
+                    s.w += v.w;
+                }
+            }
+            *reinterpret_cast<float4 *>(&red[s4][c4]) = s;
+        } else {
+            float s = 0.f;
+            if (c < a.d) {
+#pragma unroll 8
+                for (int i = seg; i < n; i += 8)
+                    s += a.part[((int64_t)(i == 0 ? kind0 : kind) * a.groups + b0 + i) * a.d + c];
+            }
+            red[seg][threadIdx.x & 31] = s;
+#pragma unroll
+            for (int k = 8; k < 32; k += 8)
+                red[seg + k][threadIdx.x & 31] = 0.f;
         }
         __syncthreads();
-        red[seg][cl] = s;
-        __syncthreads();
-        s = red[0][cl];
+        float s = 0.f;
+        if (seg == 0) {
 #pragma unroll
-        for (int k = 1; k < 8; ++k)
-            s += red[k][cl];
+            for (int k = 0; k < 32; ++k)
+                s += red[k][threadIdx.x];
+        }
         return s;
     };
     if (blockIdx.y < 4) {
         float *dw = a.dw[blockIdx.y];
         if (!dw)
             return;
-        const float s = column(blockIdx.y, 0, blockIdx.y, a.wgs);
+        const float s = column(blockIdx.y, 0, blockIdx.y, a.groups);
         if (seg == 0 && c < a.d)
             dw[c] = s;
         return;
     }
-    for (int b = 1 + (int)blockIdx.y - 4; b < a.wgs; b += gridDim.y - 4) {
-        const int64_t first = (int64_t)b * a.rows;  // the first row past the boundary
-        const int64_t g = first / a.gate_span, g0 = g * a.gate_span;
-        if (g0 >= first || g0 < first - a.rows)  // not cut here, or owned by an earlier boundary
+    for (int k = (int)blockIdx.y - 4; k < a.cuts; k += gridDim.y - 4) {
+        int g;
+        if (a.gate_span >= a.rows) {
+            g = k;
+        } else {  // the gate row that boundary k | k + 1 falls into
+            g = (k + 1) * a.rows / a.gate_span;
+            if (g * a.gate_span == (k + 1) * a.rows)
+                continue;
+        }
+        const int r0 = g * a.gate_span, r1 = a.T - r0 > a.gate_span ? r0 + a.gate_span : a.T;
+        const int b0 = r0 / a.rows, b1 = (r1 + a.rows - 1) / a.rows;
+        if (b1 - b0 < 2)  // whole inside one group
             continue;
-        const int64_t g1 = g0 + a.gate_span < a.T ? g0 + a.gate_span : a.T;
-        const int b1 = (int)((g1 + a.rows - 1) / a.rows);
-        // the row begins inside workgroup b - 1: at its first row it is whole there and cut only at the end
-        const float s = column(5, b - 1, 4, b1);
+        // begun in group b0 and cut at its end, then at the first row of those that follow; where it begins with a
+        // group it is cut at that group's end too
+        const float s = column(5, b0, 4, b1);
         if (seg == 0 && c < a.d) {
             if (a.dgate.bf16)
-                ((__bf16 *)a.dgate.p)[g * a.d + c] = (__bf16)s;
+                ((__bf16 *)a.dgate.p)[(int64_t)g * a.d + c] = (__bf16)s;
             else
-                ((float *)a.dgate.p)[g * a.d + c] = s;
+                ((float *)a.dgate.p)[(int64_t)g * a.d + c] = s;
         }
     }
 }
 
-int block_norm_wgs(int T)
+// Row groups of the backward pass: about three workgroups of 256 threads per CU,
+// as many as its registers allow; each adds up its own rows' weight gradients.
+static int bn_row_threads(int d) { return d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
+
+int block_norm_groups(int T, int d)
 {
-    const int rows = (T + BN_BWD_WGS - 1) / BN_BWD_WGS;
+    const int most = BN_BWD_THREADS / bn_row_threads(d);
+    const int rows = (T + most - 1) / most;
     return rows > 0 ? (T + rows - 1) / rows : 0;
 }
 
-template <bool LAYER, bool VEC> static hipError_t bn_go(const BnArgs &a, bool backward, hipStream_t s)
+// Workgroups of the forward pass: enough to fill the GPU; rows beyond that come
+// one after another with the weights in registers.
+constexpr int BN_FWD_THREADS = 256 * 2048;
+
+template <bool LAYER, BnLay L> static hipError_t bn_go(const BnArgs &a, bool backward, hipStream_t s)
 {
     auto go = [&](auto nt) {
         constexpr int NT = decltype(nt)::value;
+        constexpr int threads = bn_threads<NT>(), per = threads / NT, most = BN_FWD_THREADS / threads;
         if (backward) {
-            block_norm_backward_kernel<LAYER, VEC, NT><<<dim3(a.wgs), dim3(NT), 0, s>>>(a);
+            const dim3 grid((a.groups + per - 1) / per);
+            if (a.dw[1] || a.dw[3])
+                block_norm_backward_kernel<LAYER, true, L, NT><<<grid, dim3(threads), 0, s>>>(a);
+            else
+                block_norm_backward_kernel<LAYER, false, L, NT><<<grid, dim3(threads), 0, s>>>(a);
         } else {
-            constexpr int RPW = bn_threads<NT>() / NT;
-            block_norm_kernel<LAYER, VEC, NT><<<dim3((a.T + RPW - 1) / RPW), dim3(bn_threads<NT>()), 0, s>>>(a);
+            const int wgs = (int)(((int64_t)a.T + per - 1) / per);
+            block_norm_kernel<LAYER, L, NT><<<dim3(wgs < most ? wgs : most), dim3(threads), 0, s>>>(a);
         }
         return hipGetLastError();
     };
-    if (a.d <= 512)
+    switch (bn_row_threads(a.d)) {
+    case 64:
         return go(std::integral_constant<int, 64>{});
-    if (a.d <= 1024)
+    case 128:
         return go(std::integral_constant<int, 128>{});
-    if (a.d <= 2048)
+    case 256:
         return go(std::integral_constant<int, 256>{});
-    if (a.d <= 4096)
+    case 512:
         return go(std::integral_constant<int, 512>{});
-    return go(std::integral_constant<int, 1024>{});
+    default:
+        return go(std::integral_constant<int, 1024>{});
+    }
 }
 
 static hipError_t bn_dispatch(const BnArgs &a, bool layer, bool vec, bool backward, hipStream_t s)
 {
+    int wide = 0, narrow = 0;  // tensors of rows in fp32 and in bf16
+    for (const BnTensor *t : {&a.res, &a.y, &a.out, &a.n, &a.dout, &a.dn, &a.dres, &a.dy})
+        if (t->p)
+            ++(t->bf16 ? narrow : wide);
+    // (narrow rows too: BN_8 would leave half of the threads idle)
+    const BnLay lay = !vec ? BN_ANY : wide > narrow || a.d <= 4 * bn_row_threads(a.d) ? BN_4 : BN_8;
     if (layer)
-        return vec ? bn_go<true, true>(a, backward, s) : bn_go<true, false>(a, backward, s);
-    return vec ? bn_go<false, true>(a, backward, s) : bn_go<false, false>(a, backward, s);
+        return lay == BN_ANY ? bn_go<true, BN_ANY>(a, backward, s)
+               : lay == BN_4 ? bn_go<true, BN_4>(a, backward, s)
+                             : bn_go<true, BN_8>(a, backward, s);
+    return lay == BN_ANY ? bn_go<false, BN_ANY>(a, backward, s)
+           : lay == BN_4 ? bn_go<false, BN_4>(a, backward, s)
+                         : bn_go<false, BN_8>(a, backward, s);
 }
 
 hipError_t launch_block_norm(const BnArgs &a, bool layer, bool vec, hipStream_t s)
@@ -476,12 +584,12 @@ hipError_t launch_block_norm_backward(const BnArgs &a, bool layer, bool vec, hip
         if (e != hipSuccess)
             return e;
     }
-    const bool cut = a.gate_span > 1 && a.wgs > 1 && a.rows % a.gate_span != 0;
-    const bool vectors = a.dw[0] || a.dw[1] || a.dw[2] || a.dw[3];
-    if (!cut && !vectors)
+    const bool cut = a.gate_span > 1 && a.groups > 1 && a.rows % a.gate_span != 0;
+    BnArgs r = a;
+    r.cuts = !cut ? 0 : a.gate_span >= a.rows ? (int)(((int64_t)a.T + a.gate_span - 1) / a.gate_span) : a.groups - 1;
+    if (!cut && !a.dw[0] && !a.dw[1] && !a.dw[2] && !a.dw[3])
         return hipSuccess;
-    const int bounds = cut ? (a.wgs - 1 < 16 ? a.wgs - 1 : 16) : 0;
-    block_norm_reduce_kernel<<<dim3((a.d + 31) / 32, 4 + bounds), dim3(256), 0, s>>>(a);
+    block_norm_reduce_kernel<<<dim3((a.d + 31) / 32, 4 + (r.cuts < 32 ? r.cuts : 32)), dim3(256), 0, s>>>(r);
     return hipGetLastError();
 }
 

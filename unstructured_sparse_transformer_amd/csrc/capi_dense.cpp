@@ -223,7 +223,7 @@ size_t twell_block_norm_workspace_bytes(int32_t T, int32_t d)
 {
     if (T < 0 || d < 1 || d > twell::BN_MAX_D)
         return 0;
-    return (size_t)6 * twell::block_norm_wgs(T) * d * sizeof(float);
+    return (size_t)6 * twell::block_norm_groups(T, d) * d * sizeof(float);
 }
 
 int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, const void *y, const void *dout,
@@ -270,8 +270,8 @@ int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, con
     a.dw[2] = dw_pre;
     a.dw[3] = db_pre;
     a.part = static_cast<float *>(workspace);
-    a.wgs = twell::block_norm_wgs(bn->T);
-    a.rows = a.wgs ? (bn->T + a.wgs - 1) / a.wgs : 0;
+    a.groups = twell::block_norm_groups(bn->T, bn->d);
+    a.rows = a.groups ? (bn->T + a.groups - 1) / a.groups : 0;
     return hip_status(twell::launch_block_norm_backward(a, bn->kind == TWELL_NORM_LAYER, bn_wide(a),
                                                         static_cast<hipStream_t>(stream)));
 }
