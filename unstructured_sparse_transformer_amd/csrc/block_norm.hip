@@ -38,6 +38,10 @@ template <BnLay L, int NT> __device__ __forceinline__ int bn_col(int tid, int e)
     return L == BN_8 ? tid * 8 + e : L == BN_4 ? (e >> 2) * 4 * NT + tid * 4 + (e & 3) : e * NT + tid;
 }
 
+// Keeps the compiler from holding an address per element and tensor over a loop
+// of rows (more than 256 registers): they are one addition each.
+__device__ __forceinline__ void bn_forget(int &v) { asm volatile("" : "+v"(v)); }
+
 // 8 elements of a row as they lie in memory, requested now and used later.
 struct Raw8 {
     u32x4 a, b;
@@ -58,9 +62,9 @@ __device__ __forceinline__ Raw8 bn_load(BnTensor t, int64_t row, int d, int tid)
     if constexpr (L == BN_8) {
         if (tid * 8 < d) {
             if (t.bf16) {
-                r.a = bn_ld16<ONCE>((const __bf16 *)t.p + row * d + tid * 8);
+                r.a = bn_ld16<ONCE>((const __bf16 *)t.p + row * d + (uint32_t)(tid * 8));
             } else {
-                const float *q = (const float *)t.p + row * d + tid * 8;
+                const float *q = (const float *)t.p + row * d + (uint32_t)(tid * 8);
                 r.a = bn_ld16<ONCE>(q);
                 r.b = bn_ld16<ONCE>(q + 4);
             }
@@ -83,20 +87,26 @@ __device__ __forceinline__ Raw8 bn_load(BnTensor t, int64_t row, int d, int tid)
                 r.b = bn_ld16<ONCE>(q + c1);
         }
     } else {
+        // columns past d read column d - 1 and count as 0: no load waits behind a branch
+        uint32_t w[8];
+        bn_forget(tid);
+        if (t.bf16) {
+            const uint16_t *q = (const uint16_t *)t.p + row * d;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = e * NT + tid;
-            uint32_t w = 0;
-            if (c < d)
-                w = t.bf16 ? (uint32_t)((const uint16_t *)t.p)[row * d + c] : ((const uint32_t *)t.p)[row * d + c];
-            if (t.bf16) {
-                r.a[e >> 1] |= w << (16 * (e & 1));
-            } else if (e < 4) {
-                r.a[e] = w;
-            } else {
-                r.b[e - 4] = w;
-            }
+            for (int e = 0; e < 8; ++e)
+                w[e] = q[(uint32_t)(e * NT + tid < d ? e * NT + tid : d - 1)];
+        } else {
+            const uint32_t *q = (const uint32_t *)t.p + row * d;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                w[e] = q[(uint32_t)(e * NT + tid < d ? e * NT + tid : d - 1)];
         }
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            w[e] = e * NT + tid < d ? w[e] : 0u;
+        r.a = t.bf16 ? u32x4{w[0] | w[1] << 16, w[2] | w[3] << 16, w[4] | w[5] << 16, w[6] | w[7] << 16}
+                     : u32x4{w[0], w[1], w[2], w[3]};
+        r.b = u32x4{w[4], w[5], w[6], w[7]};
     }
     return r;
 }
@@ -123,10 +133,10 @@ __device__ __forceinline__ void bn_store(BnTensor t, int64_t row, int d, int tid
     if constexpr (L == BN_8) {
         if (tid * 8 < d) {
             if (t.bf16) {
-                *reinterpret_cast<u32x4 *>((__bf16 *)t.p + row * d + tid * 8) =
+                *reinterpret_cast<u32x4 *>((__bf16 *)t.p + row * d + (uint32_t)(tid * 8)) =
                     u32x4{bn_pack(v[0], v[1]), bn_pack(v[2], v[3]), bn_pack(v[4], v[5]), bn_pack(v[6], v[7])};
             } else {
-                float *q = (float *)t.p + row * d + tid * 8;
+                float *q = (float *)t.p + row * d + (uint32_t)(tid * 8);
                 *reinterpret_cast<float4 *>(q) = make_float4(v[0], v[1], v[2], v[3]);
                 *reinterpret_cast<float4 *>(q + 4) = make_float4(v[4], v[5], v[6], v[7]);
             }
@@ -145,15 +155,19 @@ __device__ __forceinline__ void bn_store(BnTensor t, int64_t row, int d, int tid
             }
         }
     } else {
+        bn_forget(tid);
+        if (t.bf16) {
+            __bf16 *q = (__bf16 *)t.p + row * d;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) {
-            const int c = e * NT + tid;
-            if (c < d) {
-                if (t.bf16)
-                    ((__bf16 *)t.p)[row * d + c] = (__bf16)v[e];
-                else
-                    ((float *)t.p)[row * d + c] = v[e];
-            }
+            for (int e = 0; e < 8; ++e)
+                if (e * NT + tid < d)
+                    q[(uint32_t)(e * NT + tid)] = (__bf16)v[e];
+        } else {
+            float *q = (float *)t.p + row * d;
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                if (e * NT + tid < d)
+                    q[(uint32_t)(e * NT + tid)] = v[e];
         }
     }
 }
@@ -266,7 +280,8 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_kernel(BnArgs a)
     int slot = 0;
     const int tid = threadIdx.x % NT;
     const int64_t step = (int64_t)gridDim.x * RPW;
-    int64_t row = (int64_t)blockIdx.x * RPW + threadIdx.x / NT;
+    // (a wave's threads have the same row: known as such, its address is scalar)
+    int64_t row = (int64_t)blockIdx.x * RPW + (RPW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / NT) : 0);
     if (row >= a.T)  // whole waves: a row is a multiple of 64 threads
         return;
     const bool block = a.y.p, next = a.n.p;
@@ -516,7 +531,12 @@ static int bn_row_threads(int d) { return d <= 512 ? 64 : d <= 1024 ? 128 : d <=
 int block_norm_groups(int T, int d)
 {
     const int most = BN_BWD_THREADS / bn_row_threads(d);
-    const int rows = (T + most - 1) / most;
+    int rows = (T + most - 1) / most;
+    // few rows: up to 4 of them a group, until there is a workgroup of 256 threads per CU; each group costs a partial
+    // row per vector (777 x 1001: 28 us at 195 groups, 24 at 389, 28 at 777)
+    const int full = 256 * 256 / bn_row_threads(d);
+    const int few = (T + full - 1) / full < 4 ? (T + full - 1) / full : 4;
+    rows = rows > few ? rows : few;
     return rows > 0 ? (T + rows - 1) / rows : 0;
 }
 
