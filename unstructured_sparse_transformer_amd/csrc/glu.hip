@@ -577,8 +577,8 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
         return hipGetLastError();
     }
     const int tile = mul_plan(p.T, 2 * (int64_t)p.F, p.d, 4, 1).tile;
-    p.tiles = dg_tiles(ceil_div(p.T, MUL_TILES[tile].bm), ceil_div(p.F, MUL_TILES[tile].bn / 2));
-    const dim3 grid(8 * p.tiles.rows * p.tiles.cols);
+    p.tiles = dg_tiles(ceil_div(p.T, MUL_TILES[tile].bm), ceil_div(p.F, MUL_TILES[tile].bn / 2), 1);
+    const dim3 grid((unsigned)dg_grid(p.tiles));
     switch (tile) {
     case 0:
         glu_kernel<256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(p);
@@ -635,8 +635,8 @@ template <bool A_KC, bool B_KC> static hipError_t mul_go(int vdtype, GluMul p, h
         glu_mul_f32_kernel<A_KC, B_KC><<<dim3(p.MT * p.NT * p.splits), dim3(256), 0, s>>>(p);
     } else {
         const MulTile &tile = MUL_TILES[plan.tile];
-        p.tiles = dg_tiles(ceil_div(p.M, tile.bm), ceil_div(p.N, tile.bn));
-        const dim3 grid(8 * p.tiles.rows * p.tiles.cols * p.splits);
+        p.tiles = dg_tiles(ceil_div(p.M, tile.bm), ceil_div(p.N, tile.bn), p.splits);
+        const dim3 grid((unsigned)dg_grid(p.tiles));
         if (plan.tile == 0)
             glu_mul_kernel<256, 256, 64, 128, 2, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
         else if (plan.tile == 1)
