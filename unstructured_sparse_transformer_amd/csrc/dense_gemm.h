@@ -346,14 +346,22 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int 
 
 // A wave's block of 32 rows by 32 NB columns in bf16, from accumulators
 // (value(fn, i)) to memory by way of LDS: 16-byte stores of whole row pieces.
-// `lds`: dg_stage_bytes<NB>() bytes of the wave's own (16 bytes between the rows
-// spread their pieces over the banks).
-template <int NB> constexpr int dg_stage_bytes() { return 32 * (64 * NB + 16); }
+// `lds`: dg_stage_bytes<NB>() bytes of the wave's own.  A row's 16-byte chunks are
+// XORed with the row's index among the rows that share a place in the 256-byte
+// bank window, and rows 16 on swap a chunk's halves, so that the 32 rows' 8-byte
+// pieces of one write, and 16 chunks of one read, meet every bank once.
+template <int NB> constexpr int dg_stage_bytes() { return 32 * 64 * NB; }
+template <int NB> __device__ __forceinline__ int dg_stage_chunk(int row, int chunk)
+{
+    constexpr int LOG = NB == 4 ? 0 : NB == 2 ? 1 : 2;  // log2(rows per bank window)
+    static_assert(NB == 1 || NB == 2 || NB == 4, "rows of 64, 128 or 256 bytes");
+    return row * (64 * NB) + ((chunk ^ ((row >> LOG) & (4 * NB - 1))) << 4);
+}
 template <int NB, typename V>
 __device__ __forceinline__ void dg_store_rows(char *lds, int lane, V value, __bf16 *out, int64_t ld, int m0, int n0,
                                               int M, int N)
 {
-    constexpr int PITCH = 64 * NB + 16;
+    const int row = lane & 31, half = (lane >> 5) ^ (row >> 4);
     asm volatile("" ::: "memory");
 #pragma unroll
     for (int fn = 0; fn < NB; ++fn)
@@ -361,15 +369,17 @@ __device__ __forceinline__ void dg_store_rows(char *lds, int lane, V value, __bf
         for (int i = 0; i < 16; i += 4) {
             const bf16x2 lo = {(__bf16)value(fn, i), (__bf16)value(fn, i + 1)};
             const bf16x2 hi = {(__bf16)value(fn, i + 2), (__bf16)value(fn, i + 3)};
-            *reinterpret_cast<uint2 *>(lds + (lane & 31) * PITCH + (fn * 32 + acc_row(i, lane)) * 2) =
+            *reinterpret_cast<uint2 *>(lds + dg_stage_chunk<NB>(row, fn * 4 + (i >> 2)) + half * 8) =
                 make_uint2(__builtin_bit_cast(uint32_t, lo), __builtin_bit_cast(uint32_t, hi));
         }
     asm volatile("" ::: "memory");
     constexpr int CPR = 4 * NB;  // 16-byte chunks of a row
 #pragma unroll
     for (int c0 = 0; c0 < 32 * CPR; c0 += 64) {
-        const int c = c0 + lane, r = c / CPR, q = c % CPR;
-        const u32x4 v = *reinterpret_cast<const u32x4 *>(lds + r * PITCH + q * 16);
+        const int r = c0 / CPR + lane / CPR, q = lane % CPR;
+        u32x4 v = *reinterpret_cast<const u32x4 *>(lds + dg_stage_chunk<NB>(r, q));
+        if (c0 / CPR >= 16)
+            v = u32x4{v[2], v[3], v[0], v[1]};
         if (m0 + r < M && n0 + q * 8 < N)
             *reinterpret_cast<u32x4 *>(out + (int64_t)(m0 + r) * ld + n0 + q * 8) = v;
     }
