@@ -399,8 +399,8 @@ TWELL_API int twell_ffn_backward(const twell_hybrid_t *hy, const void *x, const 
  * h = act(x . W_g) * (x . W_u): the gated FFN's hidden activation without
  * sparsity, for layers or models whose activation is not sparse (or not ReLU).
  * x [T][d], W_g^T and W_u^T [F][d], h [T][F], all vdtype (TWELL_BF16 with fp32
- * accumulation, or TWELL_F32), 16-byte aligned; d and F multiples of 64, d <=
- * 2^20, F <= 2^19. */
+ * accumulation, or TWELL_F32), 16-byte aligned; T <= 2^30, d and F multiples of
+ * 64, d <= 2^20, F <= 2^19. */
 enum twell_act {
     TWELL_ACT_RELU = 0,
     TWELL_ACT_SILU = 1,     /* g / (1 + exp(-g)) */
@@ -449,7 +449,7 @@ TWELL_API size_t twell_glu_backward_workspace_bytes(int32_t T, int32_t d, int32_
 enum twell_norm { TWELL_NORM_RMS = 0, TWELL_NORM_LAYER = 1 };
 
 typedef struct twell_block_norm_t {
-    int32_t T, d;       /* rows >= 0, 1 <= d <= 8192 */
+    int32_t T, d;       /* 0 <= T <= 2^30 rows, 1 <= d <= 8192 */
     int32_t kind;       /* enum twell_norm */
     int32_t post;       /* 1: a norm after the block */
     float eps, alpha;   /* eps > 0 */

@@ -72,7 +72,7 @@ def test_block_norm_validation():
     assert f(_bn(rdtype=1, ydtype=1, ndtype=1), GOOD, GOOD, GOOD + 1, GOOD, None) == ALIGN
     for kw in (dict(kind=2), dict(d=8193), dict(rdtype=2), dict(ydtype=-1), dict(ndtype=5), dict(wdtype=2)):
         assert f(_bn(**kw), GOOD, GOOD, GOOD, GOOD, None) == UNSUPPORTED, kw
-    for kw in (dict(T=-1), dict(d=0), dict(gate_span=-1), dict(eps=0.0), dict(eps=float("nan"))):
+    for kw in (dict(T=-1), dict(T=(1 << 30) + 1), dict(d=0), dict(gate_span=-1), dict(eps=0.0), dict(eps=float("nan"))):
         assert f(_bn(**kw), GOOD, GOOD, GOOD, GOOD, None) == SHAPE, kw
     size = lib.twell_block_norm_workspace_bytes
     assert size(-1, 64) == 0 and size(8, 0) == 0 and size(8, 8193) == 0 and size(0, 64) == 0
@@ -103,7 +103,7 @@ def test_glu_validation():
         assert f(**{k: None}) == NULL and f(**{k: GOOD + 8}) == ALIGN, k
     assert f(g=GOOD + 2) == ALIGN and f(u=GOOD + 8) == ALIGN
     assert f(T=0, x=None, h=None) == 0
-    for kw in (dict(T=-1), dict(d=0), dict(d=96), dict(F=100), dict(F=0), dict(d=-64)):
+    for kw in (dict(T=-1), dict(T=(1 << 30) + 1), dict(d=0), dict(d=96), dict(F=100), dict(F=0), dict(d=-64)):
         assert f(**kw) == SHAPE, kw
     for kw in (dict(vd=2), dict(act=-1), dict(act=4), dict(d=(1 << 20) + 64), dict(F=(1 << 19) + 64)):
         assert f(**kw) == UNSUPPORTED, kw

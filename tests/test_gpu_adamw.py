@@ -153,6 +153,18 @@ def test_adamw_many_tensors_with_coefficient(gpu_lib, bits):
 
 
 @pytest.mark.parametrize("bits", [32, 8])
+@pytest.mark.parametrize("offset", [0, 3])
+def test_adamw_large_tensors(gpu_lib, bits, offset):
+    """Enough elements for workgroups of several passes, ending inside a block, a wave's pair of blocks and a pass."""
+    import torch
+    say(f"case adamw large {bits} offset {offset}")
+    sets = _tensors([2_000_003, 8192 * 5 + 256, 300_001], bits, torch.float32, torch.bfloat16, offset, seed=2)
+    before = [(_host(t, "p"), _host(t, "grad"), *_state(t, bits)) for t in sets]
+    _step(gpu_lib, sets)
+    _check(sets, before, bits, torch.float32)
+
+
+@pytest.mark.parametrize("bits", [32, 8])
 @pytest.mark.parametrize("bad", [0.0, float("inf"), float("-inf"), float("nan")])
 def test_adamw_unusable_gradients_change_nothing(gpu_lib, bits, bad):
     import torch

@@ -10,7 +10,7 @@ constexpr int AW_QBLOCK = 256;  // elements that share one scale of the 8-bit st
 constexpr int AW_BATCH = 40;    // tensors per launch: their table travels in the kernel's arguments
 constexpr int AW_THREADS = 256;
 constexpr int AW_PASS = AW_THREADS * 8;  // elements a workgroup handles at once
-constexpr int AW_CHUNK = 4 * AW_PASS;    // elements of one workgroup
+constexpr int AW_PASSES = 4;             // passes of one workgroup, or 1 where that leaves CUs without one
 
 enum : uint32_t { AW_P_BF16 = 1, AW_G_BF16 = 2, AW_VEC = 4 };
 
@@ -29,7 +29,7 @@ struct AwTensor {
 
 struct AwBatch {
     AwTensor t[AW_BATCH];
-    int32_t count;
+    int32_t count, passes;
     float beta1, omb1, beta2, omb2, eps;
     float size;  // lr / (1 - beta1^step)
     float root;  // 1 / sqrt(1 - beta2^step)
@@ -46,7 +46,7 @@ struct AwUnpack {
         int32_t chunk0;
         uint32_t vec;
     } t[AW_BATCH];
-    int32_t count;
+    int32_t count, passes;
 };
 static_assert(sizeof(AwUnpack) <= 4096, "kernel arguments");
 

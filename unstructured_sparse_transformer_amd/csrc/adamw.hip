@@ -204,7 +204,7 @@ __device__ __forceinline__ void adamw_chunk(const AwBatch &b, const AwTensor &t,
     const int lane = threadIdx.x & 63;
     const int64_t w0 = c0 + (threadIdx.x >> 6) * (2 * AW_QBLOCK);
 #pragma unroll 1
-    for (int pass = 0; pass < AW_CHUNK / AW_PASS; ++pass) {
+    for (int pass = 0; pass < b.passes; ++pass) {
         const int64_t b0 = w0 + pass * AW_PASS;  // the wave's first block
         if (!WIDE && b0 >= t.n)
             return;
@@ -297,9 +297,10 @@ template <bool CODED> __global__ __launch_bounds__(AW_THREADS) void adamw_kernel
             return;
     }
     const AwTensor &t = b.t[aw_find(b, blockIdx.x)];
-    const int64_t c0 = (int64_t)((int)blockIdx.x - t.chunk0) * AW_CHUNK;
+    const int chunk = b.passes * AW_PASS;
+    const int64_t c0 = (int64_t)((int)blockIdx.x - t.chunk0) * chunk;
     const bool pb = t.flags & AW_P_BF16, gb = t.flags & AW_G_BF16;
-    if ((t.flags & AW_VEC) && c0 + AW_CHUNK <= t.n) {
+    if ((t.flags & AW_VEC) && c0 + chunk <= t.n) {
         if (pb)
             gb ? adamw_chunk<CODED, true, true, true>(b, t, c0, gs) : adamw_chunk<CODED, true, false, true>(b, t, c0, gs);
         else
@@ -313,9 +314,9 @@ template <bool CODED> __global__ __launch_bounds__(AW_THREADS) void adamw_kernel
 }
 
 // m_values = m, v_values = sqrt(v)^2 of the codes: 2 + 8 bytes an element.
-template <typename T, bool WIDE> __device__ __forceinline__ void unpack_chunk(T t, int64_t c0)
+template <typename T, int PASSES, bool WIDE> __device__ __forceinline__ void unpack_chunk(T t, int64_t c0)
 {
-    constexpr int N = AW_CHUNK / AW_THREADS / 4;
+    constexpr int N = PASSES * AW_PASS / AW_THREADS / 4;
     uint32_t cm[N], cv[N];
     float sm[N], sv[N];
 #pragma unroll
@@ -343,14 +344,14 @@ template <typename T, bool WIDE> __device__ __forceinline__ void unpack_chunk(T 
     }
 }
 
-__global__ __launch_bounds__(AW_THREADS) void adamw_unpack_kernel(AwUnpack b)
+template <int PASSES> __global__ __launch_bounds__(AW_THREADS) void adamw_unpack_kernel(AwUnpack b)
 {
     const auto &t = b.t[aw_find(b, blockIdx.x)];
-    const int64_t c0 = (int64_t)((int)blockIdx.x - t.chunk0) * AW_CHUNK;
-    if (t.vec && c0 + AW_CHUNK <= t.n)
-        unpack_chunk<decltype(t), true>(t, c0);
+    const int64_t c0 = (int64_t)((int)blockIdx.x - t.chunk0) * (PASSES * AW_PASS);
+    if (t.vec && c0 + PASSES * AW_PASS <= t.n)
+        unpack_chunk<decltype(t), PASSES, true>(t, c0);
     else
-        unpack_chunk<decltype(t), false>(t, c0);
+        unpack_chunk<decltype(t), PASSES, false>(t, c0);
 }
 
 hipError_t launch_adamw(const AwBatch &b, bool coded, int chunks, hipStream_t s)
@@ -364,7 +365,10 @@ hipError_t launch_adamw(const AwBatch &b, bool coded, int chunks, hipStream_t s)
 
 hipError_t launch_adamw_unpack(const AwUnpack &b, int chunks, hipStream_t s)
 {
-    adamw_unpack_kernel<<<dim3(chunks), dim3(AW_THREADS), 0, s>>>(b);
+    if (b.passes == AW_PASSES)
+        adamw_unpack_kernel<AW_PASSES><<<dim3(chunks), dim3(AW_THREADS), 0, s>>>(b);
+    else
+        adamw_unpack_kernel<1><<<dim3(chunks), dim3(AW_THREADS), 0, s>>>(b);
     return hipGetLastError();
 }
 

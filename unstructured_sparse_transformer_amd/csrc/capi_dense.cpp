@@ -15,6 +15,9 @@ namespace {
 
 bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 
+// Rows of a call: row numbers and roundings of them stay below 2^31.
+constexpr int32_t MOST_ROWS = 1 << 30;
+
 bool known_dtype(int32_t dt) { return dt == TWELL_F32 || dt == TWELL_BF16; }
 
 // A vector of elements of size es: NULL and alignment.
@@ -30,7 +33,7 @@ int check_glu(int32_t T, int32_t d, int32_t F, int32_t vdtype, int32_t act)
 {
     if (!known_dtype(vdtype) || act < TWELL_ACT_RELU || act > TWELL_ACT_GELU_TANH)
         return TWELL_E_UNSUPPORTED;
-    if (T < 0 || d <= 0 || F <= 0 || d % 64 != 0 || F % 64 != 0)
+    if (T < 0 || T > MOST_ROWS || d <= 0 || F <= 0 || d % 64 != 0 || F % 64 != 0)
         return TWELL_E_SHAPE;
     // a tile's rows are addressed with 32-bit offsets
     if (d > (1 << 20) || F > (1 << 19))
@@ -48,7 +51,7 @@ int check_block_norm(const twell_block_norm_t *bn, bool gated)
         !known_dtype(bn->ydtype) || !known_dtype(bn->ndtype) || !known_dtype(bn->wdtype) ||
         bn->d > twell::BN_MAX_D)
         return TWELL_E_UNSUPPORTED;
-    if (bn->T < 0 || bn->d < 1 || bn->gate_span < 0 || !(bn->eps > 0))
+    if (bn->T < 0 || bn->T > MOST_ROWS || bn->d < 1 || bn->gate_span < 0 || !(bn->eps > 0))
         return TWELL_E_SHAPE;
     for (const void *w : {bn->w_post, bn->b_post, bn->w_pre, bn->b_pre})
         if (w)
@@ -109,9 +112,19 @@ int check_adamw(const twell_adamw_tensor_t &t, bool coded, bool unpack)
     return t.copy ? check_vec(t.copy, 2) : TWELL_OK;
 }
 
-// Chunks of AW_CHUNK elements; a launch's total fits a grid.
+// A launch's workgroups fit a grid.
 constexpr int64_t AW_MOST_CHUNKS = (int64_t)1 << 30;
-int64_t aw_chunks(int64_t n) { return (n + twell::AW_CHUNK - 1) / twell::AW_CHUNK; }
+int64_t aw_chunks(int64_t n, int passes) { return (n + passes * twell::AW_PASS - 1) / (passes * twell::AW_PASS); }
+
+// Passes of a workgroup: AW_PASSES (fewer searches for the tensor), but one
+// where the call's elements would then leave some of the 256 CUs idle.
+int aw_passes(const twell_adamw_tensor_t *tensors, int32_t count)
+{
+    int64_t chunks = 0;
+    for (int32_t i = 0; i < count; ++i)
+        chunks += aw_chunks(tensors[i].n, twell::AW_PASSES);
+    return chunks < 256 ? 1 : twell::AW_PASSES;
+}
 
 }  // namespace
 
@@ -221,7 +234,7 @@ int twell_block_norm_forward(const twell_block_norm_t *bn, const void *res, cons
 
 size_t twell_block_norm_workspace_bytes(int32_t T, int32_t d)
 {
-    if (T < 0 || d < 1 || d > twell::BN_MAX_D)
+    if (T < 0 || T > MOST_ROWS || d < 1 || d > twell::BN_MAX_D)
         return 0;
     return (size_t)6 * twell::block_norm_groups(T, d) * d * sizeof(float);
 }
@@ -302,10 +315,11 @@ int twell_adamw_step(const twell_adamw_tensor_t *tensors, int32_t count, int32_t
     b.size = (float)(lr / (1 - std::pow(beta1, (double)step)));
     b.root = (float)(1 / std::sqrt(1 - std::pow(beta2, (double)step)));
     b.grad_scale = grad_scale;
+    b.passes = aw_passes(tensors, count);
     int64_t chunks = 0;
     for (int32_t i = 0; i < count; ++i) {
         const twell_adamw_tensor_t &t = tensors[i];
-        const int64_t c = aw_chunks(t.n);
+        const int64_t c = aw_chunks(t.n, b.passes);
         if (c == 0)
             continue;
         if (b.count == twell::AW_BATCH || chunks + c > AW_MOST_CHUNKS) {
@@ -346,10 +360,11 @@ int twell_adamw_unpack(const twell_adamw_tensor_t *tensors, int32_t count, void 
         TWELL_TRY(check_adamw(tensors[i], true, true));
     hipStream_t s = static_cast<hipStream_t>(stream);
     twell::AwUnpack b{};
+    b.passes = aw_passes(tensors, count);
     int64_t chunks = 0;
     for (int32_t i = 0; i < count; ++i) {
         const twell_adamw_tensor_t &t = tensors[i];
-        const int64_t c = aw_chunks(t.n);
+        const int64_t c = aw_chunks(t.n, b.passes);
         if (c == 0)
             continue;
         if (b.count == twell::AW_BATCH || chunks + c > AW_MOST_CHUNKS) {
