@@ -87,6 +87,12 @@ def test_acts(gpu_lib, act, T, dtype):
     _check_backward(gpu_lib, T, 256, 512, dtype, act)
 
 
+@pytest.mark.parametrize("T,d,F", [(700, 1024, 2048), (1003, 1024, 4096), (90, 2048, 4096), (600, 64, 8192)])
+def test_forward_middle_tiles(gpu_lib, T, d, F):
+    say(f"case glu forward middle tiles T={T} d={d} F={F}")
+    _check_forward(gpu_lib, T, d, F, "bfloat16", "silu")
+
+
 @pytest.mark.parametrize("T,F", [(8192, 1024), (4097, 1600), (2049, 3008)])
 def test_forward_large_tiles(gpu_lib, T, F):
     say(f"case glu forward large tiles T={T} F={F}")
@@ -104,7 +110,8 @@ def test_backward_shapes(gpu_lib, shape, dtype):
     _check_backward(gpu_lib, *shape, dtype, "silu")
 
 
-@pytest.mark.parametrize("shape", [(4000, 4096, 256), (200, 2112, 6400), (12300, 1024, 128), (4097, 3008, 64)])
+@pytest.mark.parametrize("shape", [(1003, 1024, 4096), (4096, 1024, 1024), (300, 4096, 2048), (4000, 4096, 256), (200, 2112, 6400),
+                                    (12300, 1024, 128), (4097, 3008, 64)])
 def test_backward_large_tiles(gpu_lib, shape):
     say(f"case glu backward large tiles {shape}")
     _check_backward(gpu_lib, *shape, "bfloat16", "gelu_tanh")

@@ -427,10 +427,11 @@ def hybrid_workspace(hy: "Hybrid", d: int, device="cuda"):
 
 # ---------------------------------------------------------------- the dense gated product
 def _device(fn: str, t) -> int:
-    """The GPU a call's tensors have to be on."""
+    """The GPU a call's tensors have to be on: the current one, whose streams the kernels run on."""
+    import torch
     dev = t.get_device()
-    if dev < 0:
-        raise ValueError(f"{fn}: tensors on a GPU are needed, got one on {t.device}")
+    if dev < 0 or dev != torch.cuda.current_device():
+        raise ValueError(f"{fn}: tensors on the current GPU are needed, got one on {t.device}")
     return dev
 
 

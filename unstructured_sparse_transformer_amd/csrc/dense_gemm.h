@@ -209,6 +209,13 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
     }
 };
 
+// Waves of WM x WN on tiles of BM x BN, S LDS slots of a stage.  256 x 256 tiles
+// of 8 waves reach 1.40 PFLOP/s at 8192^3 with both operands KC, 1.29 at 8192 x
+// 2048 x 16384 with B KS and 1.30 at 16384 x 2048 x 8192 with both KS.  There the
+// chip runs at about 1.7 GHz under its power cap with the MFMA pipes 0.7 busy;
+// the same kernels on zeros reach 1.76 PFLOP/s.  4 waves of 128 x 128 (a third
+// fewer LDS reads, one wave a SIMD) measured 3-6% slower, 16 waves of 64 x 64 5%,
+// v_mfma_f32_16x16x32_bf16 in the place of 32x32x16 4-7%.
 template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int S = 2> struct DgCore {
     static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, THREADS = NW * 64;
     static constexpr int FM = WM / 32, FN = WN / 32;
@@ -238,10 +245,10 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int 
     // One sub-step: the MFMAs of fragments af, bf, and between them, in this
     // order, the reads of the next sub-step's fragments (one before each of the
     // first MFMAs) and copies C0..C1-1 of the operands' present stage.  Spread like this neither
-    // queue fills up and the MFMA pipe is not held by either: all reads first
-    // cost 2-3% of a large product, all copies at once 3-4%.  The order of the
-    // products changes one fragment at a time (fewer operand bits toggle; the
-    // clock is set by the power that is drawn).
+    // queue fills up and the MFMA pipe is not held by either (all reads first
+    // cost 2-4% of a large product).  The order of the products changes one
+    // fragment at a time: fewer operand bits toggle, and the power that is drawn
+    // sets the clock (0.5%).
     template <int C0, int C1>
     __device__ __forceinline__ void step(const char *rbuf, int rss, u32x4 (&an)[FM], u32x4 (&bn)[FN],
                                          const u32x4 (&af)[FM], const u32x4 (&bf)[FN], f32x16 (&acc)[FM][FN], int wm,
