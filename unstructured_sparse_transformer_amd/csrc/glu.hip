@@ -226,10 +226,21 @@ template <typename TI, int BM, int NB, int S> __global__ __launch_bounds__(256) 
 }
 
 // ------------------------------------------------------------------ backward
-// dg and du from g, u, dh: 10 bytes an element (bf16), bound by memory.  Rows T
-// to the next multiple of 64 are zeros: they are the K rows that dW's last
-// stage reads past T.
-template <typename TI> __global__ __launch_bounds__(256) void glu_dact_kernel(GluBwd p, int rows)
+// dg and du from g, u, dh: 10 bytes an element (bf16), bound by memory (115 us,
+// 5.8 TB/s, at 8192 x 8192).  ONCE: the inputs are more than the 256 MB behind the
+// L2s keep until here, and are read past the caches (122 us through them; where
+// they do fit it is the other way round, 9.3 against 10.0 us at 1003 x 4096).
+// Rows T to the next multiple of 64 are zeros: they are the K rows that dW's
+// last stage reads past T.
+template <bool ONCE> __device__ __forceinline__ u32x4 glu_load(const void *p)
+{
+    const u32x4 *q = reinterpret_cast<const u32x4 *>(p);
+    if constexpr (ONCE)
+        return __builtin_nontemporal_load(q);
+    return *q;
+}
+
+template <typename TI, bool ONCE> __global__ __launch_bounds__(256) void glu_dact_kernel(GluBwd p, int rows)
 {
     constexpr int E = Elt<TI>::PER_CHUNK;
     const int per_row = p.F / E;
@@ -239,7 +250,8 @@ template <typename TI> __global__ __launch_bounds__(256) void glu_dact_kernel(Gl
         u32x4 og{}, ou{};
         if (t < p.T) {
             const int64_t at = t * p.F + j;
-            const u32x4 g = ldg16((const TI *)p.g + at), u = ldg16((const TI *)p.u + at), dh = ldg16((const TI *)p.dh + at);
+            const u32x4 g = glu_load<ONCE>((const TI *)p.g + at), u = glu_load<ONCE>((const TI *)p.u + at),
+                        dh = glu_load<ONCE>((const TI *)p.dh + at);
             TI rg[E], ru[E];
 #pragma unroll
             for (int e = 0; e < E; ++e) {
@@ -664,10 +676,13 @@ hipError_t launch_glu_backward(int vdtype, const GluBwd &p, hipStream_t s)
     if (rows > 0) {
         const int64_t wgs = ceil_div((int64_t)rows * p.F * es / 16, 256);
         const dim3 grid((unsigned)(wgs < 8192 ? wgs : 8192));
-        if (vdtype == 1)
-            glu_dact_kernel<__bf16><<<grid, dim3(256), 0, s>>>(p, rows);
+        const bool once = 3 * (int64_t)p.T * p.F * es > ((int64_t)256 << 20);
+        if (vdtype == 1 && once)
+            glu_dact_kernel<__bf16, true><<<grid, dim3(256), 0, s>>>(p, rows);
+        else if (vdtype == 1)
+            glu_dact_kernel<__bf16, false><<<grid, dim3(256), 0, s>>>(p, rows);
         else
-            glu_dact_kernel<float><<<grid, dim3(256), 0, s>>>(p, rows);
+            glu_dact_kernel<float, false><<<grid, dim3(256), 0, s>>>(p, rows);
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
     }
