@@ -413,8 +413,9 @@ enum twell_act {
  * and u before they are rounded.  For T <= 64 (bf16) the kernels are organised
  * for few tokens.  Inputs are finite; a NaN or an infinity spoils at most its
  * own row (of x) or column (of a weight).
- * workspace : device, >= twell_glu_workspace_bytes(T, d, F, vdtype) (0 bytes:
- * may be NULL), 256-byte aligned, content ignored on entry. */
+ * workspace : device, >= twell_glu_workspace_bytes(T, d, F, vdtype) (0 for
+ * most sizes: then it may be NULL), 256-byte aligned, content ignored on entry
+ * (it holds partial sums where few tiles are split over d). */
 TWELL_API int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
                                 int32_t vdtype, int32_t act, void *h, void *g, void *u, void *workspace,
                                 size_t workspace_bytes, void *stream);

@@ -93,6 +93,21 @@ def test_forward_middle_tiles(gpu_lib, T, d, F):
     _check_forward(gpu_lib, T, d, F, "bfloat16", "silu")
 
 
+@pytest.mark.parametrize("shape", [(128, 4096, 512), (70, 2112, 64), (100, 4096, 1024), (513, 2048, 320)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_forward_split(gpu_lib, shape, dtype):
+    """Few tiles and a long d: K is split and the parts joined in a workspace, without which the call is refused."""
+    import torch
+    say(f"case glu forward split {shape} {dtype}")
+    T, d, F = shape
+    assert gpu_lib.twell_glu_workspace_bytes(T, d, F, getattr(torch, dtype)) > 0
+    _check_forward(gpu_lib, *shape, dtype, "gelu")
+    _check_forward(gpu_lib, *shape, dtype, "relu", save=False)
+    x, wg, wu = _inputs(T, d, F, dtype)
+    with pytest.raises(gpu_lib.TwellError):
+        gpu_lib.twell_glu_forward(x, wg, wu, "relu", torch.empty((T, F), dtype=x.dtype, device="cuda"))
+
+
 @pytest.mark.parametrize("T,F", [(8192, 1024), (4097, 1600), (2049, 3008)])
 def test_forward_large_tiles(gpu_lib, T, F):
     say(f"case glu forward large tiles T={T} F={F}")

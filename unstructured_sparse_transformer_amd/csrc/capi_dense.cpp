@@ -132,8 +132,7 @@ extern "C" {
 
 size_t twell_glu_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype)
 {
-    (void)T, (void)d, (void)F, (void)vdtype;
-    return 0;
+    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_forward_ws(T, d, F, vdtype) : 0;
 }
 
 int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
@@ -161,6 +160,7 @@ int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t
     a.h = h;
     a.g = g;
     a.u = u;
+    a.part = static_cast<float *>(workspace);
     return hip_status(twell::launch_glu(vdtype, a, static_cast<hipStream_t>(stream)));
 }
 

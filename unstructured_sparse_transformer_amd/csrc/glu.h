@@ -19,6 +19,8 @@ struct GluFwd {
     DgTiles tiles;  // bf16 tiles
     const void *x, *wg, *wu;
     void *h, *g, *u;  // g, u may be NULL
+    float *part;      // [splits][g | u][T][F] partial sums
+    int splits;       // of K, when the tiles alone leave CUs idle
 };
 
 struct GluBwd {
@@ -39,6 +41,8 @@ struct GluWs {
     size_t dgu, part, bytes;  // offsets
 };
 GluWs glu_backward_ws(int T, int d, int F, int vdtype);
+
+size_t glu_forward_ws(int T, int d, int F, int vdtype);  // bytes
 
 hipError_t launch_glu(int vdtype, const GluFwd &a, hipStream_t s);
 hipError_t launch_glu_backward(int vdtype, const GluBwd &a, hipStream_t s);

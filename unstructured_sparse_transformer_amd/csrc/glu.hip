@@ -89,8 +89,24 @@ glu_kernel(GluFwd p)
     core.a.setup(p.x, p.x, ld, mt * BM, p.T, p.d, 0, wave, lane);
     core.b.setup(p.wg, p.wu, ld, nt * BN, p.F, p.d, 0, wave, lane);
     f32x16 acc[Core::FM][Core::FN];
-    core.run(0, p.d >> 6, smem, tid, acc);
+    const int nk = p.d >> 6, per = (nk + p.splits - 1) / p.splits, k0 = split * per;
+    core.run(k0, k0 + per < nk ? k0 + per : nk, smem, tid, acc);
     const int m0 = mt * BM + wave / Core::NWN * WM, n0 = nt * (BN / 2) + wave % Core::NWN * DB;
+    if (p.splits > 1) {
+#pragma unroll
+        for (int fm = 0; fm < Core::FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < Core::FN; ++fn)
+#pragma unroll
+                for (int i = 0; i < 16; i += 4) {
+                    const int m = m0 + fm * 32 + (lane & 31), n = n0 + fn % NB * 32 + acc_row(i, lane);
+                    const f32x16 &v = acc[fm][fn];
+                    if (m < p.T && n < p.F)
+                        *reinterpret_cast<float4 *>(p.part + ((int64_t)(split * 2 + fn / NB) * p.T + m) * p.F + n) =
+                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+                }
+        return;
+    }
     char *stage = smem + wave * dg_stage_bytes<NB>();
 #pragma unroll
     for (int fm = 0; fm < Core::FM; ++fm) {
@@ -222,6 +238,38 @@ template <typename TI, int BM, int NB, int S> __global__ __launch_bounds__(256) 
         if (p.u)
             store_elem((TI *)p.u + o, u);
         store_elem((TI *)p.h + o, glu_act<sizeof(TI) == 2>(g, p.act) * u);
+    }
+}
+
+// h (and g, u) from the splits' parts, added in order; 4 columns a thread.
+template <typename TI> __global__ __launch_bounds__(256) void glu_join_act_kernel(GluFwd p)
+{
+    const int64_t n4 = (int64_t)p.T * p.F / 4;
+    for (int64_t c = blockIdx.x * 256LL + threadIdx.x; c < n4; c += gridDim.x * 256LL) {
+        float v[2][4];
+#pragma unroll
+        for (int w = 0; w < 2; ++w) {
+            float4 s = reinterpret_cast<const float4 *>(p.part)[w * n4 + c];
+            for (int k = 1; k < p.splits; ++k) {
+                const float4 t = reinterpret_cast<const float4 *>(p.part)[(2 * k + w) * n4 + c];
+                s.x += t.x;
+                s.y += t.y;
+                s.z += t.z;
+                s.w += t.w;
+            }
+            v[w][0] = s.x;
+            v[w][1] = s.y;
+            v[w][2] = s.z;
+            v[w][3] = s.w;
+        }
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+            if (p.g)
+                store_elem((TI *)p.g + c * 4 + e, v[0][e]);
+            if (p.u)
+                store_elem((TI *)p.u + c * 4 + e, v[1][e]);
+            store_elem((TI *)p.h + c * 4 + e, glu_act<sizeof(TI) == 2>(v[0][e], p.act) * v[1][e]);
+        }
     }
 }
 
@@ -469,14 +517,16 @@ __global__ __launch_bounds__(256) void glu_f32_kernel(GluFwd p)
 {
     using Core = F32Core<true, true, 32>;
     __shared__ __attribute__((aligned(16))) float smem[2 * Core::SLOT];
+    const int tiles = p.MT * p.NT, split = blockIdx.x / tiles;
     int mt, nt;
-    tile_coords(blockIdx.x, p.MT, p.NT, mt, nt);
+    tile_coords(blockIdx.x - split * tiles, p.MT, p.NT, mt, nt);
     const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const int nk = p.d / 16, per = (nk + p.splits - 1) / p.splits, k0 = split * per;
     Core core;
     core.a.setup(p.x, p.x, p.d, mt * 64, p.T, p.d, p.d, tid);
     core.b.setup(p.wg, p.wu, p.d, nt * 128, p.F, p.d, p.d, tid);
     f32x16 acc[2];
-    core.run(0, p.d / 16, smem, tid, acc);
+    core.run(k0, k0 + per < nk ? k0 + per : nk, smem, tid, acc);
     const int n = nt * 64 + (wave & 1) * 32 + (lane & 31);
 #pragma unroll
     for (int i = 0; i < 16; ++i) {
@@ -484,6 +534,12 @@ __global__ __launch_bounds__(256) void glu_f32_kernel(GluFwd p)
         if (m < p.T && n < p.F) {
             const int64_t o = (int64_t)m * p.F + n;
             const float g = acc[0][i], u = acc[1][i];
+            if (p.splits > 1) {
+                const int64_t part = (int64_t)p.T * p.F;
+                p.part[2 * split * part + o] = g;
+                p.part[(2 * split + 1) * part + o] = u;
+                continue;
+            }
             if (p.g)
                 ((float *)p.g)[o] = g;
             if (p.u)
@@ -529,34 +585,33 @@ template <bool A_KC, bool B_KC> __global__ __launch_bounds__(256) void glu_mul_f
 // ------------------------------------------------------------------ host
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The workgroup tiles of the bf16 products, and what one stage of 64 K elements
-// and the rest of a tile cost on a CU (us, measured on products of many sizes
-// with one tile per CU): larger tiles move fewer bytes per product, smaller ones
-// give every CU work.
+// The workgroup tiles of the products, and what one stage of 64 K elements and the
+// rest of a tile cost on a CU (us, measured on products of many sizes with
+// `per_cu` tiles per CU): larger tiles move fewer bytes per product, smaller ones give every
+// CU work.  Splitting K does too; the parts are written and read once more.
 struct MulTile {
-    int bm, bn;
+    int bm, bn, per_cu;
     double stage;
 };
-constexpr MulTile MUL_TILES[] = {{256, 256, 1.5}, {256, 128, 0.88}, {128, 128, 0.52}, {128, 64, 0.36}};
+constexpr MulTile MUL_TILES[] = {{256, 256, 1, 1.5}, {256, 128, 1, 0.88}, {128, 128, 1, 0.52}, {128, 64, 1, 0.36}};
+constexpr MulTile MUL_TILE_F32 = {64, 128, 2, 2.9};  // two on a CU
 constexpr double MUL_TILE_US = 5, MUL_JOIN_US = 4, MUL_PART_BYTES_PER_US = 4e6;
-constexpr int CUS = 256;
+constexpr int CUS = 256, MUL_MOST_SPLITS = 16;
 
 struct MulPlan {
     int tile, splits;
 };
 
 // The tile and the number of K splits with the least estimated time.
-static MulPlan mul_plan(int64_t M, int64_t N, int64_t K, int tiles, int most_splits)
+static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, int64_t K)
 {
     MulPlan best{0, 1};
     double best_us = 1e300;
-    const int64_t stages = (K + 63) / 64;
+    const int64_t stages = ceil_div(K, 64);
     for (int t = 0; t < tiles; ++t)
-        for (int splits = 1; splits <= most_splits && splits <= stages; splits *= 2) {
-            const int64_t wgs = ((M + MUL_TILES[t].bm - 1) / MUL_TILES[t].bm) *
-                                ((N + MUL_TILES[t].bn - 1) / MUL_TILES[t].bn) * splits;
-            const double rounds = (double)((wgs + CUS - 1) / CUS), per = (double)((stages + splits - 1) / splits);
-            double us = rounds * (per * MUL_TILES[t].stage + MUL_TILE_US);
+        for (int splits = 1; splits <= MUL_MOST_SPLITS && (splits == 1 || splits <= stages); splits *= 2) {
+            const int64_t wgs = ceil_div(M, tile[t].bm) * ceil_div(N, tile[t].bn) * splits;
+            double us = (double)ceil_div(wgs, CUS * tile[t].per_cu) * ((double)ceil_div(stages, splits) * tile[t].stage + MUL_TILE_US);
             if (splits > 1)
                 us += MUL_JOIN_US + (double)M * N * 8 * splits / MUL_PART_BYTES_PER_US;
             if (us < best_us) {
@@ -565,6 +620,25 @@ static MulPlan mul_plan(int64_t M, int64_t N, int64_t K, int tiles, int most_spl
             }
         }
     return best;
+}
+
+static MulPlan forward_plan(int vdtype, int T, int d, int F)
+{
+    if (T <= GLU_FEW)
+        return {0, 1};
+    return vdtype == 1 ? mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d) : mul_plan(&MUL_TILE_F32, 1, T, 2 * (int64_t)F, d);
+}
+
+size_t glu_forward_ws(int T, int d, int F, int vdtype)
+{
+    const int splits = forward_plan(vdtype, T, d, F).splits;
+    return splits > 1 ? (size_t)splits * 2 * T * F * sizeof(float) : 0;
+}
+
+static dim3 join_grid(int64_t n)
+{
+    const int64_t wgs = ceil_div(n / 4, 256);
+    return dim3((unsigned)(wgs < 4096 ? wgs : 4096));
 }
 
 hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
@@ -582,45 +656,47 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
             glu_stream_kernel<float, 64, 16, 6><<<grid, block, 0, s>>>(p);
         return hipGetLastError();
     }
+    const MulPlan plan = forward_plan(vdtype, p.T, p.d, p.F);
+    p.splits = plan.splits;
     if (vdtype == 0) {
         p.MT = (int)ceil_div(p.T, 64);
         p.NT = (int)ceil_div(p.F, 64);
-        glu_f32_kernel<<<dim3(p.MT * p.NT), dim3(256), 0, s>>>(p);
-        return hipGetLastError();
+        glu_f32_kernel<<<dim3(p.MT * p.NT * p.splits), dim3(256), 0, s>>>(p);
+    } else {
+        const MulTile &tile = MUL_TILES[plan.tile];
+        p.tiles = dg_tiles(ceil_div(p.T, tile.bm), ceil_div(p.F, tile.bn / 2), p.splits);
+        const dim3 grid((unsigned)dg_grid(p.tiles));
+        switch (plan.tile) {
+        case 0:
+            glu_kernel<256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(p);
+            break;
+        case 1:
+            glu_kernel<256, 128, 64, 64, 3><<<grid, dim3(512), 0, s>>>(p);
+            break;
+        case 2:
+            glu_kernel<128, 128, 32, 64, 4><<<grid, dim3(512), 0, s>>>(p);
+            break;
+        default:
+            glu_kernel<128, 64, 32, 64, 3><<<grid, dim3(256), 0, s>>>(p);
+            break;
+        }
     }
-    const int tile = mul_plan(p.T, 2 * (int64_t)p.F, p.d, 4, 1).tile;
-    p.tiles = dg_tiles(ceil_div(p.T, MUL_TILES[tile].bm), ceil_div(p.F, MUL_TILES[tile].bn / 2), 1);
-    const dim3 grid((unsigned)dg_grid(p.tiles));
-    switch (tile) {
-    case 0:
-        glu_kernel<256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(p);
-        break;
-    case 1:
-        glu_kernel<256, 128, 64, 64, 3><<<grid, dim3(512), 0, s>>>(p);
-        break;
-    case 2:
-        glu_kernel<128, 128, 32, 64, 4><<<grid, dim3(512), 0, s>>>(p);
-        break;
-    default:
-        glu_kernel<128, 64, 32, 64, 3><<<grid, dim3(256), 0, s>>>(p);
-        break;
-    }
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.splits == 1)
+        return e;
+    if (vdtype == 1)
+        glu_join_act_kernel<__bf16><<<join_grid((int64_t)p.T * p.F), dim3(256), 0, s>>>(p);
+    else
+        glu_join_act_kernel<float><<<join_grid((int64_t)p.T * p.F), dim3(256), 0, s>>>(p);
     return hipGetLastError();
 }
 
-// Tiles and splits of a product of the backward pass.  fp32 has one tile, 64 x
-// 128, and splits until there are two workgroups per CU.
+// Tiles and splits of a product of the backward pass.
 static MulPlan backward_plan(int vdtype, int64_t M, int64_t N, int64_t K)
 {
     if (M == 0 || N == 0 || K == 0)
         return {0, 1};
-    if (vdtype == 1)
-        return mul_plan(M, N, K, 3, 16);
-    const int64_t tiles = ceil_div(M, 64) * ceil_div(N, 128), stages = ceil_div(K, 64);
-    int splits = 1;
-    while (splits < 16 && tiles * splits * 2 <= 512 && stages / (splits * 2) >= 8)
-        splits *= 2;
-    return {0, splits};
+    return vdtype == 1 ? mul_plan(MUL_TILES, 3, M, N, K) : mul_plan(&MUL_TILE_F32, 1, M, N, K);
 }
 
 static size_t up256_(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -659,8 +735,7 @@ template <bool A_KC, bool B_KC> static hipError_t mul_go(int vdtype, GluMul p, h
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
-    const int64_t wgs = ceil_div((int64_t)p.M * p.N / 4, 256);
-    const dim3 join((unsigned)(wgs < 4096 ? wgs : 4096));
+    const dim3 join = join_grid((int64_t)p.M * p.N);
     if (vdtype == 1)
         glu_join_kernel<__bf16><<<join, dim3(256), 0, s>>>(p);
     else
