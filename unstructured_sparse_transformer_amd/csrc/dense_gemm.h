@@ -356,7 +356,8 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int 
 // `lds`: dg_stage_bytes<NB>() bytes of the wave's own.  A row's 16-byte chunks are
 // XORed with the row's index among the rows that share a place in the 256-byte
 // bank window, and rows 16 on swap a chunk's halves, so that the 32 rows' 8-byte
-// pieces of one write, and 16 chunks of one read, meet every bank once.
+// pieces of one write, and 16 chunks of one read, meet every bank once.  ONCE:
+// not read again soon, written past the caches.
 template <int NB> constexpr int dg_stage_bytes() { return 32 * 64 * NB; }
 template <int NB> __device__ __forceinline__ int dg_stage_chunk(int row, int chunk)
 {
@@ -364,7 +365,7 @@ template <int NB> __device__ __forceinline__ int dg_stage_chunk(int row, int chu
     static_assert(NB == 1 || NB == 2 || NB == 4, "rows of 64, 128 or 256 bytes");
     return row * (64 * NB) + ((chunk ^ ((row >> LOG) & (4 * NB - 1))) << 4);
 }
-template <int NB, typename V>
+template <int NB, bool ONCE = false, typename V>
 __device__ __forceinline__ void dg_store_rows(char *lds, int lane, V value, __bf16 *out, int64_t ld, int m0, int n0,
                                               int M, int N)
 {
@@ -387,8 +388,13 @@ __device__ __forceinline__ void dg_store_rows(char *lds, int lane, V value, __bf
         u32x4 v = *reinterpret_cast<const u32x4 *>(lds + dg_stage_chunk<NB>(r, q));
         if (c0 / CPR >= 16)
             v = u32x4{v[2], v[3], v[0], v[1]};
-        if (m0 + r < M && n0 + q * 8 < N)
-            *reinterpret_cast<u32x4 *>(out + (int64_t)(m0 + r) * ld + n0 + q * 8) = v;
+        u32x4 *o = reinterpret_cast<u32x4 *>(out + (int64_t)(m0 + r) * ld + n0 + q * 8);
+        if (m0 + r < M && n0 + q * 8 < N) {
+            if constexpr (ONCE)
+                __builtin_nontemporal_store(v, o);
+            else
+                *o = v;
+        }
     }
     asm volatile("" ::: "memory");
 }
