@@ -191,6 +191,20 @@ def test_non_finite_row_stays_alone(gpu_lib):
         assert torch.isnan(bad[3]).all()
 
 
+@pytest.mark.parametrize("T,d,F", [(1, 64, 64), (65, 64, 192), (1003, 1024, 512), (2000, 512, 2048)])
+@pytest.mark.parametrize("dtype", ["bfloat16", "float32"])
+def test_infinite_last_row(gpu_lib, T, d, F, dtype):
+    """An infinity in x's last row gives infinite gradients of the weights, and no NaN from rows that are not there."""
+    import torch
+    say(f"case glu infinite last row {T} {d} {F} {dtype}")
+    x, wg, wu = _inputs(T, d, F, dtype)
+    x[-1, 3] = float("inf")
+    one = torch.ones((T, F), dtype=x.dtype, device="cuda")
+    got = _backward(gpu_lib, x, wg, wu, one, one, one, "relu", dx=False)
+    for k in ("dwg", "dwu"):
+        assert (got[k][:, 3] == float("inf")).all() and torch.isfinite(got[k][:, :3]).all() and torch.isfinite(got[k][:, 4:]).all(), k
+
+
 def test_same_bits_on_a_stream(gpu_lib):
     import torch
     say("case glu same bits")

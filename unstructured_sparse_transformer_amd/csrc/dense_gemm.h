@@ -1,29 +1,34 @@
 // dense_gemm.h -- the matrix-product core of the gated product (gfx950).
 //
 // C[m][n] = sum_k A(m, k) B(k, n) on workgroup tiles of BM x BN, K in stages of
-// 64 bf16 elements, fp32 accumulators (v_mfma_f32_32x32x16_bf16).  B's fragment
-// is the instruction's first operand: a lane then holds 4 consecutive n of one m
-// (element i of lane l of a block: n = 8 (i / 4) + 4 (l / 32) + i % 4, m = l % 32),
-// which leave as one 8-byte piece of a row.  Each operand is read as it lies in
-// memory:
+// 64 bf16 or 32 fp32 elements, fp32 accumulators (v_mfma_f32_32x32x16_bf16, or 4
+// of v_mfma_f32_32x32x2f32 on a lane's 4 elements).  In bf16 B's
+// fragment is the instruction's first operand: a lane then holds 4 consecutive n
+// of one m (element i of lane l of a block: n = 8 (i / 4) + 4 (l / 32) + i % 4,
+// m = l % 32), which leave as one 8-byte piece of a row.  In fp32 it is A's: a
+// lane has one n, and 32 lanes store 128 bytes of a row (16-byte pieces of 32 rows: 4096
+// x 64 x 512 forward 14.3 us, 11.7 so; products in parts 1% the other way).
+// Each operand is read as it lies in memory:
 //   KC  rows of its M (or N) index, K contiguous:   x and W of the forward pass
 //   KS  rows of K, its M (or N) index contiguous:   W in dx, x and dg in dW
 // A stage of either is 128 bytes per M (or N) index, copied by global->LDS
 // instructions of 1 KiB per wave.  KC stages keep 128-byte rows with XORed
 // 16-byte chunks (lds_off); KS stages keep the raw rows, their chunks XORed so
-// that a transposing LDS read (ds_read_b64_tr_b16) of 4 rows meets every bank
-// once.
+// that a transposing LDS read (ds_read_b64_tr_b16) of 4 bf16 rows, or a read of
+// one element a lane of 2 fp32 rows, meets every bank once.
 #pragma once
 
 #include "twell_device.h"
 
 namespace twell {
 
-// Tiles' 64-bit base addresses with 32-bit offsets inside a tile: the matrices
-// themselves have no size limit.
+// Tiles' 64-bit base addresses with offsets below 2^31 inside a tile: the matrices
+// themselves have no size limit.  An offset of DG_NONE is out of the descriptor's
+// range, and reads as zeros.
+constexpr int DG_NONE = (int)0x80000000u;
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t dg_rsrc(const void *base)
 {
-    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, -1, 0x00020000);
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(base), (short)0, DG_NONE, 0x00020000);
 }
 
 // Waits until at most N copies of this wave are in flight, and for its LDS reads.
@@ -93,10 +98,12 @@ __device__ __forceinline__ uint2 dg_read_tr(__attribute__((address_space(3))) dg
 // One operand of a workgroup: IDX tile indices, NW waves.  DB > 0 (KC only):
 // the tile's rows alternate between two matrices in blocks of DB (row 2 DB q +
 // r, r < DB, is column DB q + r of the first, row 2 DB q + DB + r of the second).
-template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
+template <typename TI, int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
+    static constexpr int ES = sizeof(TI), EPC = 16 / ES;
+    static constexpr int SK = 128 / ES;              // K elements of a stage
     static constexpr int BYTES = IDX * 128;
     static constexpr int LD = IDX / 8 / NW;          // 1 KiB copies per wave and stage
-    static constexpr int RAW = IDX * 2;              // KS: bytes of a raw row
+    static constexpr int RAW = IDX * ES;             // KS: bytes of a raw row
     static constexpr int RPI = KC ? 8 : 1024 / RAW;  // rows per copy
     static_assert(IDX % (8 * NW) == 0, "copies split over the waves");
     static_assert(KC || (RAW >= 256 && RAW <= 1024), "raw rows span whole 256-byte bank windows");
@@ -110,15 +117,15 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
     int turn, last;   // KS: first stage of the second matrix, last stage of all
     int voff[LD], vlast[LD];
 
-    __device__ __forceinline__ static int raw_slot(int r, int c) { return c ^ ((r & 3) << 2); }
+    __device__ __forceinline__ static int raw_slot(int r, int c) { return c ^ (ES == 2 ? (r & 3) << 2 : (r & 4) << 1); }
 
     // idx0: the workgroup's first index, n: indices there are, ld: bytes between rows, k: K elements there are (KS:
-    // the last stage's rows past k repeat row k - 1; the other operand holds zeros there).
+    // the last stage's rows past k are zeros).
     __device__ __forceinline__ void setup(const void *p, const void *p2, int64_t ld, int idx0, int n, int k, int turn_,
                                           int wave, int lane)
     {
         turn = turn_;
-        last = (k - 1) >> 6;
+        last = (k - 1) / SK;
         if constexpr (KC) {
             const int first = DB > 0 ? idx0 / 2 : idx0;  // DB: idx0 counts the rows of both
             ptr = (const char *)p + (int64_t)first * ld;
@@ -136,17 +143,16 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
                 voff[j] = q * (int)ld + c * 16;
             }
         } else {
-            ptr = (const char *)p + (int64_t)idx0 * 2;
-            step = 64 * ld;
+            ptr = (const char *)p + (int64_t)idx0 * ES;
+            step = SK * ld;
             other = (const char *)p2 - (const char *)p - turn_ * step;
 #pragma unroll
             for (int j = 0; j < LD; ++j) {
                 const int r = (j * NW + wave) * RPI + lane / (RAW / 16);
-                int c = raw_slot(r, lane % (RAW / 16)) * 8;
-                c = idx0 + c <= n - 8 ? c : n - 8 - idx0;
-                voff[j] = r * (int)ld + c * 2;
-                const int rl = last * 64 + r < k ? r : k - 1 - last * 64;
-                vlast[j] = rl * (int)ld + c * 2;
+                int c = raw_slot(r, lane % (RAW / 16)) * EPC;
+                c = idx0 + c <= n - EPC ? c : n - EPC - idx0;
+                voff[j] = r * (int)ld + c * ES;
+                vlast[j] = last * SK + r < k ? voff[j] : DG_NONE;
             }
         }
     }
@@ -184,12 +190,21 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
         dma16(dg_rsrc(second ? ptr + other : ptr), lds + (j * NW + wave) * 1024, voff[j], 0);
     }
 
-    // The fragment of 32 indices from i0, K sub-step ss (16 elements): lane l
-    // holds index i0 + l % 32, elements 16 ss + 8 (l / 32) .. + 7.
+    // The fragment of 32 indices from i0, K sub-step ss (16 elements, fp32: 8):
+    // lane l holds index i0 + l % 32, elements 16 ss + 8 (l / 32) .. + 7 (fp32:
+    // 8 ss + 4 (l / 32) .. + 3).
     __device__ __forceinline__ static u32x4 fragment(const char *lds, int i0, int ss, int lane)
     {
         if constexpr (KC) {
             return *reinterpret_cast<const u32x4 *>(lds + lds_off<128>(i0 + (lane & 31), ss * 2 + (lane >> 5)));
+        } else if constexpr (ES == 4) {
+            const int r = ss * 8 + ((lane >> 5) << 2), i = i0 + (lane & 31);
+            const char *a = lds + r * RAW + (raw_slot(r, i >> 2) << 4) + ((i & 3) << 2);
+            u32x4 v;
+#pragma unroll
+            for (int e = 0; e < 4; ++e)
+                v[e] = *reinterpret_cast<const uint32_t *>(a + e * RAW);
+            return v;
         } else {
             // Within a 16-lane group the transposing read hands lane i element i % 4 of the 8-byte pieces addressed
             // by lanes i / 4 + 4 j (j < 4) as its values j: lane p addresses row k0 + p / 4 (+ 4 for the second
@@ -216,11 +231,11 @@ template <int IDX, bool KC, int NW, int DB = 0> struct DgOperand {
 // the same kernels on zeros reach 1.76 PFLOP/s.  4 waves of 128 x 128 (a third
 // fewer LDS reads, one wave a SIMD) measured 3-6% slower, 16 waves of 64 x 64 5%,
 // v_mfma_f32_16x16x32_bf16 in the place of 32x32x16 4-7%.
-template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int S = 2> struct DgCore {
+template <typename TI, int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int S = 2> struct DgCore {
     static constexpr int NWM = BM / WM, NWN = BN / WN, NW = NWM * NWN, THREADS = NW * 64;
     static constexpr int FM = WM / 32, FN = WN / 32;
-    using A = DgOperand<BM, A_KC, NW>;
-    using B = DgOperand<BN, B_KC, NW, DB>;
+    using A = DgOperand<TI, BM, A_KC, NW>;
+    using B = DgOperand<TI, BN, B_KC, NW, DB>;
     static constexpr int STAGE = A::BYTES + B::BYTES;
     static constexpr int LDS = S * STAGE;  // S slots
     static constexpr int COPIES = A::LD + B::LD;
@@ -269,7 +284,10 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int 
                 }
             __builtin_amdgcn_sched_barrier(0);
             const int fn = q / FM, fm = fn & 1 ? FM - 1 - q % FM : q % FM;
-            mfma_chunk(__bf16{}, bf[fn], af[fm], acc[fm][fn]);
+            if constexpr (sizeof(TI) == 4)
+                mfma_chunk(TI{}, af[fm], bf[fn], acc[fm][fn]);
+            else
+                mfma_chunk(TI{}, bf[fn], af[fm], acc[fm][fn]);
 #pragma unroll
             for (int c = C0; c < C1; ++c)
                 if ((c - C0) * NM / (NC > 0 ? NC : 1) == q && on)
@@ -350,6 +368,29 @@ template <int BM, int BN, int WM, int WN, bool A_KC, bool B_KC, int DB = 0, int 
         __syncthreads();
     }
 };
+
+// A block of 32 x 32 accumulators to memory, in fp32.
+template <typename TI>
+__device__ __forceinline__ void dg_store_block(const f32x16 &v, int lane, float *out, int64_t ld, int m0, int n0, int M, int N)
+{
+    if constexpr (sizeof(TI) == 4) {
+        const int n = n0 + (lane & 31);
+#pragma unroll
+        for (int i = 0; i < 16; ++i) {
+            const int m = m0 + acc_row(i, lane);
+            if (m < M && n < N)
+                out[m * ld + n] = v[i];
+        }
+    } else {
+        const int m = m0 + (lane & 31);
+#pragma unroll
+        for (int i = 0; i < 16; i += 4) {
+            const int n = n0 + acc_row(i, lane);
+            if (m < M && n < N)
+                *reinterpret_cast<float4 *>(out + m * ld + n) = make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
+        }
+    }
+}
 
 // A wave's block of 32 rows by 32 NB columns in bf16, from accumulators
 // (value(fn, i)) to memory by way of LDS: 16-byte stores of whole row pieces.

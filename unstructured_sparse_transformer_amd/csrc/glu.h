@@ -15,8 +15,7 @@ constexpr int GLU_FEW = 64;  // rows up to which the forward pass streams the we
 
 struct GluFwd {
     int T, d, F, act;
-    int MT, NT;     // fp32 tiles
-    DgTiles tiles;  // bf16 tiles
+    DgTiles tiles;
     const void *x, *wg, *wu;
     void *h, *g, *u;  // g, u may be NULL
     float *part;      // [splits][g | u][T][F] partial sums

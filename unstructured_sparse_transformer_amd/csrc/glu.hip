@@ -71,25 +71,31 @@ template <bool FAST> __device__ __forceinline__ float glu_act_grad(float g, int 
 }
 
 // ------------------------------------------------------------------ forward
-template <int BM, int BN, int WM, int WN, int S>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
+// Bound by the matrix units.  bf16, 8192 x 2048 x 8192 with g and u kept: 487 us,
+// 1.13 PFLOP/s; the product by itself takes 420 us at the clock the chip's power
+// cap leaves it, the rest is 403 MB of results that leave between the tiles
+// (workgroups started up to 13 us apart, so that some store while others
+// multiply: no change).  fp32, 1500 x 2048 x 2048: 188 us, 134 of 157 TFLOP/s.
+// fp32 tiles are small and several share a CU, hence the waves per SIMD.
+template <typename TI, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, sizeof(TI) == 4 ? 4 : 2))) void
 glu_kernel(GluFwd p)
 {
     constexpr int DB = WN / 2, NB = DB / 32;
-    using Core = DgCore<BM, BN, WM, WN, true, true, DB, S>;
+    using Core = DgCore<TI, BM, BN, WM, WN, true, true, DB, S>;
     __shared__ __attribute__((aligned(16))) char smem[Core::LDS];
-    static_assert(Core::NW * dg_stage_bytes<NB>() <= Core::LDS, "the stores' staging fits");
+    static_assert(sizeof(TI) == 4 || Core::NW * dg_stage_bytes<NB>() <= Core::LDS, "the stores' staging fits");
     int mt, nt, split;
     if (!dg_tile(p.tiles, blockIdx.x, mt, nt, split))
         return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Core core;
-    const int64_t ld = (int64_t)p.d * 2;
+    const int64_t ld = (int64_t)p.d * sizeof(TI);
     core.a.setup(p.x, p.x, ld, mt * BM, p.T, p.d, 0, wave, lane);
     core.b.setup(p.wg, p.wu, ld, nt * BN, p.F, p.d, 0, wave, lane);
     f32x16 acc[Core::FM][Core::FN];
-    const int nk = p.d >> 6, per = (nk + p.splits - 1) / p.splits, k0 = split * per;
+    const int nk = p.d / Core::A::SK, per = (nk + p.splits - 1) / p.splits, k0 = split * per;
     core.run(k0, k0 + per < nk ? k0 + per : nk, smem, tid, acc);
     const int m0 = mt * BM + wave / Core::NWN * WM, n0 = nt * (BN / 2) + wave % Core::NWN * DB;
     if (p.splits > 1) {
@@ -97,14 +103,27 @@ glu_kernel(GluFwd p)
         for (int fm = 0; fm < Core::FM; ++fm)
 #pragma unroll
             for (int fn = 0; fn < Core::FN; ++fn)
+                dg_store_block<TI>(acc[fm][fn], lane, p.part + (int64_t)(split * 2 + fn / NB) * p.T * p.F, p.F,
+                                   m0 + fm * 32, n0 + fn % NB * 32, p.T, p.F);
+        return;
+    }
+    if constexpr (sizeof(TI) == 4) {
 #pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int m = m0 + fm * 32 + (lane & 31), n = n0 + fn % NB * 32 + acc_row(i, lane);
-                    const f32x16 &v = acc[fm][fn];
-                    if (m < p.T && n < p.F)
-                        *reinterpret_cast<float4 *>(p.part + ((int64_t)(split * 2 + fn / NB) * p.T + m) * p.F + n) =
-                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                }
+        for (int fm = 0; fm < Core::FM; ++fm)
+#pragma unroll
+            for (int fn = 0; fn < NB; ++fn) {
+                const int m = m0 + fm * 32, n = n0 + fn * 32;
+                const f32x16 &g = acc[fm][fn], &u = acc[fm][fn + NB];
+                if (p.g)
+                    dg_store_block<TI>(g, lane, (float *)p.g, p.F, m, n, p.T, p.F);
+                if (p.u)
+                    dg_store_block<TI>(u, lane, (float *)p.u, p.F, m, n, p.T, p.F);
+                f32x16 h;
+#pragma unroll
+                for (int i = 0; i < 16; ++i)
+                    h[i] = glu_act<false>(g[i], p.act) * u[i];
+                dg_store_block<TI>(h, lane, (float *)p.h, p.F, m, n, p.T, p.F);
+            }
         return;
     }
     char *stage = smem + wave * dg_stage_bytes<NB>();
@@ -198,10 +217,10 @@ template <typename TI, int BM, int NB, int S> __global__ __launch_bounds__(256) 
         u32x4 a[FM], b[FN];
 #pragma unroll
         for (int f = 0; f < FM; ++f)
-            a[f] = DgOperand<32, true, 1>::fragment(cur, f * 32, wave, lane);
+            a[f] = DgOperand<TI, 32, true, 1>::fragment(cur, f * 32, wave, lane);
 #pragma unroll
         for (int f = 0; f < FN; ++f)
-            b[f] = DgOperand<32, true, 1>::fragment(cur + A_BYTES, f * 32, wave, lane);
+            b[f] = DgOperand<TI, 32, true, 1>::fragment(cur + A_BYTES, f * 32, wave, lane);
 #pragma unroll
         for (int fm = 0; fm < FM; ++fm)
 #pragma unroll
@@ -330,27 +349,29 @@ struct GluMul {
     int m_turn;
     float *part;
     int splits;
-    int MT, NT;     // fp32 tiles
-    DgTiles tiles;  // bf16 tiles
+    DgTiles tiles;
 };
 
-template <int BM, int BN, int WM, int WN, int S, bool A_KC, bool B_KC>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, 2))) void
+// Bound by the matrix units: the 2B-like layer's dx takes 425 us and its dW 425
+// (1.29 PFLOP/s each); fp32, 1500 x 2048 x 2048: about 196 and 190 us, 130 TFLOP/s.
+template <typename TI, int BM, int BN, int WM, int WN, int S, bool A_KC, bool B_KC>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, sizeof(TI) == 4 ? 4 : 2))) void
 glu_mul_kernel(GluMul p)
 {
-    using Core = DgCore<BM, BN, WM, WN, A_KC, B_KC, 0, S>;
+    using Core = DgCore<TI, BM, BN, WM, WN, A_KC, B_KC, 0, S>;
+    constexpr int SK = Core::A::SK;
     __shared__ __attribute__((aligned(16))) char smem[Core::LDS];
-    static_assert(Core::NW * dg_stage_bytes<Core::FN>() <= Core::LDS, "the stores' staging fits");
+    static_assert(sizeof(TI) == 4 || Core::NW * dg_stage_bytes<Core::FN>() <= Core::LDS, "the stores' staging fits");
     int mt, nt, split;
     if (!dg_tile(p.tiles, blockIdx.x, mt, nt, split))
         return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
     Core core;
-    const int nk = (p.K + 63) >> 6, per = (nk + p.splits - 1) / p.splits;
+    const int nk = (p.K + SK - 1) / SK, per = (nk + p.splits - 1) / p.splits;
     const int k0 = split * per, k1 = k0 + per < nk ? k0 + per : nk;
-    core.a.setup(p.a, p.a, p.lda, mt * BM, p.M, nk * 64, nk, wave, lane);
-    core.b.setup(p.b, p.b2, p.ldb, nt * BN, p.N, p.K, p.k_turn >> 6, wave, lane);
+    core.a.setup(p.a, p.a, p.lda, mt * BM, p.M, nk * SK, nk, wave, lane);
+    core.b.setup(p.b, p.b2, p.ldb, nt * BN, p.N, p.K, p.k_turn / SK, wave, lane);
     f32x16 acc[Core::FM][Core::FN];
     core.run(k0, k1, smem, tid, acc);
     const int m0 = mt * BM + wave / Core::NWN * WM, n0 = nt * BN + wave % Core::NWN * WN;
@@ -359,24 +380,25 @@ glu_mul_kernel(GluMul p)
         for (int fm = 0; fm < Core::FM; ++fm)
 #pragma unroll
             for (int fn = 0; fn < Core::FN; ++fn)
-#pragma unroll
-                for (int i = 0; i < 16; i += 4) {
-                    const int m = m0 + fm * 32 + (lane & 31), n = n0 + fn * 32 + acc_row(i, lane);
-                    const f32x16 &v = acc[fm][fn];
-                    if (m < p.M && n < p.N)
-                        *reinterpret_cast<float4 *>(p.part + ((int64_t)split * p.M + m) * p.N + n) =
-                            make_float4(v[i], v[i + 1], v[i + 2], v[i + 3]);
-                }
+                dg_store_block<TI>(acc[fm][fn], lane, p.part + (int64_t)split * p.M * p.N, p.N, m0 + fm * 32, n0 + fn * 32,
+                                   p.M, p.N);
         return;
     }
-    char *stage = smem + wave * dg_stage_bytes<Core::FN>();
+    [[maybe_unused]] char *stage = smem + wave * dg_stage_bytes<Core::FN>();
 #pragma unroll
     for (int fm = 0; fm < Core::FM; ++fm) {
-        const int m = m0 + fm * 32;  // m_turn is a multiple of 64: a block of 32 rows lies on one side
+        int m = m0 + fm * 32;  // m_turn is a multiple of 64: a block of 32 rows lies on one side
         const bool second = m >= p.m_turn;
-        dg_store_rows<Core::FN>(stage, lane, [&](int fn, int i) { return acc[fm][fn][i]; },
-                                (__bf16 *)(second ? p.out2 : p.out), p.N, second ? m - p.m_turn : m, n0,
-                                second ? p.M - p.m_turn : p.M < p.m_turn ? p.M : p.m_turn, p.N);
+        TI *out = (TI *)(second ? p.out2 : p.out);
+        const int M = second ? p.M - p.m_turn : p.M < p.m_turn ? p.M : p.m_turn;
+        m -= second ? p.m_turn : 0;
+        if constexpr (sizeof(TI) == 4) {
+#pragma unroll
+            for (int fn = 0; fn < Core::FN; ++fn)
+                dg_store_block<TI>(acc[fm][fn], lane, out, p.N, m, n0 + fn * 32, M, p.N);
+        } else {
+            dg_store_rows<Core::FN>(stage, lane, [&](int fn, int i) { return acc[fm][fn][i]; }, out, p.N, m, n0, M, p.N);
+        }
     }
 }
 
@@ -402,201 +424,28 @@ template <typename TI> __global__ __launch_bounds__(256) void glu_join_kernel(Gl
     }
 }
 
-// ------------------------------------------------------------------ fp32
-// 64 x 128 tiles, 4 waves of 32 x 64, v_mfma_f32_32x32x2f32: a lane supplies one
-// element, index l % 32 at K index l / 32, so LDS keeps [K][index] rows for both
-// layouts and is read without conflicts.  K in steps of 16, two LDS slots, the
-// next F32_AHEAD steps' elements on their way in registers meanwhile (one step
-// ahead left a load's whole latency to wait for: 59 us at 300 x 1024 x 1024).
-constexpr int F32_AHEAD = 4;
-template <int IDX, bool KC, int DB> struct F32Operand {
-    static constexpr int V = IDX / 64;  // float4 a thread
-    static constexpr int PITCH = IDX + 4;
-    const float *base[V];
-    int64_t step;
-    int k[V], idx[V];
-    const float *second[V];
-    int turn, K;
-
-    __device__ __forceinline__ void setup(const void *p, const void *p2, int64_t ld, int idx0, int n, int K_, int turn_,
-                                          int tid)
-    {
-        K = K_;
-        turn = turn_;
-        step = KC ? 16 : 16 * ld;
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const int u = v * 256 + tid;
-            if constexpr (KC) {
-                idx[v] = u >> 2;
-                k[v] = (u & 3) * 4;
-                constexpr int D = DB > 0 ? DB : 1;
-                int q = DB > 0 ? idx0 / 2 + idx[v] / (2 * D) * D + idx[v] % D : idx0 + idx[v];
-                q = q < n ? q : n - 1;
-                base[v] = (const float *)(DB > 0 && ((idx[v] / D) & 1) ? p2 : p) + q * ld + k[v];
-                second[v] = base[v];
-            } else {
-                k[v] = u / (IDX / 4);
-                idx[v] = u % (IDX / 4) * 4;
-                const int q = idx0 + idx[v] <= n - 4 ? idx0 + idx[v] : n - 4;
-                base[v] = (const float *)p + k[v] * ld + q;
-                second[v] = (const float *)p2 + k[v] * ld + q;
-            }
-        }
-    }
-    __device__ __forceinline__ void load(int kt, float4 (&r)[V]) const
-    {
-#pragma unroll
-        for (int v = 0; v < V; ++v)
-            r[v] = kt * 16 + k[v] >= K ? make_float4(0.f, 0.f, 0.f, 0.f)
-                                       : *reinterpret_cast<const float4 *>(kt < turn ? base[v] + kt * step
-                                                                                     : second[v] + (kt - turn) * step);
-    }
-    __device__ __forceinline__ void store(float *lds, const float4 (&r)[V]) const
-    {
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            if constexpr (KC) {
-                lds[(k[v] + 0) * PITCH + idx[v]] = r[v].x;
-                lds[(k[v] + 1) * PITCH + idx[v]] = r[v].y;
-                lds[(k[v] + 2) * PITCH + idx[v]] = r[v].z;
-                lds[(k[v] + 3) * PITCH + idx[v]] = r[v].w;
-            } else {
-                *reinterpret_cast<float4 *>(lds + k[v] * PITCH + idx[v]) = r[v];
-            }
-        }
-    }
-};
-
-template <bool A_KC, bool B_KC, int DB> struct F32Core {
-    static constexpr int BM = 64, BN = 128, SLOT = 16 * (BM + 4) + 16 * (BN + 4);
-    F32Operand<BM, A_KC, 0> a;
-    F32Operand<BN, B_KC, DB> b;
-    __device__ __forceinline__ void run(int k0, int k1, float *smem, int tid, f32x16 (&acc)[2]) const
-    {
-        const int lane = tid & 63, wave = tid >> 6, wm = wave >> 1, wn = wave & 1;
-#pragma unroll
-        for (int fn = 0; fn < 2; ++fn)
-#pragma unroll
-            for (int i = 0; i < 16; ++i)
-                acc[fn][i] = 0.f;
-        float4 ra[F32_AHEAD][1], rb[F32_AHEAD][2];
-#pragma unroll
-        for (int j = 0; j < F32_AHEAD; ++j)
-            if (k0 + j < k1) {
-                a.load(k0 + j, ra[j]);
-                b.load(k0 + j, rb[j]);
-            }
-        for (int kt = k0; kt < k1; kt += F32_AHEAD) {
-#pragma unroll
-            for (int j = 0; j < F32_AHEAD; ++j) {
-                if (kt + j >= k1)
-                    break;
-                float *sa = smem + (j & 1) * SLOT, *sb = sa + 16 * (BM + 4);
-                a.store(sa, ra[j]);
-                b.store(sb, rb[j]);
-                __syncthreads();  // the other slot's readers have passed the barrier before
-                if (kt + j + F32_AHEAD < k1) {
-                    a.load(kt + j + F32_AHEAD, ra[j]);
-                    b.load(kt + j + F32_AHEAD, rb[j]);
-                }
-#pragma unroll
-                for (int k = 0; k < 16; k += 2) {
-                    const int kk = k + (lane >> 5), col = lane & 31;
-                    const float av = sa[kk * (BM + 4) + wm * 32 + col];
-#pragma unroll
-                    for (int fn = 0; fn < 2; ++fn)
-                        acc[fn] = __builtin_amdgcn_mfma_f32_32x32x2f32(av, sb[kk * (BN + 4) + wn * 64 + fn * 32 + col],
-                                                                       acc[fn], 0, 0, 0);
-                }
-            }
-        }
-    }
-};
-
-__global__ __launch_bounds__(256) void glu_f32_kernel(GluFwd p)
-{
-    using Core = F32Core<true, true, 32>;
-    __shared__ __attribute__((aligned(16))) float smem[2 * Core::SLOT];
-    const int tiles = p.MT * p.NT, split = blockIdx.x / tiles;
-    int mt, nt;
-    tile_coords(blockIdx.x - split * tiles, p.MT, p.NT, mt, nt);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int nk = p.d / 16, per = (nk + p.splits - 1) / p.splits, k0 = split * per;
-    Core core;
-    core.a.setup(p.x, p.x, p.d, mt * 64, p.T, p.d, p.d, tid);
-    core.b.setup(p.wg, p.wu, p.d, nt * 128, p.F, p.d, p.d, tid);
-    f32x16 acc[2];
-    core.run(k0, k0 + per < nk ? k0 + per : nk, smem, tid, acc);
-    const int n = nt * 64 + (wave & 1) * 32 + (lane & 31);
-#pragma unroll
-    for (int i = 0; i < 16; ++i) {
-        const int m = mt * 64 + (wave >> 1) * 32 + acc_row(i, lane);
-        if (m < p.T && n < p.F) {
-            const int64_t o = (int64_t)m * p.F + n;
-            const float g = acc[0][i], u = acc[1][i];
-            if (p.splits > 1) {
-                const int64_t part = (int64_t)p.T * p.F;
-                p.part[2 * split * part + o] = g;
-                p.part[(2 * split + 1) * part + o] = u;
-                continue;
-            }
-            if (p.g)
-                ((float *)p.g)[o] = g;
-            if (p.u)
-                ((float *)p.u)[o] = u;
-            ((float *)p.h)[o] = glu_act<false>(g, p.act) * u;
-        }
-    }
-}
-
-template <bool A_KC, bool B_KC> __global__ __launch_bounds__(256) void glu_mul_f32_kernel(GluMul p)
-{
-    using Core = F32Core<A_KC, B_KC, 0>;
-    __shared__ __attribute__((aligned(16))) float smem[2 * Core::SLOT];
-    const int tiles = p.MT * p.NT;
-    const int split = blockIdx.x / tiles;
-    int mt, nt;
-    tile_coords(blockIdx.x - split * tiles, p.MT, p.NT, mt, nt);
-    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
-    const int nk = (p.K + 15) >> 4, per = (nk + p.splits - 1) / p.splits;
-    const int k0 = split * per, k1 = k0 + per < nk ? k0 + per : nk;
-    Core core;
-    core.a.setup(p.a, p.a, p.lda / 4, mt * 64, p.M, p.K, nk, tid);
-    core.b.setup(p.b, p.b2, p.ldb / 4, nt * 128, p.N, p.K, p.k_turn >> 4, tid);
-    f32x16 acc[2];
-    core.run(k0, k1, smem, tid, acc);
-#pragma unroll
-    for (int fn = 0; fn < 2; ++fn)
-#pragma unroll
-        for (int i = 0; i < 16; ++i) {
-            const int m = mt * 64 + (wave >> 1) * 32 + acc_row(i, lane);
-            const int n = nt * 128 + (wave & 1) * 64 + fn * 32 + (lane & 31);
-            if (m >= p.M || n >= p.N)
-                continue;
-            if (p.splits > 1)
-                p.part[((int64_t)split * p.M + m) * p.N + n] = acc[fn][i];
-            else if (m < p.m_turn)
-                ((float *)p.out)[(int64_t)m * p.N + n] = acc[fn][i];
-            else
-                ((float *)p.out2)[(int64_t)(m - p.m_turn) * p.N + n] = acc[fn][i];
-        }
-}
-
 // ------------------------------------------------------------------ host
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// The workgroup tiles of the products, and what one stage of 64 K elements and the
-// rest of a tile cost on a CU (us, measured on products of many sizes with
-// `per_cu` tiles per CU): larger tiles move fewer bytes per product, smaller ones give every
-// CU work.  Splitting K does too; the parts are written and read once more.
+// The workgroup tiles of the products, and what they cost (us, measured on
+// products of many sizes): `stage` 64 K elements of a tile and `rest` the tile's
+// beginning and end, where every CU has its share of the tiles, and a tile that
+// has a CU to itself takes `alone` times that.  Larger tiles move fewer bytes per
+// product, smaller ones give every CU work.  Splitting K does too; the parts are
+// written and read once more.
+// bf16: a tile fills a CU.  fp32: 2 to 4 tiles run on one, the matrix unit alone
+// sets the time (157 TFLOP/s), and what matters is that no CU is left with one
+// tile more than the others: 1500 x 2048 x 2048 forward takes 188 us in tiles of
+// 64 x 128 (134 TFLOP/s) and 243 us in 128 x 128, 2000 x 512 x 4096 137 and 132;
+// dx of the first 203 us in 64 x 64 and 260 us in 128 x 128, dW 210 and 196.
 struct MulTile {
-    int bm, bn, per_cu;
-    double stage;
+    int bm, bn;
+    double stage, rest, alone;
 };
-constexpr MulTile MUL_TILES[] = {{256, 256, 1, 1.5}, {256, 128, 1, 0.88}, {128, 128, 1, 0.52}, {128, 64, 1, 0.36}};
-constexpr MulTile MUL_TILE_F32 = {64, 128, 2, 2.9};  // two on a CU
-constexpr double MUL_TILE_US = 5, MUL_JOIN_US = 4, MUL_PART_BYTES_PER_US = 4e6;
+constexpr MulTile MUL_TILES[] = {{256, 256, 1.5, 5, 1}, {256, 128, 0.88, 5, 1}, {128, 128, 0.52, 5, 1}, {128, 64, 0.36, 5, 1}};
+constexpr MulTile FWD_TILES_F32[] = {{128, 128, 3.7, 4, 1.05}, {64, 128, 1.9, 2, 1.1}};
+constexpr MulTile MUL_TILES_F32[] = {{128, 128, 3.8, 4, 1.05}, {64, 64, 1.0, 1.5, 1.3}};
+constexpr double MUL_JOIN_US = 4, MUL_PART_BYTES_PER_US = 4e6;
 constexpr int CUS = 256, MUL_MOST_SPLITS = 16;
 
 struct MulPlan {
@@ -612,7 +461,9 @@ static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, in
     for (int t = 0; t < tiles; ++t)
         for (int splits = 1; splits <= MUL_MOST_SPLITS && (splits == 1 || splits <= stages); splits *= 2) {
             const int64_t wgs = ceil_div(M, tile[t].bm) * ceil_div(N, tile[t].bn) * splits;
-            double us = (double)ceil_div(wgs, CUS * tile[t].per_cu) * ((double)ceil_div(stages, splits) * tile[t].stage + MUL_TILE_US);
+            double us = (double)ceil_div(wgs, CUS) * ((double)ceil_div(stages, splits) * tile[t].stage + tile[t].rest);
+            if (wgs <= CUS)
+                us *= tile[t].alone;
             if (splits > 1)
                 us += MUL_JOIN_US + (double)M * N * 8 * splits / MUL_PART_BYTES_PER_US;
             if (us < best_us) {
@@ -627,7 +478,7 @@ static MulPlan forward_plan(int vdtype, int T, int d, int F)
 {
     if (T <= GLU_FEW)
         return {0, 1};
-    return vdtype == 1 ? mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d) : mul_plan(&MUL_TILE_F32, 1, T, 2 * (int64_t)F, d);
+    return vdtype == 1 ? mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d) : mul_plan(FWD_TILES_F32, 2, T, 2 * (int64_t)F, d);
 }
 
 size_t glu_forward_ws(int T, int d, int F, int vdtype)
@@ -659,26 +510,27 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
     }
     const MulPlan plan = forward_plan(vdtype, p.T, p.d, p.F);
     p.splits = plan.splits;
+    const MulTile &tile = (vdtype == 1 ? MUL_TILES : FWD_TILES_F32)[plan.tile];
+    p.tiles = dg_tiles(ceil_div(p.T, tile.bm), ceil_div(p.F, tile.bn / 2), p.splits);
+    const dim3 grid((unsigned)dg_grid(p.tiles));
     if (vdtype == 0) {
-        p.MT = (int)ceil_div(p.T, 64);
-        p.NT = (int)ceil_div(p.F, 64);
-        glu_f32_kernel<<<dim3(p.MT * p.NT * p.splits), dim3(256), 0, s>>>(p);
+        if (plan.tile == 0)
+            glu_kernel<float, 128, 128, 32, 64, 2><<<grid, dim3(512), 0, s>>>(p);
+        else
+            glu_kernel<float, 64, 128, 32, 64, 2><<<grid, dim3(256), 0, s>>>(p);
     } else {
-        const MulTile &tile = MUL_TILES[plan.tile];
-        p.tiles = dg_tiles(ceil_div(p.T, tile.bm), ceil_div(p.F, tile.bn / 2), p.splits);
-        const dim3 grid((unsigned)dg_grid(p.tiles));
         switch (plan.tile) {
         case 0:
-            glu_kernel<256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(p);
+            glu_kernel<__bf16, 256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(p);
             break;
         case 1:
-            glu_kernel<256, 128, 64, 64, 3><<<grid, dim3(512), 0, s>>>(p);
+            glu_kernel<__bf16, 256, 128, 64, 64, 3><<<grid, dim3(512), 0, s>>>(p);
             break;
         case 2:
-            glu_kernel<128, 128, 32, 64, 4><<<grid, dim3(512), 0, s>>>(p);
+            glu_kernel<__bf16, 128, 128, 32, 64, 4><<<grid, dim3(512), 0, s>>>(p);
             break;
         default:
-            glu_kernel<128, 64, 32, 64, 3><<<grid, dim3(256), 0, s>>>(p);
+            glu_kernel<__bf16, 128, 64, 32, 64, 3><<<grid, dim3(256), 0, s>>>(p);
             break;
         }
     }
@@ -697,7 +549,7 @@ static MulPlan backward_plan(int vdtype, int64_t M, int64_t N, int64_t K)
 {
     if (M == 0 || N == 0 || K == 0)
         return {0, 1};
-    return vdtype == 1 ? mul_plan(MUL_TILES, 3, M, N, K) : mul_plan(&MUL_TILE_F32, 1, M, N, K);
+    return vdtype == 1 ? mul_plan(MUL_TILES, 3, M, N, K) : mul_plan(MUL_TILES_F32, 2, M, N, K);
 }
 
 static size_t up256_(size_t b) { return (b + 255) & ~(size_t)255; }
@@ -718,20 +570,21 @@ template <bool A_KC, bool B_KC> static hipError_t mul_go(int vdtype, GluMul p, h
 {
     const MulPlan plan = backward_plan(vdtype, p.M, p.N, p.K);
     p.splits = plan.splits;
+    const MulTile &tile = (vdtype == 1 ? MUL_TILES : MUL_TILES_F32)[plan.tile];
+    p.tiles = dg_tiles(ceil_div(p.M, tile.bm), ceil_div(p.N, tile.bn), p.splits);
+    const dim3 grid((unsigned)dg_grid(p.tiles));
     if (vdtype == 0) {
-        p.MT = (int)ceil_div(p.M, 64);
-        p.NT = (int)ceil_div(p.N, 128);
-        glu_mul_f32_kernel<A_KC, B_KC><<<dim3(p.MT * p.NT * p.splits), dim3(256), 0, s>>>(p);
-    } else {
-        const MulTile &tile = MUL_TILES[plan.tile];
-        p.tiles = dg_tiles(ceil_div(p.M, tile.bm), ceil_div(p.N, tile.bn), p.splits);
-        const dim3 grid((unsigned)dg_grid(p.tiles));
         if (plan.tile == 0)
-            glu_mul_kernel<256, 256, 64, 128, 2, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
-        else if (plan.tile == 1)
-            glu_mul_kernel<256, 128, 64, 64, 3, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+            glu_mul_kernel<float, 128, 128, 32, 64, 2, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
         else
-            glu_mul_kernel<128, 128, 32, 64, 4, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+            glu_mul_kernel<float, 64, 64, 32, 32, 3, A_KC, B_KC><<<grid, dim3(256), 0, s>>>(p);
+    } else {
+        if (plan.tile == 0)
+            glu_mul_kernel<__bf16, 256, 256, 64, 128, 2, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+        else if (plan.tile == 1)
+            glu_mul_kernel<__bf16, 256, 128, 64, 64, 3, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+        else
+            glu_mul_kernel<__bf16, 128, 128, 32, 64, 4, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
     }
     hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
