@@ -39,51 +39,40 @@ template <int N> __device__ __forceinline__ void dg_wait()
 }
 
 // Tiles to workgroups.  Workgroup g runs on XCD g % 8, and each XCD has an L2 of
-// its own: the 8 XCDs are xs groups that share out the K splits, and within a
-// group the tile grid is cut into rectangles of `rows` x `cols` tiles, xm of them
-// down, one per XCD.  A rectangle is walked in bands of 8 tile rows, so that the
-// 32 workgroups an XCD runs at once form a block of 8 x 4 tiles of one split and
-// read 12 operand tiles instead of up to 33 (1003 x 1024, K = 8192 in 4 splits:
-// 30 us with all splits on every XCD).
+// its own: the tiles of all K splits stand in one row, split after split, a
+// split's in bands of `h` tile rows walked column by column, and each XCD takes an
+// eighth of that row.  The 32 workgroups an XCD runs at once then form a block
+// of 8 x 4 tiles of one split and read 12 operand tiles instead of up to 33
+// (1003 x 1024, K = 8192 in 4 splits: 29 us, and 30 us with all splits on every
+// XCD), and no XCD has a tile more than its share.
 struct DgTiles {
-    int MT, NT, splits, xs, xm, rows, cols;
+    int MT, NT, splits, h, per;  // per: tiles of an XCD
 };
 
-// Tile (mt, nt) and K split of workgroup g.  False: a rectangle's place past the
-// grid's edge.
+// Tile (mt, nt) and K split of workgroup g.  False: no tile is left for it.
 __device__ __forceinline__ bool dg_tile(const DgTiles &t, int g, int &mt, int &nt, int &split)
 {
-    const int xcd = g & 7, xr = xcd / t.xs, per = t.rows * t.cols;
-    int s = g >> 3;
-    split = s / per;
-    s -= split * per;
-    split = split * t.xs + xcd % t.xs;
-    const int band = s / (8 * t.cols), r = s - band * 8 * t.cols;
-    const int left = t.rows - band * 8, h = left < 8 ? left : 8;
-    mt = xr % t.xm * t.rows + band * 8 + r % h;
-    nt = xr / t.xm * t.cols + r / h;
-    return mt < t.MT && nt < t.NT;
+    const int at = (g & 7) * t.per + (g >> 3), tiles = t.MT * t.NT;
+    split = at / tiles;
+    const int r = at - split * tiles, band = r / (t.h * t.NT), q = r - band * t.h * t.NT;
+    const int left = t.MT - band * t.h, h = left < t.h ? left : t.h;
+    nt = q / h;
+    mt = band * t.h + q - nt * h;
+    return split < t.splits;
 }
 
-// The cut with the fewest workgroups per XCD (places past the edge idle), then
-// the fewest operand tiles per tile in flight.
+// Bands of equal height, up to the height of the block that an XCD runs at once
+// (twice as high as wide).
 inline DgTiles dg_tiles(int64_t MT, int64_t NT, int splits)
 {
-    DgTiles best{};
-    double best_cost = 1e300;
-    for (int xs = 1; xs <= 8 && splits % xs == 0; xs *= 2)
-        for (int xm = 1; xm * xs <= 8; xm *= 2) {
-            const int64_t xn = 8 / xs / xm, rows = (MT + xm - 1) / xm, cols = (NT + xn - 1) / xn;
-            const double h = rows < 8 ? rows : 8, w = cols < 32 / h ? cols : (int64_t)(32 / h);
-            const double cost = (double)(rows * cols * (splits / xs)) + (h + w) / (h * w) / 4;
-            if (cost < best_cost) {
-                best_cost = cost;
-                best = DgTiles{(int)MT, (int)NT, splits, xs, xm, (int)rows, (int)cols};
-            }
-        }
-    return best;
+    const int64_t per = (MT * NT * splits + 7) / 8;
+    int64_t most = 1;
+    while (most < 8 && most * most < 2 * per)
+        ++most;
+    const int64_t bands = (MT + most - 1) / most;
+    return DgTiles{(int)MT, (int)NT, splits, (int)((MT + bands - 1) / bands), (int)per};
 }
-inline int64_t dg_grid(const DgTiles &t) { return (int64_t)8 * t.rows * t.cols * (t.splits / t.xs); }
+inline int64_t dg_grid(const DgTiles &t) { return (int64_t)8 * t.per; }
 
 // A transposing LDS read.  `restrict` gives the instruction alias information
 // of its own: without any, the compiler waits for every global->LDS copy in
