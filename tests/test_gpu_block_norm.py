@@ -136,6 +136,15 @@ def test_gate_spans(gpu_lib, T, span):
     _check(gpu_lib, _case(T, 72, span=span))
 
 
+@pytest.mark.parametrize("d", [1, 4, 15, 16, 17, 32, 33, 64, 100, 128, 129, 160, 256, 257])
+@pytest.mark.parametrize("T,span", [(1, 0), (3, 1), (50, 3), (61, 16), (64, 64), (3000, 17), (4097, 1), (20011, 20011),
+                                    (9001, 4500)])
+def test_narrow_rows(gpu_lib, d, T, span):
+    """Rows that share a wave: their own sums, columns past d, the last rows of a wave, gate rows that end inside one."""
+    say(f"case block norm narrow T={T} d={d} span={span}")
+    _check(gpu_lib, _case(T, d, kind="layer" if d % 3 else "rms", bias=T % 2 == 1, span=span, y="bfloat16"))
+
+
 @pytest.mark.parametrize("offset", [1, 2, 8])
 def test_alignment(gpu_lib, offset):
     say(f"case block norm offset {offset}")

@@ -33,6 +33,7 @@ struct BnArgs {
 
 hipError_t launch_block_norm(const BnArgs &a, bool layer, bool vec, hipStream_t s);
 hipError_t launch_block_norm_backward(const BnArgs &a, bool layer, bool vec, hipStream_t s);
-int block_norm_groups(int T, int d);
+int block_norm_groups(int T, int d);  // row groups of the backward pass
+int block_norm_rows(int T, int d);    // rows of each, none of them empty
 
 }  // namespace twell

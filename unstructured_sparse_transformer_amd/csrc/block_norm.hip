@@ -15,10 +15,12 @@
 // The statistics come again from the rows that the backward pass reads anyway.
 //
 // Bound by memory: every row of every tensor moves once.  A row is held in
-// registers by NT threads of 8 elements (NT = 64 to 1024 by the width), so a
+// registers by NT threads of 8 elements (NT = 2 to 1024 by the width), so a
 // mean and a variance are two passes over registers, not over memory.  All
-// sums are fp32: per thread, then over the wave by DPP, then over the waves
-// through LDS.
+// sums are fp32: per thread, then over the row's lanes by DPP, then over the
+// waves through LDS.  8192 x 2048: forward 26 us in bf16 (134 MB, 5.2 TB/s),
+// backward 52 us in bf16 (201 MB) and 88 us with fp32 streams (403 MB, 4.6 TB/s),
+// 6 us of them the second launch's sums of the partial rows.
 #include "block_norm.h"
 #include "twell_device.h"
 #include "wave_ops.h"
@@ -186,13 +188,43 @@ __device__ __forceinline__ void bn_weights(BnTensor t, int d, int tid, float non
     }
 }
 
+// Sum over a row's NT < 64 lanes: pairs, quads, halves of 16 and 16 lanes by DPP,
+// the two 16s of a row of 32 lanes by a shuffle.  The same bits in every lane.
+template <int NT> __device__ __forceinline__ float bn_lanes_sum(float v)
+{
+    auto dpp = [](float x, auto ctrl) {
+        return __int_as_float(__builtin_amdgcn_update_dpp(0, __float_as_int(x), decltype(ctrl)::value, 0xf, 0xf, false));
+    };
+    v += dpp(v, std::integral_constant<int, 0xB1>{});  // quad_perm 1 0 3 2
+    if constexpr (NT >= 4)
+        v += dpp(v, std::integral_constant<int, 0x4E>{});  // quad_perm 2 3 0 1
+    if constexpr (NT >= 8)
+        v += dpp(v, std::integral_constant<int, 0x141>{});  // row_half_mirror
+    if constexpr (NT >= 16)
+        v += dpp(v, std::integral_constant<int, 0x140>{});  // row_mirror
+    if constexpr (NT >= 32)
+        v += __shfl_xor(v, 16, 64);
+    return v;
+}
+
+// Rows that a wave holds side by side, and sums over them, column by column.
+template <int NT> constexpr int bn_wave_rows() { return NT < 64 ? 64 / NT : 1; }
+template <int NT> __device__ __forceinline__ void bn_rows_sum(float (&v)[8])
+{
+#pragma unroll
+    for (int o = NT; o < 64; o *= 2)
+#pragma unroll
+        for (int e = 0; e < 8; ++e)
+            v[e] += __shfl_xor(v[e], o, 64);
+}
+
 // Sums of N values over the NT threads of a row, the same in every thread.
 // `slot` alternates between two LDS areas, so one barrier a sum is enough.
 template <int NT, int N> __device__ __forceinline__ void row_sums(float (&v)[N], float *red, int &slot)
 {
 #pragma unroll
     for (int i = 0; i < N; ++i)
-        v[i] = wave_sum(v[i]);
+        v[i] = NT < 64 ? bn_lanes_sum<NT < 64 ? NT : 2>(v[i]) : wave_sum(v[i]);
     if constexpr (NT > 64) {
         constexpr int NW = NT / 64;
         float *r = red + slot * (NW * 2);
@@ -268,9 +300,9 @@ __device__ __forceinline__ void bn_hat_grad(float (&g)[8], const float (&hat)[8]
         g[e] = (g[e] - m1 - hat[e] * m0) * rstd;
 }
 
-// Rows of NT = 64 threads share a workgroup of 4 (no LDS); wider rows have a
-// workgroup each.
-template <int NT> constexpr int bn_threads() { return NT == 64 ? 256 : NT; }
+// Rows of up to 64 threads share a workgroup of 256 (no LDS), narrow ones a wave
+// too; wider rows have a workgroup each.
+template <int NT> constexpr int bn_threads() { return NT <= 64 ? 256 : NT; }
 
 template <bool LAYER, BnLay L, int NT>
 __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_kernel(BnArgs a)
@@ -281,8 +313,9 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_kernel(BnArgs a)
     const int tid = threadIdx.x % NT;
     const int64_t step = (int64_t)gridDim.x * RPW;
     // (a wave's threads have the same row: known as such, its address is scalar)
-    int64_t row = (int64_t)blockIdx.x * RPW + (RPW > 1 ? __builtin_amdgcn_readfirstlane(threadIdx.x / NT) : 0);
-    if (row >= a.T)  // whole waves: a row is a multiple of 64 threads
+    const int first = RPW > 1 ? (int)threadIdx.x / NT : 0;
+    int64_t row = (int64_t)blockIdx.x * RPW + (NT == 64 ? __builtin_amdgcn_readfirstlane(first) : first);
+    if (row >= a.T)  // whole rows' threads: the sums stay within them
         return;
     const bool block = a.y.p, next = a.n.p;
     Raw8 rr{}, ry{}, rg{};
@@ -329,8 +362,9 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_kernel(BnArgs a)
     }
 }
 
-// Row group b (the NT threads of a row; 4 of them in a workgroup when NT = 64)
-// takes the rows [b rows, (b + 1) rows).  Its sums over those rows stay in
+// Row group b (the NT threads of a row, or a wave of several rows; 4 waves in a
+// workgroup when NT <= 64) takes the rows [b rows, (b + 1) rows), a wave of several
+// that many at a step.  Its sums over those rows stay in
 // registers and leave as one partial row per vector.  A gate row whose rows all
 // lie in the group is finished here; one cut at the group's first row leaves in
 // slot 4, one cut at its last row only in slot 5.
@@ -340,7 +374,9 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_backward_kernel(B
     __shared__ float red[NT > 64 ? 4 * (NT / 64) : 1];
     int slot = 0;
     const int tid = threadIdx.x % NT;
-    const int grp = NT == 64 ? (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : (int)blockIdx.x;
+    constexpr int K = bn_wave_rows<NT>();
+    const int seg = K > 1 ? (int)(threadIdx.x & 63) / NT : 0;
+    const int grp = NT <= 64 ? (int)blockIdx.x * 4 + __builtin_amdgcn_readfirstlane(threadIdx.x / 64) : (int)blockIdx.x;
     if (grp >= a.groups)
         return;
     const int64_t r0 = (int64_t)grp * a.rows;
@@ -356,89 +392,120 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_backward_kernel(B
         for (int k = 0; k < 4; ++k)
             acc[k][e] = 0.f;
     }
-    int64_t group = a.gate_span ? (int)r0 / a.gate_span : 0;
-    for (int64_t row = r0; row < r1; ++row) {
-        Raw8 ro{}, rd{}, rn{}, ry{}, rg{};
-        if (a.dout.p)
-            rd = bn_load<L, NT, true>(a.dout, row, a.d, tid);
-        if (a.dn.p) {
-            ro = bn_load<L, NT, true>(a.res, row, a.d, tid);
-            rn = bn_load<L, NT, true>(a.dn, row, a.d, tid);
-        }
-        if (a.y.p)
-            ry = bn_load<L, NT, true>(a.y, row, a.d, tid);
-        if (a.gate_span)
-            rg = bn_load<L, NT>(a.gate, (int)row / a.gate_span, a.d, tid);
-        float dr[8];
-        bn_values(rd, a.dout.bf16, dr);
-        if (a.dn.p) {
-            float hat[8], dn[8];
-            bn_values(ro, a.res.bf16, hat);
-            bn_values(rn, a.dn.bf16, dn);
-            const float rstd = bn_hat<LAYER, L, NT>(hat, a.d, tid, a.eps, red, slot);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc[2][e] += dn[e] * hat[e];
-                if constexpr (BIAS)
-                    acc[3][e] += dn[e];
-                dn[e] *= wpre[e];
-            }
-            bn_hat_grad<LAYER, L, NT>(dn, hat, rstd, a.d, tid, red, slot);
+    int64_t group = a.gate_span ? (int)r0 / a.gate_span : 0;  // the gate row that ag belongs to
+    for (int64_t base = r0; base < r1; base += K) {
+        const int64_t row = base + seg;
+        float gp[8];  // this row's part of the gate's gradient, of rows side by side
+        if constexpr (K > 1) {
 #pragma unroll
             for (int e = 0; e < 8; ++e)
-                dr[e] += dn[e];
+                gp[e] = 0.f;
         }
-        bn_store<L, NT>(a.dres, row, a.d, tid, dr);
-        if (!a.y.p)
-            continue;
-        float hat[8], rstd = 1.f;
-        bn_values(ry, a.y.bf16, hat);
-        if (a.post)
-            rstd = bn_hat<LAYER, L, NT>(hat, a.d, tid, a.eps, red, slot);
-#pragma unroll
-        for (int e = 0; e < 8; ++e)
-            dr[e] = bn_col<L, NT>(tid, e) < a.d ? dr[e] * a.alpha : 0.f;
-        if (a.gate_span) {
-            float g[8];
-            bn_values(rg, a.gate.bf16, g);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                ag[e] += dr[e] * (a.post ? hat[e] * wpost[e] + bpost[e] : hat[e]);
-                dr[e] *= g[e];
-            }
-            const int64_t next = (int)(row + 1) / a.gate_span;
-            if (next != group || row + 1 == r1) {
-                const bool head = group * a.gate_span < r0;
-                const bool tail = (group + 1) * a.gate_span > r1 && r1 < a.T;
-                if (!head && !tail) {
-                    bn_store<L, NT>(a.dgate, group, a.d, tid, ag);
-                } else {
-                    const BnTensor t{a.part + ((int64_t)(head ? 4 : 5) * a.groups + grp) * a.d, 0};
-                    bn_store<L, NT>(t, 0, a.d, tid, ag);
+        if (row < r1)
+            [&] {
+                Raw8 ro{}, rd{}, rn{}, ry{}, rg{};
+                if (a.dout.p)
+                    rd = bn_load<L, NT, true>(a.dout, row, a.d, tid);
+                if (a.dn.p) {
+                    ro = bn_load<L, NT, true>(a.res, row, a.d, tid);
+                    rn = bn_load<L, NT, true>(a.dn, row, a.d, tid);
                 }
-                group = next;
+                if (a.y.p)
+                    ry = bn_load<L, NT, true>(a.y, row, a.d, tid);
+                if (a.gate_span)
+                    rg = bn_load<L, NT>(a.gate, (int)row / a.gate_span, a.d, tid);
+                float dr[8];
+                bn_values(rd, a.dout.bf16, dr);
+                if (a.dn.p) {
+                    float hat[8], dn[8];
+                    bn_values(ro, a.res.bf16, hat);
+                    bn_values(rn, a.dn.bf16, dn);
+                    const float rstd = bn_hat<LAYER, L, NT>(hat, a.d, tid, a.eps, red, slot);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        acc[2][e] += dn[e] * hat[e];
+                        if constexpr (BIAS)
+                            acc[3][e] += dn[e];
+                        dn[e] *= wpre[e];
+                    }
+                    bn_hat_grad<LAYER, L, NT>(dn, hat, rstd, a.d, tid, red, slot);
+#pragma unroll
+                    for (int e = 0; e < 8; ++e)
+                        dr[e] += dn[e];
+                }
+                bn_store<L, NT>(a.dres, row, a.d, tid, dr);
+                if (!a.y.p)
+                    return;
+                float hat[8], rstd = 1.f;
+                bn_values(ry, a.y.bf16, hat);
+                if (a.post)
+                    rstd = bn_hat<LAYER, L, NT>(hat, a.d, tid, a.eps, red, slot);
 #pragma unroll
                 for (int e = 0; e < 8; ++e)
-                    ag[e] = 0.f;
-            }
-        }
-        if (a.post) {
+                    dr[e] = bn_col<L, NT>(tid, e) < a.d ? dr[e] * a.alpha : 0.f;
+                if (a.gate_span) {
+                    float g[8];
+                    bn_values(rg, a.gate.bf16, g);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                acc[0][e] += dr[e] * hat[e];
-                if constexpr (BIAS)
-                    acc[1][e] += dr[e];
-                dr[e] *= wpost[e];
-            }
-            bn_hat_grad<LAYER, L, NT>(dr, hat, rstd, a.d, tid, red, slot);
+                    for (int e = 0; e < 8; ++e) {
+                        const float p = dr[e] * (a.post ? hat[e] * wpost[e] + bpost[e] : hat[e]);
+                        if constexpr (K > 1)
+                            gp[e] = p;
+                        else
+                            ag[e] += p;
+                        dr[e] *= g[e];
+                    }
+                }
+                if (a.post) {
+#pragma unroll
+                    for (int e = 0; e < 8; ++e) {
+                        acc[0][e] += dr[e] * hat[e];
+                        if constexpr (BIAS)
+                            acc[1][e] += dr[e];
+                        dr[e] *= wpost[e];
+                    }
+                    bn_hat_grad<LAYER, L, NT>(dr, hat, rstd, a.d, tid, red, slot);
+                }
+                bn_store<L, NT>(a.dy, row, a.d, tid, dr);
+            }();
+        if (!a.gate_span)
+            continue;
+        if (K > 1 && a.gate_span == 1) {
+            if (row < r1)
+                bn_store<L, NT>(a.dgate, row, a.d, tid, gp);
+            continue;
         }
-        bn_store<L, NT>(a.dy, row, a.d, tid, dr);
+        // the gate rows that these rows belong to, each left when its last row in the group has been added
+        const int64_t end = base + K < r1 ? base + K : r1;
+        const int64_t stop = end < r1 ? (int)end / a.gate_span : (int64_t)(int)(r1 - 1) / a.gate_span + 1;
+        const int mine = K > 1 ? (int)row / a.gate_span : 0;
+        while (true) {
+            if constexpr (K > 1) {
+#pragma unroll
+                for (int e = 0; e < 8; ++e)
+                    ag[e] += mine == group ? gp[e] : 0.f;
+            }
+            if (group == stop)
+                break;
+            bn_rows_sum<NT>(ag);
+            const bool head = group * a.gate_span < r0;
+            const bool tail = (group + 1) * a.gate_span > r1 && r1 < a.T;
+            const BnTensor t = head || tail ? BnTensor{a.part + ((int64_t)(head ? 4 : 5) * a.groups + grp) * a.d, 0} : a.dgate;
+            if (seg == 0)
+                bn_store<L, NT>(t, head || tail ? 0 : group, a.d, tid, ag);
+#pragma unroll
+            for (int e = 0; e < 8; ++e)
+                ag[e] = 0.f;
+            ++group;
+        }
     }
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (a.dw[k]) {
             const BnTensor t{a.part + ((int64_t)k * a.groups + grp) * a.d, 0};
-            bn_store<L, NT>(t, 0, a.d, tid, acc[k]);
+            bn_rows_sum<NT>(acc[k]);
+            if (seg == 0)
+                bn_store<L, NT>(t, 0, a.d, tid, acc[k]);
         }
 }
 
@@ -524,20 +591,36 @@ __global__ __launch_bounds__(256) void block_norm_reduce_kernel(BnArgs a)
     }
 }
 
+// The threads of a row, and how many rows a wave holds at once.  Narrow rows side
+// by side: 65536 rows of 64 take 8 us forward (29 us with a wave for each) and 34
+// backward (95), 262144 rows of 16 take 8 (101) and 36 (302).
+static int bn_row_threads(int d)
+{
+    return d <= 16 ? 2 : d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : d <= 256 ? 32 : d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024;
+}
+static int bn_rows_at_once(int d) { return bn_row_threads(d) < 64 ? 64 / bn_row_threads(d) : 1; }
+
 // Row groups of the backward pass: about three workgroups of 256 threads per CU,
 // as many as its registers allow; each adds up its own rows' weight gradients.
-static int bn_row_threads(int d) { return d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024; }
-
 int block_norm_groups(int T, int d)
 {
-    const int most = BN_BWD_THREADS / bn_row_threads(d);
-    int rows = (T + most - 1) / most;
-    // few rows: up to 4 of them a group, until there is a workgroup of 256 threads per CU; each group costs a partial
+    const int k = bn_rows_at_once(d), threads = bn_row_threads(d) * k;
+    const int steps = (T + k - 1) / k;
+    const int most = BN_BWD_THREADS / threads;
+    int per = (steps + most - 1) / most;
+    // few rows: up to 4 steps a group, until there is a workgroup of 256 threads per CU; each group costs a partial
     // row per vector (777 x 1001: 28 us at 195 groups, 24 at 389, 28 at 777)
-    const int full = 256 * 256 / bn_row_threads(d);
-    const int few = (T + full - 1) / full < 4 ? (T + full - 1) / full : 4;
-    rows = rows > few ? rows : few;
-    return rows > 0 ? (T + rows - 1) / rows : 0;
+    const int full = 256 * 256 / threads;
+    const int few = (steps + full - 1) / full < 4 ? (steps + full - 1) / full : 4;
+    per = per > few ? per : few;
+    return per > 0 ? (steps + per - 1) / per : 0;
+}
+
+// Whole steps (that a wave holds at once), so that (groups - 1) of them end before row T.
+int block_norm_rows(int T, int d)
+{
+    const int groups = block_norm_groups(T, d), k = bn_rows_at_once(d);
+    return groups ? ((T + groups - 1) / groups + k - 1) / k * k : 0;
 }
 
 // Workgroups of the forward pass: enough to fill the GPU; rows beyond that come
@@ -550,7 +633,8 @@ template <bool LAYER, BnLay L> static hipError_t bn_go(const BnArgs &a, bool bac
         constexpr int NT = decltype(nt)::value;
         constexpr int threads = bn_threads<NT>(), per = threads / NT, most = BN_FWD_THREADS / threads;
         if (backward) {
-            const dim3 grid((a.groups + per - 1) / per);
+            constexpr int groups = NT <= 64 ? 4 : 1;
+            const dim3 grid((a.groups + groups - 1) / groups);
             if (a.dw[1] || a.dw[3])
                 block_norm_backward_kernel<LAYER, true, L, NT><<<grid, dim3(threads), 0, s>>>(a);
             else
@@ -562,6 +646,16 @@ template <bool LAYER, BnLay L> static hipError_t bn_go(const BnArgs &a, bool bac
         return hipGetLastError();
     };
     switch (bn_row_threads(a.d)) {
+    case 2:
+        return go(std::integral_constant<int, 2>{});
+    case 4:
+        return go(std::integral_constant<int, 4>{});
+    case 8:
+        return go(std::integral_constant<int, 8>{});
+    case 16:
+        return go(std::integral_constant<int, 16>{});
+    case 32:
+        return go(std::integral_constant<int, 32>{});
     case 64:
         return go(std::integral_constant<int, 64>{});
     case 128:

@@ -284,7 +284,7 @@ int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, con
     a.dw[3] = db_pre;
     a.part = static_cast<float *>(workspace);
     a.groups = twell::block_norm_groups(bn->T, bn->d);
-    a.rows = a.groups ? (bn->T + a.groups - 1) / a.groups : 0;
+    a.rows = twell::block_norm_rows(bn->T, bn->d);
     return hip_status(twell::launch_block_norm_backward(a, bn->kind == TWELL_NORM_LAYER, bn_wide(a),
                                                         static_cast<hipStream_t>(stream)));
 }
