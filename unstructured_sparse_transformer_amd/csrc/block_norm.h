@@ -15,6 +15,9 @@ struct BnTensor {
     int bf16;
 };
 
+// Elements from one partial row to the next: whole pieces of 16 bytes.
+__host__ __device__ inline int64_t bn_pitch(int d) { return (d + 3) & ~3; }
+
 struct BnArgs {
     int T, d;
     int post;            // a norm after the block
@@ -25,7 +28,7 @@ struct BnArgs {
     // backward
     BnTensor dout, dn, dres, dy, dgate;
     float *dw[4];        // dw_post, db_post, dw_pre, db_pre (or NULL)
-    float *part;         // [6][groups][d]: the four vectors, then the gate rows cut at a group's first and last row
+    float *part;         // [6][groups][bn_pitch(d)]: the four vectors, then the gate rows cut at a group's first and last row
     int groups;          // row groups of the backward pass
     int rows;            // rows of a group
     int cuts;            // gate rows or group boundaries to look for cut gate rows at

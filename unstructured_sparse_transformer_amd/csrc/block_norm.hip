@@ -550,7 +550,7 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_backward_kernel(B
             bn_rows_sum<NT>(ag);
             const bool head = group * a.gate_span < r0;
             const bool tail = (group + 1) * a.gate_span > r1 && r1 < a.T;
-            const BnTensor t = head || tail ? BnTensor{a.part + ((int64_t)(head ? 4 : 5) * a.groups + grp) * a.d, 0} : a.dgate;
+            const BnTensor t = head || tail ? BnTensor{a.part + ((int64_t)(head ? 4 : 5) * a.groups + grp) * bn_pitch(a.d), 0} : a.dgate;
             if (seg == 0)
                 bn_store<L, NT>(t, head || tail ? 0 : group, a.d, tid, ag);
 #pragma unroll
@@ -562,7 +562,7 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_backward_kernel(B
 #pragma unroll
     for (int k = 0; k < 4; ++k)
         if (a.dw[k]) {
-            const BnTensor t{a.part + ((int64_t)k * a.groups + grp) * a.d, 0};
+            const BnTensor t{a.part + ((int64_t)k * a.groups + grp) * bn_pitch(a.d), 0};
             bn_rows_sum<NT>(acc[k]);
             if (seg == 0)
                 bn_store<L, NT>(t, 0, a.d, tid, acc[k]);
@@ -570,8 +570,7 @@ __global__ __launch_bounds__(bn_threads<NT>()) void block_norm_backward_kernel(B
 }
 
 // Column sums over the row groups' partial rows in a fixed order: 32 columns a
-// workgroup, 32 threads of 4 columns each for them (8 of one column where d is no
-// multiple of 4).  blockIdx.y < 4: a weight gradient.  Above: the gate rows that
+// workgroup, 32 threads of 4 columns each for them.  blockIdx.y < 4: a weight gradient.  Above: the gate rows that
 // are cut between groups, found from the gate rows or from the groups' boundaries,
 // whichever are fewer (a.cuts of them, dealt out over the rest of grid y).
 __global__ __launch_bounds__(256) void block_norm_reduce_kernel(BnArgs a)
@@ -581,33 +580,20 @@ __global__ __launch_bounds__(256) void block_norm_reduce_kernel(BnArgs a)
     auto column = [&](int kind0, int b0, int kind, int b1) {  // partial rows b0 (of kind0), then b0 + 1 .. b1 - 1
         const int n = b1 - b0;
         __syncthreads();
-        if (a.d % 4 == 0) {
-            const int c4 = (threadIdx.x & 7) * 4, s4 = threadIdx.x >> 3;
-            float4 s = make_float4(0.f, 0.f, 0.f, 0.f);
-            if (blockIdx.x * 32 + c4 < a.d) {
+        const int c4 = (threadIdx.x & 7) * 4, s4 = threadIdx.x >> 3;
+        float4 p = make_float4(0.f, 0.f, 0.f, 0.f);
+        if (blockIdx.x * 32 + c4 < a.d) {
 #pragma unroll 8
-                for (int i = s4; i < n; i += 32) {
-                    const float4 v = *reinterpret_cast<const float4 *>(
-                        a.part + ((int64_t)(i == 0 ? kind0 : kind) * a.groups + b0 + i) * a.d + blockIdx.x * 32 + c4);
-                    s.x += v.x;
-                    s.y += v.y;
-                    s.z += v.z;
-                    s.w += v.w;
-                }
+            for (int i = s4; i < n; i += 32) {
+                const float4 v = *reinterpret_cast<const float4 *>(
+                    a.part + ((int64_t)(i == 0 ? kind0 : kind) * a.groups + b0 + i) * bn_pitch(a.d) + blockIdx.x * 32 + c4);
+                p.x += v.x;
+                p.y += v.y;
+                p.z += v.z;
+                p.w += v.w;
             }
-            *reinterpret_cast<float4 *>(&red[s4][c4]) = s;
-        } else {
-            float s = 0.f;
-            if (c < a.d) {
-#pragma unroll 8
-                for (int i = seg; i < n; i += 8)
-                    s += a.part[((int64_t)(i == 0 ? kind0 : kind) * a.groups + b0 + i) * a.d + c];
-            }
-            red[seg][threadIdx.x & 31] = s;
-#pragma unroll
-            for (int k = 8; k < 32; k += 8)
-                red[seg + k][threadIdx.x & 31] = 0.f;
         }
+        *reinterpret_cast<float4 *>(&red[s4][c4]) = p;
         __syncthreads();
         float s = 0.f;
         if (seg == 0) {

@@ -236,7 +236,7 @@ size_t twell_block_norm_workspace_bytes(int32_t T, int32_t d)
 {
     if (T < 0 || T > MOST_ROWS || d < 1 || d > twell::BN_MAX_D)
         return 0;
-    return (size_t)6 * twell::block_norm_groups(T, d) * d * sizeof(float);
+    return (size_t)6 * twell::block_norm_groups(T, d) * twell::bn_pitch(d) * sizeof(float);
 }
 
 int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, const void *y, const void *dout,
