@@ -758,7 +758,10 @@ hipError_t launch_block_norm_backward(const BnArgs &a, bool layer, bool vec, hip
     r.cuts = !cut ? 0 : a.gate_span >= a.rows ? (int)(((int64_t)a.T + a.gate_span - 1) / a.gate_span) : a.groups - 1;
     if (!cut && !a.dw[0] && !a.dw[1] && !a.dw[2] && !a.dw[3])
         return hipSuccess;
-    block_norm_reduce_kernel<<<dim3((a.d + 31) / 32, 4 + (r.cuts < 32 ? r.cuts : 32)), dim3(256), 0, s>>>(r);
+    // cut gate rows are dealt out over about 8 workgroups per CU (131072 x 32, 20 rows a gate row: 35 us, over 32
+    // of them 75)
+    const int cols = (a.d + 31) / 32, most = (2048 + cols - 1) / cols;
+    block_norm_reduce_kernel<<<dim3(cols, 4 + (r.cuts < most ? r.cuts : most)), dim3(256), 0, s>>>(r);
     return hipGetLastError();
 }
 
