@@ -200,8 +200,8 @@ int twell_glu_backward(const void *x, const void *wg_t, const void *wu_t, const 
     a.dx = dx;
     a.dwg = dwg;
     a.dwu = dwu;
-    a.dgu = static_cast<char *>(workspace) + w.dgu;
-    a.part = reinterpret_cast<float *>(static_cast<char *>(workspace) + w.part);
+    a.dgu = workspace;
+    a.ws = w;
     return hip_status(twell::launch_glu_backward(vdtype, a, static_cast<hipStream_t>(stream)));
 }
 

@@ -22,12 +22,26 @@ struct GluFwd {
     int splits;       // of K, when the tiles alone leave CUs idle
 };
 
+struct MulPlan {
+    int tile, splits;  // of a product: which of the tiles, and into how many parts K is split
+};
+
+// The backward pass's workspace (dg and du first, then the splits' parts), and
+// what it is laid out for.
+struct GluWs {
+    size_t part_dx, part_dw, bytes;
+    MulPlan dx, dw;
+    bool together;  // both products in one launch, with one tile
+    bool dx_first;  // dx's workgroups first in it
+};
+GluWs glu_backward_ws(int T, int d, int F, int vdtype);
+
 struct GluBwd {
     int T, d, F, act;
     const void *x, *wg, *wu, *g, *u, *dh;
     void *dx, *dwg, *dwu;  // NULL: not wanted
-    void *dgu;             // [T to a multiple of 64] rows of glu_pitch(F): a row's dg, then its du
-    float *part;           // split-K partial sums
+    void *dgu;             // the workspace: [T to a multiple of 64] rows of glu_pitch(F), a row's dg, then its du
+    GluWs ws;
 };
 
 // Elements from one row of dgu to the next.  64 more than it holds: rows that
@@ -35,11 +49,6 @@ struct GluBwd {
 // the same columns of 256 of them (dx at the 2B-like layer: 425 us with the
 // gap, 437 us without).
 __host__ __device__ inline int64_t glu_pitch(int F) { return 2 * (int64_t)F + 64; }
-
-struct GluWs {
-    size_t dgu, part, bytes;  // offsets
-};
-GluWs glu_backward_ws(int T, int d, int F, int vdtype);
 
 size_t glu_forward_ws(int T, int d, int F, int vdtype);  // bytes
 

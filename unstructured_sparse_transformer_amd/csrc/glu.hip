@@ -350,20 +350,18 @@ struct GluMul {
     float *part;
     int splits;
     DgTiles tiles;
+    int wg0, wgs;  // its workgroups of the launch (0: not wanted)
 };
 
-// Bound by the matrix units: the 2B-like layer's dx takes 425 us and its dW 425
-// (1.29 PFLOP/s each); fp32, 1500 x 2048 x 2048: about 196 and 190 us, 130 TFLOP/s.
-template <typename TI, int BM, int BN, int WM, int WN, int S, bool A_KC, bool B_KC>
-__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, sizeof(TI) == 4 ? 4 : 2))) void
-glu_mul_kernel(GluMul p)
+// Workgroup wg's tile of one product of the backward pass.
+template <typename TI, int BM, int BN, int WM, int WN, int S, bool A_KC>
+__device__ __forceinline__ void glu_mul_tile(const GluMul &p, int wg, char *smem)
 {
-    using Core = DgCore<TI, BM, BN, WM, WN, A_KC, B_KC, 0, S>;
+    using Core = DgCore<TI, BM, BN, WM, WN, A_KC, false, 0, S>;
     constexpr int SK = Core::A::SK;
-    __shared__ __attribute__((aligned(16))) char smem[Core::LDS];
     static_assert(sizeof(TI) == 4 || Core::NW * dg_stage_bytes<Core::FN>() <= Core::LDS, "the stores' staging fits");
     int mt, nt, split;
-    if (!dg_tile(p.tiles, blockIdx.x, mt, nt, split))
+    if (!dg_tile(p.tiles, wg, mt, nt, split))
         return;
     const int tid = threadIdx.x, lane = tid & 63;
     const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
@@ -402,8 +400,23 @@ glu_mul_kernel(GluMul p)
     }
 }
 
+// dx and dW in one launch: neither fills the GPU by itself where rows are few, and
+// a launch costs 3 to 4 us.  Bound by the matrix units: the 2B-like layer's two products take 425 us each
+// (1.29 PFLOP/s); fp32, 1500 x 2048 x 2048: about 196 and 190 us, 130 TFLOP/s.
+template <typename TI, int BM, int BN, int WM, int WN, int S>
+__global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, sizeof(TI) == 4 ? 4 : 2))) void
+glu_mul_kernel(GluMul dx, GluMul dw)
+{
+    __shared__ __attribute__((aligned(16))) char smem[DgCore<TI, BM, BN, WM, WN, true, false, 0, S>::LDS];
+    const int at = (int)blockIdx.x - dx.wg0;
+    if (at >= 0 && at < dx.wgs)
+        glu_mul_tile<TI, BM, BN, WM, WN, S, true>(dx, at, smem);
+    else
+        glu_mul_tile<TI, BM, BN, WM, WN, S, false>(dw, (int)blockIdx.x - dw.wg0, smem);
+}
+
 // out = sum over the splits of their parts, in order; 4 columns a thread.
-template <typename TI> __global__ __launch_bounds__(256) void glu_join_kernel(GluMul p)
+template <typename TI> __device__ __forceinline__ void glu_join(const GluMul &p)
 {
     const int64_t n4 = (int64_t)p.M * p.N / 4, turn = (int64_t)p.m_turn * p.N;
     for (int64_t c = blockIdx.x * 256LL + threadIdx.x; c < n4; c += gridDim.x * 256LL) {
@@ -422,6 +435,13 @@ template <typename TI> __global__ __launch_bounds__(256) void glu_join_kernel(Gl
         store_elem(o + 2, s.z);
         store_elem(o + 3, s.w);
     }
+}
+template <typename TI> __global__ __launch_bounds__(256) void glu_join_kernel(GluMul dx, GluMul dw)
+{
+    if (dx.wgs > 0 && dx.splits > 1)
+        glu_join<TI>(dx);
+    if (dw.wgs > 0 && dw.splits > 1)
+        glu_join<TI>(dw);
 }
 
 // ------------------------------------------------------------------ host
@@ -444,15 +464,11 @@ struct MulTile {
     int bm, bn;
     double stage, rest, alone;
 };
-constexpr MulTile MUL_TILES[] = {{256, 256, 1.5, 4, 1}, {256, 128, 0.74, 5.5, 1}, {128, 128, 0.6, 5, 1}, {128, 64, 0.41, 6, 1}};
+constexpr MulTile MUL_TILES[] = {{256, 256, 1.5, 4, 1}, {256, 128, 0.8, 5.5, 1}, {128, 128, 0.6, 5, 1}, {128, 64, 0.41, 6, 1}};
 constexpr MulTile FWD_TILES_F32[] = {{128, 128, 3.7, 4, 1.05}, {64, 128, 1.9, 2, 1.1}};
 constexpr MulTile MUL_TILES_F32[] = {{128, 128, 3.8, 4, 1.05}, {64, 64, 1.0, 1.5, 1.3}};
 constexpr double MUL_JOIN_US = 4, MUL_SPLIT_US = 0.45, MUL_PART_BYTES_PER_US = 5e6;
 constexpr int CUS = 256, MUL_MOST_SPLITS = 16;
-
-struct MulPlan {
-    int tile, splits;
-};
 
 // The tile and the number of K splits with the least estimated time.
 static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, int64_t K)
@@ -546,56 +562,100 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
     return hipGetLastError();
 }
 
-// Tiles and splits of a product of the backward pass.
-static MulPlan backward_plan(int vdtype, int64_t M, int64_t N, int64_t K)
+// The backward pass's products: one launch for both, with one tile, in which an
+// XCD's CUs take the workgroups of the product with the longer ones first and the
+// other's fill what the last round of those leaves; or one each (6202 x 1984 x
+// 6272 640 us in two launches, 700 us in one; 4096 x 1024 x 4096 166 and 147, 300
+// x 512 x 512 20 and 15).  The tiles and the splits of each with the least estimated time.
+constexpr double MUL_LAUNCH_US = 3, MUL_SURE = 0.94;  // closer than that the estimates do not tell
+
+static GluWs backward_plan(int vdtype, int64_t T, int64_t d, int64_t F)
 {
-    if (M == 0 || N == 0 || K == 0)
-        return {0, 1};
-    return vdtype == 1 ? mul_plan(MUL_TILES, 3, M, N, K) : mul_plan(MUL_TILES_F32, 2, M, N, K);
+    const MulTile *tile = vdtype == 1 ? MUL_TILES : MUL_TILES_F32;
+    const int tiles = vdtype == 1 ? 3 : 2, xcd_cus = CUS / 8;
+    const int64_t M[2] = {T, 2 * F}, K[2] = {2 * F, T};
+    GluWs best{};
+    MulPlan alone[2] = {{0, 1}, {0, 1}};
+    double best_us = 1e300, alone_us[2] = {1e300, 1e300};
+    for (int t = 0; t < tiles; ++t) {
+        struct {
+            int64_t n;  // workgroups of an XCD
+            double us, join;
+        } c[2][5];
+        int kinds[2];
+        for (int w = 0; w < 2; ++w) {
+            const int64_t stages = ceil_div(K[w], 64), wgs = ceil_div(M[w], tile[t].bm) * ceil_div(d, tile[t].bn);
+            int k = 0;
+            for (int splits = 1; splits <= MUL_MOST_SPLITS && (splits == 1 || splits <= stages); splits *= 2, ++k) {
+                auto &p = c[w][k];
+                p.n = ceil_div(wgs * splits, 8);
+                p.us = (double)ceil_div(stages, splits) * tile[t].stage + tile[t].rest;
+                p.join = splits == 1 ? 0 : MUL_SPLIT_US * splits + (double)M[w] * d * 8 * splits / MUL_PART_BYTES_PER_US;
+                const double us = (double)ceil_div(p.n, xcd_cus) * p.us * (p.n <= xcd_cus ? tile[t].alone : 1) + p.join +
+                                  (splits > 1 ? MUL_JOIN_US : 0);
+                if (us < alone_us[w]) {
+                    alone_us[w] = us;
+                    alone[w] = MulPlan{t, splits};
+                }
+            }
+            kinds[w] = k;
+        }
+        for (int i = 0; i < kinds[0]; ++i)
+            for (int j = 0; j < kinds[1]; ++j) {
+                const bool dx_first = c[0][i].us >= c[1][j].us;
+                const auto &l = dx_first ? c[0][i] : c[1][j], &s = dx_first ? c[1][j] : c[0][i];
+                const int64_t over = l.n % xcd_cus, rounds = l.n / xcd_cus + (over > 0);
+                const int64_t left = s.n - (over ? (xcd_cus - over) * (int64_t)(l.us / s.us) : 0);
+                double us = (double)rounds * l.us + (left > 0 ? (double)ceil_div(left, xcd_cus) * s.us : 0);
+                if (l.n + s.n <= xcd_cus)
+                    us *= tile[t].alone;
+                us += c[0][i].join + c[1][j].join + (i + j > 0 ? MUL_JOIN_US : 0);
+                if (us < best_us) {
+                    best_us = us;
+                    best.dx = best.dw = MulPlan{t, 1 << i};
+                    best.dw.splits = 1 << j;
+                    best.dx_first = dx_first;
+                }
+            }
+    }
+    best.together = best_us <= MUL_SURE * (alone_us[0] + alone_us[1] + MUL_LAUNCH_US);
+    if (!best.together) {
+        best.dx = alone[0];
+        best.dw = alone[1];
+    }
+    return best;
 }
 
 static size_t up256_(size_t b) { return (b + 255) & ~(size_t)255; }
 
 GluWs glu_backward_ws(int T, int d, int F, int vdtype)
 {
-    GluWs w{};
+    GluWs w = backward_plan(vdtype, T, d, F);
     const size_t es = vdtype == 1 ? 2 : 4;
-    w.part = up256_((size_t)ceil_div(T, 64) * 64 * glu_pitch(F) * es);
-    const MulPlan dx = backward_plan(vdtype, T, d, 2 * (int64_t)F), dw = backward_plan(vdtype, 2 * (int64_t)F, d, T);
-    const size_t a = dx.splits > 1 ? (size_t)dx.splits * T * d * 4 : 0;
-    const size_t b = dw.splits > 1 ? (size_t)dw.splits * 2 * F * d * 4 : 0;
-    w.bytes = w.part + (a > b ? a : b);
+    w.part_dx = up256_((size_t)ceil_div(T, 64) * 64 * glu_pitch(F) * es);
+    w.part_dw = w.part_dx + up256_(w.dx.splits > 1 ? (size_t)w.dx.splits * T * d * 4 : 0);
+    w.bytes = w.part_dw + (w.dw.splits > 1 ? (size_t)w.dw.splits * 2 * F * d * 4 : 0);
     return w;
 }
 
-template <bool A_KC, bool B_KC> static hipError_t mul_go(int vdtype, GluMul p, hipStream_t s)
+// One launch of the products' workgroups (either may have none).
+static hipError_t launch_muls(int vdtype, int tile, const GluMul &dx, const GluMul &dw, hipStream_t s)
 {
-    const MulPlan plan = backward_plan(vdtype, p.M, p.N, p.K);
-    p.splits = plan.splits;
-    const MulTile &tile = (vdtype == 1 ? MUL_TILES : MUL_TILES_F32)[plan.tile];
-    p.tiles = dg_tiles(ceil_div(p.M, tile.bm), ceil_div(p.N, tile.bn), p.splits);
-    const dim3 grid((unsigned)dg_grid(p.tiles));
+    const dim3 grid(dx.wgs + dw.wgs);
+    if (grid.x == 0)
+        return hipSuccess;
     if (vdtype == 0) {
-        if (plan.tile == 0)
-            glu_mul_kernel<float, 128, 128, 32, 64, 2, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+        if (tile == 0)
+            glu_mul_kernel<float, 128, 128, 32, 64, 2><<<grid, dim3(512), 0, s>>>(dx, dw);
         else
-            glu_mul_kernel<float, 64, 64, 32, 32, 3, A_KC, B_KC><<<grid, dim3(256), 0, s>>>(p);
+            glu_mul_kernel<float, 64, 64, 32, 32, 3><<<grid, dim3(256), 0, s>>>(dx, dw);
+    } else if (tile == 0) {
+        glu_mul_kernel<__bf16, 256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(dx, dw);
+    } else if (tile == 1) {
+        glu_mul_kernel<__bf16, 256, 128, 64, 64, 3><<<grid, dim3(512), 0, s>>>(dx, dw);
     } else {
-        if (plan.tile == 0)
-            glu_mul_kernel<__bf16, 256, 256, 64, 128, 2, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
-        else if (plan.tile == 1)
-            glu_mul_kernel<__bf16, 256, 128, 64, 64, 3, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
-        else
-            glu_mul_kernel<__bf16, 128, 128, 32, 64, 4, A_KC, B_KC><<<grid, dim3(512), 0, s>>>(p);
+        glu_mul_kernel<__bf16, 128, 128, 32, 64, 4><<<grid, dim3(512), 0, s>>>(dx, dw);
     }
-    hipError_t e = hipGetLastError();
-    if (e != hipSuccess || p.splits == 1)
-        return e;
-    const dim3 join = join_grid((int64_t)p.M * p.N);
-    if (vdtype == 1)
-        glu_join_kernel<__bf16><<<join, dim3(256), 0, s>>>(p);
-    else
-        glu_join_kernel<float><<<join, dim3(256), 0, s>>>(p);
     return hipGetLastError();
 }
 
@@ -617,34 +677,54 @@ hipError_t launch_glu_backward(int vdtype, const GluBwd &p, hipStream_t s)
         if ((e = hipGetLastError()) != hipSuccess)
             return e;
     }
-    GluMul m{};
-    m.a = p.dgu;
-    m.lda = glu_pitch(p.F) * es;
-    m.ldb = (int64_t)p.d * es;
-    m.N = p.d;
-    m.part = p.part;
-    if (p.dx && p.T > 0) {
-        m.M = p.T;
-        m.K = 2 * p.F;
-        m.b = p.wg;
-        m.b2 = p.wu;
-        m.k_turn = p.F;
-        m.out = m.out2 = p.dx;
-        m.m_turn = (int)ceil_div(p.T, 64) * 64;
-        if ((e = mul_go<true, false>(vdtype, m, s)) != hipSuccess)
-            return e;
+    const GluWs &w = p.ws;
+    GluMul dx{};
+    dx.a = p.dgu;
+    dx.lda = glu_pitch(p.F) * es;
+    dx.ldb = (int64_t)p.d * es;
+    dx.N = p.d;
+    GluMul dw = dx;
+    dx.M = p.T;
+    dx.K = 2 * p.F;
+    dx.b = p.wg;
+    dx.b2 = p.wu;
+    dx.k_turn = p.F;
+    dx.out = dx.out2 = p.dx;
+    dx.m_turn = rows;
+    dx.splits = w.dx.splits;
+    dx.part = (float *)((char *)p.dgu + w.part_dx);
+    dw.M = 2 * p.F;
+    dw.K = p.T;
+    dw.b = dw.b2 = p.x;
+    dw.k_turn = 1 << 30;
+    dw.out = p.dwg;
+    dw.out2 = p.dwu;
+    dw.m_turn = p.F;
+    dw.splits = w.dw.splits;
+    dw.part = (float *)((char *)p.dgu + w.part_dw);
+    for (GluMul *m : {&dx, &dw}) {
+        if (!m->out || m->M == 0)
+            continue;
+        const MulTile &tile = (vdtype == 1 ? MUL_TILES : MUL_TILES_F32)[m == &dx ? w.dx.tile : w.dw.tile];
+        m->tiles = dg_tiles(ceil_div(m->M, tile.bm), ceil_div(m->N, tile.bn), m->splits);
+        m->wgs = (int)dg_grid(m->tiles);
     }
-    if (p.dwg) {
-        m.M = 2 * p.F;
-        m.K = p.T;
-        m.b = m.b2 = p.x;
-        m.k_turn = 1 << 30;
-        m.out = p.dwg;
-        m.out2 = p.dwu;
-        m.m_turn = p.F;
-        return mul_go<false, false>(vdtype, m, s);
+    if (w.together) {
+        (w.dx_first ? dw : dx).wg0 = (w.dx_first ? dx : dw).wgs;
+        e = launch_muls(vdtype, w.dx.tile, dx, dw, s);
+    } else {
+        e = launch_muls(vdtype, w.dx.tile, dx, GluMul{}, s);
+        if (e == hipSuccess)
+            e = launch_muls(vdtype, w.dw.tile, GluMul{}, dw, s);
     }
-    return hipSuccess;
+    const int64_t parts = (dx.wgs > 0 && dx.splits > 1 ? (int64_t)dx.M * dx.N : 0) + (dw.wgs > 0 && dw.splits > 1 ? (int64_t)dw.M * dw.N : 0);
+    if (e != hipSuccess || parts == 0)
+        return e;
+    if (vdtype == 1)
+        glu_join_kernel<__bf16><<<join_grid(parts), dim3(256), 0, s>>>(dx, dw);
+    else
+        glu_join_kernel<float><<<join_grid(parts), dim3(256), 0, s>>>(dx, dw);
+    return hipGetLastError();
 }
 
 }  // namespace twell
