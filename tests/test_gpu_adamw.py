@@ -256,3 +256,6 @@ def test_adamw_refusals(gpu_lib):
             tw.twell_adamw_step(params, h["lr"], h["beta1"], h["beta2"], h["eps"], h["step"])
     with pytest.raises(ValueError):
         tw.twell_adamw_unpack(tw.AdamWTensors(_tensors([64], 32, torch.float32, torch.float32)))
+    for scale in (torch.ones(1), torch.ones(2, device="cuda"), torch.ones(1, device="cuda", dtype=torch.float64)):
+        with pytest.raises((ValueError, TypeError)):
+            tw.twell_adamw_step(params, HYPER["lr"], HYPER["beta1"], HYPER["beta2"], HYPER["eps"], 1, grad_scale=scale)

@@ -251,3 +251,6 @@ def test_refusals(gpu_lib):
     with pytest.raises(tw.TwellError):  # a workspace that is too small
         tw.twell_block_norm_backward(tw.BlockNorm(), c["res"], None, c["dout"], c["dn"], n, None,
                                      torch.empty(256, dtype=torch.uint8, device="cuda"))
+    with pytest.raises(ValueError):  # a workspace in host memory
+        tw.twell_block_norm_backward(tw.BlockNorm(), c["res"], None, c["dout"], c["dn"], n, None,
+                                     torch.empty(1 << 20, dtype=torch.uint8))

@@ -271,3 +271,6 @@ def test_refusals(gpu_lib):
         tw.twell_glu_backward(x, wg, wu, h, h, h, "silu", None, wg.clone(), None, tw.glu_backward_workspace(4, 64, 128, x.dtype))
     with pytest.raises(tw.TwellError):  # no workspace
         tw.twell_glu_backward(x, wg, wu, h, h, h, "silu", x.clone(), None, None, None)
+    for ws in (torch.empty(1 << 20, dtype=torch.uint8), torch.empty((1 << 11, 1 << 10), dtype=torch.uint8, device="cuda").t()):
+        with pytest.raises(ValueError):
+            tw.twell_glu_backward(x, wg, wu, h, h, h, "silu", x.clone(), None, None, ws)

@@ -450,6 +450,15 @@ def _tensor(fn: str, name: str, t, shape, dev: int, dtype=None) -> int:
     raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
 
 
+def _workspace(fn: str, t, dev: int) -> tuple:
+    """The pointer and the bytes of a workspace (or None)."""
+    if t is None:
+        return None, 0
+    if t.get_device() != dev or not t.is_contiguous():
+        raise ValueError(f"{fn}: the workspace must be contiguous and on cuda:{dev}")
+    return t.data_ptr(), t.numel() * t.element_size()
+
+
 ACTS = {"relu": 0, "silu": 1, "gelu": 2, "gelu_tanh": 3}
 
 
@@ -478,8 +487,7 @@ def twell_glu_forward(x, wg_t, wu_t, act: str, h, workspace=None, g=None, u=None
          _tensor(fn, "wu_t", wu_t, (F, d), dev, dt))
     out = (_tensor(fn, "h", h, (T, F), dev, dt), None if g is None else _tensor(fn, "g", g, (T, F), dev, dt),
            None if u is None else _tensor(fn, "u", u, (T, F), dev, dt))
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(fn, load().twell_glu_forward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *out, _ptr(workspace), nbytes,
+    _check(fn, load().twell_glu_forward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *out, *_workspace(fn, workspace, dev),
                                         _stream(stream)))
 
 
@@ -501,8 +509,7 @@ def twell_glu_backward(x, wg_t, wu_t, g, u, dh, act: str, dx, dwg, dwu, workspac
                                                        ("g", g, (T, F)), ("u", u, (T, F)), ("dh", dh, (T, F)))]
     o = [None if t is None else _tensor(fn, k, t, s, dev, dt)
          for k, t, s in (("dx", dx, (T, d)), ("dwg", dwg, (F, d)), ("dwu", dwu, (F, d)))]
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
-    _check(fn, load().twell_glu_backward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *o, _ptr(workspace), nbytes,
+    _check(fn, load().twell_glu_backward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *o, *_workspace(fn, workspace, dev),
                                          _stream(stream)))
 
 
@@ -584,10 +591,9 @@ def twell_block_norm_backward(bn: BlockNorm, out, y, dout, dn, dres, dy, workspa
     p_dgate = None if dgate is None else _tensor(fn, "dgate", dgate, gate.shape if gate is not None else (), dev, dt)
     dw = [None if t is None else _tensor(fn, k, t, (shape[1],), dev, torch.float32)
           for k, t in (("dw_post", dw_post), ("db_post", db_post), ("dw_pre", dw_pre), ("db_pre", db_pre))]
-    nbytes = 0 if workspace is None else workspace.numel() * workspace.element_size()
     _check(fn, load().twell_block_norm_backward(o, p["out"], _ptr(y), p["dout"], p["dn"],
                                                 TWELL_F32 if dn is None else vdtype_of(dn.dtype), p_dres, p["dy"],
-                                                p_dgate, *dw, _ptr(workspace), nbytes, _stream(stream)))
+                                                p_dgate, *dw, *_workspace(fn, workspace, dev), _stream(stream)))
 
 
 # ---------------------------------------------------------------- the optimizer
@@ -650,13 +656,20 @@ def twell_adamw_step(params: AdamWTensors, lr: float, beta1: float, beta2: float
                      grad_scale=None, stream=None):
     """One step; step counts from 1; grad_scale: a float32 tensor of one element on the GPU (0, inf or NaN in it:
     nothing changes); seed: of the 8-bit states' rounding, another one each step."""
-    _check("twell_adamw_step",
-           load().twell_adamw_step(params.desc, len(params.tensors), params.state_bits, lr, beta1, beta2, eps, step,
-                                   seed & 0xFFFFFFFF, _ptr(grad_scale), _stream(stream)))
+    import torch
+    fn, scale = "twell_adamw_step", None
+    if params.tensors:
+        dev = _device(fn, params.tensors[0]["p"])
+        if grad_scale is not None:
+            scale = _tensor(fn, "grad_scale", grad_scale.reshape(-1), (1,), dev, torch.float32)
+    _check(fn, load().twell_adamw_step(params.desc, len(params.tensors), params.state_bits, lr, beta1, beta2, eps, step,
+                                       seed & 0xFFFFFFFF, scale, _stream(stream)))
 
 
 def twell_adamw_unpack(params: AdamWTensors, stream=None):
     """Writes the values of 8-bit states to m_values and v_values."""
     if not params.can_unpack:
         raise ValueError("twell_adamw_unpack: 8-bit states with m_values and v_values are needed")
+    if params.tensors:
+        _device("twell_adamw_unpack", params.tensors[0]["p"])
     _check("twell_adamw_unpack", load().twell_adamw_unpack(params.desc, len(params.tensors), _stream(stream)))
