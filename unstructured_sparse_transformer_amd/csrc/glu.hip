@@ -71,8 +71,8 @@ template <bool FAST> __device__ __forceinline__ float glu_act_grad(float g, int 
 }
 
 // ------------------------------------------------------------------ forward
-// Bound by the matrix units.  bf16, 8192 x 2048 x 8192 with g and u kept: 487 us,
-// 1.13 PFLOP/s; the product by itself takes 420 us at the clock the chip's power
+// Bound by the matrix units.  bf16, 8192 x 2048 x 8192 with g and u kept: 478 us,
+// 1.15 PFLOP/s; the product by itself takes 420 us at the clock the chip's power
 // cap leaves it, the rest is 403 MB of results that leave between the tiles
 // (workgroups started up to 13 us apart, so that some store while others
 // multiply: no change).  fp32, 1500 x 2048 x 2048: 188 us, 134 of 157 TFLOP/s.
