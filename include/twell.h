@@ -467,8 +467,7 @@ typedef struct twell_block_norm_t {
 /* res, y, out, n : device [T][d].  y NULL: no block before this norm (out is
  * not written).  n NULL: no norm after the sum; out NULL: the sum is not
  * wanted (one of the two is).  out may be res.  Pointers need the alignment of
- * their elements; with 16-byte aligned pointers and d a multiple of 8 the
- * accesses are wide. */
+ * their elements; 16-byte aligned pointers and d a multiple of 8 are fastest. */
 TWELL_API int twell_block_norm_forward(const twell_block_norm_t *bn, const void *res, const void *y, void *out,
                                        void *n, void *stream);
 

@@ -151,6 +151,19 @@ def test_alignment(gpu_lib, offset):
     _check(gpu_lib, _case(11, 256, r="bfloat16", y="bfloat16", n="bfloat16", dn="bfloat16", span=2, offset=offset))
 
 
+@pytest.mark.parametrize("d", [9, 15, 100, 511, 513, 519, 1001, 1025, 1031, 2049, 4100, 8191])
+@pytest.mark.parametrize("post", [False, True])
+def test_sum_in_place(gpu_lib, d, post):
+    """out may be res: the same bits as with a tensor of its own."""
+    import torch
+    say(f"case block norm in place d={d} post={post}")
+    c = _case(600, d, post=post, span=3)
+    want = _forward(gpu_lib, c)
+    out, n = c["res"].clone(), torch.empty_like(want["n"])
+    gpu_lib.twell_block_norm_forward(_bn(gpu_lib, c), out, c["y"], out, n, gate=c["gate"], gate_span=3)
+    assert torch.equal(out, want["out"]) and torch.equal(n, want["n"])
+
+
 def test_rows_of_one_value(gpu_lib):
     """Rows without deviation, rows of zeros, and very large and small values stay finite and within the bounds."""
     import torch

@@ -33,9 +33,10 @@ namespace twell {
 // ones (16 bytes of bf16); BN_4
 // two groups of four, the second 4 NT columns on (16 bytes of fp32, so that a
 // wave's accesses to fp32 have no gaps); BN_END, for any width from 8 on and any
-// alignment of the elements, as BN_8, but the last thread has the row's last
-// eight columns: those that the thread before it has too get the same values from
-// both and count once in sums; BN_ANY, for widths below 8, one by one.  (One by one at any
+// alignment of the elements, as BN_8, but counted from the row's end: the first
+// thread's eight columns overlap with the second's, which get the same values from
+// both and count once in sums (both lie in one wave, which has loaded them before
+// it stores: a result may take its input's place); BN_ANY, for widths below 8, one by one.  (One by one at any
 // odd width: 8192 x 1001 forward in bf16 22.5 us, 16.8 so, backward 52 and 39.)
 enum BnLay { BN_ANY, BN_8, BN_4, BN_END };
 
@@ -48,10 +49,17 @@ template <BnLay L, int NT> __device__ __forceinline__ bool bn_in(int tid, int e,
                           : e * NT + tid) < d;
 }
 
+// BN_END: the first column of a thread.
+__device__ __forceinline__ int bn_end(int tid, int d)
+{
+    const int c = tid * 8 - (-d & 7);
+    return c > 0 ? c : 0;
+}
+
 // v where element e counts in the row's sums (elements past d are 0).
 template <BnLay L> __device__ __forceinline__ float bn_once(float v, int tid, int e, int d)
 {
-    return L == BN_END && tid * 8 + 8 - d > e ? 0.f : v;
+    return L == BN_END && tid == 0 && e >= 8 - (-d & 7) ? 0.f : v;
 }
 
 typedef uint32_t u32x4_al2 __attribute__((ext_vector_type(4), aligned(2)));
@@ -91,7 +99,7 @@ __device__ __forceinline__ Raw8 bn_load(BnTensor t, int64_t row, int d, int tid)
     } else if constexpr (L == BN_END) {
         if (tid * 8 < d) {
             // (through the caches: threads share lines)
-            const uint32_t c = tid * 8 < d - 8 ? tid * 8 : d - 8;
+            const uint32_t c = bn_end(tid, d);
             if (t.bf16) {
                 r.a = bn_ld16<false, u32x4_al2>((const __bf16 *)t.p + row * d + c);
             } else {
@@ -174,7 +182,7 @@ __device__ __forceinline__ void bn_store(BnTensor t, int64_t row, int d, int tid
         }
     } else if constexpr (L == BN_END) {
         if (tid * 8 < d) {
-            const uint32_t c = tid * 8 < d - 8 ? tid * 8 : d - 8;
+            const uint32_t c = bn_end(tid, d);
             if (t.bf16) {
                 *reinterpret_cast<u32x4_al2 *>((__bf16 *)t.p + row * d + c) =
                     u32x4_al2{bn_pack(v[0], v[1]), bn_pack(v[2], v[3]), bn_pack(v[4], v[5]), bn_pack(v[6], v[7])};
