@@ -1,0 +1,35 @@
+"""The Python side of the dense layer's operators on the host (no GPU needed):
+what a call hands to the C side."""
+
+import pytest
+import torch
+
+import unstructured_sparse_transformer_amd as tw
+
+CPU = -1  # a host tensor's device number, in the place of a GPU's
+
+
+@pytest.mark.parametrize("span", [7, 8, (1 << 31) - 1, 1 << 31, 1 << 32, (1 << 32) + 1, (1 << 32) + 3, 1 << 40])
+def test_gate_row_of_any_span(span):
+    """One gate row for all rows is that, however large the span is that says so."""
+    rows, gate = torch.zeros(7, 16), torch.zeros(1, 16)
+    o = tw.BlockNorm().desc("f", CPU, rows, rows, gate, span)
+    assert o.T == 7 and o.gate_span >= 7
+
+
+def test_counts_past_32_bits_are_refused():
+    """More rows than an argument holds stay more than the C side takes."""
+    T, most = (1 << 32) + 128, 1 << 30
+    rows = torch.zeros((T, 0))
+    assert tw.BlockNorm().desc("f", CPU, rows, None, None, 0).T > most
+    with pytest.raises(tw.TwellError):
+        tw._check("f", tw.load().twell_block_norm_forward(tw.BlockNorm().desc("f", CPU, rows, None, None, 0), None, None,
+                                                          None, None, None))
+    for dt in (torch.bfloat16, torch.float32):
+        assert tw.twell_glu_workspace_bytes(128, 4096, 512, dt) > 0
+        assert tw.twell_glu_workspace_bytes(T, 4096, 512, dt) == 0
+        assert tw.twell_glu_workspace_bytes(128, (1 << 32) + 4096, 512, dt) == 0
+        assert tw.twell_glu_backward_workspace_bytes(T, 128, 128, dt) == 0
+        assert tw.twell_glu_backward_workspace_bytes(128, 128, (1 << 32) + 128, dt) == 0
+    assert tw.twell_block_norm_workspace_bytes(T, 64) == 0
+    assert tw.twell_block_norm_workspace_bytes(64, (1 << 32) + 64) == 0

@@ -450,6 +450,12 @@ def _tensor(fn: str, name: str, t, shape, dev: int, dtype=None) -> int:
     raise TypeError(f"{fn}: {name} must be {dtype}, not {t.dtype}")
 
 
+def _i32(n: int) -> int:
+    """A count for a 32-bit argument.  One that does not fit becomes the largest, which is past the bounds that the C
+    side checks (ctypes alone would keep its lower 32 bits)."""
+    return max(-1, min(n, (1 << 31) - 1))
+
+
 def _workspace(fn: str, t, dev: int) -> tuple:
     """The pointer and the bytes of a workspace (or None)."""
     if t is None:
@@ -469,7 +475,7 @@ def _act(fn: str, act: str) -> int:
 
 
 def twell_glu_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
-    return int(load().twell_glu_workspace_bytes(T, d, F, vdtype_of(dtype)))
+    return int(load().twell_glu_workspace_bytes(_i32(T), _i32(d), _i32(F), vdtype_of(dtype)))
 
 
 def glu_workspace(T: int, d: int, F: int, dtype, device="cuda"):
@@ -487,12 +493,12 @@ def twell_glu_forward(x, wg_t, wu_t, act: str, h, workspace=None, g=None, u=None
          _tensor(fn, "wu_t", wu_t, (F, d), dev, dt))
     out = (_tensor(fn, "h", h, (T, F), dev, dt), None if g is None else _tensor(fn, "g", g, (T, F), dev, dt),
            None if u is None else _tensor(fn, "u", u, (T, F), dev, dt))
-    _check(fn, load().twell_glu_forward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *out, *_workspace(fn, workspace, dev),
-                                        _stream(stream)))
+    _check(fn, load().twell_glu_forward(*p, _i32(T), _i32(d), _i32(F), vdtype_of(dt), _act(fn, act), *out,
+                                        *_workspace(fn, workspace, dev), _stream(stream)))
 
 
 def twell_glu_backward_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
-    return int(load().twell_glu_backward_workspace_bytes(T, d, F, vdtype_of(dtype)))
+    return int(load().twell_glu_backward_workspace_bytes(_i32(T), _i32(d), _i32(F), vdtype_of(dtype)))
 
 
 def glu_backward_workspace(T: int, d: int, F: int, dtype, device="cuda"):
@@ -509,8 +515,8 @@ def twell_glu_backward(x, wg_t, wu_t, g, u, dh, act: str, dx, dwg, dwu, workspac
                                                        ("g", g, (T, F)), ("u", u, (T, F)), ("dh", dh, (T, F)))]
     o = [None if t is None else _tensor(fn, k, t, s, dev, dt)
          for k, t, s in (("dx", dx, (T, d)), ("dwg", dwg, (F, d)), ("dwu", dwu, (F, d)))]
-    _check(fn, load().twell_glu_backward(*p, T, d, F, vdtype_of(dt), _act(fn, act), *o, *_workspace(fn, workspace, dev),
-                                         _stream(stream)))
+    _check(fn, load().twell_glu_backward(*p, _i32(T), _i32(d), _i32(F), vdtype_of(dt), _act(fn, act), *o,
+                                         *_workspace(fn, workspace, dev), _stream(stream)))
 
 
 # ---------------------------------------------------------------- block norms
@@ -541,14 +547,14 @@ class BlockNorm:
         if self.d is not None and (d != self.d or dev != self.dev):
             raise ValueError(f"{fn}: rows of {d} on cuda:{dev}, weights of {self.d} on cuda:{self.dev}")
         o = TwellBlockNormT.from_buffer_copy(self._desc)
-        o.T, o.d, o.rdtype = T, d, vdtype_of(rows.dtype)
+        o.T, o.d, o.rdtype = _i32(T), _i32(d), vdtype_of(rows.dtype)
         if y is not None:
             _tensor(fn, "y", y, (T, d), dev)
             o.ydtype = vdtype_of(y.dtype)
         if gate is not None:
             if gate_span < 1:
                 raise ValueError(f"{fn}: gate_span {gate_span}: a gate row serves at least one row")
-            o.gate_span = gate_span
+            o.gate_span = _i32(gate_span)
             o.gate = _tensor(fn, "gate", gate, (-(-T // gate_span), d), dev, rows.dtype)
         return o
 
@@ -568,7 +574,7 @@ def twell_block_norm_forward(bn: BlockNorm, res, y, out, n, gate=None, gate_span
 
 
 def twell_block_norm_workspace_bytes(T: int, d: int) -> int:
-    return int(load().twell_block_norm_workspace_bytes(T, d))
+    return int(load().twell_block_norm_workspace_bytes(_i32(T), _i32(d)))
 
 
 def block_norm_workspace(T: int, d: int, device="cuda"):
