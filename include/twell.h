@@ -525,7 +525,8 @@ typedef struct twell_adamw_tensor_t {
     int32_t gdtype;     /* enum twell_dtype of grad */
 } twell_adamw_tensor_t;
 
-/* The step.  step >= 1 counts the steps of this state, 0 <= beta < 1, eps > 0.
+/* The step.  step >= 1 counts the steps of this state, 0 <= beta < 1, eps > 0 as
+ * a float.
  * grad_scale : device float, or NULL for 1: multiplies every gradient (the
  *     inverse of a loss scale, a clip coefficient).  Where it is 0, infinite or
  *     NaN the call changes nothing.

@@ -1,6 +1,8 @@
 """The Python side of the dense layer's operators on the host (no GPU needed):
 what a call hands to the C side."""
 
+import ctypes
+
 import pytest
 import torch
 
@@ -33,3 +35,12 @@ def test_counts_past_32_bits_are_refused():
         assert tw.twell_glu_backward_workspace_bytes(128, 128, (1 << 32) + 128, dt) == 0
     assert tw.twell_block_norm_workspace_bytes(T, 64) == 0
     assert tw.twell_block_norm_workspace_bytes(64, (1 << 32) + 64) == 0
+
+
+def test_adamw_eps_is_one_of_32_bits():
+    """An eps that is 0 as a float divides 0 by 0 where an element has no moments yet: refused as 0 is."""
+    at = 4096  # an aligned, never dereferenced fake device address
+    t = tw.TwellAdamWTensorT(n=1000, p=at, grad=at, m=at, v=at)
+    step = lambda eps: tw.load().twell_adamw_step(  # noqa: E731
+        ctypes.byref(t), 1, 32, 1e-3, 0.9, 0.99, eps, 1, 0, None, None)
+    assert [step(eps) for eps in (0.0, 1e-46, 7e-46, 5e-324, float("nan"))] == [-3] * 5

@@ -292,7 +292,9 @@ int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, con
 int twell_adamw_step(const twell_adamw_tensor_t *tensors, int32_t count, int32_t state_bits, double lr, double beta1,
                      double beta2, double eps, int64_t step, uint32_t seed, const float *grad_scale, void *stream)
 {
-    if (count < 0 || step < 1 || !(lr >= 0) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) || !(eps > 0))
+    // (eps as the kernel has it: in 32 bits)
+    if (count < 0 || step < 1 || !(lr >= 0) || !(beta1 >= 0 && beta1 < 1) || !(beta2 >= 0 && beta2 < 1) ||
+        !((float)eps > 0))
         return TWELL_E_SHAPE;
     if (state_bits != 8 && state_bits != 32)
         return TWELL_E_UNSUPPORTED;
