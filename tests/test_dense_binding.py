@@ -44,3 +44,17 @@ def test_adamw_eps_is_one_of_32_bits():
     step = lambda eps: tw.load().twell_adamw_step(  # noqa: E731
         ctypes.byref(t), 1, 32, 1e-3, 0.9, 0.99, eps, 1, 0, None, None)
     assert [step(eps) for eps in (0.0, 1e-46, 7e-46, 5e-324, float("nan"))] == [-3] * 5
+
+
+def test_a_block_s_tensors_need_the_block(monkeypatch):
+    """A gate, or a place for a block's gradient, without the block's y is refused, not left as it is."""
+    monkeypatch.setattr(tw, "_device", lambda fn, t: CPU)
+    rows, gate, bn = torch.ones(6, 16), torch.ones(2, 16), tw.BlockNorm()
+    new = lambda: torch.empty(6, 16)  # noqa: E731
+    with pytest.raises(ValueError, match="gate"):
+        tw.twell_block_norm_forward(bn, rows, None, None, new(), gate=gate, gate_span=3, stream=0)
+    back = lambda dy, **kw: tw.twell_block_norm_backward(bn, rows, None, rows, rows, new(), dy, None, stream=0, **kw)  # noqa: E731
+    with pytest.raises(ValueError, match="gate"):
+        back(None, gate=gate, gate_span=3, dgate=gate.clone())
+    with pytest.raises(ValueError, match="dy"):
+        back(new())

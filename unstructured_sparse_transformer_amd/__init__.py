@@ -552,6 +552,8 @@ class BlockNorm:
             _tensor(fn, "y", y, (T, d), dev)
             o.ydtype = vdtype_of(y.dtype)
         if gate is not None:
+            if y is None:
+                raise ValueError(f"{fn}: a gate without a block's y")
             if gate_span < 1:
                 raise ValueError(f"{fn}: gate_span {gate_span}: a gate row serves at least one row")
             o.gate_span = _i32(gate_span)
@@ -591,6 +593,8 @@ def twell_block_norm_backward(bn: BlockNorm, out, y, dout, dn, dres, dy, workspa
     fn = "twell_block_norm_backward"
     dev, shape, dt = _device(fn, dres), dres.shape, dres.dtype
     o = bn.desc(fn, dev, dres, y, gate, gate_span)
+    if dy is not None and y is None:
+        raise ValueError(f"{fn}: dy without a block's y")
     want = {"out": (out, dt), "dout": (dout, dt), "dn": (dn, None), "dy": (dy, None if y is None else y.dtype)}
     p = {k: None if t is None else _tensor(fn, k, t, shape, dev, w) for k, (t, w) in want.items()}
     p_dres = _tensor(fn, "dres", dres, shape, dev)
