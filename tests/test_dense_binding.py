@@ -58,3 +58,25 @@ def test_a_block_s_tensors_need_the_block(monkeypatch):
         back(None, gate=gate, gate_span=3, dgate=gate.clone())
     with pytest.raises(ValueError, match="dy"):
         back(new())
+
+
+def test_weights_that_moved(monkeypatch):
+    """A weight whose data is another tensor's by the time of a call is read where it is then, and checked anew."""
+    monkeypatch.setattr(tw, "_device", lambda fn, t: CPU)
+    rows, w, b = torch.ones(6, 16), torch.ones(16), torch.zeros(16)
+    bn = tw.BlockNorm(w_pre=w, b_pre=b)
+    desc = lambda: bn.desc("f", CPU, rows, None, None, 0)  # noqa: E731
+    assert (desc().w_pre, desc().b_pre, desc().wdtype) == (w.data_ptr(), b.data_ptr(), tw.TWELL_F32)
+    old = w.data
+    w.data = torch.ones(16)
+    assert old.data_ptr() != w.data_ptr()
+    assert (desc().w_pre, desc().b_pre) == (w.data_ptr(), b.data_ptr())
+    w.data, b.data = w.data.bfloat16(), b.data.bfloat16()
+    assert (desc().w_pre, desc().wdtype) == (w.data_ptr(), tw.TWELL_BF16)
+    good, at = b.data, b.data_ptr()
+    for bad in (torch.zeros(8, dtype=torch.bfloat16), torch.zeros(16), torch.zeros(32, dtype=torch.bfloat16)[::2]):
+        b.data = bad
+        with pytest.raises((ValueError, TypeError)):
+            desc()
+    b.data = good
+    assert (desc().w_pre, desc().b_pre) == (w.data_ptr(), at)

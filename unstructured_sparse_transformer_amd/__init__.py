@@ -533,17 +533,31 @@ class BlockNorm:
             raise ValueError(f"BlockNorm: kind {kind!r}: one of {', '.join(NORM_KINDS)}")
         self.kind, self.eps, self.alpha, self.post = kind, eps, alpha, post
         self.weights = {"w_post": w_post, "b_post": b_post, "w_pre": w_pre, "b_pre": b_pre}
-        given = [w for w in self.weights.values() if w is not None]
-        dev = _device("BlockNorm", given[0]) if given else None
-        self._desc = TwellBlockNormT(kind=NORM_KINDS[kind], eps=eps, alpha=alpha, post=int(bool(post)),
-                                     wdtype=vdtype_of(given[0].dtype) if given else TWELL_F32)
-        for k, w in self.weights.items():
-            if w is not None:
-                setattr(self._desc, k, _tensor("BlockNorm", k, w, given[0].shape, dev, given[0].dtype))
-        self.d, self.dev = (given[0].numel(), dev) if given else (None, None)
+        self._desc = TwellBlockNormT(kind=NORM_KINDS[kind], eps=eps, alpha=alpha, post=int(bool(post)), wdtype=TWELL_F32)
+        self.d, self.dev, self._bound = None, None, []
+        self._bind()
+
+    def _bind(self):
+        """Checks the weights and takes their addresses."""
+        given = [(k, w) for k, w in self.weights.items() if w is not None]
+        if not given:
+            return
+        first = given[0][1]
+        dev = _device("BlockNorm", first)
+        at = {k: _tensor("BlockNorm", k, w, first.shape, dev, first.dtype) for k, w in given}
+        self._desc.wdtype = vdtype_of(first.dtype)
+        for k, p in at.items():
+            setattr(self._desc, k, p)
+        self.d, self.dev = first.numel(), dev
+        self._bound = [(w, w.data_ptr(), w.shape, w.dtype) for _, w in given]
 
     def desc(self, fn, dev, rows, y, gate, gate_span) -> TwellBlockNormT:
         T, d = rows.shape
+        for w, at, shape, dtype in self._bound:
+            # (its data may have been set anew)
+            if w.data_ptr() != at or w.shape != shape or w.dtype is not dtype or not w.is_contiguous():
+                self._bind()
+                break
         if self.d is not None and (d != self.d or dev != self.dev):
             raise ValueError(f"{fn}: rows of {d} on cuda:{dev}, weights of {self.d} on cuda:{self.dev}")
         o = TwellBlockNormT.from_buffer_copy(self._desc)
