@@ -413,9 +413,10 @@ enum twell_act {
  * and u before they are rounded.  For T <= 64 (bf16) the kernels are organised
  * for few tokens.  Inputs are finite; a NaN or an infinity spoils at most its
  * own row (of x) or column (of a weight).
- * workspace : device, >= twell_glu_workspace_bytes(T, d, F, vdtype) (0 for
- * most sizes: then it may be NULL), 256-byte aligned, content ignored on entry
- * (it holds partial sums where few tiles are split over d). */
+ * workspace : device, >= twell_glu_workspace_bytes(T, d, F, vdtype) (where that
+ * is 0 it may be NULL), 256-byte aligned, content ignored on entry (it holds
+ * partial sums where few tiles are split over d).  The bytes never shrink as T
+ * grows: the workspace for the most rows serves every call with fewer. */
 TWELL_API int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
                                 int32_t vdtype, int32_t act, void *h, void *g, void *u, void *workspace,
                                 size_t workspace_bytes, void *stream);
@@ -427,8 +428,9 @@ TWELL_API size_t twell_glu_workspace_bytes(int32_t T, int32_t d, int32_t F, int3
  *   dx = dg . W_g^T + du . W_u^T [T][d],  dwg = dg^T . x,  dwu = du^T . x [F][d],
  * vdtype, overwritten, sums in fp32 in a fixed order.  dx NULL: not computed;
  * dwg and dwu NULL: not computed (both or neither).
- * workspace : device, >= twell_glu_backward_workspace_bytes(T, d, F, vdtype),
- * 256-byte aligned, content ignored on entry (it holds dg and du). */
+ * workspace : device, >= twell_glu_backward_workspace_bytes(T, d, F, vdtype)
+ * (never shrinking as T grows), 256-byte aligned, content ignored on entry (it
+ * holds dg and du, and partial sums). */
 TWELL_API int twell_glu_backward(const void *x, const void *wg_t, const void *wu_t, const void *g, const void *u,
                                  const void *dh, int32_t T, int32_t d, int32_t F, int32_t vdtype, int32_t act,
                                  void *dx, void *dwg, void *dwu, void *workspace, size_t workspace_bytes,
@@ -471,7 +473,8 @@ typedef struct twell_block_norm_t {
 TWELL_API int twell_block_norm_forward(const twell_block_norm_t *bn, const void *res, const void *y, void *out,
                                        void *n, void *stream);
 
-/* Bytes of device workspace of the backward pass (0 for invalid sizes). */
+/* Bytes of device workspace of the backward pass (0 for invalid sizes); they
+ * never shrink as T grows. */
 TWELL_API size_t twell_block_norm_workspace_bytes(int32_t T, int32_t d);
 
 /* Gradients of twell_block_norm_forward.  out : the forward's out (its res,

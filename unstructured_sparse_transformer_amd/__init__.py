@@ -479,7 +479,7 @@ def twell_glu_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
 
 
 def glu_workspace(T: int, d: int, F: int, dtype, device="cuda"):
-    """A workspace tensor for twell_glu_forward, or None when it needs none."""
+    """A workspace tensor for twell_glu_forward with up to T rows, or None where none of these needs one."""
     import torch
     n = twell_glu_workspace_bytes(T, d, F, dtype)
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
@@ -502,7 +502,7 @@ def twell_glu_backward_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
 
 
 def glu_backward_workspace(T: int, d: int, F: int, dtype, device="cuda"):
-    """A workspace tensor for twell_glu_backward."""
+    """A workspace tensor for twell_glu_backward with up to T rows."""
     import torch
     return torch.empty(max(twell_glu_backward_workspace_bytes(T, d, F, dtype), 256), dtype=torch.uint8, device=device)
 
@@ -594,7 +594,7 @@ def twell_block_norm_workspace_bytes(T: int, d: int) -> int:
 
 
 def block_norm_workspace(T: int, d: int, device="cuda"):
-    """A workspace tensor for twell_block_norm_backward."""
+    """A workspace tensor for twell_block_norm_backward with up to T rows."""
     import torch
     return torch.empty(max(twell_block_norm_workspace_bytes(T, d), 256), dtype=torch.uint8, device=device)
 

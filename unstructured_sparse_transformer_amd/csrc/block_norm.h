@@ -38,5 +38,9 @@ hipError_t launch_block_norm(const BnArgs &a, bool layer, bool vec, hipStream_t 
 hipError_t launch_block_norm_backward(const BnArgs &a, bool layer, bool vec, hipStream_t s);
 int block_norm_groups(int T, int d);  // row groups of the backward pass
 int block_norm_rows(int T, int d);    // rows of each, none of them empty
+int block_norm_most_groups(int T, int d);  // the most groups of any call with up to T rows
+
+// Bytes of the partial rows of so many groups.
+inline size_t block_norm_ws(int groups, int d) { return (size_t)6 * groups * bn_pitch(d) * sizeof(float); }
 
 }  // namespace twell

@@ -656,18 +656,33 @@ static int bn_rows_at_once(int d) { return bn_row_threads(d) < 64 ? 64 / bn_row_
 
 // Row groups of the backward pass: about three workgroups of 256 threads per CU,
 // as many as its registers allow; each adds up its own rows' weight gradients.
-int block_norm_groups(int T, int d)
+struct BnSteps {
+    int steps, most, full;  // a wave's or a workgroup's steps; groups for all registers, and for a workgroup per CU
+};
+static BnSteps bn_steps(int T, int d)
 {
     const int k = bn_rows_at_once(d), threads = bn_row_threads(d) * k;
-    const int steps = (T + k - 1) / k;
-    const int most = BN_BWD_THREADS / threads;
+    return BnSteps{(T + k - 1) / k, BN_BWD_THREADS / threads, 256 * 256 / threads};
+}
+int block_norm_groups(int T, int d)
+{
+    const auto [steps, most, full] = bn_steps(T, d);
     int per = (steps + most - 1) / most;
     // few rows: up to 4 steps a group, until there is a workgroup of 256 threads per CU; each group costs a partial
     // row per vector (777 x 1001: 28 us at 195 groups, 24 at 389, 28 at 777)
-    const int full = 256 * 256 / threads;
     const int few = (steps + full - 1) / full < 4 ? (steps + full - 1) / full : 4;
     per = per > few ? per : few;
     return per > 0 ? (steps + per - 1) / per : 0;
+}
+
+// One step a group up to `full` groups, then no more until 4 steps each, then 4
+// steps a group up to `most`: what the rule above stays below.
+int block_norm_most_groups(int T, int d)
+{
+    const auto [steps, most, full] = bn_steps(T, d);
+    if (steps <= 4 * full)
+        return steps < full ? steps : full;
+    return (steps + 3) / 4 < most ? (steps + 3) / 4 : most;
 }
 
 // Whole steps (that a wave holds at once), so that (groups - 1) of them end before row T.

@@ -132,7 +132,7 @@ extern "C" {
 
 size_t twell_glu_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype)
 {
-    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_forward_ws(T, d, F, vdtype) : 0;
+    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_forward_most_ws(T, d, F, vdtype) : 0;
 }
 
 int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
@@ -148,7 +148,7 @@ int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t
     TWELL_TRY(check_mat(h));
     if (!aligned16(g) || !aligned16(u))
         return TWELL_E_ALIGN;
-    TWELL_TRY(check_ws(workspace, workspace_bytes, twell_glu_workspace_bytes(T, d, F, vdtype)));
+    TWELL_TRY(check_ws(workspace, workspace_bytes, twell::glu_forward_ws(T, d, F, vdtype)));
     twell::GluFwd a{};
     a.T = T;
     a.d = d;
@@ -166,7 +166,7 @@ int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t
 
 size_t twell_glu_backward_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype)
 {
-    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_backward_ws(T, d, F, vdtype).bytes : 0;
+    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_backward_most_ws(T, d, F, vdtype) : 0;
 }
 
 int twell_glu_backward(const void *x, const void *wg_t, const void *wu_t, const void *g, const void *u, const void *dh,
@@ -236,7 +236,7 @@ size_t twell_block_norm_workspace_bytes(int32_t T, int32_t d)
 {
     if (T < 0 || T > MOST_ROWS || d < 1 || d > twell::BN_MAX_D)
         return 0;
-    return (size_t)6 * twell::block_norm_groups(T, d) * twell::bn_pitch(d) * sizeof(float);
+    return twell::block_norm_ws(twell::block_norm_most_groups(T, d), d);
 }
 
 int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, const void *y, const void *dout,
@@ -268,7 +268,8 @@ int twell_block_norm_backward(const twell_block_norm_t *bn, const void *out, con
         }
         if (gated)
             TWELL_TRY(check_vec(dgate, rs));
-        TWELL_TRY(check_ws(workspace, workspace_bytes, twell_block_norm_workspace_bytes(bn->T, bn->d)));
+        TWELL_TRY(check_ws(workspace, workspace_bytes,
+                           twell::block_norm_ws(twell::block_norm_groups(bn->T, bn->d), bn->d)));
     }
     twell::BnArgs a = bn_args(bn, y != nullptr);
     a.res = bn_tensor(dn ? out : nullptr, bn->rdtype);

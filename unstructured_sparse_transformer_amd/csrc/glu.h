@@ -24,6 +24,7 @@ struct GluFwd {
 
 struct MulPlan {
     int tile, splits;  // of a product: which of the tiles, and into how many parts K is split
+    bool operator==(const MulPlan &o) const { return tile == o.tile && splits == o.splits; }
 };
 
 // The backward pass's workspace (dg and du first, then the splits' parts), and
@@ -51,6 +52,9 @@ struct GluBwd {
 __host__ __device__ inline int64_t glu_pitch(int F) { return 2 * (int64_t)F + 64; }
 
 size_t glu_forward_ws(int T, int d, int F, int vdtype);  // bytes
+// The most bytes of any call with up to T rows.
+size_t glu_forward_most_ws(int T, int d, int F, int vdtype);
+size_t glu_backward_most_ws(int T, int d, int F, int vdtype);
 
 hipError_t launch_glu(int vdtype, const GluFwd &a, hipStream_t s);
 hipError_t launch_glu_backward(int vdtype, const GluBwd &a, hipStream_t s);

@@ -499,10 +499,48 @@ static MulPlan forward_plan(int vdtype, int T, int d, int F)
     return vdtype == 1 ? mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d) : mul_plan(FWD_TILES_F32, 2, T, 2 * (int64_t)F, d);
 }
 
-size_t glu_forward_ws(int T, int d, int F, int vdtype)
+// The most bytes that a call with up to T rows needs; need(t) is a call's with t
+// rows: its plan and its bytes.  Inside 64 rows that fill the same tiles every
+// plan's estimate is linear in t (the parts' bytes): a plan that is the cheapest at
+// both ends of a range is so throughout, and needs the most at the range's end.
+// (18 us of the host at T = 8192, 2048 x 8192, for the backward pass 140.)
+template <typename N> static size_t most_bytes(int lo, const N &need, int hi, decltype(need(0)) first, decltype(need(0)) last)
 {
-    const int splits = forward_plan(vdtype, T, d, F).splits;
-    return splits > 1 ? (size_t)splits * 2 * T * F * sizeof(float) : 0;
+    const size_t most = first.bytes > last.bytes ? first.bytes : last.bytes;
+    if (hi - lo <= 1 || first.plan == last.plan)
+        return most;
+    const int mid = lo + (hi - lo) / 2;
+    const auto at = need(mid);
+    const size_t l = most_bytes(lo, need, mid, first, at), r = most_bytes(mid, need, hi, at, last);
+    return l > r ? l : r;
+}
+template <typename N> static size_t most_bytes_to(int T, const N &need)
+{
+    size_t most = 0;
+    for (int lo = (T - 1) / 64 * 64 + 1; lo > 0 && T > 0; lo -= 64) {
+        const int hi = T - lo < 63 ? T : lo + 63;
+        const size_t n = most_bytes(lo, need, hi, need(lo), need(hi));
+        most = n > most ? n : most;
+    }
+    return most;
+}
+
+static size_t forward_bytes(const MulPlan &plan, int T, int F)
+{
+    return plan.splits > 1 ? (size_t)plan.splits * 2 * T * F * sizeof(float) : 0;
+}
+size_t glu_forward_ws(int T, int d, int F, int vdtype) { return forward_bytes(forward_plan(vdtype, T, d, F), T, F); }
+
+size_t glu_forward_most_ws(int T, int d, int F, int vdtype)
+{
+    struct Need {
+        MulPlan plan;
+        size_t bytes;
+    };
+    return most_bytes_to(T, [&](int t) {
+        const MulPlan plan = forward_plan(vdtype, t, d, F);
+        return Need{plan, forward_bytes(plan, t, F)};
+    });
 }
 
 static dim3 join_grid(int64_t n)
@@ -636,6 +674,25 @@ GluWs glu_backward_ws(int T, int d, int F, int vdtype)
     w.part_dw = w.part_dx + up256_(w.dx.splits > 1 ? (size_t)w.dx.splits * T * d * 4 : 0);
     w.bytes = w.part_dw + (w.dw.splits > 1 ? (size_t)w.dw.splits * 2 * F * d * 4 : 0);
     return w;
+}
+
+size_t glu_backward_most_ws(int T, int d, int F, int vdtype)
+{
+    struct Plan {
+        MulPlan dx, dw;
+        bool together;
+        bool operator==(const Plan &o) const { return dx == o.dx && dw == o.dw && together == o.together; }
+    };
+    struct Need {
+        Plan plan;
+        size_t bytes;
+    };
+    auto need = [&](int t) {
+        const GluWs w = glu_backward_ws(t, d, F, vdtype);
+        return Need{Plan{w.dx, w.dw, w.together}, w.bytes};
+    };
+    const size_t none = need(0).bytes, most = most_bytes_to(T, need);
+    return most > none ? most : none;
 }
 
 // One launch of the products' workgroups (either may have none).
