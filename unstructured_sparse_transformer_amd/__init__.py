@@ -161,11 +161,12 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
-def _stream(stream) -> int | None:
+def _stream(stream, dev=None) -> int | None:
+    """A stream's handle; None: the current one, of the current GPU `dev` where the caller knows it."""
     if stream is None:
         import torch
         raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object (2.7 us less)
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return raw(torch.cuda.current_device() if dev is None else dev) if raw else torch.cuda.current_stream().cuda_stream
     return getattr(stream, "cuda_stream", stream)
 
 
@@ -453,7 +454,7 @@ def _tensor(fn: str, name: str, t, shape, dev: int, dtype=None) -> int:
 def _i32(n: int) -> int:
     """A count for a 32-bit argument.  One that does not fit becomes the largest, which is past the bounds that the C
     side checks (ctypes alone would keep its lower 32 bits)."""
-    return max(-1, min(n, (1 << 31) - 1))
+    return n if -1 <= n <= 0x7FFFFFFF else -1 if n < 0 else 0x7FFFFFFF
 
 
 def _workspace(fn: str, t, dev: int) -> tuple:
@@ -494,7 +495,7 @@ def twell_glu_forward(x, wg_t, wu_t, act: str, h, workspace=None, g=None, u=None
     out = (_tensor(fn, "h", h, (T, F), dev, dt), None if g is None else _tensor(fn, "g", g, (T, F), dev, dt),
            None if u is None else _tensor(fn, "u", u, (T, F), dev, dt))
     _check(fn, load().twell_glu_forward(*p, _i32(T), _i32(d), _i32(F), vdtype_of(dt), _act(fn, act), *out,
-                                        *_workspace(fn, workspace, dev), _stream(stream)))
+                                        *_workspace(fn, workspace, dev), _stream(stream, dev)))
 
 
 def twell_glu_backward_workspace_bytes(T: int, d: int, F: int, dtype) -> int:
@@ -516,7 +517,7 @@ def twell_glu_backward(x, wg_t, wu_t, g, u, dh, act: str, dx, dwg, dwu, workspac
     o = [None if t is None else _tensor(fn, k, t, s, dev, dt)
          for k, t, s in (("dx", dx, (T, d)), ("dwg", dwg, (F, d)), ("dwu", dwu, (F, d)))]
     _check(fn, load().twell_glu_backward(*p, _i32(T), _i32(d), _i32(F), vdtype_of(dt), _act(fn, act), *o,
-                                         *_workspace(fn, workspace, dev), _stream(stream)))
+                                         *_workspace(fn, workspace, dev), _stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- block norms
@@ -549,13 +550,13 @@ class BlockNorm:
         for k, p in at.items():
             setattr(self._desc, k, p)
         self.d, self.dev = first.numel(), dev
-        self._bound = [(w, w.data_ptr(), w.shape, w.dtype) for _, w in given]
+        self._bound = [(w, w.data_ptr(), self.d, w.dtype) for _, w in given]
 
     def desc(self, fn, dev, rows, y, gate, gate_span) -> TwellBlockNormT:
         T, d = rows.shape
-        for w, at, shape, dtype in self._bound:
+        for w, at, n, dtype in self._bound:
             # (its data may have been set anew)
-            if w.data_ptr() != at or w.shape != shape or w.dtype is not dtype or not w.is_contiguous():
+            if w.data_ptr() != at or w.numel() != n or w.dtype is not dtype or not w.is_contiguous():
                 self._bind()
                 break
         if self.d is not None and (d != self.d or dev != self.dev):
@@ -586,7 +587,7 @@ def twell_block_norm_forward(bn: BlockNorm, res, y, out, n, gate=None, gate_span
     if n is not None:
         p_n = _tensor(fn, "n", n, shape, dev)
         o.ndtype = vdtype_of(n.dtype)
-    _check(fn, load().twell_block_norm_forward(o, p_res, _ptr(y), p_out, p_n, _stream(stream)))
+    _check(fn, load().twell_block_norm_forward(o, p_res, _ptr(y), p_out, p_n, _stream(stream, dev)))
 
 
 def twell_block_norm_workspace_bytes(T: int, d: int) -> int:
@@ -617,7 +618,7 @@ def twell_block_norm_backward(bn: BlockNorm, out, y, dout, dn, dres, dy, workspa
           for k, t in (("dw_post", dw_post), ("db_post", db_post), ("dw_pre", dw_pre), ("db_pre", db_pre))]
     _check(fn, load().twell_block_norm_backward(o, p["out"], _ptr(y), p["dout"], p["dn"],
                                                 TWELL_F32 if dn is None else vdtype_of(dn.dtype), p_dres, p["dy"],
-                                                p_dgate, *dw, *_workspace(fn, workspace, dev), _stream(stream)))
+                                                p_dgate, *dw, *_workspace(fn, workspace, dev), _stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- the optimizer
