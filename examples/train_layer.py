@@ -1,11 +1,11 @@
-"""Training steps of a small stack of feed-forward layers, every step of it in the library's kernels.
+"""Training steps of a small stack of feed-forward layers in the library's kernels.
 
     python examples/train_layer.py [--ffn gated|sparse] [--steps 50] [--bits 8|32]
 
 A layer adds alpha * gate * norm(FFN(norm(stream))) to a 32-bit residual stream.  The norm after one FFN, the gate, the
 sum and the norm before the next FFN are one call.  The FFN is the dense gated product followed by a plain matrix
-product (``gated``), or the ReLU-sparse one on its hybrid activations (``sparse``).  The weights are 32-bit masters with
-16-bit copies for the layers; one call updates all of them.
+product of torch's (``gated``; its backward pass takes two more), or the ReLU-sparse one on its hybrid activations
+(``sparse``).  The weights are 32-bit masters with 16-bit copies for the layers; one call updates all of them.
 """
 
 import argparse

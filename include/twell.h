@@ -410,8 +410,8 @@ enum twell_act {
 
 /* g = x . W_g and u = x . W_u are written too where their pointers (device
  * [T][F] vdtype) are not NULL: the backward pass takes them.  h comes from g
- * and u before they are rounded.  For T <= 64 (bf16) the kernels are organised
- * for few tokens.  Inputs are finite; a NaN or an infinity spoils at most its
+ * and u before they are rounded.  For T <= 64 the kernels are organised for
+ * few tokens.  Inputs are finite; a NaN or an infinity spoils at most its
  * own row (of x) or column (of a weight).
  * workspace : device, >= twell_glu_workspace_bytes(T, d, F, vdtype) (where that
  * is 0 it may be NULL), 256-byte aligned, content ignored on entry (it holds

@@ -10,7 +10,7 @@
 // that an 8-bit code never depends on how a compiler groups the sums.
 //
 // Bound by memory: p, m, v read and written, the gradient read, the 16-bit
-// copy written, 30 bytes an element with 32-bit states and a bf16 gradient, 16
+// copy written, 28 bytes an element with 32-bit states and a bf16 gradient, 16
 // with 8-bit states.  One launch covers up to AW_BATCH tensors: their table is
 // in the kernel's arguments (no table to build in device memory, and a captured
 // graph keeps it), a workgroup finds its tensor by a binary search over the
@@ -19,9 +19,9 @@
 // consecutive elements a lane left gaps of 16 bytes between a store's pieces),
 // and the 256 elements that share a scale are one wave, so their largest value
 // needs no LDS.  All but the copies is read and written past the caches
-// (nontemporal): nothing of it is used again before the next step.  Measured: 233
-// us for 50 M elements with 32-bit states (6.5 TB/s; 268 us through the caches),
-// 320 us for 100 M with 8-bit states (5.0 TB/s; 326 us), 176 us to unpack those
+// (nontemporal): nothing of it is used again before the next step.  Measured: 235
+// us for 50 M elements with 32-bit states (6.0 TB/s; 268 us through the caches),
+// 311 us for 100 M with 8-bit states (5.2 TB/s; 326 us), 176 us to unpack those
 // (5.7 TB/s; 184 us).
 //
 // 8-bit states.  m: sign and 7 bits, sqrt(v): 8 bits, both the upper bits of

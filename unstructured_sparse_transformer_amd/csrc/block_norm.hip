@@ -19,8 +19,9 @@
 // mean and a variance are two passes over registers, not over memory.  All
 // sums are fp32: per thread, then over the row's lanes by DPP, then over the
 // waves through LDS.  8192 x 2048: forward 26 us in bf16 (134 MB, 5.2 TB/s),
-// backward 52 us in bf16 (201 MB) and 88 us with fp32 streams (403 MB, 4.6 TB/s),
-// 6 us of them the second launch's sums of the partial rows.
+// backward 53 us in bf16 (201 MB) and 88 us with fp32 streams (403 MB, 4.6 TB/s),
+// 6 us of them the second launch's sums of the partial rows; 29 and 97 us (forward,
+// and backward in fp32) where a call's inputs are others than the last one's.
 #include "block_norm.h"
 #include "twell_device.h"
 #include "wave_ops.h"
@@ -646,8 +647,8 @@ __global__ __launch_bounds__(256) void block_norm_reduce_kernel(BnArgs a)
 }
 
 // The threads of a row, and how many rows a wave holds at once.  Narrow rows side
-// by side: 65536 rows of 64 take 8 us forward (29 us with a wave for each) and 34
-// backward (95), 262144 rows of 16 take 8 (101) and 36 (302).
+// by side: 65536 rows of 64 take 9 us forward in bf16 (29 us with a wave for each) and
+// 36 backward with fp32 streams (95), 262144 rows of 16 take 9 (101) and 36 (302).
 static int bn_row_threads(int d)
 {
     return d <= 16 ? 2 : d <= 32 ? 4 : d <= 64 ? 8 : d <= 128 ? 16 : d <= 256 ? 32 : d <= 512 ? 64 : d <= 1024 ? 128 : d <= 2048 ? 256 : d <= 4096 ? 512 : 1024;

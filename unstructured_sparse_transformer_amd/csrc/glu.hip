@@ -9,7 +9,9 @@
 //   dg = dh u act'(g), du = dh act(g)            one pass, [T][dg | du]
 //   dx = dg W_g + du W_u                         one product, K = 2 F
 //   dW_g = dg^T x, dW_u = du^T x                 one product, M = 2 F, K = T
-// dg and du are rounded to the element type, as the matrix units take them.
+// dg and du are rounded to the element type, as the matrix units take them: in
+// bf16 the gradients are off by 2.3e-3 of their size, where products rounded once are
+// by 1.7e-3; operands of 32 bits would take the fp32 units, a ninth of the rate.
 #include "dense_gemm.h"
 #include "glu.h"
 
@@ -71,8 +73,8 @@ template <bool FAST> __device__ __forceinline__ float glu_act_grad(float g, int 
 }
 
 // ------------------------------------------------------------------ forward
-// Bound by the matrix units.  bf16, 8192 x 2048 x 8192 with g and u kept: 478 us,
-// 1.15 PFLOP/s; the product by itself takes 420 us at the clock the chip's power
+// Bound by the matrix units.  bf16, 8192 x 2048 x 8192 with g and u kept: 471 us
+// on the same inputs again, 487 us on others (1.13 PFLOP/s); the product by itself takes 420 us at the clock the chip's power
 // cap leaves it, the rest is 403 MB of results that leave between the tiles
 // (workgroups started up to 13 us apart, so that some store while others
 // multiply: no change).  fp32, 1500 x 2048 x 2048: 188 us, 134 of 157 TFLOP/s.
@@ -144,8 +146,8 @@ glu_kernel(GluFwd p)
 // Few rows: the weights stream through a ring of S LDS slots, one stage (128
 // bytes, 64 bf16 or 32 fp32 K elements, of the workgroup's NB rows of W_g, its NB of W_u, and of x) a slot,
 // with the copies of S - 1 stages in flight, two workgroups per CU.  Bound by
-// reading the weights once: 67 MB of the 2B-like layer in 12.9 us at T = 1
-// (5.2 TB/s) and 13.5 us at T = 64.  Workgroups start at different stages:
+// reading the weights once: 67 MB of the 2B-like layer in 12.7 us at T = 1
+// (5.3 TB/s) and 13.4 us at T = 64.  Workgroups start at different stages:
 // W's rows are a power of two apart, and all of them at the same columns meet
 // few of the memory channels (17.6 us).  The 4 waves share a stage by K,
 // 16 elements each, and their partial products meet in LDS at the end, added in
