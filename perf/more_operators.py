@@ -168,14 +168,14 @@ def prepare(case, seed):
         del z
         if op == "logprob_fwd":
             k = case["k"]
-            st.update(logp=new(T), lse=new(T), entropy=new(T), top_logp=new(T, k) if k else None,
+            st.update(logp=new(T), norm=new(T, 2), entropy=new(T), top_logp=new(T, k) if k else None,
                       top_idx=torch.empty((T, k), device="cuda", dtype=torch.int32) if k else None)
             if own:
                 import unstructured_sparse_transformer_amd as tw
                 st["ws"] = tw.logprob_workspace(T, V, k)
         else:
             got = _logprob(st, 0)
-            st.update(lse=got["lse"], entropy=got["entropy"], dlogp=rnd(T, scale=1 / T),
+            st.update(norm=got["norm"], entropy=got["entropy"], dlogp=rnd(T, scale=1 / T),
                       dentropy=rnd(T, scale=0.1 / T) if case["entropy"] else None, dlogits=torch.empty_like(st["logits"]))
     elif op == "act_pack":
         d = case["d"]
@@ -221,36 +221,38 @@ def _masked(z):
 def _logprob(st, k):
     c = st["case"]
     z, none = _masked(st["logits"].float())
-    z *= c["scale"]
     top = z.amax(1, keepdim=True)
     z -= top
+    z *= c["scale"]
     e = torch.exp(z).masked_fill_(none, 0)
     total, weighted = e.sum(1), z.masked_fill_(none, 0).mul_(e).sum(1)
     del z, e
     empty = none.all(1)
-    lse = (top[:, 0] + torch.log(total)).masked_fill(empty, -math.inf)
-    got = {"lse": lse, "entropy": (torch.log(total) - weighted / total).masked_fill(empty, 0)}
+    size = torch.log(total).masked_fill_(empty, 0)
+    got = {"norm": torch.stack((top[:, 0].masked_fill(empty, -math.inf), size), 1),
+           "entropy": (size - weighted / total).masked_fill(empty, 0)}
     at = st["targets"].long()
     there = (at >= 0) & (at < c["V"])
     at = at.clamp(0, c["V"] - 1)[:, None]
-    logp = st["logits"].gather(1, at).float()[:, 0] * c["scale"] - lse.masked_fill(empty, 0)
-    got["logp"] = logp.masked_fill(~there, 0)
+    logp = (st["logits"].gather(1, at).float() - top)[:, 0] * c["scale"] - size
+    got["logp"] = logp.masked_fill(empty, -math.inf).masked_fill(~there, 0)
     if k:
         # the value's bits in an order of whole numbers, then the index, lowest first
         b = st["logits"].float().view(torch.int32).to(torch.int64)
         b = torch.where(b < 0, -(b & 0x7FFFFFFF), b)
         idx = torch.arange(c["V"], device="cuda")
         got["top_idx"] = torch.topk((b << 32) - idx, k, dim=1).indices.to(torch.int32)
-        val = st["logits"].gather(1, got["top_idx"].long()).float() * c["scale"]
-        got["top_logp"] = val - lse.masked_fill(empty, 0)[:, None]
+        val = st["logits"].gather(1, got["top_idx"].long()).float() - top
+        got["top_logp"] = (val * c["scale"] - size[:, None]).masked_fill(empty[:, None], -math.inf)
     return got
 
 
 def _plain_logprob_bwd(st):
     c = st["case"]
     z, none = _masked(st["logits"].float())
-    empty = st["lse"] == -math.inf
-    logp = z * c["scale"] - st["lse"].masked_fill(empty, 0)[:, None]
+    top, size = st["norm"].unbind(1)
+    empty = top == -math.inf
+    logp = (z - top.masked_fill(empty, 0)[:, None]) * c["scale"] - size[:, None]
     p = torch.exp(logp).masked_fill_(none, 0)
     at = st["targets"].long()
     there = (at >= 0) & (at < c["V"]) & ~empty
@@ -327,11 +329,11 @@ def run(st):
         tw.twell_embed_backward(st["ids"], st["dout"], st["dtable"], st["ws"], scale=st["scale"], accumulate=c["accumulate"])
         return {"dtable": st["dtable"]}
     if op == "logprob_fwd":
-        tw.twell_logprob_forward(st["logits"], st["targets"], st["logp"], st["lse"], st["ws"], scale=c["scale"],
+        tw.twell_logprob_forward(st["logits"], st["targets"], st["logp"], st["norm"], st["ws"], scale=c["scale"],
                                  entropy=st["entropy"], top_logp=st["top_logp"], top_idx=st["top_idx"])
-        return {k: st[k] for k in ("lse", "entropy", "logp", "top_idx", "top_logp") if st[k] is not None}
+        return {k: st[k] for k in ("norm", "entropy", "logp", "top_idx", "top_logp") if st[k] is not None}
     if op == "logprob_bwd":
-        tw.twell_logprob_backward(st["logits"], st["targets"], st["lse"], st["dlogp"], st["dlogits"], scale=c["scale"],
+        tw.twell_logprob_backward(st["logits"], st["targets"], st["norm"], st["dlogp"], st["dlogits"], scale=c["scale"],
                                   entropy=st["entropy"], dentropy=st["dentropy"])
         return {"dlogits": st["dlogits"]}
     if op == "act_pack":
@@ -386,7 +388,9 @@ def exact(case, seed):
         given = st["targets"] >= 0
         at = torch.where(given, st["targets"], 0).long()[:, None]
         if op == "logprob_fwd":
-            got = {"lse": lse[:, 0], "entropy": entropy[:, 0].clone(), "logp": torch.where(given, logp.gather(1, at)[:, 0], 0.0)}
+            top = st["logits"].double().amax(1)
+            size = torch.where(empty[:, 0], 0.0, lse[:, 0] - top * case["scale"])
+            got = {"norm": torch.stack((top, size), 1), "entropy": entropy[:, 0].clone(), "logp": torch.where(given, logp.gather(1, at)[:, 0], 0.0)}
             if case["k"]:  # the indices are whole numbers: the values at the largest ones, whichever of equal ones they are
                 got.update(top_idx=None, top_logp=torch.topk(logp, case["k"], dim=1).values)
             return got
