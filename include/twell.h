@@ -19,7 +19,11 @@
  *   training    twell_dense_to_hybrid, twell_hybrid_to_dense,
  *               twell_compact_hybrid, twell_compact_to_dense, twell_ffn_backward
  *   dense       twell_glu_forward, twell_glu_backward
+ *   8 bits      twell_act_pack, twell_act_unpack, twell_glu_forward_packed,
+ *               twell_glu_backward_packed
  *   norms       twell_block_norm_forward, twell_block_norm_backward
+ *   tokens      twell_embed_forward, twell_embed_backward,
+ *               twell_logprob_forward, twell_logprob_backward
  *   optimizer   twell_adamw_step, twell_adamw_unpack
  *
  * Notation: T tokens (rows), d model width, F hidden width (d_ff), w tile
@@ -437,6 +441,44 @@ TWELL_API int twell_glu_backward(const void *x, const void *wg_t, const void *wu
                                  void *stream);
 TWELL_API size_t twell_glu_backward_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype);
 
+/* ---- Activations kept in 8 bits --------------------------------------------
+ * What a training step keeps for its backward pass, in half the memory: 32
+ * consecutive elements of a row (the last block of a row may have fewer) share a
+ * scale, their largest magnitude / 127 in bf16, rounded up; code = x / scale
+ * rounded to nearest even, value = code * scale.  A block below 1e-30 is held as
+ * zeros; one that meets an infinity or a NaN reads back as NaN as a whole.  The
+ * struct is HOST memory, read during the call only. */
+typedef struct twell_packed_t {
+    int8_t *code; /* device [T][d] */
+    void *scale;  /* device [T][ceil(d / 32)] bf16 */
+} twell_packed_t;
+
+/* x, out : device [T][d] vdtype, aligned as their elements; T <= 2^30,
+ * d <= 2^20. */
+TWELL_API int twell_act_pack(const void *x, int32_t T, int32_t d, int32_t vdtype, const twell_packed_t *to,
+                             void *stream);
+TWELL_API int twell_act_unpack(const twell_packed_t *from, int32_t T, int32_t d, int32_t vdtype, void *out,
+                               void *stream);
+
+/* twell_glu_forward in bf16 (same sizes and types) that keeps g and u, before
+ * they are rounded to bf16, in 8 bits ([T][F], codes 16-byte aligned); h is the
+ * same.  An fp32 layer packs what twell_glu_forward stores.
+ * workspace : >= twell_glu_packed_workspace_bytes(T, d, F), otherwise as there. */
+TWELL_API int twell_glu_forward_packed(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d,
+                                       int32_t F, int32_t act, void *h, const twell_packed_t *g,
+                                       const twell_packed_t *u, void *workspace, size_t workspace_bytes, void *stream);
+TWELL_API size_t twell_glu_packed_workspace_bytes(int32_t T, int32_t d, int32_t F);
+
+/* twell_glu_backward in bf16 from the values that g's and u's codes stand for.
+ * h (device [T][F] bf16, or NULL) receives act(g) * u of those values, for the
+ * gradient of the product after it: the forward's h need not be kept.  Any of h,
+ * dx, and dwg with dwu may be NULL, not all.
+ * workspace : >= twell_glu_backward_workspace_bytes(T, d, F, TWELL_BF16). */
+TWELL_API int twell_glu_backward_packed(const void *x, const void *wg_t, const void *wu_t, const twell_packed_t *g,
+                                        const twell_packed_t *u, const void *dh, int32_t T, int32_t d, int32_t F,
+                                        int32_t act, void *h, void *dx, void *dwg, void *dwu, void *workspace,
+                                        size_t workspace_bytes, void *stream);
+
 /* ---- Block norms -----------------------------------------------------------
  * The norms before and after a block with the block's gate, residual scale and
  * residual sum, for T rows of d:
@@ -490,6 +532,61 @@ TWELL_API int twell_block_norm_backward(const twell_block_norm_t *bn, const void
                                         const void *dout, const void *dn, int32_t dndtype, void *dres, void *dy,
                                         void *dgate, float *dw_post, float *db_post, float *dw_pre, float *db_pre,
                                         void *workspace, size_t workspace_bytes, void *stream);
+
+/* ---- Token embedding -------------------------------------------------------
+ * out[t] = scale * table[ids[t]] for T tokens, rows of d of a table of V.
+ * ids : device [T] of int32 or int64 (id_bits 32 or 64).  An id outside 0 .. V-1
+ * (padding) gives a row of zeros, and adds to no gradient.
+ * table [V][d] vdtype, out [T][d] odtype: TWELL_BF16 or TWELL_F32 each, aligned as
+ * their elements.  T, V <= 2^30, d <= 2^20, T d < 2^41. */
+TWELL_API int twell_embed_forward(const void *ids, int32_t id_bits, int32_t T, const void *table, int32_t V, int32_t d,
+                                  int32_t vdtype, float scale, void *out, int32_t odtype, void *stream);
+
+/* The table's gradient: row v of dtable is scale * the sum of dout's rows whose id
+ * is v, in fp32 and in an order fixed by the ids alone (no float atomics).
+ *   accumulate 0 : dtable [V][d] vdtype is overwritten (rows without tokens: 0);
+ *              1 : the sums are added to what is there (a table that the head
+ *                  shares), and rows without tokens are not touched.
+ * workspace : device, >= twell_embed_workspace_bytes(T, V, d) (never shrinking as
+ * T grows), 256-byte aligned, content ignored on entry. */
+TWELL_API int twell_embed_backward(const void *ids, int32_t id_bits, int32_t T, const void *dout, int32_t dodtype,
+                                   int32_t V, int32_t d, float scale, int32_t accumulate, void *dtable, int32_t vdtype,
+                                   void *workspace, size_t workspace_bytes, void *stream);
+TWELL_API size_t twell_embed_workspace_bytes(int32_t T, int32_t V, int32_t d);
+
+/* ---- Log probabilities -----------------------------------------------------
+ * From logits z [T][V] (vdtype, rows `ld` >= V elements apart, aligned as their
+ * elements) times scale > 0 (an inverse temperature), for each row:
+ *   norm     [T][2] float: m = the largest logit, and L = log sum exp(scale (z - m))
+ *   logp     [T] float: of the token targets[t], scale (z - m) - L.  targets :
+ *            device int32 or int64 [T] (id_bits); one outside 0 .. V-1 has logp 0
+ *            and no gradient from dlogp.
+ *   entropy  [T] float: - sum p log p
+ *   top_idx, top_logp [T][k] int32, float: the k tokens with the largest logits,
+ *            largest first, of equal ones the lowest index first, and their log
+ *            probabilities; k <= 64, k <= V.
+ * Each of logp (then targets too), norm and entropy may be NULL, k may be 0; not
+ * all of them.  A logit of -inf is a masked token: p = 0, logp = -inf.  A row of
+ * nothing else has m = logp = -inf, L = entropy = 0.  A NaN or +inf in a row makes
+ * its results NaN, and its top_idx 0 .. k-1.  Sums are fp32 in a fixed order.
+ * workspace : device, >= twell_logprob_workspace_bytes(T, V, k) (where that is 0 it
+ * may be NULL; never shrinking as T grows), 256-byte aligned, content ignored on
+ * entry. */
+TWELL_API int twell_logprob_forward(const void *logits, int64_t ld, int32_t T, int32_t V, int32_t vdtype, float scale,
+                                    const void *targets, int32_t id_bits, float *logp, float *norm, float *entropy,
+                                    float *top_logp, int32_t *top_idx, int32_t k, void *workspace,
+                                    size_t workspace_bytes, void *stream);
+TWELL_API size_t twell_logprob_workspace_bytes(int32_t T, int32_t V, int32_t k);
+
+/* The logits' gradient from the forward's norm, dlogp [T] float (with targets) and
+ * dentropy [T] float (with the forward's entropy), either of which may be NULL:
+ *   dz[v] = scale (dlogp (1[v = target] - p[v]) - dentropy p[v] (log p[v] + entropy))
+ * dlogits [T] rows of V, vdtype, `ldd` elements apart; may be logits (then ldd =
+ * ld).  A row of masked tokens only gets zeros, one with a NaN in norm NaN. */
+TWELL_API int twell_logprob_backward(const void *logits, int64_t ld, int32_t T, int32_t V, int32_t vdtype, float scale,
+                                     const void *targets, int32_t id_bits, const float *norm, const float *entropy,
+                                     const float *dlogp, const float *dentropy, void *dlogits, int64_t ldd,
+                                     void *stream);
 
 /* ---- Optimizer -------------------------------------------------------------
  * One AdamW step over many tensors at once: for every element

@@ -15,7 +15,10 @@ The functions carry the C names (``include/twell.h``):
 ``twell_compact_to_dense``, ``twell_ffn_backward``,
 ``twell_ffn_backward_workspace_bytes``, ``twell_glu_forward``, ``twell_glu_workspace_bytes``,
 ``twell_glu_backward``, ``twell_glu_backward_workspace_bytes``, ``twell_block_norm_forward``,
-``twell_block_norm_workspace_bytes``, ``twell_block_norm_backward``, ``twell_adamw_step``, ``twell_adamw_unpack``.
+``twell_block_norm_workspace_bytes``, ``twell_block_norm_backward``, ``twell_adamw_step``, ``twell_adamw_unpack``,
+``twell_act_pack``, ``twell_act_unpack``, ``twell_glu_forward_packed``, ``twell_glu_packed_workspace_bytes``,
+``twell_glu_backward_packed``, ``twell_embed_forward``, ``twell_embed_backward``, ``twell_embed_workspace_bytes``,
+``twell_logprob_forward``, ``twell_logprob_workspace_bytes``, ``twell_logprob_backward``.
 
 One layer's forward pass, bf16 (x [T][d], W_g^T and W_u^T [F][d], W_d [F][d],
 all contiguous on the GPU; y [T][d] fp32)::
@@ -51,6 +54,9 @@ EXPORTS = ("twell_ffn_forward", "twell_ffn_from_gate", "twell_pack_gate", "twell
            "twell_ffn_backward_workspace_bytes", "twell_ffn_backward", "twell_glu_workspace_bytes",
            "twell_glu_forward", "twell_glu_backward_workspace_bytes", "twell_glu_backward", "twell_block_norm_forward",
            "twell_block_norm_workspace_bytes", "twell_block_norm_backward", "twell_adamw_step", "twell_adamw_unpack",
+           "twell_act_pack", "twell_act_unpack", "twell_glu_forward_packed", "twell_glu_packed_workspace_bytes",
+           "twell_glu_backward_packed", "twell_embed_forward", "twell_embed_backward", "twell_embed_workspace_bytes",
+           "twell_logprob_forward", "twell_logprob_workspace_bytes", "twell_logprob_backward",
            "twell_status_str", "twell_version")
 
 
@@ -73,6 +79,10 @@ class TwellBlockNormT(ctypes.Structure):
                 ("wdtype", ctypes.c_int32), ("reserved", ctypes.c_int32), ("gate", ctypes.c_void_p),
                 ("w_post", ctypes.c_void_p), ("b_post", ctypes.c_void_p), ("w_pre", ctypes.c_void_p),
                 ("b_pre", ctypes.c_void_p)]
+
+
+class TwellPackedT(ctypes.Structure):
+    _fields_ = [("code", ctypes.c_void_p), ("scale", ctypes.c_void_p)]
 
 
 class TwellAdamWTensorT(ctypes.Structure):
@@ -141,6 +151,18 @@ def load(path: str = LIB_PATH):
     F64 = ctypes.c_double
     lib.twell_adamw_step.argtypes = [P, I32, I32, F64, F64, F64, F64, ctypes.c_int64, ctypes.c_uint32, P, P]
     lib.twell_adamw_unpack.argtypes = [P, I32, P]
+    F32, I64, SIZE, PK = ctypes.c_float, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(TwellPackedT)
+    lib.twell_act_pack.argtypes = [P, I32, I32, I32, PK, P]
+    lib.twell_act_unpack.argtypes = [PK, I32, I32, I32, P, P]
+    lib.twell_glu_forward_packed.argtypes = [P, P, P, I32, I32, I32, I32, P, PK, PK, P, SIZE, P]
+    lib.twell_glu_backward_packed.argtypes = [P, P, P, PK, PK, P, I32, I32, I32, I32, P, P, P, P, P, SIZE, P]
+    lib.twell_embed_forward.argtypes = [P, I32, I32, P, I32, I32, I32, F32, P, I32, P]
+    lib.twell_embed_backward.argtypes = [P, I32, I32, P, I32, I32, I32, F32, I32, P, I32, P, SIZE, P]
+    lib.twell_logprob_forward.argtypes = [P, I64, I32, I32, I32, F32, P, I32, P, P, P, P, P, I32, P, SIZE, P]
+    lib.twell_logprob_backward.argtypes = [P, I64, I32, I32, I32, F32, P, I32, P, P, P, P, P, I64, P]
+    for fn in (lib.twell_glu_packed_workspace_bytes, lib.twell_embed_workspace_bytes, lib.twell_logprob_workspace_bytes):
+        fn.argtypes = [I32, I32, I32]
+        fn.restype = SIZE
     lib.twell_status_str.argtypes = [ctypes.c_int]
     lib.twell_status_str.restype = ctypes.c_char_p
     lib.twell_version.restype = ctypes.c_int
@@ -150,7 +172,9 @@ def load(path: str = LIB_PATH):
                lib.twell_dense_to_hybrid, lib.twell_hybrid_to_dense, lib.twell_compact_hybrid,
                lib.twell_compact_to_dense, lib.twell_ffn_backward, lib.twell_glu_forward,
                lib.twell_glu_backward, lib.twell_block_norm_forward,
-               lib.twell_block_norm_backward, lib.twell_adamw_step, lib.twell_adamw_unpack):
+               lib.twell_block_norm_backward, lib.twell_adamw_step, lib.twell_adamw_unpack, lib.twell_act_pack,
+               lib.twell_act_unpack, lib.twell_glu_forward_packed, lib.twell_glu_backward_packed, lib.twell_embed_forward,
+               lib.twell_embed_backward, lib.twell_logprob_forward, lib.twell_logprob_backward):
         fn.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -518,6 +542,204 @@ def twell_glu_backward(x, wg_t, wu_t, g, u, dh, act: str, dx, dwg, dwu, workspac
          for k, t, s in (("dx", dx, (T, d)), ("dwg", dwg, (F, d)), ("dwu", dwu, (F, d)))]
     _check(fn, load().twell_glu_backward(*p, _i32(T), _i32(d), _i32(F), vdtype_of(dt), _act(fn, act), *o,
                                          *_workspace(fn, workspace, dev), _stream(stream, dev)))
+
+
+# ---------------------------------------------------------------- activations kept in 8 bits
+ACT_BLOCK = 32  # elements of a row that share a scale
+
+
+@dataclass
+class PackedAct:
+    """Activations [T][d] in 8 bits: ``code`` int8 [T][d], ``scale`` bfloat16 [T][ceil(d / 32)]."""
+    code: object
+    scale: object
+
+    @classmethod
+    def empty(cls, T, d, device="cuda"):
+        import torch
+        return cls(torch.empty((T, d), dtype=torch.int8, device=device),
+                   torch.empty((T, -(-d // ACT_BLOCK)), dtype=torch.bfloat16, device=device))
+
+    def desc(self, fn: str, name: str, shape, dev: int) -> TwellPackedT:
+        import torch
+        T, d = shape
+        return TwellPackedT(_tensor(fn, name + ".code", self.code, (T, d), dev, torch.int8),
+                            _tensor(fn, name + ".scale", self.scale, (T, -(-d // ACT_BLOCK)), dev, torch.bfloat16))
+
+
+def _packed(fn: str, name: str, p, shape, dev: int) -> TwellPackedT:
+    if not isinstance(p, PackedAct):
+        raise TypeError(f"{fn}: {name} must be a PackedAct, not {type(p).__name__}")
+    return p.desc(fn, name, shape, dev)
+
+
+def twell_act_pack(x, packed: PackedAct, stream=None):
+    """The codes and scales of x [T][d] (float32 or bfloat16)."""
+    fn = "twell_act_pack"
+    dev, (T, d) = _device(fn, x), x.shape
+    p = _tensor(fn, "x", x, (T, d), dev)
+    to = _packed(fn, "packed", packed, (T, d), dev)
+    _check(fn, load().twell_act_pack(p, _i32(T), _i32(d), vdtype_of(x.dtype), to, _stream(stream, dev)))
+
+
+def twell_act_unpack(packed: PackedAct, out, stream=None):
+    """The values that the codes stand for, in out's type (float32: as they are, bfloat16: rounded)."""
+    fn = "twell_act_unpack"
+    dev, (T, d) = _device(fn, out), out.shape
+    p = _tensor(fn, "out", out, (T, d), dev)
+    source = _packed(fn, "packed", packed, (T, d), dev)
+    _check(fn, load().twell_act_unpack(source, _i32(T), _i32(d), vdtype_of(out.dtype), p, _stream(stream, dev)))
+
+
+def twell_glu_packed_workspace_bytes(T: int, d: int, F: int) -> int:
+    return int(load().twell_glu_packed_workspace_bytes(_i32(T), _i32(d), _i32(F)))
+
+
+def glu_packed_workspace(T: int, d: int, F: int, device="cuda"):
+    """A workspace tensor for twell_glu_forward_packed with up to T rows, or None where none of these needs one."""
+    import torch
+    n = twell_glu_packed_workspace_bytes(T, d, F)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def twell_glu_forward_packed(x, wg_t, wu_t, act: str, h, g: PackedAct, u: PackedAct, workspace=None, stream=None):
+    """twell_glu_forward in bfloat16, with g and u kept in 8 bits."""
+    import torch
+    fn = "twell_glu_forward_packed"
+    dev, (T, d), F = _device(fn, x), x.shape, wg_t.shape[0]
+    p = [_tensor(fn, k, t, s, dev, torch.bfloat16) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)),
+                                                                   ("wu_t", wu_t, (F, d)), ("h", h, (T, F)))]
+    kept = [_packed(fn, k, t, (T, F), dev) for k, t in (("g", g), ("u", u))]
+    _check(fn, load().twell_glu_forward_packed(*p[:3], _i32(T), _i32(d), _i32(F), _act(fn, act), p[3], *kept,
+                                               *_workspace(fn, workspace, dev), _stream(stream, dev)))
+
+
+def twell_glu_backward_packed(x, wg_t, wu_t, g: PackedAct, u: PackedAct, dh, act: str, dx, dwg, dwu, workspace, h=None,
+                              stream=None):
+    """twell_glu_backward in bfloat16 from g and u in 8 bits (workspace: glu_backward_workspace); h (optional) receives
+    act(g) * u of these.  dx, or both of dwg and dwu, may be None."""
+    import torch
+    fn = "twell_glu_backward_packed"
+    dev, (T, d), F = _device(fn, x), x.shape, wg_t.shape[0]
+    p = [_tensor(fn, k, t, s, dev, torch.bfloat16) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)),
+                                                                   ("wu_t", wu_t, (F, d)), ("dh", dh, (T, F)))]
+    kept = [_packed(fn, k, t, (T, F), dev) for k, t in (("g", g), ("u", u))]
+    o = [None if t is None else _tensor(fn, k, t, s, dev, torch.bfloat16)
+         for k, t, s in (("h", h, (T, F)), ("dx", dx, (T, d)), ("dwg", dwg, (F, d)), ("dwu", dwu, (F, d)))]
+    _check(fn, load().twell_glu_backward_packed(*p[:3], *kept, p[3], _i32(T), _i32(d), _i32(F), _act(fn, act), *o,
+                                                *_workspace(fn, workspace, dev), _stream(stream, dev)))
+
+
+# ---------------------------------------------------------------- token embedding
+def _ids(fn: str, name: str, t, T: int, dev: int) -> tuple:
+    """The pointer of token ids [T] and their bits."""
+    import torch
+    p = _tensor(fn, name, t, (T,), dev)
+    if t.dtype is torch.int64:
+        return p, 64
+    if t.dtype is torch.int32:
+        return p, 32
+    raise TypeError(f"{fn}: {name} must be torch.int32 or torch.int64, not {t.dtype}")
+
+
+def twell_embed_forward(ids, table, out, scale: float = 1.0, stream=None):
+    """out [T][d] = scale * table [V][d] at ids [T] (int32 or int64); zeros where an id is none of 0 .. V-1."""
+    fn = "twell_embed_forward"
+    dev, (V, d), T = _device(fn, table), table.shape, ids.shape[0]
+    p, bits = _ids(fn, "ids", ids, T, dev)
+    rows, to = _tensor(fn, "table", table, (V, d), dev), _tensor(fn, "out", out, (T, d), dev)
+    _check(fn, load().twell_embed_forward(p, bits, _i32(T), rows, _i32(V), _i32(d), vdtype_of(table.dtype), scale, to,
+                                          vdtype_of(out.dtype), _stream(stream, dev)))
+
+
+def twell_embed_workspace_bytes(T: int, V: int, d: int) -> int:
+    return int(load().twell_embed_workspace_bytes(_i32(T), _i32(V), _i32(d)))
+
+
+def embed_workspace(T: int, V: int, d: int, device="cuda"):
+    """A workspace tensor for twell_embed_backward with up to T tokens."""
+    import torch
+    return torch.empty(max(twell_embed_workspace_bytes(T, V, d), 256), dtype=torch.uint8, device=device)
+
+
+def twell_embed_backward(ids, dout, dtable, workspace, scale: float = 1.0, accumulate: bool = False, stream=None):
+    """dtable [V][d] = scale * the sums of dout's rows [T][d] by id, overwritten, or with accumulate added to."""
+    fn = "twell_embed_backward"
+    dev, (V, d), T = _device(fn, dtable), dtable.shape, ids.shape[0]
+    p, bits = _ids(fn, "ids", ids, T, dev)
+    rows, to = _tensor(fn, "dout", dout, (T, d), dev), _tensor(fn, "dtable", dtable, (V, d), dev)
+    _check(fn, load().twell_embed_backward(p, bits, _i32(T), rows, vdtype_of(dout.dtype), _i32(V), _i32(d), scale,
+                                           int(bool(accumulate)), to, vdtype_of(dtable.dtype),
+                                           *_workspace(fn, workspace, dev), _stream(stream, dev)))
+
+
+# ---------------------------------------------------------------- log probabilities
+def _logits(fn: str, name: str, t, dev: int) -> tuple:
+    """The pointer of logits [T][V] whose rows are contiguous, and the elements from one row to the next."""
+    T, V = t.shape
+    if t.get_device() != dev:
+        raise ValueError(f"{fn}: {name} is on {t.device}, not on cuda:{dev}")
+    ld = t.stride(0) if T > 1 else V
+    if (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"{fn}: {name} must have contiguous rows that do not overlap")
+    return t.data_ptr(), ld
+
+
+def twell_logprob_workspace_bytes(T: int, V: int, k: int = 0) -> int:
+    return int(load().twell_logprob_workspace_bytes(_i32(T), _i32(V), _i32(k)))
+
+
+def logprob_workspace(T: int, V: int, k: int = 0, device="cuda"):
+    """A workspace tensor for twell_logprob_forward with up to T rows, or None where none of these needs one."""
+    import torch
+    n = twell_logprob_workspace_bytes(T, V, k)
+    return torch.empty(n, dtype=torch.uint8, device=device) if n else None
+
+
+def twell_logprob_forward(logits, targets, logp, norm, workspace=None, scale: float = 1.0, entropy=None, top_logp=None,
+                          top_idx=None, stream=None):
+    """From logits [T][V] (rows may be strided) times scale: logp [T] of targets [T] (int32 or int64; both may be None),
+    norm [T][2] (each row's largest logit, and the logarithm of the sum relative to it), entropy [T], and the k most
+    likely tokens top_idx [T][k] (int32) with their top_logp [T][k]; float32, each may be None (see include/twell.h)."""
+    import torch
+    fn = "twell_logprob_forward"
+    dev, (T, V) = _device(fn, logits), logits.shape
+    z, ld = _logits(fn, "logits", logits, dev)
+    if (logp is None) != (targets is None):
+        raise ValueError(f"{fn}: targets and logp go together")
+    if (top_logp is None) != (top_idx is None):
+        raise ValueError(f"{fn}: top_logp and top_idx go together")
+    ids, bits = (None, 32) if targets is None else _ids(fn, "targets", targets, T, dev)
+    k = 0 if top_idx is None else top_idx.shape[-1]
+    o = [None if t is None else _tensor(fn, name, t, s, dev, torch.float32)
+         for name, t, s in (("logp", logp, (T,)), ("norm", norm, (T, 2)), ("entropy", entropy, (T,)),
+                            ("top_logp", top_logp, (T, k)))]
+    idx = None if top_idx is None else _tensor(fn, "top_idx", top_idx, (T, k), dev, torch.int32)
+    _check(fn, load().twell_logprob_forward(z, ld, _i32(T), _i32(V), vdtype_of(logits.dtype), scale, ids, bits, *o, idx,
+                                            _i32(k), *_workspace(fn, workspace, dev), _stream(stream, dev)))
+
+
+def twell_logprob_backward(logits, targets, norm, dlogp, dlogits, scale: float = 1.0, entropy=None, dentropy=None,
+                           stream=None):
+    """dlogits [T][V] (logits' type; may be logits) from the forward's norm, dlogp [T] (with targets) and dentropy [T]
+    (with the forward's entropy), float32; one of the two may be None."""
+    import torch
+    fn = "twell_logprob_backward"
+    dev, (T, V) = _device(fn, logits), logits.shape
+    z, ld = _logits(fn, "logits", logits, dev)
+    if dlogits.shape != logits.shape or dlogits.dtype is not logits.dtype:
+        raise ValueError(f"{fn}: dlogits must have the logits' shape and type")
+    dz, ldd = _logits(fn, "dlogits", dlogits, dev)
+    if dlogp is not None and targets is None:
+        raise ValueError(f"{fn}: dlogp without targets")
+    if dentropy is not None and entropy is None:
+        raise ValueError(f"{fn}: dentropy without the forward's entropy")
+    ids, bits = (None, 32) if dlogp is None else _ids(fn, "targets", targets, T, dev)
+    n = _tensor(fn, "norm", norm, (T, 2), dev, torch.float32)
+    v = [None if t is None else _tensor(fn, name, t, (T,), dev, torch.float32)
+         for name, t in (("entropy", entropy), ("dlogp", dlogp), ("dentropy", dentropy))]
+    _check(fn, load().twell_logprob_backward(z, ld, _i32(T), _i32(V), vdtype_of(logits.dtype), scale, ids, bits, n, *v, dz,
+                                             ldd, _stream(stream, dev)))
 
 
 # ---------------------------------------------------------------- block norms

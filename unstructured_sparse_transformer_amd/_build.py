@@ -20,7 +20,7 @@ OUT_DIR = os.path.join(ROOT, "_build")
 LIB = os.path.join(PKG, "libtwell.so")
 
 SOURCES = ["capi.cpp", "gate_twell.hip", "ffn_fused.hip", "hybrid.hip", "decode.hip", "convert.hip", "compact.hip", "backward.hip",
-           "capi_dense.cpp", "adamw.hip", "block_norm.hip", "glu.hip"]
+           "capi_dense.cpp", "adamw.hip", "block_norm.hip", "glu.hip", "act8.hip", "capi_tokens.cpp", "embed.hip", "logprob.hip"]
 
 HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 ARCH = "gfx950"

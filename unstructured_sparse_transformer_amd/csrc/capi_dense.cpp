@@ -6,27 +6,13 @@
 
 #include <hip/hip_runtime.h>
 
+#include "act8.h"
 #include "adamw.h"
 #include "block_norm.h"
 #include "checks.h"
 #include "glu.h"
 
 namespace {
-
-bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
-
-// Rows of a call: row numbers and roundings of them stay below 2^31.
-constexpr int32_t MOST_ROWS = 1 << 30;
-
-bool known_dtype(int32_t dt) { return dt == TWELL_F32 || dt == TWELL_BF16; }
-
-// A vector of elements of size es: NULL and alignment.
-int check_vec(const void *p, size_t es)
-{
-    if (!p)
-        return TWELL_E_NULL;
-    return aligned_to(p, es) ? TWELL_OK : TWELL_E_ALIGN;
-}
 
 // Sizes and types of the gated product.
 int check_glu(int32_t T, int32_t d, int32_t F, int32_t vdtype, int32_t act)
@@ -40,6 +26,25 @@ int check_glu(int32_t T, int32_t d, int32_t F, int32_t vdtype, int32_t act)
         return TWELL_E_UNSUPPORTED;
     // workgroups of 64 x 64 results, split up to 16 times
     return ((int64_t)T + 63) / 64 * (F / 64 > d / 64 ? F / 64 : d / 64) * 16 < ((int64_t)1 << 31) ? TWELL_OK : TWELL_E_SHAPE;
+}
+
+// Codes and scales of 8-bit activations.
+int check_packed(const twell_packed_t *p, size_t code_align)
+{
+    if (!p)
+        return TWELL_E_NULL;
+    TWELL_TRY(check_vec(p->code, code_align));
+    return check_vec(p->scale, 2);
+}
+
+twell::Packed8 packed8(const twell_packed_t *p) { return twell::Packed8{p->code, static_cast<uint16_t *>(p->scale)}; }
+
+// Sizes of rows that are packed.
+int check_act(int32_t T, int32_t d, int32_t vdtype)
+{
+    if (!known_dtype(vdtype))
+        return TWELL_E_UNSUPPORTED;
+    return T < 0 || T > MOST_ROWS || d < 1 || d > (1 << 20) ? TWELL_E_SHAPE : TWELL_OK;
 }
 
 // The descriptor of the block norms, and with `gated` its gate pointer.
@@ -132,7 +137,7 @@ extern "C" {
 
 size_t twell_glu_workspace_bytes(int32_t T, int32_t d, int32_t F, int32_t vdtype)
 {
-    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_forward_most_ws(T, d, F, vdtype) : 0;
+    return check_glu(T, d, F, vdtype, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_forward_most_ws(T, d, F, vdtype, false) : 0;
 }
 
 int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
@@ -148,7 +153,7 @@ int twell_glu_forward(const void *x, const void *wg_t, const void *wu_t, int32_t
     TWELL_TRY(check_mat(h));
     if (!aligned16(g) || !aligned16(u))
         return TWELL_E_ALIGN;
-    TWELL_TRY(check_ws(workspace, workspace_bytes, twell::glu_forward_ws(T, d, F, vdtype)));
+    TWELL_TRY(check_ws(workspace, workspace_bytes, twell::glu_forward_ws(T, d, F, vdtype, false)));
     twell::GluFwd a{};
     a.T = T;
     a.d = d;
@@ -203,6 +208,101 @@ int twell_glu_backward(const void *x, const void *wg_t, const void *wu_t, const 
     a.dgu = workspace;
     a.ws = w;
     return hip_status(twell::launch_glu_backward(vdtype, a, static_cast<hipStream_t>(stream)));
+}
+
+size_t twell_glu_packed_workspace_bytes(int32_t T, int32_t d, int32_t F)
+{
+    return check_glu(T, d, F, TWELL_BF16, TWELL_ACT_RELU) == TWELL_OK ? twell::glu_forward_most_ws(T, d, F, TWELL_BF16, true)
+                                                                      : 0;
+}
+
+int twell_glu_forward_packed(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
+                             int32_t act, void *h, const twell_packed_t *g, const twell_packed_t *u, void *workspace,
+                             size_t workspace_bytes, void *stream)
+{
+    TWELL_TRY(check_glu(T, d, F, TWELL_BF16, act));
+    if (T == 0)
+        return TWELL_OK;
+    for (const void *p : {x, wg_t, wu_t, (const void *)h})
+        TWELL_TRY(check_mat(p));
+    TWELL_TRY(check_packed(g, 16));
+    TWELL_TRY(check_packed(u, 16));
+    TWELL_TRY(check_ws(workspace, workspace_bytes, twell::glu_forward_ws(T, d, F, TWELL_BF16, true)));
+    twell::GluFwd a{};
+    a.T = T;
+    a.d = d;
+    a.F = F;
+    a.act = act;
+    a.x = x;
+    a.wg = wg_t;
+    a.wu = wu_t;
+    a.h = h;
+    a.g8 = packed8(g);
+    a.u8 = packed8(u);
+    a.part = static_cast<float *>(workspace);
+    return hip_status(twell::launch_glu(TWELL_BF16, a, static_cast<hipStream_t>(stream)));
+}
+
+int twell_glu_backward_packed(const void *x, const void *wg_t, const void *wu_t, const twell_packed_t *g,
+                              const twell_packed_t *u, const void *dh, int32_t T, int32_t d, int32_t F, int32_t act,
+                              void *h, void *dx, void *dwg, void *dwu, void *workspace, size_t workspace_bytes,
+                              void *stream)
+{
+    TWELL_TRY(check_glu(T, d, F, TWELL_BF16, act));
+    if (T > 0) {
+        for (const void *p : {x, wg_t, wu_t, dh})
+            TWELL_TRY(check_mat(p));
+        TWELL_TRY(check_packed(g, 16));
+        TWELL_TRY(check_packed(u, 16));
+        if (!dx && !dwg && !h)
+            return TWELL_E_NULL;
+    }
+    if (!dwg != !dwu)
+        return TWELL_E_NULL;
+    if (!aligned16(dx) || !aligned16(dwg) || !aligned16(dwu) || !aligned16(h))
+        return TWELL_E_ALIGN;
+    const twell::GluWs w = twell::glu_backward_ws(T, d, F, TWELL_BF16);
+    TWELL_TRY(check_ws(workspace, workspace_bytes, w.bytes));
+    twell::GluBwd a{};
+    a.T = T;
+    a.d = d;
+    a.F = F;
+    a.act = act;
+    a.x = x;
+    a.wg = wg_t;
+    a.wu = wu_t;
+    a.dh = dh;
+    if (T > 0) {
+        a.g8 = packed8(g);
+        a.u8 = packed8(u);
+    }
+    a.h = h;
+    a.dx = dx;
+    a.dwg = dwg;
+    a.dwu = dwu;
+    a.dgu = workspace;
+    a.ws = w;
+    return hip_status(twell::launch_glu_backward(TWELL_BF16, a, static_cast<hipStream_t>(stream)));
+}
+
+int twell_act_pack(const void *x, int32_t T, int32_t d, int32_t vdtype, const twell_packed_t *to, void *stream)
+{
+    TWELL_TRY(check_act(T, d, vdtype));
+    if (T == 0)
+        return TWELL_OK;
+    TWELL_TRY(check_vec(x, elem_size(vdtype)));
+    TWELL_TRY(check_packed(to, 1));
+    return hip_status(twell::launch_act_pack(vdtype, x, T, d, packed8(to), static_cast<hipStream_t>(stream)));
+}
+
+int twell_act_unpack(const twell_packed_t *from, int32_t T, int32_t d, int32_t vdtype, void *out, void *stream)
+{
+    TWELL_TRY(check_act(T, d, vdtype));
+    if (T == 0)
+        return TWELL_OK;
+    TWELL_TRY(check_packed(from, 1));
+    TWELL_TRY(check_vec(out, elem_size(vdtype)));
+    return hip_status(twell::launch_act_unpack(vdtype, packed8(from), T, d, out, static_cast<hipStream_t>(stream)));
 }
 
 int twell_block_norm_forward(const twell_block_norm_t *bn, const void *res, const void *y, void *out, void *n,

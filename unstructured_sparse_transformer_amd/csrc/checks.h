@@ -11,6 +11,13 @@ inline bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 
 
 inline int elem_size(int32_t vdtype) { return vdtype == TWELL_BF16 ? 2 : 4; }
 
+inline bool aligned_to(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
+
+// Rows of a call: row numbers and roundings of them stay below 2^31.
+constexpr int32_t MOST_ROWS = 1 << 30;
+
+inline bool known_dtype(int32_t dt) { return dt == TWELL_F32 || dt == TWELL_BF16; }
+
 inline int check_mat(const void *p)
 {
     if (!p)
@@ -26,6 +33,14 @@ inline int hip_status(hipError_t e) { return e == hipSuccess ? TWELL_OK : TWELL_
         if (_st != TWELL_OK)             \
             return _st;                  \
     } while (0)
+
+// A vector of elements of size es: NULL and alignment.
+inline int check_vec(const void *p, size_t es)
+{
+    if (!p)
+        return TWELL_E_NULL;
+    return aligned_to(p, es) ? TWELL_OK : TWELL_E_ALIGN;
+}
 
 inline size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 

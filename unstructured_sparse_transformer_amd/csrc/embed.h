@@ -1,0 +1,40 @@
+// embed.h -- arguments of the embedding lookup and its gradient (host and
+// device side).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace twell {
+
+constexpr int EMB_WINDOW = 32;      // sorted tokens that one sum takes at most
+constexpr int EMB_FEW = 8192;       // tokens up to which ranks are counted in one launch
+constexpr int EMB_DIGIT_BITS = 9;   // of a sorting pass
+constexpr int EMB_MOST_BLOCKS = 256;  // workgroups of a sorting pass
+
+struct EmbArgs {
+    int T, V, d;
+    int id64, bf16_rows, bf16_table;  // types of ids, of out / dout, of table / dtable
+    int accumulate;
+    float scale;
+    const void *ids;
+    const void *in;   // forward: table; backward: dout
+    void *out;        // forward: out; backward: dtable
+    // backward: the workspace
+    int32_t *key, *perm;    // [T] the tokens' keys in ascending order (V: no id), and their rows
+    int32_t *key2, *perm2;  // [T] the other side of a sorting pass
+    int32_t *counts;        // [blocks][2^EMB_DIGIT_BITS]
+    float *part;            // [2 windows][emb_pitch(d)] sums of runs that windows cut
+};
+
+inline int64_t emb_windows(int64_t T) { return (T + EMB_WINDOW - 1) / EMB_WINDOW; }
+__host__ __device__ inline int64_t emb_pitch(int d) { return ((int64_t)d + 3) & ~(int64_t)3; }
+
+// Places the workspace's parts at `base`; returns its bytes (never less for more tokens).
+size_t emb_layout(EmbArgs &a, void *base);
+
+hipError_t launch_embed(const EmbArgs &a, hipStream_t s);
+hipError_t launch_embed_backward(const EmbArgs &a, hipStream_t s);
+
+}  // namespace twell

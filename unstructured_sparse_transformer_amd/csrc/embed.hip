@@ -1,0 +1,482 @@
+// embed.hip -- rows of a table for token ids (twell_embed_forward) and the
+// table's gradient (twell_embed_backward).
+//
+//   out[t] = scale * table[ids[t]]
+//   dtable[v] = [old +] scale * sum over the tokens t with ids[t] = v of dout[t]
+// A token whose id is none of 0 .. V-1 gets zeros and adds to no row.
+//
+// Both are bound by memory.  The gradient's sums run in the order of t: the
+// tokens are sorted by id first (stable), so that a row of the table is summed by
+// one thread per piece of columns, without float atomics.
+#include "embed.h"
+#include "rows.h"
+
+#include <type_traits>
+
+namespace twell {
+
+// Work item i of a launch's n: rows of `pieces` pieces each, one after another.  A
+// workgroup's first row is found once, in 64 bits; its threads count on from there.
+struct EmbItem {
+    int64_t row;
+    int piece;
+};
+__device__ __forceinline__ EmbItem emb_item(int64_t first, int add, int pieces)
+{
+    const int64_t row = first / pieces;
+    const uint32_t r = (uint32_t)(first - row * pieces) + (uint32_t)add;
+    const uint32_t up = r / (uint32_t)pieces;
+    return EmbItem{row + up, (int)(r - up * (uint32_t)pieces)};
+}
+
+// ------------------------------------------------------------------ forward
+// U items a thread, whose ids and rows are loaded together.
+constexpr int EMB_U = 4;
+
+template <typename ID, typename TT, typename TO, int E> __global__ __launch_bounds__(256) void embed_kernel(EmbArgs p)
+{
+    const int pieces = (p.d + E - 1) / E;
+    const int64_t first = (int64_t)blockIdx.x * (256 * EMB_U);
+    EmbItem it[EMB_U];
+    int key[EMB_U];
+#pragma unroll
+    for (int u = 0; u < EMB_U; ++u) {
+        it[u] = emb_item(first, u * 256 + threadIdx.x, pieces);
+        key[u] = it[u].row < p.T ? token_key((const ID *)p.ids, it[u].row, p.V) : p.V;
+    }
+    RowPiece<TT, E> v[EMB_U];
+#pragma unroll
+    for (int u = 0; u < EMB_U; ++u)
+        if (key[u] < p.V) {
+            int from;
+            const int c = rows_column<E>(it[u].piece, p.d, from);
+            v[u].load((const TT *)p.in + (int64_t)key[u] * p.d + c);
+        }
+#pragma unroll
+    for (int u = 0; u < EMB_U; ++u) {
+        if (it[u].row >= p.T)
+            continue;
+        int from;
+        const int c = rows_column<E>(it[u].piece, p.d, from);
+        float o[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            o[e] = key[u] < p.V ? v[u].at(e) * p.scale : 0.f;
+        rows_store<E>((TO *)p.out + it[u].row * p.d + c, o, from);
+    }
+}
+
+// ------------------------------------------------------------------ sorting
+// Zeros for the table's gradient, from workgroups behind those that sort: they
+// take the time that the sorting leaves the memory idle.
+__device__ __forceinline__ void emb_fill(const EmbArgs &p, int wg, int wgs)
+{
+    const int64_t bytes = (int64_t)p.V * p.d * (p.bf16_table ? 2 : 4);
+    char *at = (char *)p.out, *end = at + bytes;
+    char *a = (char *)(((uintptr_t)at + 15) & ~(uintptr_t)15);
+    char *z = (char *)((uintptr_t)end & ~(uintptr_t)15);
+    if (a > z)
+        a = z = end;  // (fewer than 16 bytes)
+    if (wg == 0) {
+        for (char *q = at + threadIdx.x * 2; q < a && q < end; q += blockDim.x * 2)
+            *(uint16_t *)q = 0;
+        for (char *q = z + threadIdx.x * 2; q < end; q += blockDim.x * 2)
+            *(uint16_t *)q = 0;
+    }
+    const int64_t n = (z - a) / 16;
+    for (int64_t i = (int64_t)wg * blockDim.x + threadIdx.x; i < n; i += (int64_t)wgs * blockDim.x)
+        reinterpret_cast<u32x4 *>(a)[i] = u32x4{0, 0, 0, 0};
+}
+
+// Up to EMB_FEW tokens in one launch: a token's place is the number of tokens
+// with a smaller key, or the same key and an earlier row.  A workgroup takes 32
+// tokens, 8 threads each, which compare with every key from LDS (two operations
+// a key: T^2 / 256 CUs of them are 4 us at 8192 tokens).
+template <typename ID> __global__ __launch_bounds__(256) void emb_rank_kernel(EmbArgs p, int wgs)
+{
+    __shared__ __attribute__((aligned(16))) int keys[EMB_FEW];
+    __shared__ int count[8][32];
+    if ((int)blockIdx.x >= wgs) {
+        emb_fill(p, (int)blockIdx.x - wgs, (int)gridDim.x - wgs);
+        return;
+    }
+    const int tid = threadIdx.x, groups = (p.T + 31) / 32;
+    for (int t = tid; t < groups * 32; t += 256)
+        keys[t] = t < p.T ? token_key((const ID *)p.ids, t, p.V) : 0x7FFFFFF0;  // (above V)
+    __syncthreads();
+    const int own = (int)blockIdx.x, mine = tid & 31, key = keys[own * 32 + mine];
+    int n = 0;
+    for (int g = tid >> 5; g < groups; g += 8) {
+        const int4 *q = reinterpret_cast<const int4 *>(keys + g * 32);
+        if (g != own) {
+            const int below = key + (g < own);  // of the tokens before, those with the same key count
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                const int4 k = q[j];
+                n += k.x < below;
+                n += k.y < below;
+                n += k.z < below;
+                n += k.w < below;
+            }
+        } else {
+            for (int j = 0; j < 32; ++j)
+                n += keys[g * 32 + j] < key + (j < mine);
+        }
+    }
+    count[tid >> 5][mine] = n;
+    __syncthreads();
+    if (tid < 32 && own * 32 + tid < p.T) {
+        int at = 0;
+#pragma unroll
+        for (int s = 0; s < 8; ++s)
+            at += count[s][tid];
+        p.key[at] = keys[own * 32 + tid];
+        p.perm[at] = own * 32 + tid;
+    }
+}
+
+// More tokens: passes over digits of the key, least significant first, each a
+// count of every workgroup's digits and a stable move.  A workgroup takes `per`
+// (a multiple of 512) consecutive tokens.
+constexpr int EMB_BINS = 1 << EMB_DIGIT_BITS, EMB_SORT_THREADS = 512;
+static_assert(EMB_BINS == EMB_SORT_THREADS, "a thread a digit");
+
+struct EmbPass {
+    const int32_t *key, *perm;  // NULL: the ids, in their order
+    int32_t *key_out, *perm_out;
+    int shift, mask, per, blocks;
+};
+
+template <typename ID> __device__ __forceinline__ int emb_key(const EmbArgs &p, const EmbPass &q, int64_t i)
+{
+    return q.key ? q.key[i] : token_key((const ID *)p.ids, i, p.V);
+}
+
+template <typename ID>
+__global__ __launch_bounds__(EMB_SORT_THREADS) void emb_count_kernel(EmbArgs p, EmbPass q)
+{
+    __shared__ int hist[EMB_BINS];
+    if ((int)blockIdx.x >= q.blocks) {
+        emb_fill(p, (int)blockIdx.x - q.blocks, (int)gridDim.x - q.blocks);
+        return;
+    }
+    const int tid = threadIdx.x;
+    hist[tid] = 0;
+    __syncthreads();
+    const int64_t first = (int64_t)blockIdx.x * q.per, end = first + q.per < p.T ? first + q.per : p.T;
+    for (int64_t i = first + tid; i < end; i += EMB_SORT_THREADS)
+        atomicAdd(&hist[(emb_key<ID>(p, q, i) >> q.shift) & q.mask], 1);
+    __syncthreads();
+    p.counts[blockIdx.x * EMB_BINS + tid] = hist[tid];
+}
+
+template <typename ID>
+__global__ __launch_bounds__(EMB_SORT_THREADS) void emb_move_kernel(EmbArgs p, EmbPass q)
+{
+    constexpr int NW = EMB_SORT_THREADS / 64;
+    __shared__ int at[NW][EMB_BINS];
+    __shared__ int sums[NW];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6, own = blockIdx.x;
+    // this thread's digit: tokens with it in all workgroups, and in those before this one
+    int total = 0, before = 0;
+    for (int b = 0; b < q.blocks; ++b) {
+        const int c = p.counts[b * EMB_BINS + tid];
+        total += c;
+        before += b < own ? c : 0;
+    }
+    int scan = total;
+#pragma unroll
+    for (int o = 1; o < 64; o <<= 1) {
+        const int v = __shfl_up(scan, o, 64);
+        scan += lane >= o ? v : 0;
+    }
+    if (lane == 63)
+        sums[wave] = scan;
+    __syncthreads();
+    int base = scan - total + before;
+    for (int w = 0; w < wave; ++w)
+        base += sums[w];
+    const int64_t first = (int64_t)own * q.per, end = first + q.per < p.T ? first + q.per : p.T;
+    for (int64_t i0 = first; i0 < end; i0 += EMB_SORT_THREADS) {
+#pragma unroll
+        for (int w = 0; w < NW; ++w)
+            at[w][tid] = 0;
+        __syncthreads();
+        const int64_t i = i0 + tid;
+        const bool on = i < end;
+        const int key = on ? emb_key<ID>(p, q, i) : 0;
+        const int digit = (key >> q.shift) & q.mask;
+        // the wave's lanes with the same digit
+        uint64_t same = __ballot(on);
+        for (int b = 0; b < EMB_DIGIT_BITS; ++b) {
+            const uint64_t set = __ballot((digit >> b) & 1);
+            same &= (digit >> b) & 1 ? set : ~set;
+        }
+        const int rank = __popcll(same & ((1ull << lane) - 1));
+        if (on && rank == 0)
+            at[wave][digit] = __popcll(same);
+        __syncthreads();
+#pragma unroll
+        for (int w = 0; w < NW; ++w) {
+            const int c = at[w][tid];
+            at[w][tid] = base;
+            base += c;
+        }
+        __syncthreads();
+        if (on) {
+            const int to = at[wave][digit] + rank;
+            q.key_out[to] = key;
+            q.perm_out[to] = q.perm ? q.perm[i] : (int)i;
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ sums
+// The table's row of a sum, or the sum and what was there.
+template <typename TT, int E>
+__device__ __forceinline__ void emb_write(const EmbArgs &p, int key, int c, int from, const float (&sum)[E])
+{
+    TT *o = (TT *)p.out + (int64_t)key * p.d + c;
+    float v[E];
+    if (p.accumulate) {
+        RowPiece<TT, E> old;
+        old.load(o);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            v[e] = fmaf(sum[e], p.scale, old.at(e));
+    } else {
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            v[e] = sum[e] * p.scale;
+    }
+    rows_store<E>(o, v, from);
+}
+
+// A run (the sorted tokens of one id) is cut at multiples of EMB_WINDOW.  The
+// thread at the first token of a run, or of a window that goes on with one, adds
+// the rows up to the run's or the window's end; the others have nothing to do.
+// The sums of cut runs go to `part`: a window's first rows, if the run began
+// before it, to its slot 0, its last ones, if the run begins in it, to slot 1.
+template <typename TD, typename TT, int E> __global__ __launch_bounds__(256) void emb_sum_kernel(EmbArgs p)
+{
+    constexpr int B = 8;  // rows on their way at once
+    const int pieces = (p.d + E - 1) / E;
+    const EmbItem it = emb_item((int64_t)blockIdx.x * 256, threadIdx.x, pieces);
+    if (it.row >= p.T)
+        return;
+    const int at = (int)it.row, key = p.key[at];
+    if (key >= p.V)
+        return;
+    const bool goes_on = at > 0 && p.key[at - 1] == key;
+    if (goes_on && at % EMB_WINDOW != 0)
+        return;
+    const int last = at / EMB_WINDOW * EMB_WINDOW + EMB_WINDOW, end = last < p.T ? last : p.T;
+    int from;
+    const int c = rows_column<E>(it.piece, p.d, from);
+    const TD *rows = (const TD *)p.in + c;
+    float sum[E];
+    {
+        RowPiece<TD, E> v;
+        v.load(rows + (int64_t)p.perm[at] * p.d);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            sum[e] = v.at(e);
+    }
+    int i = at + 1;
+    for (bool more = i < end; more;) {
+        int row[B];
+        bool in[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b) {
+            const int j = i + b < end ? i + b : end - 1;
+            in[b] = i + b < end && p.key[j] == key;
+            row[b] = p.perm[j];
+        }
+        RowPiece<TD, E> v[B];
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (in[b])
+                v[b].load(rows + (int64_t)row[b] * p.d);
+#pragma unroll
+        for (int b = 0; b < B; ++b)
+            if (in[b]) {
+                ++i;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    sum[e] += v[b].at(e);
+            }
+        more = in[B - 1] && i < end;
+    }
+    const bool goes_past = i == last && last < p.T && p.key[last] == key;
+    if (goes_on || goes_past)
+        rows_store<E>(p.part + (2 * (int64_t)(at / EMB_WINDOW) + !goes_on) * emb_pitch(p.d) + c, sum, 0);
+    else
+        emb_write<TT, E>(p, key, c, from, sum);
+}
+
+// The cut runs: the sums of a run's windows, added by 16 waves, each every 16th
+// in order, whose results are added in order.
+constexpr int EMB_JOIN_WAVES = 16;
+template <typename TT, int E> __global__ __launch_bounds__(EMB_JOIN_WAVES * 64) void emb_join_kernel(EmbArgs p)
+{
+    __shared__ float all[EMB_JOIN_WAVES][E][64];
+    const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+    const int pieces = (p.d + E - 1) / E, piece = blockIdx.y * 64 + lane;
+    const int windows = (p.T + EMB_WINDOW - 1) / EMB_WINDOW;
+    const bool on = piece < pieces;
+    int from = 0;
+    const int c = on ? rows_column<E>(piece, p.d, from) : 0;
+    for (int w = blockIdx.x; w + 1 < windows; w += gridDim.x) {
+        const int first = w * EMB_WINDOW, next = first + EMB_WINDOW, key = p.key[next];
+        // a run that begins in window w and goes on in the next
+        if (key >= p.V || p.key[next - 1] != key || (p.key[first] == key && first > 0 && p.key[first - 1] == key))
+            continue;
+        int lo = w + 1, hi = windows;  // the first window after it that does not begin with it
+        while (hi - lo > 1) {
+            const int mid = lo + (hi - lo) / 2;
+            if (p.key[mid * EMB_WINDOW] == key)
+                lo = mid;
+            else
+                hi = mid;
+        }
+        const int n = hi - w;  // sums: slot 1 of w, then slots 0
+        float sum[E];
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            sum[e] = 0.f;
+        if (on) {
+#pragma unroll 4
+            for (int i = wave; i < n; i += EMB_JOIN_WAVES) {
+                RowPiece<float, E> v;
+                v.load(p.part + (2 * (int64_t)(w + i) + (i == 0)) * emb_pitch(p.d) + c);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    sum[e] += v.at(e);
+            }
+        }
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            all[wave][e][lane] = sum[e];
+        __syncthreads();
+        if (wave == 0 && on) {
+            for (int k = 1; k < EMB_JOIN_WAVES && k < n; ++k)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    sum[e] += all[k][e][lane];
+            emb_write<TT, E>(p, key, c, from, sum);
+        }
+        __syncthreads();
+    }
+}
+
+// ------------------------------------------------------------------ host
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+static size_t up256_(size_t b) { return (b + 255) & ~(size_t)255; }
+
+size_t emb_layout(EmbArgs &a, void *base)
+{
+    char *at = (char *)base;
+    const size_t list = up256_((size_t)a.T * 4);
+    auto take = [&](size_t bytes) {
+        char *p = at;
+        at += bytes;
+        return p;
+    };
+    a.key = (int32_t *)take(list);
+    a.perm = (int32_t *)take(list);
+    a.part = (float *)take(a.T > EMB_WINDOW ? up256_((size_t)2 * emb_windows(a.T) * emb_pitch(a.d) * 4) : 0);
+    if (a.T > EMB_FEW) {
+        a.key2 = (int32_t *)take(list);
+        a.perm2 = (int32_t *)take(list);
+        a.counts = (int32_t *)take((size_t)EMB_MOST_BLOCKS * EMB_BINS * 4);
+    }
+    return at - (char *)base;
+}
+
+template <typename ID, typename TT, typename TO> static hipError_t run_embed(const EmbArgs &p, hipStream_t s)
+{
+    constexpr int E = std::is_same_v<TT, __bf16> && std::is_same_v<TO, __bf16> ? 8 : 4;
+    const int per = p.d >= E ? E : 1;
+    const dim3 grid((unsigned)ceil_div((int64_t)p.T * ceil_div(p.d, per), 256 * EMB_U));
+    if (per == E)
+        embed_kernel<ID, TT, TO, E><<<grid, dim3(256), 0, s>>>(p);
+    else
+        embed_kernel<ID, TT, TO, 1><<<grid, dim3(256), 0, s>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_embed(const EmbArgs &p, hipStream_t s)
+{
+    auto with_id = [&](auto id) {
+        using ID = decltype(id);
+        if (p.bf16_table)
+            return p.bf16_rows ? run_embed<ID, __bf16, __bf16>(p, s) : run_embed<ID, __bf16, float>(p, s);
+        return p.bf16_rows ? run_embed<ID, float, __bf16>(p, s) : run_embed<ID, float, float>(p, s);
+    };
+    return p.id64 ? with_id(int64_t{}) : with_id(int32_t{});
+}
+
+template <typename ID> static hipError_t run_sort(EmbArgs &p, hipStream_t s)
+{
+    const int64_t bytes = (int64_t)p.V * p.d * (p.bf16_table ? 2 : 4);
+    const int64_t want = p.accumulate ? 0 : ceil_div(bytes, 256 * 16 * 4);
+    const int fill = (int)(want < 2048 ? want : 2048);
+    if (p.T <= EMB_FEW) {
+        const int wgs = (int)ceil_div(p.T, 32);
+        if (wgs + fill > 0)
+            emb_rank_kernel<ID><<<dim3(wgs + fill), dim3(256), 0, s>>>(p, wgs);
+        return hipGetLastError();
+    }
+    int bits = 1;
+    while (((int64_t)1 << bits) <= p.V)  // keys are 0 .. V
+        ++bits;
+    const int passes = (int)ceil_div(bits, EMB_DIGIT_BITS), each = (int)ceil_div(bits, passes);
+    EmbPass q{};
+    q.per = (int)(ceil_div(ceil_div(p.T, EMB_MOST_BLOCKS), EMB_SORT_THREADS) * EMB_SORT_THREADS);
+    q.blocks = (int)ceil_div(p.T, q.per);
+    q.mask = (1 << each) - 1;
+    for (int i = 0; i < passes; ++i) {
+        const bool last_side = (passes - 1 - i) % 2 == 0;  // the last pass ends in key and perm
+        q.key_out = last_side ? p.key : p.key2;
+        q.perm_out = last_side ? p.perm : p.perm2;
+        q.shift = i * each;
+        emb_count_kernel<ID><<<dim3(q.blocks + (i == 0 ? fill : 0)), dim3(EMB_SORT_THREADS), 0, s>>>(p, q);
+        emb_move_kernel<ID><<<dim3(q.blocks), dim3(EMB_SORT_THREADS), 0, s>>>(p, q);
+        q.key = q.key_out;
+        q.perm = q.perm_out;
+    }
+    return hipGetLastError();
+}
+
+template <typename TD, typename TT, int E> static hipError_t run_sums(const EmbArgs &p, hipStream_t s)
+{
+    const int64_t pieces = ceil_div(p.d, E);
+    emb_sum_kernel<TD, TT, E><<<dim3((unsigned)ceil_div(p.T * pieces, 256)), dim3(256), 0, s>>>(p);
+    const int64_t windows = emb_windows(p.T), y = ceil_div(pieces, 64);
+    if (windows > 1) {
+        const int64_t most = ceil_div(2048, y), x = windows - 1 < most ? windows - 1 : most;
+        emb_join_kernel<TT, E><<<dim3((unsigned)x, (unsigned)y), dim3(EMB_JOIN_WAVES * 64), 0, s>>>(p);
+    }
+    return hipGetLastError();
+}
+
+hipError_t launch_embed_backward(const EmbArgs &args, hipStream_t s)
+{
+    EmbArgs p = args;
+    if (p.T == 0 && p.accumulate)
+        return hipSuccess;
+    const hipError_t e = p.id64 ? run_sort<int64_t>(p, s) : run_sort<int32_t>(p, s);
+    if (e != hipSuccess || p.T == 0)
+        return e;
+    auto with = [&](auto rows, auto table) {
+        using TD = decltype(rows);
+        using TT = decltype(table);
+        return p.d >= 4 ? run_sums<TD, TT, 4>(p, s) : run_sums<TD, TT, 1>(p, s);
+    };
+    if (p.bf16_table)
+        return p.bf16_rows ? with(__bf16{}, __bf16{}) : with(float{}, __bf16{});
+    return p.bf16_rows ? with(__bf16{}, float{}) : with(float{}, float{});
+}
+
+}  // namespace twell

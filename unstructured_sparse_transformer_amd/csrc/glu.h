@@ -5,6 +5,7 @@
 #include <stddef.h>
 #include <stdint.h>
 
+#include "act8.h"
 #include "dense_gemm.h"
 
 namespace twell {
@@ -18,6 +19,7 @@ struct GluFwd {
     DgTiles tiles;
     const void *x, *wg, *wu;
     void *h, *g, *u;  // g, u may be NULL
+    Packed8 g8, u8;   // g and u in 8 bits instead (code NULL: not wanted), bf16 only
     float *part;      // [splits][g | u][T][F] partial sums
     int splits;       // of K, when the tiles alone leave CUs idle
 };
@@ -40,6 +42,8 @@ GluWs glu_backward_ws(int T, int d, int F, int vdtype);
 struct GluBwd {
     int T, d, F, act;
     const void *x, *wg, *wu, *g, *u, *dh;
+    Packed8 g8, u8;        // in the place of g and u (code NULL: those), bf16 only
+    void *h;               // with g8 and u8: act(g) u again, or NULL
     void *dx, *dwg, *dwu;  // NULL: not wanted
     void *dgu;             // the workspace: [T to a multiple of 64] rows of glu_pitch(F), a row's dg, then its du
     GluWs ws;
@@ -51,9 +55,10 @@ struct GluBwd {
 // gap, 437 us without).
 __host__ __device__ inline int64_t glu_pitch(int F) { return 2 * (int64_t)F + 64; }
 
-size_t glu_forward_ws(int T, int d, int F, int vdtype);  // bytes
-// The most bytes of any call with up to T rows.
-size_t glu_forward_most_ws(int T, int d, int F, int vdtype);
+// Bytes of a forward call (packed: with g and u in 8 bits), and the most of any
+// call with up to T rows.
+size_t glu_forward_ws(int T, int d, int F, int vdtype, bool packed);
+size_t glu_forward_most_ws(int T, int d, int F, int vdtype, bool packed);
 size_t glu_backward_most_ws(int T, int d, int F, int vdtype);
 
 hipError_t launch_glu(int vdtype, const GluFwd &a, hipStream_t s);

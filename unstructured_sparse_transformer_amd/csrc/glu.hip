@@ -72,6 +72,40 @@ template <bool FAST> __device__ __forceinline__ float glu_act_grad(float g, int 
     return slope == 0.f ? s : s + g * slope * dz;  // far out, where g or dz may be infinite
 }
 
+// ------------------------------------------------------------------ 8 bits
+// A wave's block of 32 rows by 32 NB columns as 8-bit codes, from accumulators
+// (value(fn, i)) to memory.  32 columns of a row, a block of the codes, are 16
+// values of a lane and 16 of the lane 32 further: one exchange gives both the
+// largest.  Two swaps of the lanes' halves turn their pieces of 4 columns into 16
+// consecutive ones a lane.
+template <int NB, typename V>
+__device__ __forceinline__ void glu_pack_rows(int lane, V value, const Packed8 &to, int64_t ld, int m0, int n0, int M, int N)
+{
+    const int m = m0 + (lane & 31), half = lane >> 5;
+#pragma unroll
+    for (int fn = 0; fn < NB; ++fn) {
+        float top = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i)
+            top = a8_max(top, value(fn, i));
+        top = a8_max(top, __shfl_xor(top, 32, 64));
+        const A8Scale s(top);
+        uint32_t c[4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+            c[i] = a8_codes(value(fn, 4 * i), value(fn, 4 * i + 1), value(fn, 4 * i + 2), value(fn, 4 * i + 3), s.inv);
+        // lane l of the lower half has columns 0-3, 8-11, 16-19, 24-27 of row l, lane l + 32 the others
+        const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
+        const auto b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
+        const int n = n0 + fn * 32;
+        if (m < M && n < N) {
+            *reinterpret_cast<u32x4 *>(to.code + m * ld + n + half * 16) = u32x4{a[0], a[1], b[0], b[1]};
+            if (half == 0)
+                to.scale[m * (ld / A8_BLOCK) + n / A8_BLOCK] = s.bits;
+        }
+    }
+}
+
 // ------------------------------------------------------------------ forward
 // Bound by the matrix units.  bf16, 8192 x 2048 x 8192 with g and u kept: 471 us
 // on the same inputs again, 487 us on others (1.13 PFLOP/s); the product by itself takes 420 us at the clock the chip's power
@@ -79,7 +113,7 @@ template <bool FAST> __device__ __forceinline__ float glu_act_grad(float g, int 
 // (workgroups started up to 13 us apart, so that some store while others
 // multiply: no change).  fp32, 1500 x 2048 x 2048: 188 us, 134 of 157 TFLOP/s.
 // fp32 tiles are small and several share a CU, hence the waves per SIMD.
-template <typename TI, int BM, int BN, int WM, int WN, int S>
+template <typename TI, int BM, int BN, int WM, int WN, int S, bool PACK = false>
 __global__ __launch_bounds__((BM / WM) * (BN / WN) * 64) __attribute__((amdgpu_waves_per_eu(2, sizeof(TI) == 4 ? 4 : 2))) void
 glu_kernel(GluFwd p)
 {
@@ -133,6 +167,10 @@ glu_kernel(GluFwd p)
     for (int fm = 0; fm < Core::FM; ++fm) {
         auto g = [&](int fn, int i) { return acc[fm][fn][i]; };
         auto u = [&](int fn, int i) { return acc[fm][fn + NB][i]; };
+        if constexpr (PACK) {
+            glu_pack_rows<NB>(lane, g, p.g8, p.F, m0 + fm * 32, n0, p.T, p.F);
+            glu_pack_rows<NB>(lane, u, p.u8, p.F, m0 + fm * 32, n0, p.T, p.F);
+        }
         // g and u wait for the backward pass: past the caches (1-3% of the call)
         if (p.g)
             dg_store_rows<NB, true>(stage, lane, g, (__bf16 *)p.g, p.F, m0 + fm * 32, n0, p.T, p.F);
@@ -263,8 +301,9 @@ template <typename TI, int BM, int NB, int S> __global__ __launch_bounds__(256) 
     }
 }
 
-// h (and g, u) from the splits' parts, added in order; 4 columns a thread.
-template <typename TI> __global__ __launch_bounds__(256) void glu_join_act_kernel(GluFwd p)
+// h (and g, u) from the splits' parts, added in order; 4 columns a thread, a block
+// of the 8-bit codes 8 threads.
+template <typename TI, bool PACK = false> __global__ __launch_bounds__(256) void glu_join_act_kernel(GluFwd p)
 {
     const int64_t n4 = (int64_t)p.T * p.F / 4;
     for (int64_t c = blockIdx.x * 256LL + threadIdx.x; c < n4; c += gridDim.x * 256LL) {
@@ -283,6 +322,20 @@ template <typename TI> __global__ __launch_bounds__(256) void glu_join_act_kerne
             v[w][1] = s.y;
             v[w][2] = s.z;
             v[w][3] = s.w;
+        }
+        if constexpr (PACK) {
+#pragma unroll
+            for (int w = 0; w < 2; ++w) {
+                const Packed8 &to = w ? p.u8 : p.g8;
+                float top = a8_max(a8_max(a8_max(a8_max(0.f, v[w][0]), v[w][1]), v[w][2]), v[w][3]);
+#pragma unroll
+                for (int o = 1; o < 8; o <<= 1)
+                    top = a8_max(top, __shfl_xor(top, o, 64));
+                const A8Scale s(top);
+                *reinterpret_cast<uint32_t *>(to.code + c * 4) = a8_codes(v[w][0], v[w][1], v[w][2], v[w][3], s.inv);
+                if ((c & 7) == 0)
+                    to.scale[c / 8] = s.bits;
+            }
         }
 #pragma unroll
         for (int e = 0; e < 4; ++e) {
@@ -335,6 +388,44 @@ template <typename TI, bool ONCE> __global__ __launch_bounds__(256) void glu_dac
             __builtin_memcpy(&ou, ru, 16);
         }
         TI *o = (TI *)p.dgu + t * glu_pitch(p.F) + j;
+        *reinterpret_cast<u32x4 *>(o) = og;
+        *reinterpret_cast<u32x4 *>(o + p.F) = ou;
+    }
+}
+
+// The same from 8-bit codes: 8 bytes an element, and 2 more for h.
+__global__ __launch_bounds__(256) void glu_dact8_kernel(GluBwd p, int rows)
+{
+    const int per_row = p.F / 8;
+    const int64_t n = (int64_t)rows * per_row;
+    for (int64_t c = blockIdx.x * 256LL + threadIdx.x; c < n; c += gridDim.x * 256LL) {
+        const int64_t t = c / per_row, j = (c - t * per_row) * 8;
+        u32x4 og{}, ou{};
+        if (t < p.T) {
+            const int64_t at = t * p.F + j, block = at / A8_BLOCK;
+            const uint2 g = *reinterpret_cast<const uint2 *>(p.g8.code + at), u = *reinterpret_cast<const uint2 *>(p.u8.code + at);
+            const u32x4 dh = glu_load<true>((const __bf16 *)p.dh + at);
+            const float gs = a8_scale(p.g8.scale[block]), us = a8_scale(p.u8.scale[block]);
+            __bf16 rg[8], ru[8], rh[8];
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {
+                const float gv = a8_value(e < 4 ? g.x : g.y, e & 3, gs), uv = a8_value(e < 4 ? u.x : u.y, e & 3, us);
+                float a;
+                const float da = glu_act_grad<true>(gv, p.act, a);
+                const float d = chunk_elem<__bf16>(dh, e);
+                store_elem(rg + e, d * uv * da);
+                store_elem(ru + e, d * a);
+                store_elem(rh + e, a * uv);
+            }
+            __builtin_memcpy(&og, rg, 16);
+            __builtin_memcpy(&ou, ru, 16);
+            if (p.h) {
+                u32x4 oh;
+                __builtin_memcpy(&oh, rh, 16);
+                *reinterpret_cast<u32x4 *>((__bf16 *)p.h + at) = oh;
+            }
+        }
+        __bf16 *o = (__bf16 *)p.dgu + t * glu_pitch(p.F) + j;
         *reinterpret_cast<u32x4 *>(o) = og;
         *reinterpret_cast<u32x4 *>(o + p.F) = ou;
     }
@@ -494,9 +585,9 @@ static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, in
     return best;
 }
 
-static MulPlan forward_plan(int vdtype, int T, int d, int F)
+static MulPlan forward_plan(int vdtype, int T, int d, int F, bool packed)
 {
-    if (T <= GLU_FEW)
+    if (T <= GLU_FEW && !packed)  // (the streaming kernel's workgroups hold less than a block of 8-bit codes)
         return {0, 1};
     return vdtype == 1 ? mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d) : mul_plan(FWD_TILES_F32, 2, T, 2 * (int64_t)F, d);
 }
@@ -531,16 +622,19 @@ static size_t forward_bytes(const MulPlan &plan, int T, int F)
 {
     return plan.splits > 1 ? (size_t)plan.splits * 2 * T * F * sizeof(float) : 0;
 }
-size_t glu_forward_ws(int T, int d, int F, int vdtype) { return forward_bytes(forward_plan(vdtype, T, d, F), T, F); }
+size_t glu_forward_ws(int T, int d, int F, int vdtype, bool packed)
+{
+    return forward_bytes(forward_plan(vdtype, T, d, F, packed), T, F);
+}
 
-size_t glu_forward_most_ws(int T, int d, int F, int vdtype)
+size_t glu_forward_most_ws(int T, int d, int F, int vdtype, bool packed)
 {
     struct Need {
         MulPlan plan;
         size_t bytes;
     };
     return most_bytes_to(T, [&](int t) {
-        const MulPlan plan = forward_plan(vdtype, t, d, F);
+        const MulPlan plan = forward_plan(vdtype, t, d, F, packed);
         return Need{plan, forward_bytes(plan, t, F)};
     });
 }
@@ -551,10 +645,29 @@ static dim3 join_grid(int64_t n)
     return dim3((unsigned)(wgs < 4096 ? wgs : 4096));
 }
 
+template <bool PACK> static void launch_glu_tiles(int tile, dim3 grid, const GluFwd &p, hipStream_t s)
+{
+    switch (tile) {
+    case 0:
+        glu_kernel<__bf16, 256, 256, 64, 128, 2, PACK><<<grid, dim3(512), 0, s>>>(p);
+        break;
+    case 1:
+        glu_kernel<__bf16, 256, 128, 64, 64, 3, PACK><<<grid, dim3(512), 0, s>>>(p);
+        break;
+    case 2:
+        glu_kernel<__bf16, 128, 128, 32, 64, 4, PACK><<<grid, dim3(512), 0, s>>>(p);
+        break;
+    default:
+        glu_kernel<__bf16, 128, 64, 32, 64, 3, PACK><<<grid, dim3(256), 0, s>>>(p);
+        break;
+    }
+}
+
 hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
 {
     GluFwd p = args;
-    if (p.T <= GLU_FEW) {
+    const bool packed = p.g8.code != nullptr;
+    if (p.T <= GLU_FEW && !packed) {
         const dim3 grid(p.F / 16), block(256);
         if (vdtype == 1 && p.T <= 32)
             glu_stream_kernel<__bf16, 32, 16, 9><<<grid, block, 0, s>>>(p);
@@ -566,7 +679,7 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
             glu_stream_kernel<float, 64, 16, 6><<<grid, block, 0, s>>>(p);
         return hipGetLastError();
     }
-    const MulPlan plan = forward_plan(vdtype, p.T, p.d, p.F);
+    const MulPlan plan = forward_plan(vdtype, p.T, p.d, p.F, packed);
     p.splits = plan.splits;
     const MulTile &tile = (vdtype == 1 ? MUL_TILES : FWD_TILES_F32)[plan.tile];
     p.tiles = dg_tiles(ceil_div(p.T, tile.bm), ceil_div(p.F, tile.bn / 2), p.splits);
@@ -576,26 +689,17 @@ hipError_t launch_glu(int vdtype, const GluFwd &args, hipStream_t s)
             glu_kernel<float, 128, 128, 32, 64, 2><<<grid, dim3(512), 0, s>>>(p);
         else
             glu_kernel<float, 64, 128, 32, 64, 2><<<grid, dim3(256), 0, s>>>(p);
+    } else if (packed) {
+        launch_glu_tiles<true>(plan.tile, grid, p, s);
     } else {
-        switch (plan.tile) {
-        case 0:
-            glu_kernel<__bf16, 256, 256, 64, 128, 2><<<grid, dim3(512), 0, s>>>(p);
-            break;
-        case 1:
-            glu_kernel<__bf16, 256, 128, 64, 64, 3><<<grid, dim3(512), 0, s>>>(p);
-            break;
-        case 2:
-            glu_kernel<__bf16, 128, 128, 32, 64, 4><<<grid, dim3(512), 0, s>>>(p);
-            break;
-        default:
-            glu_kernel<__bf16, 128, 64, 32, 64, 3><<<grid, dim3(256), 0, s>>>(p);
-            break;
-        }
+        launch_glu_tiles<false>(plan.tile, grid, p, s);
     }
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.splits == 1)
         return e;
-    if (vdtype == 1)
+    if (packed)
+        glu_join_act_kernel<__bf16, true><<<join_grid((int64_t)p.T * p.F), dim3(256), 0, s>>>(p);
+    else if (vdtype == 1)
         glu_join_act_kernel<__bf16><<<join_grid((int64_t)p.T * p.F), dim3(256), 0, s>>>(p);
     else
         glu_join_act_kernel<float><<<join_grid((int64_t)p.T * p.F), dim3(256), 0, s>>>(p);
@@ -727,7 +831,9 @@ hipError_t launch_glu_backward(int vdtype, const GluBwd &p, hipStream_t s)
         const int64_t wgs = ceil_div((int64_t)rows * p.F * es / 16, 256);
         const dim3 grid((unsigned)(wgs < 8192 ? wgs : 8192));
         const bool once = 3 * (int64_t)p.T * p.F * es > ((int64_t)256 << 20);
-        if (vdtype == 1 && once)
+        if (p.g8.code)
+            glu_dact8_kernel<<<grid, dim3(256), 0, s>>>(p, rows);
+        else if (vdtype == 1 && once)
             glu_dact_kernel<__bf16, true><<<grid, dim3(256), 0, s>>>(p, rows);
         else if (vdtype == 1)
             glu_dact_kernel<__bf16, false><<<grid, dim3(256), 0, s>>>(p, rows);

@@ -1,0 +1,536 @@
+// logprob.hip -- log probabilities of given tokens from logits, the rows'
+// entropy and their most likely tokens (twell_logprob_forward), and the logits'
+// gradient (twell_logprob_backward).
+//
+// A row z of V logits, scaled by c (an inverse temperature), with m = max z:
+//   S = sum exp(c (z - m)),  W = sum c (z - m) exp(c (z - m)),  L = log S
+//   logp[v] = c (z[v] - m) - L,   entropy H = L - W / S
+//   dz[v] = c (dlogp (1[v = target] - p[v]) - dH p[v] (logp[v] + H))
+// Everything is relative to m, so nothing of size c m cancels: H is a sum of two
+// terms of one sign, and a likely token's logp keeps its digits.  A row is read
+// once, with the running maximum and sums of each thread (a larger maximum scales
+// the sums before it); a logit of -inf has p = 0, and its term of W is 0.
+// Exponentials are in base 2, as the hardware has them.
+#include "logprob.h"
+#include "rows.h"
+
+namespace twell {
+
+constexpr float LP_LOG2E = 1.44269504088896340736f, LP_LN2 = 0.69314718055994530942f;
+constexpr float LP_LEAST = -150.f;  // exp2 of it is 0; in the place of -inf, whose product with 0 is none
+
+// exp2's argument of a logit: (z - m) c, at least LP_LEAST (v_max drops the NaN of -inf - -inf).
+__device__ __forceinline__ float lp_arg(float z, float m, float c) { return fmaxf((z - m) * c, LP_LEAST); }
+__device__ __forceinline__ float lp_exp2(float x) { return __builtin_amdgcn_exp2f(x); }
+
+// The larger one, or NaN if either is (v_maximum3): a row's maximum tells of a NaN in it.
+__device__ __forceinline__ float lp_max(float a, float b) { return __builtin_elementwise_maximum(a, b); }
+
+// What is known of a part of a row: its largest logit, and relative to that the
+// sums of exp2(x) and of x exp2(x).
+struct LpState {
+    float m, s, w;
+
+    // The sums relative to a maximum that is no smaller.
+    __device__ __forceinline__ void raise(float to, float c)
+    {
+        const float by = lp_arg(m, to, c), f = lp_exp2(by);
+        w = f * fmaf(s, by, w);
+        s *= f;
+        m = to;
+    }
+    __device__ __forceinline__ void join(LpState o, float c)
+    {
+        const float to = lp_max(m, o.m);
+        raise(to, c);
+        o.raise(to, c);
+        s += o.s;
+        w += o.w;
+    }
+    __device__ __forceinline__ void add(float z, float c)
+    {
+        const float x = lp_arg(z, m, c), e = lp_exp2(x);
+        s += e;
+        w = fmaf(x, e, w);
+    }
+};
+
+// A logit's place in the order of the alternatives: larger values first, then
+// lower indices (+0 and -0 are the same value).  0 comes after all of them.
+__device__ __forceinline__ uint32_t lp_order(float z)
+{
+    const uint32_t b = __float_as_uint(z + 0.f);
+    return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
+}
+__device__ __forceinline__ uint64_t lp_key(float z, int v) { return (uint64_t)lp_order(z) << 32 | (0xFFFFFFFFu - (uint32_t)v); }
+__device__ __forceinline__ float lp_key_value(uint64_t key)
+{
+    const uint32_t o = (uint32_t)(key >> 32);
+    return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+}
+__device__ __forceinline__ int lp_key_index(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
+
+// The value of a row's results from its whole sums.
+struct LpRow {
+    float m, size2, entropy;  // size2 = log2 S
+    bool bad, empty;
+    __device__ __forceinline__ LpRow(const LpState &t) : m(t.m), bad(!(t.m < INFINITY)), empty(t.m == -INFINITY)
+    {
+        size2 = empty ? 0.f : __builtin_amdgcn_logf(t.s);
+        entropy = empty ? 0.f : LP_LN2 * (size2 - t.w / t.s);
+    }
+    __device__ __forceinline__ float logp(float z, float scale) const
+    {
+        if (bad)
+            return __uint_as_float(0x7FC00000u);
+        return empty ? -INFINITY : (z - m) * scale - LP_LN2 * size2;
+    }
+};
+
+template <typename TI> __device__ __forceinline__ void lp_finish(const LpArgs &p, int64_t t, const LpState &sum)
+{
+    const LpRow row(sum);
+    const float nan = __uint_as_float(0x7FC00000u);
+    if (p.norm) {
+        p.norm[2 * t] = row.bad ? nan : row.m;
+        p.norm[2 * t + 1] = row.bad ? nan : LP_LN2 * row.size2;
+    }
+    if (p.entropy)
+        p.entropy[t] = row.bad ? nan : row.entropy;
+    if (p.logp) {
+        const int at = p.id64 ? token_key((const int64_t *)p.targets, t, p.V) : token_key((const int32_t *)p.targets, t, p.V);
+        p.logp[t] = at < p.V ? row.logp((float)((const TI *)p.logits)[t * p.ld + at], p.scale) : 0.f;
+    }
+}
+
+constexpr int LP_THREADS = 256, LP_CAND = 1024;
+
+// Workgroup-wide scratch of the alternatives.
+struct LpTop {
+    uint32_t head[LP_THREADS];
+    uint32_t tau;
+    int count;
+    int cand_threads[LP_THREADS];
+    int n_threads;
+    uint64_t cand[LP_CAND];
+    uint64_t best[LP_THREADS];
+    uint64_t win;
+};
+
+// The k best keys of LpTop::cand[0 .. n), best first, to emit(rank, key).
+template <typename F> __device__ __forceinline__ void lp_rank(const uint64_t *cand, int n, int k, int tid, F emit)
+{
+    for (int i = tid; i < n; i += LP_THREADS) {
+        const uint64_t mine = cand[i];
+        int above = 0;
+        for (int j = 0; j < n; ++j)
+            above += cand[j] > mine;
+        if (above < k)
+            emit(above, mine);
+    }
+}
+
+// The k best logits of the segment [v0, v0 + n) of a row, best first, to
+// emit(rank, key); emit(rank, 0) where there are fewer.  `largest`: the largest of
+// those that this thread has read: pieces tid, tid + 256, ... of E elements, and
+// element tid of the rest.  The k-th largest of the threads' largest is a bound:
+// k logits reach it, and only threads whose largest does have others.  Their
+// pieces, a few kilobytes that the caches hold, are read again, and the logits
+// that reach the bound ranked by comparing each with each.  Where so many reach
+// it that the list overflows (equal logits in bulk), the best is taken k times: a
+// tournament of the threads' best remaining.
+template <typename TI, int E, typename F>
+__device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, LpTop &sh, int tid, F emit)
+{
+    const int whole = n / E, rest = n - whole * E;
+    const uint32_t head = lp_order(largest);
+    sh.head[tid] = head;
+    if (tid == 0) {
+        sh.count = 0;
+        sh.n_threads = 0;
+    }
+    __syncthreads();
+    int above = 0;
+    for (int j = 0; j < LP_THREADS; j += 4) {
+        const uint4 h = *reinterpret_cast<const uint4 *>(sh.head + j);
+        above += h.x > head || (h.x == head && j < tid);
+        above += h.y > head || (h.y == head && j + 1 < tid);
+        above += h.z > head || (h.z == head && j + 2 < tid);
+        above += h.w > head || (h.w == head && j + 3 < tid);
+    }
+    if (above == k - 1)
+        sh.tau = head;
+    __syncthreads();
+    const uint32_t tau = sh.tau;
+    if (head >= tau)
+        sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
+    __syncthreads();
+    const int nt = sh.n_threads, each = (whole + LP_THREADS - 1) / LP_THREADS;
+    auto offer = [&](float x, int v) {
+        if (lp_order(x) >= tau) {
+            const int at = atomicAdd(&sh.count, 1);
+            if (at < LP_CAND)
+                sh.cand[at] = lp_key(x, v);
+        }
+    };
+    for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
+        const int t = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
+        if (j < each) {
+            const int at = (j * LP_THREADS + t) * E;
+            if (at + E <= n) {
+                RowPiece<TI, E> v;
+                v.load(z + at);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    offer(v.at(e), v0 + at + e);
+            }
+        } else if (t < rest) {
+            offer((float)z[whole * E + t], v0 + whole * E + t);
+        }
+    }
+    __syncthreads();
+    const int found = sh.count;
+    if (found <= LP_CAND) {
+        for (int r = tid; r < k; r += LP_THREADS)
+            if (r >= found)
+                emit(r, (uint64_t)0);
+        lp_rank(sh.cand, found, k, tid, emit);
+        return;
+    }
+    // a thread's best key below `under`
+    auto best_of = [&](int t, int j0, int step, uint64_t under) {
+        uint64_t b = 0;
+        auto see = [&](float x, int v) {
+            const uint64_t key = lp_key(x, v);
+            b = key < under && key > b ? key : b;
+        };
+        for (int j = j0; j < each; j += step) {
+            const int at = (j * LP_THREADS + t) * E;
+            if (at + E <= n) {
+                RowPiece<TI, E> v;
+                v.load(z + at);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    see(v.at(e), v0 + at + e);
+            }
+        }
+        if (j0 == 0 && t < rest)
+            see((float)z[whole * E + t], v0 + whole * E + t);
+        return b;
+    };
+    sh.best[tid] = best_of(tid, 0, 1, ~(uint64_t)0);
+    for (int r = 0; r < k; ++r) {
+        __syncthreads();
+        if (tid < 64) {
+            uint64_t b = 0;
+            int who = 0;
+            for (int i = tid; i < LP_THREADS; i += 64)
+                if (sh.best[i] > b) {
+                    b = sh.best[i];
+                    who = i;
+                }
+#pragma unroll
+            for (int o = 32; o > 0; o >>= 1) {
+                const uint64_t ob = __shfl_xor(b, o, 64);
+                const int ow = __shfl_xor(who, o, 64);
+                if (ob > b) {
+                    b = ob;
+                    who = ow;
+                }
+            }
+            if (tid == 0) {
+                sh.win = b;
+                sh.n_threads = who;
+                emit(r, b);
+            }
+        }
+        __syncthreads();
+        const uint64_t win = sh.win;
+        const int who = sh.n_threads;
+        // the winner's next, from all threads
+        const uint64_t b = best_of(who, tid, LP_THREADS, win);
+        if (tid == 0)
+            sh.best[who] = 0;
+        __syncthreads();
+        if (b)
+            atomicMax((unsigned long long *)&sh.best[who], (unsigned long long)b);
+    }
+}
+
+// Sums of the threads' states over the workgroup, in every thread.
+__device__ __forceinline__ LpState lp_sum(LpState t, float c, LpState *waves, int tid)
+{
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) {
+        LpState u;
+        u.m = __shfl_xor(t.m, o, 64);
+        u.s = __shfl_xor(t.s, o, 64);
+        u.w = __shfl_xor(t.w, o, 64);
+        t.join(u, c);
+    }
+    if ((tid & 63) == 0)
+        waves[tid >> 6] = t;
+    __syncthreads();
+    LpState all{-INFINITY, 0.f, 0.f};
+#pragma unroll
+    for (int w = 0; w < LP_THREADS / 64; ++w)
+        all.join(waves[w], c);
+    return all;
+}
+
+// ------------------------------------------------------------------ forward
+// One workgroup a segment of a row.
+template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_kernel(LpArgs p)
+{
+    constexpr int E = Elt<TI>::PER_CHUNK, U = 4;
+    __shared__ LpState waves[LP_THREADS / 64];
+    __shared__ __attribute__((aligned(16))) char top_mem[TOP ? sizeof(LpTop) : 16];
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x / p.segs;
+    const int s = (int)(blockIdx.x - t * p.segs), v0 = s * p.seg;
+    const int n = p.V - v0 < p.seg ? p.V - v0 : p.seg;
+    const TI *z = (const TI *)p.logits + t * p.ld + v0;
+    const float c = p.scale2;
+    LpState st{-INFINITY, 0.f, 0.f};
+    const int whole = n / E, rest = n - whole * E;
+    for (int i = tid; i < whole; i += LP_THREADS * U) {
+        RowPiece<TI, E> v[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u * LP_THREADS < whole)
+                v[u].load(z + (int64_t)(i + u * LP_THREADS) * E);
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (i + u * LP_THREADS < whole) {
+                float top = v[u].at(0);
+#pragma unroll
+                for (int e = 1; e < E; ++e)
+                    top = lp_max(top, v[u].at(e));
+                if (!(top <= st.m))
+                    st.raise(lp_max(top, st.m), c);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    st.add(v[u].at(e), c);
+            }
+    }
+    if (tid < rest) {
+        const float x = (float)z[whole * E + tid];
+        if (!(x <= st.m))
+            st.raise(lp_max(x, st.m), c);
+        st.add(x, c);
+    }
+    const float largest = st.m;
+    st = lp_sum(st, c, waves, tid);
+    if (tid == 0) {
+        if (p.segs == 1)
+            lp_finish<TI>(p, t, st);
+        else
+            p.part[t * p.segs + s] = st;
+    }
+    if constexpr (TOP) {
+        LpTop &sh = *reinterpret_cast<LpTop *>(top_mem);
+        if (p.segs == 1) {
+            const LpRow row(st);
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, sh, tid, [&](int r, uint64_t key) {
+                p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
+                p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
+            });
+        } else {
+            uint64_t *keys = p.keys + (t * p.segs + s) * p.k;
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
+        }
+    }
+}
+
+// The segments of a row joined, in order.  The k best of their sorted lists: as
+// in a segment, with the first few entries of each list for the threads' largest.
+template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_join_kernel(LpArgs p)
+{
+    constexpr int MOST = LP_MOST_TOP * LP_MOST_TOP;
+    __shared__ uint64_t head[TOP ? LP_THREADS : 1], cand[TOP ? MOST : 1];
+    __shared__ uint64_t tau;
+    __shared__ int count;
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x;
+    LpState st{-INFINITY, 0.f, 0.f};
+    for (int s = 0; s < p.segs; ++s)
+        st.join(p.part[t * p.segs + s], p.scale2);
+    if (tid == 0)
+        lp_finish<TI>(p, t, st);
+    if constexpr (TOP) {
+        const LpRow row(st);
+        const uint64_t *keys = p.keys + t * p.segs * p.k;
+        auto emit = [&](int r, uint64_t key) {
+            p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
+            p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
+        };
+        const int first = LP_THREADS / p.segs, list = tid / first, entry = tid % first;
+        const bool on = list < p.segs && entry < p.k;
+        const uint64_t mine = on ? keys[list * p.k + entry] : 0;
+        head[tid] = mine;
+        if (tid == 0)
+            count = 0;
+        __syncthreads();
+        int above = 0;
+        for (int j = 0; j < LP_THREADS; ++j) {
+            const uint64_t h = head[j];
+            above += h > mine || (h == mine && j < tid);
+        }
+        if (above == p.k - 1)
+            tau = mine;
+        __syncthreads();
+        const uint64_t bound = tau > 0 ? tau : 1;
+        for (int i = tid; i < p.segs * p.k; i += LP_THREADS) {
+            const uint64_t key = keys[i];
+            if (key >= bound) {
+                const int at = atomicAdd(&count, 1);
+                cand[at < MOST ? at : MOST - 1] = key;
+            }
+        }
+        __syncthreads();
+        lp_rank(cand, count < MOST ? count : MOST, p.k, tid, emit);
+    }
+}
+
+// ------------------------------------------------------------------ backward
+// One workgroup a chunk of a row.  Every thread has read all of its elements
+// before it writes them: dlogits may be logits.
+constexpr int LP_BACK_U = 4;
+template <typename TI> __global__ __launch_bounds__(LP_THREADS) void logprob_backward_kernel(LpArgs p)
+{
+    constexpr int E = Elt<TI>::PER_CHUNK, U = LP_BACK_U;
+    const int tid = threadIdx.x;
+    const int64_t t = blockIdx.x / p.segs;
+    const int v0 = (int)(blockIdx.x - t * p.segs) * p.seg;
+    const int n = p.V - v0 < p.seg ? p.V - v0 : p.seg;
+    const TI *z = (const TI *)p.logits + t * p.ld + v0;
+    TI *o = (TI *)p.dlogits + t * p.ldd + v0;
+    const float m = p.norm_in[2 * t], size = p.norm_in[2 * t + 1];
+    const bool empty = m == -INFINITY;
+    int at = p.V;
+    if (p.dlogp)
+        at = p.id64 ? token_key((const int64_t *)p.targets, t, p.V) : token_key((const int32_t *)p.targets, t, p.V);
+    // dz = p (a - b logp) [+ -a at the target], in base 2
+    const float h = p.dentropy ? p.dentropy[t] * p.scale : 0.f;
+    const float d = at < p.V && !empty ? p.dlogp[t] * p.scale : 0.f;
+    float a = -d - (p.dentropy ? h * p.entropy_in[t] : 0.f), b = -h * LP_LN2;
+    if (empty)
+        a = b = 0.f;
+    if (size != size)
+        a = size;
+    const float base = empty ? 0.f : m, size2 = size * LP_LOG2E;
+    auto grad = [&](float x) {
+        const float l = fmaxf(fmaf(x - base, p.scale2, -size2), LP_LEAST);
+        return lp_exp2(l) * fmaf(b, l, a);
+    };
+    const int whole = n / E, rest = n - whole * E;
+    at -= v0;
+    RowPiece<TI, E> v[U];
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (tid + u * LP_THREADS < whole)
+            v[u].load(z + (tid + u * LP_THREADS) * E);
+    TI last{};
+    if (tid < rest)
+        last = z[whole * E + tid];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+        const int i = (tid + u * LP_THREADS) * E;
+        if (i / E < whole) {
+            float g[E];
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                g[e] = grad(v[u].at(e));
+            if (at >= i && at < i + E)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    g[e] += at == i + e ? d : 0.f;
+            rows_store<E>(o + i, g, 0);
+        }
+    }
+    if (tid < rest)
+        o[whole * E + tid] = (TI)(grad((float)last) + (at == whole * E + tid ? d : 0.f));
+}
+
+// ------------------------------------------------------------------ host
+static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
+
+// Few rows are cut into segments, so that LP_WGS workgroups have work; a segment
+// has at least LP_SEG logits.
+constexpr int LP_WGS = 1024, LP_SEG = 4096, LP_MOST_SEGS = 64;
+
+static int most_segments(int V)
+{
+    const int64_t n = ceil_div(V, LP_SEG);
+    return (int)(n < LP_MOST_SEGS ? n : LP_MOST_SEGS);
+}
+
+void lp_segments(int T, int V, int &segs, int &seg)
+{
+    const int64_t want = T > 0 ? ceil_div(LP_WGS, T) : 1, most = most_segments(V);
+    const int64_t n = want < most ? want : most;
+    seg = (int)(ceil_div(ceil_div(V, n), 8) * 8);
+    segs = (int)ceil_div(V, seg);
+}
+
+static size_t bytes_of(int64_t parts, int k) { return (size_t)parts * (sizeof(LpState) + (size_t)k * 8); }
+
+size_t lp_workspace(int T, int V, int k)
+{
+    int segs, seg;
+    lp_segments(T, V, segs, seg);
+    return segs > 1 ? bytes_of((int64_t)T * segs, k) : 0;
+}
+
+// Rows t times segments: at most most_segments(V) each, and below LP_WGS + t.
+size_t lp_most_workspace(int T, int V, int k)
+{
+    const int64_t t = T < LP_WGS ? T : LP_WGS - 1, most = most_segments(V);
+    if (most == 1)
+        return 0;
+    const int64_t a = t * most, b = LP_WGS + t;
+    return bytes_of(a < b ? a : b, k);
+}
+
+hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
+{
+    LpArgs p = args;
+    p.scale2 = p.scale * LP_LOG2E;
+    lp_segments(p.T, p.V, p.segs, p.seg);
+    if (p.segs > 1) {
+        p.keys = (uint64_t *)ws;
+        p.part = (LpState *)(p.keys + (int64_t)p.T * p.segs * p.k);
+    }
+    const dim3 grid((unsigned)((int64_t)p.T * p.segs)), block(LP_THREADS);
+    if (p.bf16)
+        p.k ? logprob_kernel<__bf16, true><<<grid, block, 0, s>>>(p) : logprob_kernel<__bf16, false><<<grid, block, 0, s>>>(p);
+    else
+        p.k ? logprob_kernel<float, true><<<grid, block, 0, s>>>(p) : logprob_kernel<float, false><<<grid, block, 0, s>>>(p);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess || p.segs == 1)
+        return e;
+    const dim3 rows((unsigned)p.T);
+    if (p.bf16)
+        p.k ? logprob_join_kernel<__bf16, true><<<rows, block, 0, s>>>(p)
+            : logprob_join_kernel<__bf16, false><<<rows, block, 0, s>>>(p);
+    else
+        p.k ? logprob_join_kernel<float, true><<<rows, block, 0, s>>>(p)
+            : logprob_join_kernel<float, false><<<rows, block, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+hipError_t launch_logprob_backward(const LpArgs &args, hipStream_t s)
+{
+    LpArgs p = args;
+    p.scale2 = p.scale * LP_LOG2E;
+    p.seg = LP_THREADS * LP_BACK_U * (p.bf16 ? 8 : 4);
+    p.segs = (int)ceil_div(p.V, p.seg);
+    const dim3 grid((unsigned)((int64_t)p.T * p.segs)), block(LP_THREADS);
+    if (p.bf16)
+        logprob_backward_kernel<__bf16><<<grid, block, 0, s>>>(p);
+    else
+        logprob_backward_kernel<float><<<grid, block, 0, s>>>(p);
+    return hipGetLastError();
+}
+
+}  // namespace twell
