@@ -42,14 +42,15 @@ def embed_forward(ids, table, scale):
 
 def embed_backward(ids, dout, V, scale, old=None):
     """A sum of n terms in any order is off by at most n u of their magnitudes; the scale, and the addition to what was
-    there, are two roundings more."""
+    there, are two roundings more.  (On the host, where a sum over one id for all tokens is quick.)"""
+    device, ids, dout = dout.device, ids.cpu(), dout.cpu()
     at, ok = _there(ids, V)
     at, rows = at[ok], dout[ok].double()
     scale = float(torch.tensor(scale, dtype=torch.float32))
-    zero = torch.zeros((V, dout.shape[1]), dtype=torch.float64, device=dout.device)
-    total = zero.index_add(0, at, rows) * scale
-    size = zero.index_add(0, at, rows.abs()) * abs(scale)
-    n = torch.zeros(V, dtype=torch.float64, device=dout.device).index_add(0, at, torch.ones_like(at, dtype=torch.float64))
+    zero = torch.zeros((V, dout.shape[1]), dtype=torch.float64)
+    total = (zero.index_add(0, at, rows) * scale).to(device)
+    size = (zero.index_add(0, at, rows.abs()) * abs(scale)).to(device)
+    n = torch.zeros(V, dtype=torch.float64).index_add(0, at, torch.ones_like(at, dtype=torch.float64)).to(device)
     bound = (n[:, None] + 3) * U * size
     if old is None:
         return total, bound

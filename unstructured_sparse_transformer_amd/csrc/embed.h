@@ -8,7 +8,8 @@
 
 namespace twell {
 
-constexpr int EMB_WINDOW = 32;      // sorted tokens that one sum takes at most
+constexpr int EMB_WINDOW = 32, EMB_WINDOW_SHORT = 8;  // sorted tokens that one sum takes at most
+constexpr int EMB_SHORT = 2048;     // tokens up to which the short windows are taken
 constexpr int EMB_FEW = 8192;       // tokens up to which ranks are counted in one launch
 constexpr int EMB_DIGIT_BITS = 9;   // of a sorting pass
 constexpr int EMB_MOST_BLOCKS = 256;  // workgroups of a sorting pass
@@ -25,10 +26,16 @@ struct EmbArgs {
     int32_t *key, *perm;    // [T] the tokens' keys in ascending order (V: no id), and their rows
     int32_t *key2, *perm2;  // [T] the other side of a sorting pass
     int32_t *counts;        // [blocks][2^EMB_DIGIT_BITS]
-    float *part;            // [2 windows][emb_pitch(d)] sums of runs that windows cut
+    float *part;            // [windows][2][emb_pitch(d)] sums of runs that windows cut
 };
 
-inline int64_t emb_windows(int64_t T) { return (T + EMB_WINDOW - 1) / EMB_WINDOW; }
+// The most windows of any call with up to T tokens.
+inline int64_t emb_most_windows(int64_t T)
+{
+    const int64_t shorter = ((T < EMB_SHORT ? T : EMB_SHORT) + EMB_WINDOW_SHORT - 1) / EMB_WINDOW_SHORT;
+    const int64_t n = (T + EMB_WINDOW - 1) / EMB_WINDOW;
+    return n > shorter ? n : shorter;
+}
 __host__ __device__ inline int64_t emb_pitch(int d) { return ((int64_t)d + 3) & ~(int64_t)3; }
 
 // Places the workspace's parts at `base`; returns its bytes (never less for more tokens).

@@ -84,8 +84,9 @@ __device__ __forceinline__ void emb_fill(const EmbArgs &p, int wg, int wgs)
             *(uint16_t *)q = 0;
     }
     const int64_t n = (z - a) / 16;
-    for (int64_t i = (int64_t)wg * blockDim.x + threadIdx.x; i < n; i += (int64_t)wgs * blockDim.x)
-        reinterpret_cast<u32x4 *>(a)[i] = u32x4{0, 0, 0, 0};
+    const int64_t per = (n + wgs - 1) / wgs, stop = (wg + 1) * per < n ? (wg + 1) * per : n;
+    for (int64_t i = wg * per + threadIdx.x; i < stop; i += blockDim.x)
+        __builtin_nontemporal_store(u32x4{0, 0, 0, 0}, reinterpret_cast<u32x4 *>(a) + i);
 }
 
 // Up to EMB_FEW tokens in one launch: a token's place is the number of tokens
@@ -101,8 +102,20 @@ template <typename ID> __global__ __launch_bounds__(256) void emb_rank_kernel(Em
         return;
     }
     const int tid = threadIdx.x, groups = (p.T + 31) / 32;
-    for (int t = tid; t < groups * 32; t += 256)
-        keys[t] = t < p.T ? token_key((const ID *)p.ids, t, p.V) : 0x7FFFFFF0;  // (above V)
+    for (int t0 = 0; t0 < groups * 32; t0 += 256 * 8) {
+        int k[8];
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + i * 256 + tid;
+            k[i] = token_key((const ID *)p.ids, t < p.T ? t : p.T - 1, p.V);
+        }
+#pragma unroll
+        for (int i = 0; i < 8; ++i) {
+            const int t = t0 + i * 256 + tid;
+            if (t < groups * 32)
+                keys[t] = t < p.T ? k[i] : 0x7FFFFFF0;  // (above V)
+        }
+    }
     __syncthreads();
     const int own = (int)blockIdx.x, mine = tid & 31, key = keys[own * 32 + mine];
     int n = 0;
@@ -234,108 +247,121 @@ __global__ __launch_bounds__(EMB_SORT_THREADS) void emb_move_kernel(EmbArgs p, E
 
 // ------------------------------------------------------------------ sums
 // The table's row of a sum, or the sum and what was there.
-template <typename TT, int E>
-__device__ __forceinline__ void emb_write(const EmbArgs &p, int key, int c, int from, const float (&sum)[E])
+template <typename TT, int E, bool ADD>
+__device__ __forceinline__ void emb_write(const EmbArgs &p, int key, int c, int from, const float (&sum)[E],
+                                          const RowPiece<TT, E> &old)
 {
-    TT *o = (TT *)p.out + (int64_t)key * p.d + c;
     float v[E];
-    if (p.accumulate) {
-        RowPiece<TT, E> old;
-        old.load(o);
 #pragma unroll
-        for (int e = 0; e < E; ++e)
-            v[e] = fmaf(sum[e], p.scale, old.at(e));
-    } else {
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            v[e] = sum[e] * p.scale;
-    }
-    rows_store<E>(o, v, from);
+    for (int e = 0; e < E; ++e)
+        v[e] = ADD ? fmaf(sum[e], p.scale, old.at(e)) : sum[e] * p.scale;
+    // (without ADD the columns that two pieces have get the same values from both)
+    rows_store<E>((TT *)p.out + (int64_t)key * p.d + c, v, ADD ? from : 0);
 }
 
-// A run (the sorted tokens of one id) is cut at multiples of EMB_WINDOW.  The
-// thread at the first token of a run, or of a window that goes on with one, adds
-// the rows up to the run's or the window's end; the others have nothing to do.
-// The sums of cut runs go to `part`: a window's first rows, if the run began
-// before it, to its slot 0, its last ones, if the run begins in it, to slot 1.
-template <typename TD, typename TT, int E> __global__ __launch_bounds__(256) void emb_sum_kernel(EmbArgs p)
+// A run (the sorted tokens of one id) is cut at multiples of the window W.  A wave
+// takes a window and 64 pieces of columns: its keys come in one load, its rows (and
+// with ADD the table's, of the runs that end) in batches of 8 one batch ahead,
+// however its runs lie, and the runs are added up in order.  (All 32 rows at once in
+// unrolled code: its instructions arrive later than the rows, 15 us at 1003 tokens
+// of 1001 columns; loads and sums behind branches 17 us.)  Few tokens have windows
+// of 8: four times the waves, and one batch each.  The sums of cut runs go to `part`: a window's first rows, if the
+// run began before it, to its slot 0, its last ones, if the run begins in it and
+// goes on, to slot 1.
+template <typename TD, typename TT, int E, bool ADD, int W>
+__global__ __launch_bounds__(256) void emb_sum_kernel(EmbArgs p, int slices)
 {
-    constexpr int B = 8;  // rows on their way at once
-    const int pieces = (p.d + E - 1) / E;
-    const EmbItem it = emb_item((int64_t)blockIdx.x * 256, threadIdx.x, pieces);
-    if (it.row >= p.T)
+    constexpr int B = 8;
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (threadIdx.x >> 6));
+    const int w = wave / slices, piece = (wave - w * slices) * 64 + lane, first = w * W;
+    if (first >= p.T)
         return;
-    const int at = (int)it.row, key = p.key[at];
-    if (key >= p.V)
-        return;
-    const bool goes_on = at > 0 && p.key[at - 1] == key;
-    if (goes_on && at % EMB_WINDOW != 0)
-        return;
-    const int last = at / EMB_WINDOW * EMB_WINDOW + EMB_WINDOW, end = last < p.T ? last : p.T;
-    int from;
-    const int c = rows_column<E>(it.piece, p.d, from);
-    const TD *rows = (const TD *)p.in + c;
-    float sum[E];
-    {
-        RowPiece<TD, E> v;
-        v.load(rows + (int64_t)p.perm[at] * p.d);
-#pragma unroll
-        for (int e = 0; e < E; ++e)
-            sum[e] = v.at(e);
-    }
-    int i = at + 1;
-    for (bool more = i < end; more;) {
-        int row[B];
-        bool in[B];
+    // lane l < 32: token l of the window; lane 32: the key after the window, 33: the one before
+    const int at = lane <= W ? first + lane : first - 1;
+    const bool there = at >= 0 && at < p.T;
+    const int keys = there ? p.key[at] : p.V, rows = there && lane < W ? p.perm[at] : 0;
+    const bool on = piece < (p.d + E - 1) / E;
+    int from = 0;
+    const int c = on ? rows_column<E>(piece, p.d, from) : 0;  // (lanes past the columns read the first ones)
+    auto key = [&](int j) { return __builtin_amdgcn_readlane(keys, j); };
+    struct Batch {
+        RowPiece<TD, E> v[B];
+        RowPiece<TT, E> old[ADD ? B : 1];
+    };
+    auto load = [&](int h, Batch &t) {  // (of any token, also where its row is not wanted: no load waits behind a branch)
 #pragma unroll
         for (int b = 0; b < B; ++b) {
-            const int j = i + b < end ? i + b : end - 1;
-            in[b] = i + b < end && p.key[j] == key;
-            row[b] = p.perm[j];
+            const int j = (h + b) & (W - 1), k = key(j);
+            t.v[b].load((const TD *)p.in + (int64_t)__builtin_amdgcn_readlane(rows, j) * p.d + c);
+            if constexpr (ADD)
+                t.old[b].load((const TT *)p.out + (int64_t)(k < p.V ? k : 0) * p.d + c);
         }
-        RowPiece<TD, E> v[B];
+    };
+    float *part = p.part + 2 * (int64_t)w * emb_pitch(p.d) + c;
+    float sum[E];
 #pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (in[b])
-                v[b].load(rows + (int64_t)row[b] * p.d);
+    for (int e = 0; e < E; ++e)
+        sum[e] = 0.f;
+    bool cut = key(W + 1) == key(0);  // the run at hand began before the window
+    auto add = [&](int h, const Batch &t) {
 #pragma unroll
-        for (int b = 0; b < B; ++b)
-            if (in[b]) {
-                ++i;
+        for (int b = 0; b < B; ++b) {
+            const int k = key(h + b);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                sum[e] += t.v[b].at(e);
+            const bool ends = key(h + b + 1) != k;
+            if (ends || h + b + 1 == W) {
+                if (k < p.V && on) {
+                    if (cut || !ends)
+                        rows_store<E>(part + (cut ? 0 : emb_pitch(p.d)), sum, 0);
+                    else
+                        emb_write<TT, E, ADD>(p, k, c, from, sum, t.old[ADD ? b : 0]);
+                }
+                cut = false;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    sum[e] += v[b].at(e);
+                    sum[e] = 0.f;
             }
-        more = in[B - 1] && i < end;
+        }
+    };
+    Batch one, two;
+    load(0, one);
+    if constexpr (W == B) {
+        add(0, one);
+    } else {
+#pragma clang loop unroll(disable)
+        for (int h = 0; h < W && key(h) < p.V; h += 2 * B) {
+            load(h + B, two);
+            add(h, one);
+            load(h + 2 * B, one);
+            add(h + B, two);
+        }
     }
-    const bool goes_past = i == last && last < p.T && p.key[last] == key;
-    if (goes_on || goes_past)
-        rows_store<E>(p.part + (2 * (int64_t)(at / EMB_WINDOW) + !goes_on) * emb_pitch(p.d) + c, sum, 0);
-    else
-        emb_write<TT, E>(p, key, c, from, sum);
 }
 
-// The cut runs: the sums of a run's windows, added by 16 waves, each every 16th
-// in order, whose results are added in order.
-constexpr int EMB_JOIN_WAVES = 16;
-template <typename TT, int E> __global__ __launch_bounds__(EMB_JOIN_WAVES * 64) void emb_join_kernel(EmbArgs p)
+// The cut runs: the sums of a run's windows, added by NW waves, each every NW-th in
+// order, whose results are added in order.
+template <typename TT, int E, int NW> __global__ __launch_bounds__(NW * 64) void emb_join_kernel(EmbArgs p, int W)
 {
-    __shared__ float all[EMB_JOIN_WAVES][E][64];
+    __shared__ float all[NW][E][64];
     const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
     const int pieces = (p.d + E - 1) / E, piece = blockIdx.y * 64 + lane;
-    const int windows = (p.T + EMB_WINDOW - 1) / EMB_WINDOW;
+    const int windows = (p.T + W - 1) / W;
     const bool on = piece < pieces;
     int from = 0;
     const int c = on ? rows_column<E>(piece, p.d, from) : 0;
     for (int w = blockIdx.x; w + 1 < windows; w += gridDim.x) {
-        const int first = w * EMB_WINDOW, next = first + EMB_WINDOW, key = p.key[next];
+        const int first = w * W, next = first + W;
+        const int key = p.key[next], end = p.key[next - 1], begin = p.key[first], before = p.key[first > 0 ? first - 1 : 0];
         // a run that begins in window w and goes on in the next
-        if (key >= p.V || p.key[next - 1] != key || (p.key[first] == key && first > 0 && p.key[first - 1] == key))
+        if (key >= p.V || end != key || (begin == key && first > 0 && before == key))
             continue;
         int lo = w + 1, hi = windows;  // the first window after it that does not begin with it
         while (hi - lo > 1) {
             const int mid = lo + (hi - lo) / 2;
-            if (p.key[mid * EMB_WINDOW] == key)
+            if (p.key[mid * W] == key)
                 lo = mid;
             else
                 hi = mid;
@@ -346,8 +372,8 @@ template <typename TT, int E> __global__ __launch_bounds__(EMB_JOIN_WAVES * 64) 
         for (int e = 0; e < E; ++e)
             sum[e] = 0.f;
         if (on) {
-#pragma unroll 4
-            for (int i = wave; i < n; i += EMB_JOIN_WAVES) {
+#pragma unroll 8
+            for (int i = wave; i < n; i += NW) {
                 RowPiece<float, E> v;
                 v.load(p.part + (2 * (int64_t)(w + i) + (i == 0)) * emb_pitch(p.d) + c);
 #pragma unroll
@@ -360,11 +386,17 @@ template <typename TT, int E> __global__ __launch_bounds__(EMB_JOIN_WAVES * 64) 
             all[wave][e][lane] = sum[e];
         __syncthreads();
         if (wave == 0 && on) {
-            for (int k = 1; k < EMB_JOIN_WAVES && k < n; ++k)
+            for (int k = 1; k < NW && k < n; ++k)
 #pragma unroll
                 for (int e = 0; e < E; ++e)
                     sum[e] += all[k][e][lane];
-            emb_write<TT, E>(p, key, c, from, sum);
+            RowPiece<TT, E> old;
+            if (p.accumulate) {
+                old.load((const TT *)p.out + (int64_t)key * p.d + c);
+                emb_write<TT, E, true>(p, key, c, from, sum, old);
+            } else {
+                emb_write<TT, E, false>(p, key, c, from, sum, old);
+            }
         }
         __syncthreads();
     }
@@ -385,7 +417,7 @@ size_t emb_layout(EmbArgs &a, void *base)
     };
     a.key = (int32_t *)take(list);
     a.perm = (int32_t *)take(list);
-    a.part = (float *)take(a.T > EMB_WINDOW ? up256_((size_t)2 * emb_windows(a.T) * emb_pitch(a.d) * 4) : 0);
+    a.part = (float *)take(up256_((size_t)2 * emb_most_windows(a.T) * emb_pitch(a.d) * 4));
     if (a.T > EMB_FEW) {
         a.key2 = (int32_t *)take(list);
         a.perm2 = (int32_t *)take(list);
@@ -420,8 +452,8 @@ hipError_t launch_embed(const EmbArgs &p, hipStream_t s)
 template <typename ID> static hipError_t run_sort(EmbArgs &p, hipStream_t s)
 {
     const int64_t bytes = (int64_t)p.V * p.d * (p.bf16_table ? 2 : 4);
-    const int64_t want = p.accumulate ? 0 : ceil_div(bytes, 256 * 16 * 4);
-    const int fill = (int)(want < 2048 ? want : 2048);
+    const int64_t want = p.accumulate ? 0 : ceil_div(bytes, 256 * 16 * 2);
+    const int fill = (int)(want < (1 << 20) ? want : 1 << 20);
     if (p.T <= EMB_FEW) {
         const int wgs = (int)ceil_div(p.T, 32);
         if (wgs + fill > 0)
@@ -449,14 +481,22 @@ template <typename ID> static hipError_t run_sort(EmbArgs &p, hipStream_t s)
     return hipGetLastError();
 }
 
-template <typename TD, typename TT, int E> static hipError_t run_sums(const EmbArgs &p, hipStream_t s)
+template <typename TD, typename TT, int E, int W> static hipError_t run_sums(const EmbArgs &p, hipStream_t s)
 {
-    const int64_t pieces = ceil_div(p.d, E);
-    emb_sum_kernel<TD, TT, E><<<dim3((unsigned)ceil_div(p.T * pieces, 256)), dim3(256), 0, s>>>(p);
-    const int64_t windows = emb_windows(p.T), y = ceil_div(pieces, 64);
+    const int64_t windows = ceil_div(p.T, W), slices = ceil_div(ceil_div(p.d, E), 64);
+    const dim3 grid((unsigned)ceil_div(windows * slices, 4)), block(256);
+    if (p.accumulate)
+        emb_sum_kernel<TD, TT, E, true, W><<<grid, block, 0, s>>>(p, (int)slices);
+    else
+        emb_sum_kernel<TD, TT, E, false, W><<<grid, block, 0, s>>>(p, (int)slices);
     if (windows > 1) {
-        const int64_t most = ceil_div(2048, y), x = windows - 1 < most ? windows - 1 : most;
-        emb_join_kernel<TT, E><<<dim3((unsigned)x, (unsigned)y), dim3(EMB_JOIN_WAVES * 64), 0, s>>>(p);
+        const int64_t most = ceil_div(2048, slices), x = windows - 1 < most ? windows - 1 : most;
+        const dim3 runs((unsigned)x, (unsigned)slices);
+        // (a run has at most all windows: 64 and more for each of 4 waves from here on)
+        if (windows <= 256)
+            emb_join_kernel<TT, E, 4><<<runs, dim3(256), 0, s>>>(p, W);
+        else
+            emb_join_kernel<TT, E, 16><<<runs, dim3(1024), 0, s>>>(p, W);
     }
     return hipGetLastError();
 }
@@ -472,7 +512,9 @@ hipError_t launch_embed_backward(const EmbArgs &args, hipStream_t s)
     auto with = [&](auto rows, auto table) {
         using TD = decltype(rows);
         using TT = decltype(table);
-        return p.d >= 4 ? run_sums<TD, TT, 4>(p, s) : run_sums<TD, TT, 1>(p, s);
+        if (p.d < 4)
+            return run_sums<TD, TT, 1, EMB_WINDOW>(p, s);
+        return p.T <= EMB_SHORT ? run_sums<TD, TT, 4, EMB_WINDOW_SHORT>(p, s) : run_sums<TD, TT, 4, EMB_WINDOW>(p, s);
     };
     if (p.bf16_table)
         return p.bf16_rows ? with(__bf16{}, __bf16{}) : with(float{}, __bf16{});
