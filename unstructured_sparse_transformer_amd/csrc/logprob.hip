@@ -13,6 +13,9 @@
 // Exponentials are in base 2, as the hardware has them.
 #include "logprob.h"
 #include "rows.h"
+#include "wave_ops.h"
+
+#include <type_traits>
 
 namespace twell {
 
@@ -87,7 +90,8 @@ struct LpRow {
     }
 };
 
-template <typename TI> __device__ __forceinline__ void lp_finish(const LpArgs &p, int64_t t, const LpState &sum)
+// A row's results; `given`: its token's logit is z.
+__device__ __forceinline__ void lp_finish(const LpArgs &p, int64_t t, const LpState &sum, bool given, float z)
 {
     const LpRow row(sum);
     const float nan = __uint_as_float(0x7FC00000u);
@@ -97,32 +101,43 @@ template <typename TI> __device__ __forceinline__ void lp_finish(const LpArgs &p
     }
     if (p.entropy)
         p.entropy[t] = row.bad ? nan : row.entropy;
-    if (p.logp) {
-        const int at = p.id64 ? token_key((const int64_t *)p.targets, t, p.V) : token_key((const int32_t *)p.targets, t, p.V);
-        p.logp[t] = at < p.V ? row.logp((float)((const TI *)p.logits)[t * p.ld + at], p.scale) : 0.f;
-    }
+    if (p.logp)
+        p.logp[t] = given ? row.logp(z, p.scale) : 0.f;
 }
 
 constexpr int LP_THREADS = 256, LP_CAND = 1024;
+constexpr int LP_SEG = 4096, LP_MOST_SEGS = 64;
 
 // Workgroup-wide scratch of the alternatives.
 struct LpTop {
-    uint32_t head[LP_THREADS];
-    uint32_t tau;
-    int count;
+    uint32_t tau[LP_THREADS / 64];
+    int count, n_threads;
     int cand_threads[LP_THREADS];
-    int n_threads;
     uint64_t cand[LP_CAND];
     uint64_t best[LP_THREADS];
     uint64_t win;
 };
 
-// The k best keys of LpTop::cand[0 .. n), best first, to emit(rank, key).
+// The r-th largest (r from 1) of the wave's values.
+__device__ __forceinline__ uint32_t lp_nth(uint32_t v, int r, int lane)
+{
+    int above = 0;
+#pragma unroll 16
+    for (int j = 0; j < 64; ++j) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, j);
+        above += o > v || (o == v && j < lane);
+    }
+    const uint64_t it = __ballot(above == r - 1);
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, __builtin_ctzll(it));
+}
+
+// The k best keys of cand[0 .. n), best first, to emit(rank, key).
 template <typename F> __device__ __forceinline__ void lp_rank(const uint64_t *cand, int n, int k, int tid, F emit)
 {
     for (int i = tid; i < n; i += LP_THREADS) {
         const uint64_t mine = cand[i];
         int above = 0;
+#pragma unroll 8
         for (int j = 0; j < n; ++j)
             above += cand[j] > mine;
         if (above < k)
@@ -133,63 +148,97 @@ template <typename F> __device__ __forceinline__ void lp_rank(const uint64_t *ca
 // The k best logits of the segment [v0, v0 + n) of a row, best first, to
 // emit(rank, key); emit(rank, 0) where there are fewer.  `largest`: the largest of
 // those that this thread has read: pieces tid, tid + 256, ... of E elements, and
-// element tid of the rest.  The k-th largest of the threads' largest is a bound:
-// k logits reach it, and only threads whose largest does have others.  Their
-// pieces, a few kilobytes that the caches hold, are read again, and the logits
-// that reach the bound ranked by comparing each with each.  Where so many reach
-// it that the list overflows (equal logits in bulk), the best is taken k times: a
-// tournament of the threads' best remaining.
-template <typename TI, int E, typename F>
-__device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, LpTop &sh, int tid, F emit)
+// element tid of the rest; own(f) calls f(logit, index) for each of them.  In each
+// of the 4 waves k / 4 threads have a largest that reaches the (k / 4)-th largest of
+// the wave's: the lowest of these four values is a bound that k logits reach.  Only
+// threads whose largest reaches it have any that do; the logits that reach it are
+// ranked by comparing each with each.  Where so many do that the list overflows
+// (equal logits in bulk), those above the bound are listed, and then as many of the
+// equal ones as are wanted, the lowest indices first.  If even those above the bound
+// are too many (all in few threads), the best is taken k times: a tournament of the
+// threads' best remaining.
+template <typename TI, int E, typename O, typename F>
+__device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, O own, LpTop &sh, int tid, F emit)
 {
-    const int whole = n / E, rest = n - whole * E;
+    const int whole = n / E, rest = n - whole * E, lane = tid & 63, each = (whole + LP_THREADS - 1) / LP_THREADS;
     const uint32_t head = lp_order(largest);
-    sh.head[tid] = head;
+    const uint32_t mine = lp_nth(head, (k + LP_THREADS / 64 - 1) / (LP_THREADS / 64), lane);
+    if (lane == 0)
+        sh.tau[tid >> 6] = mine;
     if (tid == 0) {
         sh.count = 0;
         sh.n_threads = 0;
     }
     __syncthreads();
-    int above = 0;
-    for (int j = 0; j < LP_THREADS; j += 4) {
-        const uint4 h = *reinterpret_cast<const uint4 *>(sh.head + j);
-        above += h.x > head || (h.x == head && j < tid);
-        above += h.y > head || (h.y == head && j + 1 < tid);
-        above += h.z > head || (h.z == head && j + 2 < tid);
-        above += h.w > head || (h.w == head && j + 3 < tid);
-    }
-    if (above == k - 1)
-        sh.tau = head;
-    __syncthreads();
-    const uint32_t tau = sh.tau;
-    if (head >= tau)
-        sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
-    __syncthreads();
-    const int nt = sh.n_threads, each = (whole + LP_THREADS - 1) / LP_THREADS;
-    auto offer = [&](float x, int v) {
-        if (lp_order(x) >= tau) {
+    uint32_t tau = sh.tau[0];
+#pragma unroll
+    for (int w = 1; w < LP_THREADS / 64; ++w)
+        tau = sh.tau[w] < tau ? sh.tau[w] : tau;
+    auto offer = [&](float x, int v, uint32_t least) {
+        if (lp_order(x) >= least) {
             const int at = atomicAdd(&sh.count, 1);
             if (at < LP_CAND)
                 sh.cand[at] = lp_key(x, v);
         }
     };
-    for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
-        const int t = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
-        if (j < each) {
-            const int at = (j * LP_THREADS + t) * E;
-            if (at + E <= n) {
-                RowPiece<TI, E> v;
-                v.load(z + at);
+    if (each <= 4) {  // a thread looks through its own
+        if (head >= tau)
+            own([&](float x, int v) { offer(x, v, tau); });
+    } else {  // those of the few threads, a few kilobytes that the caches hold, are read again by all
+        if (head >= tau)
+            sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
+        __syncthreads();
+        const int nt = sh.n_threads;
+        for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
+            const int t = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
+            if (j < each) {
+                const int at = (j * LP_THREADS + t) * E;
+                if (at + E <= n) {
+                    RowPiece<TI, E> v;
+                    v.load(z + at);
 #pragma unroll
-                for (int e = 0; e < E; ++e)
-                    offer(v.at(e), v0 + at + e);
+                    for (int e = 0; e < E; ++e)
+                        offer(v.at(e), v0 + at + e, tau);
+                }
+            } else if (t < rest) {
+                offer((float)z[whole * E + t], v0 + whole * E + t, tau);
             }
-        } else if (t < rest) {
-            offer((float)z[whole * E + t], v0 + whole * E + t);
         }
     }
     __syncthreads();
-    const int found = sh.count;
+    int found = sh.count;
+    if (found > LP_CAND) {
+        __syncthreads();
+        if (tid == 0)
+            sh.count = 0;
+        __syncthreads();
+        if (head > tau)
+            own([&](float x, int v) { offer(x, v, tau + 1); });
+        __syncthreads();
+        found = sh.count;
+        // the equal ones in order: the pieces of one round of the threads, then the rest
+        for (int j = 0; j <= each && found < k; ++j) {
+            const int at = j < each ? (j * LP_THREADS + tid) * E : whole * E + tid, m = j < each ? (at + E <= n ? E : 0) : tid < rest;
+            uint32_t same = 0;
+            for (int e = 0; e < m; ++e)
+                same |= (uint32_t)(lp_order((float)z[at + e]) == tau) << e;
+            int total, before = wave_excl_scan(__popc(same), lane, total);
+            if (lane == 0)
+                sh.tau[tid >> 6] = (uint32_t)total;
+            __syncthreads();
+            total = 0;
+#pragma unroll
+            for (int w = 0; w < LP_THREADS / 64; ++w) {
+                before += w < tid >> 6 ? (int)sh.tau[w] : 0;
+                total += (int)sh.tau[w];
+            }
+            for (int e = 0, to = found + before; e < m && to < k; ++e)
+                if (same >> e & 1)
+                    sh.cand[to++] = (uint64_t)tau << 32 | (0xFFFFFFFFu - (uint32_t)(v0 + at + e));
+            found = found + total < k ? found + total : k;
+            __syncthreads();
+        }
+    }
     if (found <= LP_CAND) {
         for (int r = tid; r < k; r += LP_THREADS)
             if (r >= found)
@@ -279,7 +328,18 @@ __device__ __forceinline__ LpState lp_sum(LpState t, float c, LpState *waves, in
 }
 
 // ------------------------------------------------------------------ forward
-// One workgroup a segment of a row.
+// The token's logit of a row, and whether there is one: asked for before the row is
+// read, used after.
+template <typename TI> __device__ __forceinline__ bool lp_target(const LpArgs &p, int64_t t, float &z)
+{
+    if (!p.logp)
+        return false;
+    const int at = p.id64 ? token_key((const int64_t *)p.targets, t, p.V) : token_key((const int32_t *)p.targets, t, p.V);
+    z = (float)((const TI *)p.logits)[t * p.ld + (at < p.V ? at : 0)];
+    return at < p.V;
+}
+
+// One workgroup a row, or a segment of a row that is longer than LP_SEG.
 template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_kernel(LpArgs p)
 {
     constexpr int E = Elt<TI>::PER_CHUNK, U = 4;
@@ -291,6 +351,8 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
     const int n = p.V - v0 < p.seg ? p.V - v0 : p.seg;
     const TI *z = (const TI *)p.logits + t * p.ld + v0;
     const float c = p.scale2;
+    float target = 0.f;
+    const bool given = tid == 0 && p.segs == 1 && lp_target<TI>(p, t, target);
     LpState st{-INFINITY, 0.f, 0.f};
     const int whole = n / E, rest = n - whole * E;
     for (int i = tid; i < whole; i += LP_THREADS * U) {
@@ -323,72 +385,195 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
     st = lp_sum(st, c, waves, tid);
     if (tid == 0) {
         if (p.segs == 1)
-            lp_finish<TI>(p, t, st);
+            lp_finish(p, t, st, given, target);
         else
             p.part[t * p.segs + s] = st;
     }
     if constexpr (TOP) {
         LpTop &sh = *reinterpret_cast<LpTop *>(top_mem);
+        auto own = [&](auto f) {
+            for (int i = tid; i < whole; i += LP_THREADS) {
+                RowPiece<TI, E> x;
+                x.load(z + (int64_t)i * E);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    f(x.at(e), v0 + i * E + e);
+            }
+            if (tid < rest)
+                f((float)z[whole * E + tid], v0 + whole * E + tid);
+        };
         if (p.segs == 1) {
             const LpRow row(st);
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, sh, tid, [&](int r, uint64_t key) {
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
                 p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
                 p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
             });
         } else {
             uint64_t *keys = p.keys + (t * p.segs + s) * p.k;
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
         }
     }
 }
 
-// The segments of a row joined, in order.  The k best of their sorted lists: as
-// in a segment, with the first few entries of each list for the threads' largest.
+// One workgroup a segment of at most LP_SEG logits: few rows, where the time is that
+// of one trip to memory and what follows.  The pieces are all requested at once; the
+// segment's maximum comes before its exponentials, so that no sum is scaled.
+template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_segment_kernel(LpArgs p)
+{
+    constexpr int E = Elt<TI>::PER_CHUNK, U = LP_SEG / LP_THREADS / E, NW = LP_THREADS / 64;
+    __shared__ float tops[NW];
+    __shared__ LpState waves[NW];
+    __shared__ __attribute__((aligned(16))) char top_mem[TOP ? sizeof(LpTop) : 16];
+    const int tid = threadIdx.x, lane = tid & 63;
+    const int64_t t = blockIdx.x / p.segs;
+    const int s = (int)(blockIdx.x - t * p.segs), v0 = s * p.seg;
+    const int n = p.V - v0 < p.seg ? p.V - v0 : p.seg;
+    const TI *z = (const TI *)p.logits + t * p.ld + v0;
+    const float c = p.scale2;
+    float target = 0.f;
+    const bool given = tid == 0 && p.segs == 1 && lp_target<TI>(p, t, target);
+    const int whole = n / E, rest = n - whole * E;
+    RowPiece<TI, E> v[U];
+    float last = -INFINITY;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (tid + u * LP_THREADS < whole)
+            v[u].load(z + (tid + u * LP_THREADS) * E);
+    if (tid < rest)
+        last = (float)z[whole * E + tid];
+    float largest = last;
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (tid + u * LP_THREADS < whole)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                largest = lp_max(largest, v[u].at(e));
+    float top = largest;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        top = lp_max(top, __shfl_xor(top, o, 64));
+    if (lane == 0)
+        tops[tid >> 6] = top;
+    __syncthreads();
+    LpState st{lp_max(lp_max(tops[0], tops[1]), lp_max(tops[2], tops[3])), 0.f, 0.f};
+    static_assert(NW == 4, "four waves");
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+        if (tid + u * LP_THREADS < whole)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                st.add(v[u].at(e), c);
+    if (tid < rest)
+        st.add(last, c);
+    st.s = wave_sum(st.s);
+    st.w = wave_sum(st.w);
+    if (lane == 0)
+        waves[tid >> 6] = st;
+    __syncthreads();
+    st.s = waves[0].s + waves[1].s + waves[2].s + waves[3].s;
+    st.w = waves[0].w + waves[1].w + waves[2].w + waves[3].w;
+    if (tid == 0) {
+        if (p.segs == 1)
+            lp_finish(p, t, st, given, target);
+        else
+            p.part[t * p.segs + s] = st;
+    }
+    if constexpr (TOP) {
+        LpTop &sh = *reinterpret_cast<LpTop *>(top_mem);
+        auto own = [&](auto f) {
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (tid + u * LP_THREADS < whole)
+#pragma unroll
+                    for (int e = 0; e < E; ++e)
+                        f(v[u].at(e), v0 + (tid + u * LP_THREADS) * E + e);
+            if (tid < rest)
+                f(last, v0 + whole * E + tid);
+        };
+        if (p.segs == 1) {
+            const LpRow row(st);
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
+                p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
+                p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
+            });
+        } else {
+            uint64_t *keys = p.keys + (t * p.segs + s) * p.k;
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
+        }
+    }
+}
+
+// The segments of a row joined: a lane a segment, in every wave.  The k best of
+// their sorted lists: where r lists' entries number j reach a bound, r j keys do; the
+// r-th largest of these entries, with r j >= k, is one, and the few keys that reach
+// it are ranked.
 template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_join_kernel(LpArgs p)
 {
-    constexpr int MOST = LP_MOST_TOP * LP_MOST_TOP;
-    __shared__ uint64_t head[TOP ? LP_THREADS : 1], cand[TOP ? MOST : 1];
-    __shared__ uint64_t tau;
+    constexpr int MOST = LP_MOST_TOP * LP_MOST_SEGS;
+    __shared__ uint64_t cand[TOP ? MOST : 1];
     __shared__ int count;
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x, lane = tid & 63;
     const int64_t t = blockIdx.x;
-    LpState st{-INFINITY, 0.f, 0.f};
-    for (int s = 0; s < p.segs; ++s)
-        st.join(p.part[t * p.segs + s], p.scale2);
-    if (tid == 0)
-        lp_finish<TI>(p, t, st);
+    const float c = p.scale2;
+    const bool on = lane < p.segs;
+    float target = 0.f;
+    const bool given = tid == 0 && lp_target<TI>(p, t, target);
+    LpState st = p.part[t * p.segs + (on ? lane : 0)];
+    constexpr int EARLY = 4;  // keys a thread asks for before the bound is known
+    const uint64_t *keys = nullptr;
+    uint64_t early[EARLY];
+    uint32_t entry = 0;
+    int r = 0;
     if constexpr (TOP) {
-        const LpRow row(st);
-        const uint64_t *keys = p.keys + t * p.segs * p.k;
-        auto emit = [&](int r, uint64_t key) {
-            p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
-            p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
-        };
-        const int first = LP_THREADS / p.segs, list = tid / first, entry = tid % first;
-        const bool on = list < p.segs && entry < p.k;
-        const uint64_t mine = on ? keys[list * p.k + entry] : 0;
-        head[tid] = mine;
+        keys = p.keys + t * p.segs * p.k;
+        int j = (2 * p.k + p.segs - 1) / p.segs;
+        j = j < p.k ? j : p.k;
+        r = (p.k + j - 1) / j;
+        if (on)
+            entry = (uint32_t)(keys[lane * p.k + j - 1] >> 32);
+#pragma unroll
+        for (int q = 0; q < EARLY; ++q)
+            early[q] = tid + q * LP_THREADS < p.segs * p.k ? keys[tid + q * LP_THREADS] : 0;
         if (tid == 0)
             count = 0;
-        __syncthreads();
-        int above = 0;
-        for (int j = 0; j < LP_THREADS; ++j) {
-            const uint64_t h = head[j];
-            above += h > mine || (h == mine && j < tid);
-        }
-        if (above == p.k - 1)
-            tau = mine;
-        __syncthreads();
-        const uint64_t bound = tau > 0 ? tau : 1;
-        for (int i = tid; i < p.segs * p.k; i += LP_THREADS) {
-            const uint64_t key = keys[i];
-            if (key >= bound) {
-                const int at = atomicAdd(&count, 1);
-                cand[at < MOST ? at : MOST - 1] = key;
+    }
+    if (!on)
+        st = LpState{-INFINITY, 0.f, 0.f};
+    float top = st.m;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        top = lp_max(top, __shfl_xor(top, o, 64));
+    st.raise(top, c);
+    st.s = wave_sum(st.s);
+    st.w = wave_sum(st.w);
+    if (tid == 0)
+        lp_finish(p, t, st, given, target);
+    if constexpr (TOP) {
+        const LpRow row(st);
+        if (row.bad) {
+            for (int i = tid; i < p.k; i += LP_THREADS) {
+                p.top_idx[t * p.k + i] = i;
+                p.top_logp[t * p.k + i] = row.logp(0.f, 1.f);
             }
+            return;
         }
+        // (an order of 0 is no key's: one below all of them where a list is shorter than j)
+        const uint64_t bound = (uint64_t)lp_nth(entry, r, lane) << 32 | 1;
         __syncthreads();
-        lp_rank(cand, count < MOST ? count : MOST, p.k, tid, emit);
+        auto offer = [&](uint64_t key) {
+            if (key >= bound)
+                cand[atomicAdd(&count, 1)] = key;
+        };
+#pragma unroll
+        for (int q = 0; q < EARLY; ++q)
+            offer(early[q]);
+        for (int i = tid + EARLY * LP_THREADS; i < p.segs * p.k; i += LP_THREADS)
+            offer(keys[i]);
+        __syncthreads();
+        lp_rank(cand, count, p.k, tid, [&](int rank, uint64_t key) {
+            p.top_idx[t * p.k + rank] = lp_key_index(key);
+            p.top_logp[t * p.k + rank] = row.logp(lp_key_value(key), p.scale);
+        });
     }
 }
 
@@ -455,9 +640,9 @@ template <typename TI> __global__ __launch_bounds__(LP_THREADS) void logprob_bac
 // ------------------------------------------------------------------ host
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
-// Few rows are cut into segments, so that LP_WGS workgroups have work; a segment
-// has at least LP_SEG logits.
-constexpr int LP_WGS = 1024, LP_SEG = 4096, LP_MOST_SEGS = 64;
+// Few rows are cut into segments, so that LP_WGS workgroups have work: of LP_SEG
+// logits at most, where LP_MOST_SEGS of them are enough.
+constexpr int LP_WGS = 1024;
 
 static int most_segments(int V)
 {
@@ -502,10 +687,18 @@ hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
         p.part = (LpState *)(p.keys + (int64_t)p.T * p.segs * p.k);
     }
     const dim3 grid((unsigned)((int64_t)p.T * p.segs)), block(LP_THREADS);
+    auto run = [&](auto type, auto top) {
+        using TI = decltype(type);
+        constexpr bool TOP = decltype(top)::value;
+        if (p.seg <= LP_SEG)
+            logprob_segment_kernel<TI, TOP><<<grid, block, 0, s>>>(p);
+        else
+            logprob_kernel<TI, TOP><<<grid, block, 0, s>>>(p);
+    };
     if (p.bf16)
-        p.k ? logprob_kernel<__bf16, true><<<grid, block, 0, s>>>(p) : logprob_kernel<__bf16, false><<<grid, block, 0, s>>>(p);
+        p.k ? run(__bf16{}, std::true_type{}) : run(__bf16{}, std::false_type{});
     else
-        p.k ? logprob_kernel<float, true><<<grid, block, 0, s>>>(p) : logprob_kernel<float, false><<<grid, block, 0, s>>>(p);
+        p.k ? run(float{}, std::true_type{}) : run(float{}, std::false_type{});
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess || p.segs == 1)
         return e;
