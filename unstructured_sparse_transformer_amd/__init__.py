@@ -185,22 +185,34 @@ def _ptr(t) -> int | None:
     return None if t is None else t.data_ptr()
 
 
+_raw_stream = None
+
+
 def _stream(stream, dev=None) -> int | None:
     """A stream's handle; None: the current one, of the current GPU `dev` where the caller knows it."""
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # the handle without a Stream object (2.7 us less)
-        return raw(torch.cuda.current_device() if dev is None else dev) if raw else torch.cuda.current_stream().cuda_stream
+        global _raw_stream
+        if _raw_stream is None or dev is None:
+            import torch
+            # the handle without a Stream object (2.7 us less)
+            _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", lambda dev: torch.cuda.current_stream(dev).cuda_stream)
+            dev = torch.cuda.current_device() if dev is None else dev
+        return _raw_stream(dev)
     return getattr(stream, "cuda_stream", stream)
 
 
+_VDTYPES: dict = {}  # torch's element types, once torch is there
+
+
 def vdtype_of(torch_dtype) -> int:
-    import torch
-    if torch_dtype == torch.bfloat16:
-        return TWELL_BF16
-    if torch_dtype == torch.float32:
-        return TWELL_F32
-    raise TypeError(f"unsupported element type {torch_dtype}")
+    v = _VDTYPES.get(torch_dtype)
+    if v is None:
+        import torch
+        _VDTYPES.update({torch.bfloat16: TWELL_BF16, torch.float32: TWELL_F32})
+        v = _VDTYPES.get(torch_dtype)
+        if v is None:
+            raise TypeError(f"unsupported element type {torch_dtype}")
+    return v
 
 
 def _check(fn: str, st: int):
@@ -451,11 +463,18 @@ def hybrid_workspace(hy: "Hybrid", d: int, device="cuda"):
 
 
 # ---------------------------------------------------------------- the dense gated product
+_current_device = None
+
+
 def _device(fn: str, t) -> int:
     """The GPU a call's tensors have to be on: the current one, whose streams the kernels run on."""
-    import torch
+    global _current_device
     dev = t.get_device()
-    if dev < 0 or dev != torch.cuda.current_device():
+    if dev >= 0 and _current_device is None:
+        import torch
+        # (torch.cuda.current_device's own look-up: the tensor says that the GPU is in use, 0.4 us less)
+        _current_device = getattr(torch._C, "_cuda_getDevice", torch.cuda.current_device)
+    if dev < 0 or dev != _current_device():
         raise ValueError(f"{fn}: tensors on the current GPU are needed, got one on {t.device}")
     return dev
 
@@ -561,10 +580,20 @@ class PackedAct:
                    torch.empty((T, -(-d // ACT_BLOCK)), dtype=torch.bfloat16, device=device))
 
     def desc(self, fn: str, name: str, shape, dev: int) -> TwellPackedT:
-        import torch
         T, d = shape
-        return TwellPackedT(_tensor(fn, name + ".code", self.code, (T, d), dev, torch.int8),
-                            _tensor(fn, name + ".scale", self.scale, (T, -(-d // ACT_BLOCK)), dev, torch.bfloat16))
+        kinds = _PACKED_TYPES or _packed_types()
+        return TwellPackedT(_tensor(fn, name, self.code, shape, dev, kinds[0]),
+                            _tensor(fn, name, self.scale, (T, -(-d // ACT_BLOCK)), dev, kinds[1]))
+
+
+_PACKED_TYPES: tuple = ()  # of the codes and the scales, once torch is there
+
+
+def _packed_types() -> tuple:
+    global _PACKED_TYPES
+    import torch
+    _PACKED_TYPES = torch.int8, torch.bfloat16
+    return _PACKED_TYPES
 
 
 def _packed(fn: str, name: str, p, shape, dev: int) -> TwellPackedT:
@@ -631,15 +660,20 @@ def twell_glu_backward_packed(x, wg_t, wu_t, g: PackedAct, u: PackedAct, dh, act
 
 
 # ---------------------------------------------------------------- token embedding
+_ID_BITS: dict = {}
+
+
 def _ids(fn: str, name: str, t, T: int, dev: int) -> tuple:
     """The pointer of token ids [T] and their bits."""
-    import torch
     p = _tensor(fn, name, t, (T,), dev)
-    if t.dtype is torch.int64:
-        return p, 64
-    if t.dtype is torch.int32:
-        return p, 32
-    raise TypeError(f"{fn}: {name} must be torch.int32 or torch.int64, not {t.dtype}")
+    bits = _ID_BITS.get(t.dtype)
+    if bits is None:
+        import torch
+        _ID_BITS.update({torch.int64: 64, torch.int32: 32})
+        bits = _ID_BITS.get(t.dtype)
+        if bits is None:
+            raise TypeError(f"{fn}: {name} must be torch.int32 or torch.int64, not {t.dtype}")
+    return p, bits
 
 
 def twell_embed_forward(ids, table, out, scale: float = 1.0, stream=None):

@@ -358,13 +358,24 @@ template <typename TT, int E, int NW> __global__ __launch_bounds__(NW * 64) void
         // a run that begins in window w and goes on in the next
         if (key >= p.V || end != key || (begin == key && first > 0 && before == key))
             continue;
-        int lo = w + 1, hi = windows;  // the first window after it that does not begin with it
-        while (hi - lo > 1) {
-            const int mid = lo + (hi - lo) / 2;
-            if (p.key[mid * W] == key)
-                lo = mid;
-            else
-                hi = mid;
+        // the first window after it that does not begin with it: 64 at a time, and where the run is longer halving
+        int hi = w + 2;
+        {
+            const int probe = w + 2 + lane;
+            const uint64_t other = __ballot(probe >= windows || p.key[(int64_t)(probe < windows ? probe : 0) * W] != key);
+            if (other) {
+                hi += __builtin_ctzll(other);
+            } else {
+                int lo = hi + 63;
+                hi = windows;
+                while (hi - lo > 1) {
+                    const int mid = lo + (hi - lo) / 2;
+                    if (p.key[mid * W] == key)
+                        lo = mid;
+                    else
+                        hi = mid;
+                }
+            }
         }
         const int n = hi - w;  // sums: slot 1 of w, then slots 0
         float sum[E];

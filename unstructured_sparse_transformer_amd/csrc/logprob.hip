@@ -118,17 +118,34 @@ struct LpTop {
     uint64_t win;
 };
 
-// The r-th largest (r from 1) of the wave's values.
+// The largest of the wave's values (DPP row shifts and row broadcasts).
+__device__ __forceinline__ uint32_t lp_wave_max(uint32_t v)
+{
+    auto step = [&](auto ctrl, auto rows) {
+        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value,
+                                                                 0xf, false);
+        v = o > v ? o : v;
+    };
+    using std::integral_constant;
+    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
+    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});  // row_shr:2
+    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});  // row_shr:4
+    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});  // row_shr:8
+    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
+    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
+    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+
+// The r-th largest (r from 1 to 64) of the wave's values: the largest is taken out
+// r - 1 times.  (Counting the larger ones of each costs as much at r = 16.)
 __device__ __forceinline__ uint32_t lp_nth(uint32_t v, int r, int lane)
 {
-    int above = 0;
-#pragma unroll 16
-    for (int j = 0; j < 64; ++j) {
-        const uint32_t o = (uint32_t)__builtin_amdgcn_readlane((int)v, j);
-        above += o > v || (o == v && j < lane);
+    uint32_t top = lp_wave_max(v);
+    for (int i = 1; i < r; ++i) {
+        v = lane == __builtin_ctzll(__ballot(v == top)) ? 0u : v;
+        top = lp_wave_max(v);
     }
-    const uint64_t it = __ballot(above == r - 1);
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, __builtin_ctzll(it));
+    return top;
 }
 
 // The k best keys of cand[0 .. n), best first, to emit(rank, key).
@@ -145,10 +162,18 @@ template <typename F> __device__ __forceinline__ void lp_rank(const uint64_t *ca
     }
 }
 
+__device__ __forceinline__ void lp_offer(LpTop &sh, float x, int v)
+{
+    const int at = atomicAdd(&sh.count, 1);
+    if (at < LP_CAND)
+        sh.cand[at] = lp_key(x, v);
+}
+
 // The k best logits of the segment [v0, v0 + n) of a row, best first, to
 // emit(rank, key); emit(rank, 0) where there are fewer.  `largest`: the largest of
 // those that this thread has read: pieces tid, tid + 256, ... of E elements, and
-// element tid of the rest; own(f) calls f(logit, index) for each of them.  In each
+// element tid of the rest; own(f) calls f(logit, index) for each of them, and
+// list(order) adds the keys of all that reach an order to the list.  In each
 // of the 4 waves k / 4 threads have a largest that reaches the (k / 4)-th largest of
 // the wave's: the lowest of these four values is a bound that k logits reach.  Only
 // threads whose largest reaches it have any that do; the logits that reach it are
@@ -157,54 +182,23 @@ template <typename F> __device__ __forceinline__ void lp_rank(const uint64_t *ca
 // equal ones as are wanted, the lowest indices first.  If even those above the bound
 // are too many (all in few threads), the best is taken k times: a tournament of the
 // threads' best remaining.
-template <typename TI, int E, typename O, typename F>
-__device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, O own, LpTop &sh, int tid, F emit)
+template <typename TI, int E, typename O, typename L, typename F>
+__device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, O own, L list, LpTop &sh, int tid, F emit)
 {
     const int whole = n / E, rest = n - whole * E, lane = tid & 63, each = (whole + LP_THREADS - 1) / LP_THREADS;
     const uint32_t head = lp_order(largest);
-    const uint32_t mine = lp_nth(head, (k + LP_THREADS / 64 - 1) / (LP_THREADS / 64), lane);
+    uint32_t tau = lp_nth(head, (k + LP_THREADS / 64 - 1) / (LP_THREADS / 64), lane);
     if (lane == 0)
-        sh.tau[tid >> 6] = mine;
+        sh.tau[tid >> 6] = tau;
     if (tid == 0) {
         sh.count = 0;
         sh.n_threads = 0;
     }
     __syncthreads();
-    uint32_t tau = sh.tau[0];
 #pragma unroll
-    for (int w = 1; w < LP_THREADS / 64; ++w)
+    for (int w = 0; w < LP_THREADS / 64; ++w)
         tau = sh.tau[w] < tau ? sh.tau[w] : tau;
-    auto offer = [&](float x, int v, uint32_t least) {
-        if (lp_order(x) >= least) {
-            const int at = atomicAdd(&sh.count, 1);
-            if (at < LP_CAND)
-                sh.cand[at] = lp_key(x, v);
-        }
-    };
-    if (each <= 4) {  // a thread looks through its own
-        if (head >= tau)
-            own([&](float x, int v) { offer(x, v, tau); });
-    } else {  // those of the few threads, a few kilobytes that the caches hold, are read again by all
-        if (head >= tau)
-            sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
-        __syncthreads();
-        const int nt = sh.n_threads;
-        for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
-            const int t = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
-            if (j < each) {
-                const int at = (j * LP_THREADS + t) * E;
-                if (at + E <= n) {
-                    RowPiece<TI, E> v;
-                    v.load(z + at);
-#pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        offer(v.at(e), v0 + at + e, tau);
-                }
-            } else if (t < rest) {
-                offer((float)z[whole * E + t], v0 + whole * E + t, tau);
-            }
-        }
-    }
+    list(head, tau);
     __syncthreads();
     int found = sh.count;
     if (found > LP_CAND) {
@@ -213,7 +207,10 @@ __device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int 
             sh.count = 0;
         __syncthreads();
         if (head > tau)
-            own([&](float x, int v) { offer(x, v, tau + 1); });
+            own([&](float x, int v) {
+                if (lp_order(x) > tau)
+                    lp_offer(sh, x, v);
+            });
         __syncthreads();
         found = sh.count;
         // the equal ones in order: the pieces of one round of the threads, then the rest
@@ -340,7 +337,11 @@ template <typename TI> __device__ __forceinline__ bool lp_target(const LpArgs &p
 }
 
 // One workgroup a row, or a segment of a row that is longer than LP_SEG.
-template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_kernel(LpArgs p)
+// Bound by memory: 4096 x 131072 bf16 take 185 us (5.8 TB/s), with or without the
+// entropy's operations.  ONCE: more than the caches behind the L2s hold, read past
+// them (190 us through them; workgroups that start at different places of their
+// rows 195 us, segments of 4096 222 us).
+template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THREADS) void logprob_kernel(LpArgs p)
 {
     constexpr int E = Elt<TI>::PER_CHUNK, U = 4;
     __shared__ LpState waves[LP_THREADS / 64];
@@ -360,7 +361,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i + u * LP_THREADS < whole)
-                v[u].load(z + (int64_t)(i + u * LP_THREADS) * E);
+                v[u].template load<ONCE>(z + (int64_t)(i + u * LP_THREADS) * E);
 #pragma unroll
         for (int u = 0; u < U; ++u)
             if (i + u * LP_THREADS < whole) {
@@ -402,15 +403,40 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
             if (tid < rest)
                 f((float)z[whole * E + tid], v0 + whole * E + tid);
         };
+        // the pieces of the few threads that have any, a few kilobytes that the caches hold, are read again by all
+        auto list = [&](uint32_t head, uint32_t least) {
+            if (head >= least)
+                sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
+            __syncthreads();
+            const int each = (whole + LP_THREADS - 1) / LP_THREADS, nt = sh.n_threads;
+            for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
+                const int of = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
+                if (j < each) {
+                    const int at = (j * LP_THREADS + of) * E;
+                    if (at + E <= n) {
+                        RowPiece<TI, E> x;
+                        x.load(z + at);
+#pragma unroll
+                        for (int e = 0; e < E; ++e)
+                            if (lp_order(x.at(e)) >= least)
+                                lp_offer(sh, x.at(e), v0 + at + e);
+                    }
+                } else if (of < rest) {
+                    const float x = (float)z[whole * E + of];
+                    if (lp_order(x) >= least)
+                        lp_offer(sh, x, v0 + whole * E + of);
+                }
+            }
+        };
         if (p.segs == 1) {
             const LpRow row(st);
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) {
                 p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
                 p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
             });
         } else {
             uint64_t *keys = p.keys + (t * p.segs + s) * p.k;
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
         }
     }
 }
@@ -490,15 +516,46 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
             if (tid < rest)
                 f(last, v0 + whole * E + tid);
         };
+        // they are in registers: a wave counts them, takes places for them, and writes them (an atomic a logit: 2 us)
+        auto list = [&](uint32_t, uint32_t least) {
+            const float x0 = lp_key_value((uint64_t)least << 32);
+            int count = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    count += __popcll(__ballot(tid + u * LP_THREADS < whole && v[u].at(e) >= x0));
+            const uint64_t end = __ballot(tid < rest && last >= x0);
+            count += __popcll(end);
+            int at = 0;
+            if (lane == 0)
+                at = atomicAdd(&sh.count, count);
+            at = __builtin_amdgcn_readfirstlane(at);
+            auto place = [&](uint64_t hits, float x, int index) {
+                if (hits == 0)
+                    return;
+                const int to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(hits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
+                if ((hits >> lane & 1) && to < LP_CAND)
+                    sh.cand[to] = lp_key(x, index);
+                at += __popcll(hits);
+            };
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    place(__ballot(tid + u * LP_THREADS < whole && v[u].at(e) >= x0), v[u].at(e),
+                          v0 + (tid + u * LP_THREADS) * E + e);
+            place(end, last, v0 + whole * E + tid);
+        };
         if (p.segs == 1) {
             const LpRow row(st);
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) {
                 p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
                 p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
             });
         } else {
             uint64_t *keys = p.keys + (t * p.segs + s) * p.k;
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
         }
     }
 }
@@ -692,8 +749,10 @@ hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
         constexpr bool TOP = decltype(top)::value;
         if (p.seg <= LP_SEG)
             logprob_segment_kernel<TI, TOP><<<grid, block, 0, s>>>(p);
+        else if (!TOP && (int64_t)p.T * p.V * (int64_t)sizeof(TI) > ((int64_t)256 << 20))
+            logprob_kernel<TI, TOP, true><<<grid, block, 0, s>>>(p);
         else
-            logprob_kernel<TI, TOP><<<grid, block, 0, s>>>(p);
+            logprob_kernel<TI, TOP, false><<<grid, block, 0, s>>>(p);
     };
     if (p.bf16)
         p.k ? run(__bf16{}, std::true_type{}) : run(__bf16{}, std::false_type{});

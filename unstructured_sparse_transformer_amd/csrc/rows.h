@@ -11,18 +11,27 @@ typedef uint32_t rows_4x4 __attribute__((ext_vector_type(4), aligned(4)));
 typedef uint32_t rows_4x2 __attribute__((ext_vector_type(4), aligned(2)));
 typedef uint32_t rows_2x2 __attribute__((ext_vector_type(2), aligned(2)));
 
+// ONCE: past the caches.
+template <bool ONCE, typename V> __device__ __forceinline__ V rows_get(const void *p)
+{
+    const V *q = reinterpret_cast<const V *>(p);
+    if constexpr (ONCE)
+        return __builtin_nontemporal_load(q);
+    return *q;
+}
+
 // A piece as it lies in memory, requested now and used later.
 template <typename TI, int E> struct RowPiece;
 template <> struct RowPiece<float, 4> {
     u32x4 v;
-    __device__ __forceinline__ void load(const float *p) { v = *reinterpret_cast<const rows_4x4 *>(p); }
+    template <bool ONCE = false> __device__ __forceinline__ void load(const float *p) { v = rows_get<ONCE, rows_4x4>(p); }
     __device__ __forceinline__ float at(int e) const { return __uint_as_float(v[e]); }
 };
 template <> struct RowPiece<__bf16, 4> {
     uint2 v;
-    __device__ __forceinline__ void load(const __bf16 *p)
+    template <bool ONCE = false> __device__ __forceinline__ void load(const __bf16 *p)
     {
-        const rows_2x2 q = *reinterpret_cast<const rows_2x2 *>(p);
+        const rows_2x2 q = rows_get<ONCE, rows_2x2>(p);
         v = make_uint2(q[0], q[1]);
     }
     __device__ __forceinline__ float at(int e) const
@@ -33,7 +42,7 @@ template <> struct RowPiece<__bf16, 4> {
 };
 template <> struct RowPiece<__bf16, 8> {
     u32x4 v;
-    __device__ __forceinline__ void load(const __bf16 *p) { v = *reinterpret_cast<const rows_4x2 *>(p); }
+    template <bool ONCE = false> __device__ __forceinline__ void load(const __bf16 *p) { v = rows_get<ONCE, rows_4x2>(p); }
     __device__ __forceinline__ float at(int e) const { return chunk_elem<__bf16>(v, e); }
 };
 template <typename TI> struct RowPiece<TI, 1> {
