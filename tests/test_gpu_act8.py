@@ -260,3 +260,18 @@ def test_empty(gpu_lib):
     dwg, dwu = _nan(64, 128), _nan(64, 128)
     tw.twell_glu_backward_packed(x, w, w, p, p, h, "silu", None, dwg, dwu, tw.glu_backward_workspace(0, 128, 64, torch.bfloat16))
     assert not dwg.any() and not dwu.any()
+
+
+def test_every_scale(gpu_lib):
+    """Blocks whose largest is 127 steps of every mantissa of 8 bits, or next to that: the quotients that make the scale
+    and its reciprocal are those of a division."""
+    import torch
+    say("case act pack, every scale")
+    step = torch.arange(128, 256, device="cuda").float()
+    tops = torch.cat([torch.nextafter(step * 127, torch.full_like(step, to)) for to in (0.0, math.inf)] + [step * 127])
+    tops = torch.cat([tops * 2.0 ** e for e in (-90, -60, -31, -8, 0, 9, 50, 100)])
+    x = _rnd(tops.numel(), 32, dtype="float32", seed=8).clamp(-3, 3) / 4 * tops[:, None]
+    x[:, 7] = tops
+    x[::2, 7] *= -1
+    _check_pack(gpu_lib, x)
+    _check_pack(gpu_lib, _rnd(20000, 64, dtype="float32", seed=9) * torch.exp2(_rnd(20000, 1, dtype="float32", scale=12)))

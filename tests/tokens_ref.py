@@ -133,9 +133,10 @@ def pack(x):
     v = torch.nn.functional.pad(x.float(), (0, -d % BLOCK)).view(T, -1, BLOCK)
     top = v.abs().amax(2, keepdim=True)
     fine, some = torch.isfinite(top), top >= 1e-30
-    scale = ((top / 127).view(torch.int32) + 0xFFFF & -0x10000).view(torch.float32)
+    # (by a tensor: torch takes a quotient by a number as a product with its reciprocal on the GPU)
+    scale = ((top / torch.full_like(top, 127)).view(torch.int32) + 0xFFFF & -0x10000).view(torch.float32)
     scale = torch.where(some, scale, 0.0)
-    code = torch.round(torch.where(fine & some, v / 1.0 * (1 / scale), 0.0))
+    code = torch.round(torch.where(fine & some, v * (torch.ones_like(scale) / scale), 0.0))
     scale = torch.where(fine, scale, math.nan)
     value = (code * scale).view(T, -1)[:, :d]
     return code.to(torch.int8).view(T, -1)[:, :d], scale[:, :, 0], value

@@ -27,27 +27,40 @@ __device__ __forceinline__ float a8_max(float a, float x) { return __builtin_ele
 // held in bf16, rounded up, so that no code passes 127.  A block below 1e-30 is
 // held as zeros; one with an infinity or a NaN has scale NaN and reads back as NaN
 // as a whole.
+//
+// Both quotients are those of a correctly rounded division, in a third of its
+// operations (a tile of the gated product has 256 scales a lane): an estimate and
+// one exact remainder.  A quotient by 127, or of 1 by a step of 8 bits of mantissa,
+// is at least 1 / 512 of a unit in the last place away from where rounding turns, and
+// the corrected estimate within 2^-20 of one.
 struct A8Scale {
     uint16_t bits;
     float inv;
     __device__ __forceinline__ A8Scale(float top)
     {
-        const uint32_t b = (__float_as_uint(top / 127.f) + 0xFFFFu) >> 16;
-        const bool fine = top < INFINITY;
-        bits = fine ? top < 1e-30f ? 0 : (uint16_t)b : 0x7FC0;
-        inv = fine && !(top < 1e-30f) ? 1.f / __uint_as_float(b << 16) : 0.f;
+        constexpr float R127 = 1.f / 127.f;
+        const float q = top * R127;
+        const uint32_t b = (__float_as_uint(fmaf(fmaf(-q, 127.f, top), R127, q)) + 0xFFFFu) & 0xFFFF0000u;
+        const float step = __uint_as_float(b), r = __builtin_amdgcn_rcpf(step);
+        const bool fine = top < INFINITY, some = fine && !(top < 1e-30f);
+        bits = some ? (uint16_t)(b >> 16) : fine ? 0 : 0x7FC0;
+        inv = some ? fmaf(fmaf(-step, r, 1.f), r, r) : 0.f;
     }
 };
 
 // The codes of 4 values, one a byte: round to nearest even, by an addition whose
-// result has the whole number in its lowest bits (after the product's own
-// rounding: a code does not depend on whether a compiler fuses the two).
-__device__ __forceinline__ uint32_t a8_codes(float a, float b, float c, float d, float inv)
+// result has the whole number in its lowest bits.  The product is rounded by itself
+// first, so that a code does not depend on whether a compiler fuses the two; FUSED:
+// in one operation (values that no other operation has in these 32 bits).
+template <bool FUSED = false> __device__ __forceinline__ uint32_t a8_whole(float v, float inv)
 {
 #pragma clang fp contract(off)
     constexpr float WHOLE = 12582912.f;  // 1.5 2^23
-    const uint32_t x = __float_as_uint(a * inv + WHOLE), y = __float_as_uint(b * inv + WHOLE),
-                   z = __float_as_uint(c * inv + WHOLE), w = __float_as_uint(d * inv + WHOLE);
+    return __float_as_uint(FUSED ? __builtin_fmaf(v, inv, WHOLE) : v * inv + WHOLE);
+}
+template <bool FUSED = false> __device__ __forceinline__ uint32_t a8_codes(float a, float b, float c, float d, float inv)
+{
+    const uint32_t x = a8_whole<FUSED>(a, inv), y = a8_whole<FUSED>(b, inv), z = a8_whole<FUSED>(c, inv), w = a8_whole<FUSED>(d, inv);
     return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w, z, 0x0C0C0400u), __builtin_amdgcn_perm(y, x, 0x0C0C0400u), 0x05040100u);
 }
 

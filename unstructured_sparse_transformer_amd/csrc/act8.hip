@@ -6,7 +6,8 @@
 // Linear codes: what a gradient needs of an activation is its absolute error (act
 // and act' are smooth), which is at most half a step, 0.4% of the block's largest;
 // a floating 8-bit code of 3 bits of mantissa is off by up to 6% of the value
-// itself.  Bound by memory: 3.06 bytes an element of bf16 either way.
+// itself.  Bound by memory: 3.06 bytes an element of bf16 either way
+// (8192 x 8192: packed in 39 us, 5.3 TB/s; unpacked, from caches in part, in 31 us).
 #include "act8.h"
 #include "rows.h"
 
@@ -15,39 +16,46 @@ namespace twell {
 typedef uint32_t a8_2x1 __attribute__((ext_vector_type(2), aligned(1)));
 typedef uint32_t a8_1x1 __attribute__((aligned(1)));
 
-// Piece `piece` of E elements of row `row`; a row's pieces fill whole blocks.
+// Item first + add of all rows' pieces of E elements.  A workgroup's first row is
+// found once, in 64 bits; its threads count on from there.
 template <int E> struct A8Place {
     int64_t row;
     int col, left;  // elements of the row from col on
-    __device__ __forceinline__ A8Place(int64_t i, int pieces, int d)
+    __device__ __forceinline__ A8Place(int64_t first, uint32_t add, int pieces, int d)
     {
-        row = i / pieces;
-        col = (int)(i - row * pieces) * E;
+        const int64_t r0 = first / pieces;
+        const uint32_t r = (uint32_t)(first - r0 * pieces) + add, up = r / (uint32_t)pieces;
+        row = r0 + up;
+        col = (int)(r - up * (uint32_t)pieces) * E;
         left = d - col;
     }
 };
 
-template <typename TI> __global__ __launch_bounds__(256) void act_pack_kernel(const TI *x, int T, int d, Packed8 to)
+// U: items of a thread, requested together; ONCE: read past the caches.
+template <typename TI, int A8_U, bool ONCE> __global__ __launch_bounds__(256) void act_pack_kernel(const TI *x, int T, int d, Packed8 to)
 {
     constexpr int E = Elt<TI>::PER_CHUNK, LANES = A8_BLOCK / E;
     const int nb = (int)a8_blocks(d), pieces = nb * LANES;
-    const int64_t n = (int64_t)T * pieces, step = (int64_t)gridDim.x * 256;
-    for (int64_t i0 = (int64_t)blockIdx.x * 256; i0 < n; i0 += step) {
-        const int64_t i = i0 + threadIdx.x;
-        const bool on = i < n;
-        const A8Place<E> at(on ? i : n - 1, pieces, d);
-        const TI *q = x + at.row * d + at.col;
+    const int64_t first = (int64_t)blockIdx.x * (256 * A8_U);
+    RowPiece<TI, E> r[A8_U];
+#pragma unroll
+    for (int u = 0; u < A8_U; ++u) {
+        const A8Place<E> at(first, u * 256 + threadIdx.x, pieces, d);
+        if (at.row < T && at.left >= E)
+            r[u].template load<ONCE>(x + at.row * d + at.col);
+    }
+#pragma unroll
+    for (int u = 0; u < A8_U; ++u) {
+        const A8Place<E> at(first, u * 256 + threadIdx.x, pieces, d);
+        const bool on = at.row < T;
         float v[E];
-        if (at.left >= E) {
-            RowPiece<TI, E> r;
-            r.load(q);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            v[e] = r[u].at(e);
+        if (!on || at.left < E) {
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                v[e] = r.at(e);
-        } else {
-#pragma unroll
-            for (int e = 0; e < E; ++e)
-                v[e] = e < at.left ? (float)q[e] : 0.f;
+                v[e] = on && e < at.left ? (float)x[at.row * d + at.col + e] : 0.f;
         }
         float top = 0.f;
 #pragma unroll
@@ -80,61 +88,87 @@ template <typename TI> __global__ __launch_bounds__(256) void act_pack_kernel(co
     }
 }
 
-template <typename TO> __global__ __launch_bounds__(256) void act_unpack_kernel(Packed8 from, int T, int d, TO *out)
+template <typename TO, int A8_U> __global__ __launch_bounds__(256) void act_unpack_kernel(Packed8 from, int T, int d, TO *out)
 {
     constexpr int E = Elt<TO>::PER_CHUNK;
     const int nb = (int)a8_blocks(d), pieces = (d + E - 1) / E;
-    const int64_t n = (int64_t)T * pieces, step = (int64_t)gridDim.x * 256;
-    for (int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x; i < n; i += step) {
-        const A8Place<E> at(i, pieces, d);
+    const int64_t first = (int64_t)blockIdx.x * (256 * A8_U);
+    uint32_t c[A8_U][E / 4];
+    uint16_t s[A8_U];
+#pragma unroll
+    for (int u = 0; u < A8_U; ++u) {
+        const A8Place<E> at(first, u * 256 + threadIdx.x, pieces, d);
+        if (at.row >= T)
+            continue;
+        s[u] = from.scale[at.row * nb + at.col / A8_BLOCK];
         const int8_t *q = from.code + at.row * d + at.col;
-        const float s = a8_scale(from.scale[at.row * nb + at.col / A8_BLOCK]);
+        if (at.left < E)
+            continue;
+        if constexpr (E == 8) {
+            const a8_2x1 w = *reinterpret_cast<const a8_2x1 *>(q);
+            c[u][0] = w[0];
+            c[u][1] = w[1];
+        } else {
+            c[u][0] = *reinterpret_cast<const a8_1x1 *>(q);
+        }
+    }
+#pragma unroll
+    for (int u = 0; u < A8_U; ++u) {
+        const A8Place<E> at(first, u * 256 + threadIdx.x, pieces, d);
+        if (at.row >= T)
+            continue;
         TO *o = out + at.row * d + at.col;
+        const float scale = a8_scale(s[u]);
         if (at.left >= E) {
-            uint32_t c[E / 4];
-            if constexpr (E == 8) {
-                const a8_2x1 w = *reinterpret_cast<const a8_2x1 *>(q);
-                c[0] = w[0];
-                c[1] = w[1];
-            } else {
-                c[0] = *reinterpret_cast<const a8_1x1 *>(q);
-            }
             float v[E];
 #pragma unroll
             for (int e = 0; e < E; ++e)
-                v[e] = a8_value(c[e / 4], e % 4, s);
+                v[e] = a8_value(c[u][e / 4], e % 4, scale);
             rows_store<E>(o, v, 0);
         } else {
             for (int e = 0; e < at.left; ++e)
-                o[e] = (TO)((float)q[e] * s);
+                o[e] = (TO)((float)from.code[at.row * d + at.col + e] * scale);
         }
     }
 }
 
 // ------------------------------------------------------------------ host
-static dim3 a8_grid(int64_t threads)
+// From A8_LARGE elements on (more than the L2s hold) two items a thread, past the
+// caches: 8192 x 8192 bf16 39 and 31 us, 46 and 32 us with one through them; 64 x 1001
+// fp32 3.8 us with two, 2.9 us with one.
+constexpr int64_t A8_LARGE = (int64_t)1 << 24;
+
+static dim3 a8_grid(int64_t items, int each) { return dim3((unsigned)((items + 256 * each - 1) / (256 * each))); }
+
+template <typename TI> static hipError_t run_pack(const void *x, int T, int d, Packed8 to, hipStream_t s)
 {
-    const int64_t wgs = (threads + 255) / 256;
-    return dim3((unsigned)(wgs < 16384 ? wgs : 16384));
+    const int64_t items = (int64_t)T * a8_blocks(d) * (A8_BLOCK / Elt<TI>::PER_CHUNK);
+    if ((int64_t)T * d >= A8_LARGE)
+        act_pack_kernel<TI, 2, true><<<a8_grid(items, 2), dim3(256), 0, s>>>((const TI *)x, T, d, to);
+    else
+        act_pack_kernel<TI, 1, false><<<a8_grid(items, 1), dim3(256), 0, s>>>((const TI *)x, T, d, to);
+    return hipGetLastError();
+}
+
+template <typename TO> static hipError_t run_unpack(Packed8 from, int T, int d, void *out, hipStream_t s)
+{
+    constexpr int E = Elt<TO>::PER_CHUNK;
+    const int64_t items = (int64_t)T * ((d + E - 1) / E);
+    if ((int64_t)T * d >= A8_LARGE)
+        act_unpack_kernel<TO, 2><<<a8_grid(items, 2), dim3(256), 0, s>>>(from, T, d, (TO *)out);
+    else
+        act_unpack_kernel<TO, 1><<<a8_grid(items, 1), dim3(256), 0, s>>>(from, T, d, (TO *)out);
+    return hipGetLastError();
 }
 
 hipError_t launch_act_pack(int vdtype, const void *x, int T, int d, Packed8 to, hipStream_t s)
 {
-    const int64_t blocks = (int64_t)T * a8_blocks(d);
-    if (vdtype == 1)
-        act_pack_kernel<__bf16><<<a8_grid(blocks * 4), dim3(256), 0, s>>>((const __bf16 *)x, T, d, to);
-    else
-        act_pack_kernel<float><<<a8_grid(blocks * 8), dim3(256), 0, s>>>((const float *)x, T, d, to);
-    return hipGetLastError();
+    return vdtype == 1 ? run_pack<__bf16>(x, T, d, to, s) : run_pack<float>(x, T, d, to, s);
 }
 
 hipError_t launch_act_unpack(int vdtype, Packed8 from, int T, int d, void *out, hipStream_t s)
 {
-    if (vdtype == 1)
-        act_unpack_kernel<__bf16><<<a8_grid((int64_t)T * ((d + 7) / 8)), dim3(256), 0, s>>>(from, T, d, (__bf16 *)out);
-    else
-        act_unpack_kernel<float><<<a8_grid((int64_t)T * ((d + 3) / 4)), dim3(256), 0, s>>>(from, T, d, (float *)out);
-    return hipGetLastError();
+    return vdtype == 1 ? run_unpack<__bf16>(from, T, d, out, s) : run_unpack<float>(from, T, d, out, s);
 }
 
 }  // namespace twell

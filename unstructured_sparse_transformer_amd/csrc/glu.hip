@@ -93,7 +93,7 @@ __device__ __forceinline__ void glu_pack_rows(int lane, V value, const Packed8 &
         uint32_t c[4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
-            c[i] = a8_codes(value(fn, 4 * i), value(fn, 4 * i + 1), value(fn, 4 * i + 2), value(fn, 4 * i + 3), s.inv);
+            c[i] = a8_codes<true>(value(fn, 4 * i), value(fn, 4 * i + 1), value(fn, 4 * i + 2), value(fn, 4 * i + 3), s.inv);
         // lane l of the lower half has columns 0-3, 8-11, 16-19, 24-27 of row l, lane l + 32 the others
         const auto a = __builtin_amdgcn_permlane32_swap(c[0], c[2], false, false);
         const auto b = __builtin_amdgcn_permlane32_swap(c[1], c[3], false, false);
@@ -332,7 +332,7 @@ template <typename TI, bool PACK = false> __global__ __launch_bounds__(256) void
                 for (int o = 1; o < 8; o <<= 1)
                     top = a8_max(top, __shfl_xor(top, o, 64));
                 const A8Scale s(top);
-                *reinterpret_cast<uint32_t *>(to.code + c * 4) = a8_codes(v[w][0], v[w][1], v[w][2], v[w][3], s.inv);
+                *reinterpret_cast<uint32_t *>(to.code + c * 4) = a8_codes<true>(v[w][0], v[w][1], v[w][2], v[w][3], s.inv);
                 if ((c & 7) == 0)
                     to.scale[c / 8] = s.bits;
             }
