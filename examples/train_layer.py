@@ -1,14 +1,19 @@
 """Training steps of a small stack of feed-forward layers in the library's kernels.
 
-    python examples/train_layer.py [--ffn gated|sparse] [--steps 50] [--bits 8|32]
+    python examples/train_layer.py [--ffn gated|sparse] [--steps 50] [--bits 8|32] [--keep 8|16] [--vocab 4096]
 
 A layer adds alpha * gate * norm(FFN(norm(stream))) to a 32-bit residual stream.  The norm after one FFN, the gate, the
 sum and the norm before the next FFN are one call.  The FFN is the dense gated product followed by a plain matrix
 product of torch's (``gated``; its backward pass takes two more), or the ReLU-sparse one on its hybrid activations
-(``sparse``).  The weights are 32-bit masters with 16-bit copies for the layers; one call updates all of them.
+(``sparse``).  With ``--keep 8`` the gated FFN keeps its two products for the backward pass in 8 bits, and its hidden
+activation not at all.  The weights are 32-bit masters with 16-bit copies for the layers; one call updates all of them.
+
+The layers learn a function of vectors, or with ``--vocab`` the token after each token: an embedding in front of them,
+log probabilities behind them, and one table for both.
 """
 
 import argparse
+import math
 import os
 import sys
 
@@ -46,6 +51,27 @@ class Gated:
         return self.dx
 
 
+class GatedKept8(Gated):
+    """The same with g and u kept in 8 bits, and h taken from these again."""
+
+    def __init__(self, T, d, F, weights):
+        super().__init__(T, d, F, weights)
+        self.g, self.u = (tw.PackedAct.empty(T, F) for _ in range(2))
+        self.ws = tw.glu_packed_workspace(T, d, F)
+
+    def forward(self, n):
+        self.n = n
+        tw.twell_glu_forward_packed(n, self.wg, self.wu, "silu", self.h, self.g, self.u, self.ws)
+        return torch.mm(self.h, self.wd, out=self.y)
+
+    def backward(self, dy):
+        torch.mm(dy, self.wd.t(), out=self.dh)
+        tw.twell_glu_backward_packed(self.n, self.wg, self.wu, self.g, self.u, self.dh, "silu", self.dx, self.grads[0],
+                                     self.grads[1], self.ws_backward, h=self.h)
+        torch.mm(self.h.t(), dy, out=self.grads[2])
+        return self.dx
+
+
 class Sparse:
     """y = (ReLU(n W_g) * (n W_u)) W_d on the active neurons, forward and backward."""
 
@@ -74,7 +100,8 @@ class Sparse:
 class Stack:
     """`layers` feed-forward layers between norms, their gradients and their optimizer."""
 
-    def __init__(self, T, d, F, layers, ffn=Gated, bits=32, seed=0, alpha=0.5):
+    def __init__(self, T, d, F, layers, ffn=Gated, bits=32, seed=0, alpha=0.5, others=()):
+        """others: further tensors of the optimizer's step (p, copy, grad, weight_decay)."""
         gen = torch.Generator(device="cuda").manual_seed(seed)
         rnd = lambda *s: torch.randn(s, generator=gen, device="cuda")  # noqa: E731
         self.T, self.alpha, self.step_count = T, alpha, 0
@@ -99,6 +126,7 @@ class Stack:
                 for m, cs, f in zip(self.matrices, self.copies, self.ffn) for p, c, g in zip(m, cs, f.grads)]
         sets += [dict(p=p, grad=g) for p, g in zip(self.w_pre + self.w_post + self.gate,
                                                    self.dw_pre + self.dw_post + self.dgate)]
+        sets += [dict(t) for t in others]
         for t in sets:
             if bits == 8:
                 blocks = -(-t["p"].numel() // tw.ADAMW_BLOCK)
@@ -137,18 +165,89 @@ class Stack:
         tw.twell_adamw_step(self.optimizer, lr, 0.9, 0.95, 1e-8, self.step_count, seed=self.step_count)
 
 
+class Tokens:
+    """The stack between a table's rows for tokens (ids [T], int64; -1: padding) and log probabilities of the tokens after
+    them, from products with the same rows."""
+
+    def __init__(self, T, d, F, layers, V, seed=0, **stack):
+        gen = torch.Generator(device="cuda").manual_seed(seed + 100)
+        self.table = torch.randn((V, d), generator=gen, device="cuda") * d ** -0.5
+        self.copy, self.grad = self.table.to(BF16), torch.empty((V, d), dtype=BF16, device="cuda")
+        self.stack = Stack(T, d, F, layers, seed=seed, others=[dict(p=self.table, copy=self.copy, grad=self.grad)], **stack)
+        new = lambda *s, dt=F32: torch.empty(s, dtype=dt, device="cuda")  # noqa: E731
+        self.T, self.scale = T, math.sqrt(d)
+        self.x, self.logits, self.dn = new(T, d), new(T, V, dt=BF16), new(T, d, dt=BF16)
+        self.logp, self.norm = new(T), new(T, 2)
+        self.ws, self.ws_backward = tw.logprob_workspace(T, V), tw.embed_workspace(T, V, d)
+
+    def forward(self, ids, targets):
+        """The log probabilities [T] of the targets (0 where one is -1)."""
+        self.ids, self.targets = ids, targets
+        tw.twell_embed_forward(ids, self.copy, self.x, scale=self.scale)
+        self.n = self.stack.forward(self.x)
+        torch.mm(self.n, self.copy.t(), out=self.logits)
+        tw.twell_logprob_forward(self.logits, targets, self.logp, self.norm, self.ws)
+        return self.logp
+
+    def backward(self, dlogp):
+        """Gradients of all weights from that of the log probabilities; the logits make place for theirs."""
+        tw.twell_logprob_backward(self.logits, self.targets, self.norm, dlogp, self.logits)
+        torch.mm(self.logits, self.copy, out=self.dn)
+        torch.mm(self.logits.t(), self.n, out=self.grad)
+        dx = self.stack.backward(self.dn)
+        tw.twell_embed_backward(self.ids, dx, self.grad, self.ws_backward, scale=self.scale, accumulate=True)
+
+    def update(self, lr):
+        self.stack.update(lr)
+
+    def likely(self, k):
+        """The k most likely tokens after each, after forward and before backward."""
+        idx = torch.empty((self.T, k), dtype=torch.int32, device="cuda")
+        top = torch.empty((self.T, k), device="cuda")
+        tw.twell_logprob_forward(self.logits, None, None, None, tw.logprob_workspace(*self.logits.shape, k), top_logp=top,
+                                 top_idx=idx)
+        return idx, top
+
+
+def train_tokens(a, ffn):
+    T, d, F, layers = a.sizes
+    gen = torch.Generator(device="cuda").manual_seed(1)
+    after = torch.randperm(a.vocab, generator=gen, device="cuda")  # the token after each token, to be learned
+    model = Tokens(T, d, F, layers, a.vocab, ffn=ffn, bits=a.bits)
+    dlogp = torch.full((T,), -1 / T, device="cuda")
+    for step in range(a.steps):
+        u = torch.rand(T, generator=gen, device="cuda", dtype=torch.float64)
+        ids = (torch.exp(u * math.log(a.vocab + 1)).long() - 1).clamp(0, a.vocab - 1)  # few tokens are most of a text
+        loss = -model.forward(ids, after[ids]).mean()
+        hits = None
+        if step % 10 == 0 or step + 1 == a.steps:
+            hits = (model.likely(1)[0][:, 0] == after[ids]).float().mean()
+        model.backward(dlogp)
+        model.update(2e-3)
+        if hits is not None:
+            print(f"step {step:4d}  loss {loss.item():.5f}  most likely token right {hits.item():.3f}", flush=True)
+
+
 def main():
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     ap.add_argument("--ffn", choices=("gated", "sparse"), default="gated")
     ap.add_argument("--bits", type=int, choices=(8, 32), default=32)
+    ap.add_argument("--keep", type=int, choices=(8, 16), default=16)
+    ap.add_argument("--vocab", type=int, default=0)
     ap.add_argument("--steps", type=int, default=50)
     ap.add_argument("--sizes", type=int, nargs=4, default=(512, 256, 1024, 2), metavar=("T", "d", "F", "layers"))
     a = ap.parse_args()
+    if a.keep == 8 and a.ffn != "gated":
+        ap.error("--keep 8 is the gated FFN's")
+    ffn = GatedKept8 if a.keep == 8 else {"gated": Gated, "sparse": Sparse}[a.ffn]
+    if a.vocab:
+        train_tokens(a, ffn)
+        return
     T, d, F, layers = a.sizes
     gen = torch.Generator(device="cuda").manual_seed(1)
     x = torch.randn((T, d), generator=gen, device="cuda")
     target = torch.tanh(x.roll(1, 1)) + 0.5 * x  # a mixing of neighbouring channels, to be learned
-    stack = Stack(T, d, F, layers, {"gated": Gated, "sparse": Sparse}[a.ffn], a.bits)
+    stack = Stack(T, d, F, layers, ffn, a.bits)
     for step in range(a.steps):
         diff = stack.forward(x).float() - target
         stack.backward(diff * (2 / diff.numel()))
