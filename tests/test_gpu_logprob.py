@@ -78,8 +78,8 @@ def _check_backward(tw, z, targets, scale=1.0, entropy=True, logp=True, in_place
     tokens_ref.check(dz, want, bound, "dlogits")
 
 
-# widths around the pieces of 4 and 8, the workgroup's 256 threads, the segments of few rows; rows around those that are cut
-WIDTHS = [1, 2, 3, 4, 5, 7, 8, 9, 63, 255, 257, 1000, 2047, 2048, 2049, 4096, 4097, 8191, 8200, 20001, 50001]
+# widths around the pieces of 4 and 8, the workgroup's 256 threads, segments of 4096 and rows of 48 KB, which few rows are not cut below
+WIDTHS = [1, 2, 3, 4, 5, 7, 8, 9, 63, 255, 257, 1000, 2047, 2048, 2049, 4096, 4097, 8191, 8200, 12288, 12289, 20001, 24576, 24577, 50001]
 
 
 @pytest.mark.parametrize("V", WIDTHS)
@@ -92,7 +92,7 @@ def test_widths(gpu_lib, V, dtype):
         _check_backward(gpu_lib, _logits(T, V, dtype, seed=V), _targets(T, V), 0.8)
 
 
-@pytest.mark.parametrize("T,V", [(1, 131072), (2, 262145), (17, 30000), (100, 9000), (341, 12289), (1023, 4097), (1024, 8192), (1025, 4100),
+@pytest.mark.parametrize("T,V", [(1, 131072), (2, 262145), (17, 30000), (100, 9000), (341, 12289), (400, 26000), (1023, 25001), (1024, 8192), (1025, 4100),
                                  (3000, 515)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_rows(gpu_lib, T, V, dtype):
@@ -108,7 +108,7 @@ def test_rows(gpu_lib, T, V, dtype):
 def test_strided_rows(gpu_lib, extra, dtype):
     """Rows of a wider buffer, at any alignment of their elements, and the gradient in their place."""
     import torch
-    T, V = 9, 5003
+    T, V = 9, 25003
     say(f"case logprob strided {extra} {dtype}")
     z, t = _logits(T, V, dtype, ld=V + extra), _targets(T, V)
     _check_forward(gpu_lib, z, t, 1.0, 7)
@@ -123,8 +123,8 @@ def test_strided_rows(gpu_lib, extra, dtype):
 @pytest.mark.parametrize("dtype", TYPES)
 def test_flat_and_peaked_rows(gpu_lib, spread, dtype):
     say(f"case logprob spread {spread} {dtype}")
-    for T in (2, 1100):
-        z, t = _logits(T, 6001, dtype, spread=spread), _targets(T, 6001)
+    for T, V in ((2, 6001), (2, 30001), (1100, 6001)):
+        z, t = _logits(T, V, dtype, spread=spread), _targets(T, V)
         z[0] += 1e4
         _check_forward(gpu_lib, z, t, 1.0, 12)
         _check_backward(gpu_lib, z, t)
@@ -136,19 +136,18 @@ def test_sorted_rows(gpu_lib, order, dtype):
     """The maximum rises with every piece, or never."""
     import torch
     say(f"case logprob sorted {order} {dtype}")
-    for T, V in ((2, 40000), (1030, 9001)):
+    for T, V in ((2, 40000), (2, 9001), (1030, 9001)):
         z, t = _logits(T, V, dtype), _targets(T, V)
         z.copy_(torch.sort(z, dim=1, descending=order == "down").values)
         _check_forward(gpu_lib, z, t, 1.0, 64)
         _check_backward(gpu_lib, z, t)
 
 
-@pytest.mark.parametrize("T", [2, 1100])
+@pytest.mark.parametrize("T,V", [(2, 9001), (2, 31001), (1100, 9001)])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_equal_logits(gpu_lib, T, dtype):
+def test_equal_logits(gpu_lib, T, V, dtype):
     """Equal logits in bulk: the lowest indices first, +0 and -0 the same value."""
-    say(f"case logprob equal logits T={T} {dtype}")
-    V = 9001
+    say(f"case logprob equal logits T={T} V={V} {dtype}")
     t = _targets(T, V)
     z = _logits(T, V, dtype)
     z.zero_()
@@ -161,15 +160,35 @@ def test_equal_logits(gpu_lib, T, dtype):
     z[:, ::2] = -1
     _check_forward(gpu_lib, z, t, 2.0, 40)
     _check_backward(gpu_lib, z, t)
+    for few in (1, 5, 150, 250, 700):  # around the number from which on equal ones are told apart
+        z.fill_(-3)
+        z[:, 4000:4000 + few] = 5
+        z[:, 4000 + few // 2] = 6
+        for k in (1, 20, 64):
+            _check_forward(gpu_lib, z, t, 1.0, k)
 
 
-@pytest.mark.parametrize("T", [3, 1100])
+@pytest.mark.parametrize("T", [2, 1100])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_masked_logits(gpu_lib, T, dtype):
+def test_all_in_few_threads(gpu_lib, T, dtype):
+    """The largest logits lie where one thread reads them, more than the list of candidates holds among them."""
+    import torch
+    say(f"case logprob all in few threads T={T} {dtype}")
+    V, E = 300000 if T == 2 else 60000, 8 if dtype == "bfloat16" else 4
+    z, t = _logits(T, V, dtype), _targets(T, V)
+    piece = torch.arange(V, device="cuda") // E % 256
+    for thread, k in ((0, 64), (77, 20), (255, 33)):
+        x = torch.where(piece == thread, z * 0.25 + 40, z)
+        _check_forward(gpu_lib, x, t, 1.0, k)
+
+
+@pytest.mark.parametrize("T,V", [(3, 8209), (3, 30011), (1100, 8209)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_masked_logits(gpu_lib, T, V, dtype):
     """-inf and the type's lowest value: parts of a row, all but one, all."""
     import torch
-    say(f"case logprob masked T={T} {dtype}")
-    V, k = 8209, 10
+    say(f"case logprob masked T={T} V={V} {dtype}")
+    k = 10
     for blank in (-INF, float(torch.finfo(getattr(torch, dtype)).min)):
         z, t = _logits(T, V, dtype), _targets(T, V)
         z[:, 100:7000] = blank
@@ -190,13 +209,13 @@ def test_masked_logits(gpu_lib, T, dtype):
 
 
 @pytest.mark.parametrize("bad", [NAN, -NAN, INF])
-@pytest.mark.parametrize("T", [4, 1100])
+@pytest.mark.parametrize("T,V", [(4, 8197), (4, 31013), (1100, 8197)])
 @pytest.mark.parametrize("dtype", TYPES)
-def test_nan_and_infinity(gpu_lib, bad, T, dtype):
+def test_nan_and_infinity(gpu_lib, bad, T, V, dtype):
     """They spoil their own row, wherever they stand in it."""
     import torch
-    V, k = 8197, 6
-    say(f"case logprob bad {bad} T={T} {dtype}")
+    k = 6
+    say(f"case logprob bad {bad} T={T} V={V} {dtype}")
     z, t = _logits(T, V, dtype), _targets(T, V).clamp(0, V - 1)
     clean, _ = _forward(gpu_lib, z, t, 1.0, k)
     for where in (0, 4095, 5000, V - 1):
@@ -223,8 +242,8 @@ def test_parts_of_the_results(gpu_lib, dtype):
     import torch
     tw = gpu_lib
     say(f"case logprob parts {dtype}")
-    for T in (3, 1100):
-        V, k = 9000, 5
+    for T, V in ((3, 9000), (1100, 9000), (3, 30000)):
+        k = 5
         z, t = _logits(T, V, dtype), _targets(T, V)
         all_, idx = _forward(tw, z, t, 1.0, k)
         ws = tw.logprob_workspace(T, V, k)

@@ -135,7 +135,7 @@ int twell_logprob_forward(const void *logits, int64_t ld, int32_t T, int32_t V, 
         TWELL_TRY(check_vec(top_logp, 4));
         TWELL_TRY(check_vec(top_idx, 4));
     }
-    TWELL_TRY(check_ws(workspace, workspace_bytes, twell::lp_workspace(T, V, k)));
+    TWELL_TRY(check_ws(workspace, workspace_bytes, twell::lp_workspace(T, V, vdtype == TWELL_BF16, k)));
     twell::LpArgs a{};
     a.T = T;
     a.V = V;

@@ -10,6 +10,9 @@ namespace twell {
 
 constexpr int EMB_WINDOW = 32, EMB_WINDOW_SHORT = 8;  // sorted tokens that one sum takes at most
 constexpr int EMB_SHORT = 2048;     // tokens up to which the short windows are taken
+constexpr int EMB_ONE = 256;        // tokens up to which one launch does all,
+constexpr int64_t EMB_ONE_TABLE = (int64_t)1 << 23;  // with a table to be overwritten of up to so many elements
+constexpr int EMB_FILL_ROWS = 1024; // rows that a workgroup of that launch writes zeros to at most
 constexpr int EMB_FEW = 8192;       // tokens up to which ranks are counted in one launch
 constexpr int EMB_DIGIT_BITS = 9;   // of a sorting pass
 constexpr int EMB_MOST_BLOCKS = 256;  // workgroups of a sorting pass
@@ -37,6 +40,13 @@ inline int64_t emb_most_windows(int64_t T)
     return n > shorter ? n : shorter;
 }
 __host__ __device__ inline int64_t emb_pitch(int d) { return ((int64_t)d + 3) & ~(int64_t)3; }
+
+// Rows of a table of width d that such a workgroup takes: about 16384 elements.
+__host__ __device__ inline int64_t emb_fill_rows(int d)
+{
+    const int64_t n = 16384 / d;
+    return n < 1 ? 1 : n < EMB_FILL_ROWS ? n : EMB_FILL_ROWS;
+}
 
 // Places the workspace's parts at `base`; returns its bytes (never less for more tokens).
 size_t emb_layout(EmbArgs &a, void *base);

@@ -30,8 +30,8 @@ struct LpArgs {
 };
 
 // Segments of a row, and the bytes of the workspace of a call and of any call with up to T rows.
-void lp_segments(int T, int V, int &segs, int &seg);
-size_t lp_workspace(int T, int V, int k);
+void lp_segments(int T, int V, int bf16, int &segs, int &seg);
+size_t lp_workspace(int T, int V, int bf16, int k);
 size_t lp_most_workspace(int T, int V, int k);
 
 hipError_t launch_logprob(const LpArgs &a, void *ws, hipStream_t s);

@@ -106,6 +106,7 @@ __device__ __forceinline__ void lp_finish(const LpArgs &p, int64_t t, const LpSt
 }
 
 constexpr int LP_THREADS = 256, LP_CAND = 1024;
+constexpr int LP_MANY = 192;  // logits that reach a bound, from which on equal ones are told apart first
 constexpr int LP_SEG = 4096, LP_MOST_SEGS = 64;
 
 // Workgroup-wide scratch of the alternatives.
@@ -177,11 +178,11 @@ __device__ __forceinline__ void lp_offer(LpTop &sh, float x, int v)
 // of the 4 waves k / 4 threads have a largest that reaches the (k / 4)-th largest of
 // the wave's: the lowest of these four values is a bound that k logits reach.  Only
 // threads whose largest reaches it have any that do; the logits that reach it are
-// ranked by comparing each with each.  Where so many do that the list overflows
-// (equal logits in bulk), those above the bound are listed, and then as many of the
-// equal ones as are wanted, the lowest indices first.  If even those above the bound
-// are too many (all in few threads), the best is taken k times: a tournament of the
-// threads' best remaining.
+// ranked by comparing each with each.  Where many do (equal logits in bulk), those
+// above the bound are listed, and then as many of the equal ones as are wanted, the
+// lowest indices first.  If even those above the bound are more than the list holds
+// (all in few threads), the best is taken k times: a tournament of the threads' best
+// remaining.
 template <typename TI, int E, typename O, typename L, typename F>
 __device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, O own, L list, LpTop &sh, int tid, F emit)
 {
@@ -201,7 +202,7 @@ __device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int 
     list(head, tau);
     __syncthreads();
     int found = sh.count;
-    if (found > LP_CAND) {
+    if (found > LP_MANY) {
         __syncthreads();
         if (tid == 0)
             sh.count = 0;
@@ -409,6 +410,11 @@ template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THRE
                 sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
             __syncthreads();
             const int each = (whole + LP_THREADS - 1) / LP_THREADS, nt = sh.n_threads;
+            if (nt > LP_MANY) {  // at least so many logits reach it
+                if (tid == 0)
+                    sh.count = nt;
+                return;
+            }
             for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
                 const int of = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
                 if (j < each) {
@@ -579,7 +585,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
     constexpr int EARLY = 4;  // keys a thread asks for before the bound is known
     const uint64_t *keys = nullptr;
     uint64_t early[EARLY];
-    uint32_t entry = 0;
+    uint64_t entry_key = 0;
     int r = 0;
     if constexpr (TOP) {
         keys = p.keys + t * p.segs * p.k;
@@ -587,7 +593,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
         j = j < p.k ? j : p.k;
         r = (p.k + j - 1) / j;
         if (on)
-            entry = (uint32_t)(keys[lane * p.k + j - 1] >> 32);
+            entry_key = keys[lane * p.k + j - 1];
 #pragma unroll
         for (int q = 0; q < EARLY; ++q)
             early[q] = tid + q * LP_THREADS < p.segs * p.k ? keys[tid + q * LP_THREADS] : 0;
@@ -614,19 +620,34 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
             }
             return;
         }
+        const uint32_t entry = (uint32_t)(entry_key >> 32);
         // (an order of 0 is no key's: one below all of them where a list is shorter than j)
         const uint64_t bound = (uint64_t)lp_nth(entry, r, lane) << 32 | 1;
         __syncthreads();
-        auto offer = [&](uint64_t key) {
-            if (key >= bound)
-                cand[atomicAdd(&count, 1)] = key;
-        };
+        auto list = [&](uint64_t least) {
+            auto offer = [&](uint64_t key) {
+                if (key >= least)
+                    cand[atomicAdd(&count, 1)] = key;
+            };
 #pragma unroll
-        for (int q = 0; q < EARLY; ++q)
-            offer(early[q]);
-        for (int i = tid + EARLY * LP_THREADS; i < p.segs * p.k; i += LP_THREADS)
-            offer(keys[i]);
-        __syncthreads();
+            for (int q = 0; q < EARLY; ++q)
+                offer(early[q]);
+            for (int i = tid + EARLY * LP_THREADS; i < p.segs * p.k; i += LP_THREADS)
+                offer(keys[i]);
+            __syncthreads();
+        };
+        list(bound);
+        if (count > LP_MANY) {  // equal logits in bulk: of the lists' entries with that order, the one with the r-th key
+            const uint32_t order = (uint32_t)(bound >> 32);
+            const int above = __popcll(__ballot(on && entry > order));
+            const uint32_t low = on && entry == order ? (uint32_t)entry_key : 0;
+            const uint64_t exact = (uint64_t)order << 32 | lp_nth(low, r - above, lane);
+            __syncthreads();
+            if (tid == 0)
+                count = 0;
+            __syncthreads();
+            list(exact > 0 ? exact : 1);
+        }
         lp_rank(cand, count, p.k, tid, [&](int rank, uint64_t key) {
             p.top_idx[t * p.k + rank] = lp_key_index(key);
             p.top_logp[t * p.k + rank] = row.logp(lp_key_value(key), p.scale);
@@ -698,8 +719,10 @@ template <typename TI> __global__ __launch_bounds__(LP_THREADS) void logprob_bac
 static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
 // Few rows are cut into segments, so that LP_WGS workgroups have work: of LP_SEG
-// logits at most, where LP_MOST_SEGS of them are enough.
-constexpr int LP_WGS = 1024;
+// logits at most, where LP_MOST_SEGS of them are enough.  A row of up to LP_WHOLE
+// bytes takes one workgroup less time than the second launch that joins segments (4
+// us).
+constexpr int LP_WGS = 1024, LP_WHOLE = 48 << 10;
 
 static int most_segments(int V)
 {
@@ -707,9 +730,10 @@ static int most_segments(int V)
     return (int)(n < LP_MOST_SEGS ? n : LP_MOST_SEGS);
 }
 
-void lp_segments(int T, int V, int &segs, int &seg)
+void lp_segments(int T, int V, int bf16, int &segs, int &seg)
 {
-    const int64_t want = T > 0 ? ceil_div(LP_WGS, T) : 1, most = most_segments(V);
+    const bool whole = (int64_t)V * (bf16 ? 2 : 4) <= LP_WHOLE;
+    const int64_t want = T > 0 && !whole ? ceil_div(LP_WGS, T) : 1, most = most_segments(V);
     const int64_t n = want < most ? want : most;
     seg = (int)(ceil_div(ceil_div(V, n), 8) * 8);
     segs = (int)ceil_div(V, seg);
@@ -717,18 +741,18 @@ void lp_segments(int T, int V, int &segs, int &seg)
 
 static size_t bytes_of(int64_t parts, int k) { return (size_t)parts * (sizeof(LpState) + (size_t)k * 8); }
 
-size_t lp_workspace(int T, int V, int k)
+size_t lp_workspace(int T, int V, int bf16, int k)
 {
     int segs, seg;
-    lp_segments(T, V, segs, seg);
+    lp_segments(T, V, bf16, segs, seg);
     return segs > 1 ? bytes_of((int64_t)T * segs, k) : 0;
 }
 
-// Rows t times segments: at most most_segments(V) each, and below LP_WGS + t.
+// Rows t times segments, of either type: at most most_segments(V) each, and below LP_WGS + t.
 size_t lp_most_workspace(int T, int V, int k)
 {
     const int64_t t = T < LP_WGS ? T : LP_WGS - 1, most = most_segments(V);
-    if (most == 1)
+    if ((int64_t)V * 4 <= LP_WHOLE)
         return 0;
     const int64_t a = t * most, b = LP_WGS + t;
     return bytes_of(a < b ? a : b, k);
@@ -738,7 +762,7 @@ hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
 {
     LpArgs p = args;
     p.scale2 = p.scale * LP_LOG2E;
-    lp_segments(p.T, p.V, p.segs, p.seg);
+    lp_segments(p.T, p.V, p.bf16, p.segs, p.seg);
     if (p.segs > 1) {
         p.keys = (uint64_t *)ws;
         p.part = (LpState *)(p.keys + (int64_t)p.T * p.segs * p.k);
