@@ -711,6 +711,8 @@ def twell_embed_backward(ids, dout, dtable, workspace, scale: float = 1.0, accum
 def _logits(fn: str, name: str, t, dev: int) -> tuple:
     """The pointer of logits [T][V] whose rows are contiguous, and the elements from one row to the next."""
     T, V = t.shape
+    if t.is_contiguous() and t.get_device() == dev:
+        return t.data_ptr(), V
     if t.get_device() != dev:
         raise ValueError(f"{fn}: {name} is on {t.device}, not on cuda:{dev}")
     ld = t.stride(0) if T > 1 else V
@@ -744,13 +746,16 @@ def twell_logprob_forward(logits, targets, logp, norm, workspace=None, scale: fl
     if (top_logp is None) != (top_idx is None):
         raise ValueError(f"{fn}: top_logp and top_idx go together")
     ids, bits = (None, 32) if targets is None else _ids(fn, "targets", targets, T, dev)
+    f32, row = torch.float32, (T,)
     k = 0 if top_idx is None else top_idx.shape[-1]
-    o = [None if t is None else _tensor(fn, name, t, s, dev, torch.float32)
-         for name, t, s in (("logp", logp, (T,)), ("norm", norm, (T, 2)), ("entropy", entropy, (T,)),
-                            ("top_logp", top_logp, (T, k)))]
+    a = None if logp is None else _tensor(fn, "logp", logp, row, dev, f32)
+    b = None if norm is None else _tensor(fn, "norm", norm, (T, 2), dev, f32)
+    c = None if entropy is None else _tensor(fn, "entropy", entropy, row, dev, f32)
+    top = None if top_logp is None else _tensor(fn, "top_logp", top_logp, (T, k), dev, f32)
     idx = None if top_idx is None else _tensor(fn, "top_idx", top_idx, (T, k), dev, torch.int32)
-    _check(fn, load().twell_logprob_forward(z, ld, _i32(T), _i32(V), vdtype_of(logits.dtype), scale, ids, bits, *o, idx,
-                                            _i32(k), *_workspace(fn, workspace, dev), _stream(stream, dev)))
+    ws, size = _workspace(fn, workspace, dev)
+    _check(fn, load().twell_logprob_forward(z, ld, _i32(T), _i32(V), vdtype_of(logits.dtype), scale, ids, bits, a, b, c, top,
+                                            idx, _i32(k), ws, size, _stream(stream, dev)))
 
 
 def twell_logprob_backward(logits, targets, norm, dlogp, dlogits, scale: float = 1.0, entropy=None, dentropy=None,
@@ -769,10 +774,12 @@ def twell_logprob_backward(logits, targets, norm, dlogp, dlogits, scale: float =
     if dentropy is not None and entropy is None:
         raise ValueError(f"{fn}: dentropy without the forward's entropy")
     ids, bits = (None, 32) if dlogp is None else _ids(fn, "targets", targets, T, dev)
-    n = _tensor(fn, "norm", norm, (T, 2), dev, torch.float32)
-    v = [None if t is None else _tensor(fn, name, t, (T,), dev, torch.float32)
-         for name, t in (("entropy", entropy), ("dlogp", dlogp), ("dentropy", dentropy))]
-    _check(fn, load().twell_logprob_backward(z, ld, _i32(T), _i32(V), vdtype_of(logits.dtype), scale, ids, bits, n, *v, dz,
+    f32, row = torch.float32, (T,)
+    n = _tensor(fn, "norm", norm, (T, 2), dev, f32)
+    a = None if entropy is None else _tensor(fn, "entropy", entropy, row, dev, f32)
+    b = None if dlogp is None else _tensor(fn, "dlogp", dlogp, row, dev, f32)
+    c = None if dentropy is None else _tensor(fn, "dentropy", dentropy, row, dev, f32)
+    _check(fn, load().twell_logprob_backward(z, ld, _i32(T), _i32(V), vdtype_of(logits.dtype), scale, ids, bits, n, a, b, c, dz,
                                              ldd, _stream(stream, dev)))
 
 

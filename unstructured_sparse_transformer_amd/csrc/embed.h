@@ -9,7 +9,6 @@
 namespace twell {
 
 constexpr int EMB_WINDOW = 32, EMB_WINDOW_SHORT = 8;  // sorted tokens that one sum takes at most
-constexpr int EMB_SHORT = 2048;     // tokens up to which the short windows are taken
 constexpr int EMB_ONE = 256;        // tokens up to which one launch does all,
 constexpr int64_t EMB_ONE_TABLE = (int64_t)1 << 23;  // with a table to be overwritten of up to so many elements
 constexpr int EMB_FILL_ROWS = 1024; // rows that a workgroup of that launch writes zeros to at most
@@ -32,11 +31,15 @@ struct EmbArgs {
     float *part;            // [windows][2][emb_pitch(d)] sums of runs that windows cut
 };
 
+// Tokens up to which the short windows are taken: where they are too few, or their
+// rows too narrow, for the others to give every CU a few waves.
+inline int emb_short(int d) { return d <= 256 ? 8192 : 2048; }
+
 // The most windows of any call with up to T tokens.
-inline int64_t emb_most_windows(int64_t T)
+inline int64_t emb_most_windows(int64_t T, int d)
 {
-    const int64_t shorter = ((T < EMB_SHORT ? T : EMB_SHORT) + EMB_WINDOW_SHORT - 1) / EMB_WINDOW_SHORT;
-    const int64_t n = (T + EMB_WINDOW - 1) / EMB_WINDOW;
+    const int64_t few = T < emb_short(d) ? T : emb_short(d);
+    const int64_t shorter = (few + EMB_WINDOW_SHORT - 1) / EMB_WINDOW_SHORT, n = (T + EMB_WINDOW - 1) / EMB_WINDOW;
     return n > shorter ? n : shorter;
 }
 __host__ __device__ inline int64_t emb_pitch(int d) { return ((int64_t)d + 3) & ~(int64_t)3; }

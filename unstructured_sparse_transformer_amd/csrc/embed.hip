@@ -90,19 +90,21 @@ __device__ __forceinline__ void emb_fill(const EmbArgs &p, int wg, int wgs)
 }
 
 // Up to EMB_FEW tokens in one launch: a token's place is the number of tokens
-// with a smaller key, or the same key and an earlier row.  A workgroup takes 32
-// tokens, 8 threads each, which compare with every key from LDS (two operations
-// a key: T^2 / 256 CUs of them are 4 us at 8192 tokens).
+// with a smaller key, or the same key and an earlier row.  A workgroup takes 16
+// tokens, 16 threads each, which compare with every key from LDS (two operations
+// a key: T^2 / 256 CUs of them are 4 us at 8192 tokens; 32 tokens of 8 threads leave
+// half of the CUs idle at 4000 tokens, 10.5 us).
+constexpr int EMB_RANKS = 16, EMB_RANK_SLICES = 256 / EMB_RANKS;
 template <typename ID> __global__ __launch_bounds__(256) void emb_rank_kernel(EmbArgs p, int wgs)
 {
     __shared__ __attribute__((aligned(16))) int keys[EMB_FEW];
-    __shared__ int count[8][32];
+    __shared__ int count[EMB_RANK_SLICES][EMB_RANKS];
     if ((int)blockIdx.x >= wgs) {
         emb_fill(p, (int)blockIdx.x - wgs, (int)gridDim.x - wgs);
         return;
     }
-    const int tid = threadIdx.x, groups = (p.T + 31) / 32;
-    for (int t0 = 0; t0 < groups * 32; t0 += 256 * 8) {
+    const int tid = threadIdx.x, groups = (p.T + EMB_RANKS - 1) / EMB_RANKS;
+    for (int t0 = 0; t0 < groups * EMB_RANKS; t0 += 256 * 8) {
         int k[8];
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
@@ -112,19 +114,20 @@ template <typename ID> __global__ __launch_bounds__(256) void emb_rank_kernel(Em
 #pragma unroll
         for (int i = 0; i < 8; ++i) {
             const int t = t0 + i * 256 + tid;
-            if (t < groups * 32)
+            if (t < groups * EMB_RANKS)
                 keys[t] = t < p.T ? k[i] : 0x7FFFFFF0;  // (above V)
         }
     }
     __syncthreads();
-    const int own = (int)blockIdx.x, mine = tid & 31, key = keys[own * 32 + mine];
+    const int own = (int)blockIdx.x, mine = tid % EMB_RANKS, key = keys[own * EMB_RANKS + mine];
     int n = 0;
-    for (int g = tid >> 5; g < groups; g += 8) {
-        const int4 *q = reinterpret_cast<const int4 *>(keys + g * 32);
+#pragma unroll 2
+    for (int g = tid / EMB_RANKS; g < groups; g += EMB_RANK_SLICES) {
+        const int4 *q = reinterpret_cast<const int4 *>(keys + g * EMB_RANKS);
         if (g != own) {
             const int below = key + (g < own);  // of the tokens before, those with the same key count
 #pragma unroll
-            for (int j = 0; j < 8; ++j) {
+            for (int j = 0; j < EMB_RANKS / 4; ++j) {
                 const int4 k = q[j];
                 n += k.x < below;
                 n += k.y < below;
@@ -132,19 +135,19 @@ template <typename ID> __global__ __launch_bounds__(256) void emb_rank_kernel(Em
                 n += k.w < below;
             }
         } else {
-            for (int j = 0; j < 32; ++j)
-                n += keys[g * 32 + j] < key + (j < mine);
+            for (int j = 0; j < EMB_RANKS; ++j)
+                n += keys[g * EMB_RANKS + j] < key + (j < mine);
         }
     }
-    count[tid >> 5][mine] = n;
+    count[tid / EMB_RANKS][mine] = n;
     __syncthreads();
-    if (tid < 32 && own * 32 + tid < p.T) {
+    if (tid < EMB_RANKS && own * EMB_RANKS + tid < p.T) {
         int at = 0;
 #pragma unroll
-        for (int s = 0; s < 8; ++s)
+        for (int s = 0; s < EMB_RANK_SLICES; ++s)
             at += count[s][tid];
-        p.key[at] = keys[own * 32 + tid];
-        p.perm[at] = own * 32 + tid;
+        p.key[at] = keys[own * EMB_RANKS + tid];
+        p.perm[at] = own * EMB_RANKS + tid;
     }
 }
 
@@ -519,7 +522,7 @@ size_t emb_layout(EmbArgs &a, void *base)
     };
     a.key = (int32_t *)take(list);
     a.perm = (int32_t *)take(list);
-    a.part = (float *)take(up256_((size_t)2 * emb_most_windows(a.T) * emb_pitch(a.d) * 4));
+    a.part = (float *)take(up256_((size_t)2 * emb_most_windows(a.T, a.d) * emb_pitch(a.d) * 4));
     if (a.T > EMB_FEW) {
         a.key2 = (int32_t *)take(list);
         a.perm2 = (int32_t *)take(list);
@@ -557,7 +560,7 @@ template <typename ID> static hipError_t run_sort(EmbArgs &p, hipStream_t s)
     const int64_t want = p.accumulate ? 0 : ceil_div(bytes, 256 * 16 * 2);
     const int fill = (int)(want < (1 << 20) ? want : 1 << 20);
     if (p.T <= EMB_FEW) {
-        const int wgs = (int)ceil_div(p.T, 32);
+        const int wgs = (int)ceil_div(p.T, EMB_RANKS);
         if (wgs + fill > 0)
             emb_rank_kernel<ID><<<dim3(wgs + fill), dim3(256), 0, s>>>(p, wgs);
         return hipGetLastError();
@@ -594,9 +597,12 @@ template <typename TD, typename TT, int E, int W> static hipError_t run_sums(con
     if (windows > 1) {
         const int64_t most = ceil_div(2048, slices), x = windows - 1 < most ? windows - 1 : most;
         const dim3 runs((unsigned)x, (unsigned)slices);
-        // (a run has at most all windows: 64 and more for each of 4 waves from here on)
+        // (a run has at most all windows: up to 64 for each of 4 waves, 128 of 8; the more waves, the fewer of the
+        // workgroups that find no run run at once)
         if (windows <= 256)
             emb_join_kernel<TT, E, 4><<<runs, dim3(256), 0, s>>>(p, W);
+        else if (windows <= 1024)
+            emb_join_kernel<TT, E, 8><<<runs, dim3(512), 0, s>>>(p, W);
         else
             emb_join_kernel<TT, E, 16><<<runs, dim3(1024), 0, s>>>(p, W);
     }
@@ -635,7 +641,7 @@ hipError_t launch_embed_backward(const EmbArgs &args, hipStream_t s)
             return p.id64 ? run_one<int64_t, TD, TT, 1>(p, s) : run_one<int32_t, TD, TT, 1>(p, s);
         if (p.d < 4)
             return run_sums<TD, TT, 1, EMB_WINDOW>(p, s);
-        return p.T <= EMB_SHORT ? run_sums<TD, TT, 4, EMB_WINDOW_SHORT>(p, s) : run_sums<TD, TT, 4, EMB_WINDOW>(p, s);
+        return p.T <= emb_short(p.d) ? run_sums<TD, TT, 4, EMB_WINDOW_SHORT>(p, s) : run_sums<TD, TT, 4, EMB_WINDOW>(p, s);
     };
     if (p.bf16_table)
         return p.bf16_rows ? with(__bf16{}, __bf16{}) : with(float{}, __bf16{});
