@@ -582,7 +582,7 @@ TWELL_API size_t twell_logprob_workspace_bytes(int32_t T, int32_t V, int32_t k);
  * dentropy [T] float (with the forward's entropy), either of which may be NULL:
  *   dz[v] = scale (dlogp (1[v = target] - p[v]) - dentropy p[v] (log p[v] + entropy))
  * dlogits [T] rows of V, vdtype, `ldd` elements apart; may be logits (then ldd =
- * ld).  A row of masked tokens only gets zeros, one with a NaN in norm NaN. */
+ * ld), but not overlap it otherwise.  A row of masked tokens only gets zeros, one with a NaN in norm NaN. */
 TWELL_API int twell_logprob_backward(const void *logits, int64_t ld, int32_t T, int32_t V, int32_t vdtype, float scale,
                                      const void *targets, int32_t id_bits, const float *norm, const float *entropy,
                                      const float *dlogp, const float *dentropy, void *dlogits, int64_t ldd,

@@ -86,6 +86,31 @@ def test_logprob_backward():
         assert f(**kw) == UNSUPPORTED, kw
     for kw in (dict(T=-1), dict(V=0), dict(ld=99), dict(ldd=99), dict(scale=0.0), dict(scale=NAN), dict(ldd=101)):
         assert f(**kw) == SHAPE, kw
+    # dlogits partly in the logits' place: 8 rows of 100 bf16, 200 bytes apart
+    for at in (2, 198, 200, 1598, -2, -200, -1598):
+        assert f(dz=GOOD + at) == SHAPE, at
+    for at, ld in ((198, 199), (300, 200), (1450, 400)):  # in the gaps of wider rows, but not all of a row
+        assert f(dz=GOOD + at, ld=ld, ldd=ld) == SHAPE, (at, ld)
+    assert f(dz=GOOD + 200, ld=200, ldd=300) == SHAPE
+
+
+@pytest.mark.parametrize("rows", [1, 2, 7])
+def test_logprob_backward_overlaps(rows):
+    """Against the elements themselves: dlogits shares none with the logits, or lies in their place."""
+    lib, V, es = tw.load(), 6, 4
+    for ld in (6, 7, 12, 13, 20):
+        for ldd in (6, 7, 12, 13, 20):
+            a = {t * ld + v for t in range(rows) for v in range(V)}
+            for off in range(-rows * 21, rows * 21):
+                b = {off + t * ldd + v for t in range(rows) for v in range(V)}
+                # (a NULL norm ends the calls that are not refused for their places)
+                got = lib.twell_logprob_backward(GOOD * 16, ld, rows, V, 0, 1.0, GOOD, 64, GOOD, None, GOOD + 1, None,
+                                                 GOOD * 16 + off * es, ldd, None)
+                assert got in (SHAPE, ALIGN)
+                if got == ALIGN:
+                    assert not a & b or (off == 0 and (ld == ldd or rows == 1)), (ld, ldd, off)
+                elif ld == ldd:
+                    assert a & b, (ld, off)
 
 
 def _pk(code=GOOD, scale=GOOD):

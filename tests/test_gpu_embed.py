@@ -146,6 +146,26 @@ def test_backward_types(gpu_lib, dout, table, d):
             _check_backward(gpu_lib, _ids(700, 90, ids, seed=d, spread="text"), rows, 90, table, accumulate, 1.5)
 
 
+@pytest.mark.parametrize("T", [9000, 40000])
+def test_backward_large_vocabulary(gpu_lib, T):
+    """Keys of 28 bits: four sorting passes."""
+    import torch
+    V, d = (1 << 27) + 5, 3
+    say(f"case embed backward V={V} T={T}")
+    gen = torch.Generator(device="cuda").manual_seed(T)
+    few = torch.randint(-5, V + 5, (T // 3,), generator=gen, device="cuda")
+    few[:3] = torch.tensor([0, V - 1, V], device="cuda")
+    ids = few[torch.randint(0, T // 3, (T,), generator=gen, device="cuda")]
+    dout, table = _rnd(T, d), torch.zeros((V, d), device="cuda")
+    gpu_lib.twell_embed_backward(ids, dout, table, gpu_lib.embed_workspace(T, V, d), accumulate=True)
+    names, at = torch.unique(ids, return_inverse=True)
+    value, bound = tokens_ref.embed_backward(at, dout, names.numel(), 1.0)
+    real = (names >= 0) & (names < V)
+    tokens_ref.check(table[names[real]], value[real], bound[real], "dtable")
+    table[names[real]] = 0
+    assert not table.any()
+
+
 @pytest.mark.parametrize("T", [0, 5, 9000])
 def test_backward_without_ids(gpu_lib, T):
     """No token, or only padding: zeros, or nothing is changed."""

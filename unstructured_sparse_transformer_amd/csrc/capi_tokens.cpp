@@ -35,6 +35,20 @@ int check_logprob(int32_t T, int32_t V, int32_t k)
     return (int64_t)T * (((int64_t)V + 2047) / 2048) < ((int64_t)1 << 31) ? TWELL_OK : TWELL_E_SHAPE;
 }
 
+// Whether rows of `row` bytes at `b` lie apart from those at `a`, or in their place: rows ld and ldd bytes apart.
+bool apart(const void *a, int64_t ld, const void *b, int64_t ldd, int64_t T, int64_t row)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    if (x == y)
+        return ld == ldd || T == 1;
+    if (x + (T - 1) * ld + row <= y || y + (T - 1) * ldd + row <= x)
+        return true;
+    if (ld != ldd)
+        return false;
+    const uintptr_t off = (y > x ? y - x : x - y) % (uintptr_t)ld;  // side by side in one buffer
+    return off >= (uintptr_t)row && off + (uintptr_t)row <= (uintptr_t)ld;
+}
+
 bool good_scale(float scale) { return scale > 0 && std::isfinite(scale); }
 bool known_ids(int32_t id_bits) { return id_bits == 32 || id_bits == 64; }
 
@@ -167,6 +181,9 @@ int twell_logprob_backward(const void *logits, int64_t ld, int32_t T, int32_t V,
         return TWELL_OK;
     TWELL_TRY(check_vec(logits, elem_size(vdtype)));
     TWELL_TRY(check_vec(dlogits, elem_size(vdtype)));
+    const int es = elem_size(vdtype);
+    if (!apart(logits, ld * es, dlogits, ldd * es, T, (int64_t)V * es))
+        return TWELL_E_SHAPE;
     TWELL_TRY(check_vec(norm, 4));
     if (!dlogp && !dentropy)
         return TWELL_E_NULL;
@@ -178,8 +195,6 @@ int twell_logprob_backward(const void *logits, int64_t ld, int32_t T, int32_t V,
         TWELL_TRY(check_vec(dentropy, 4));
         TWELL_TRY(check_vec(entropy, 4));
     }
-    if (dlogits == logits && ldd != ld)
-        return TWELL_E_SHAPE;
     twell::LpArgs a{};
     a.T = T;
     a.V = V;
