@@ -118,9 +118,10 @@ def _check_backward(tw, ids, dout, V, table, accumulate, scale=1.0):
     return got
 
 
-# around the 256 tokens that one launch takes, the windows of 8 and 32, the counted ranks' 8192 tokens and the sorting
+# around the 1024 tokens, and 4096 slices of 256 columns of them, that one launch takes, the windows of 8 and 32, the counted ranks' 8192 tokens and the sorting
 # passes' digits of 9 bits; widths around a workgroup's zeros
-BACK = [(255, 3, 8), (256, 300, 260), (256, 5000, 3), (257, 40, 8), (200, 2, 17000), (40, 9000, 1000), (7, 700000, 12), (2048, 30, 8),
+BACK = [(255, 3, 8), (256, 300, 260), (256, 5000, 3), (257, 40, 8), (200, 2, 17000), (40, 9000, 1000), (7, 700000, 12), (1024, 40, 1024), (1024, 40, 1028), (1024, 700, 250),
+        (1025, 40, 8), (63, 900, 16400), (2048, 30, 8),
         (2049, 30, 8), (1, 1, 1), (1, 5, 64), (2, 3, 4), (31, 4, 5), (32, 1, 8), (33, 2, 3), (64, 5, 17), (65, 1, 1), (100, 1000, 96), (1000, 7, 33),
         (1003, 500, 1001), (8192, 600, 12), (8193, 511, 8), (8200, 512, 4), (20000, 100, 2), (30000, 70000, 20), (70000, 3, 5),
         (132000, 513, 4)]

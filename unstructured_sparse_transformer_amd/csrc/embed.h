@@ -9,7 +9,7 @@
 namespace twell {
 
 constexpr int EMB_WINDOW = 32, EMB_WINDOW_SHORT = 8;  // sorted tokens that one sum takes at most
-constexpr int EMB_ONE = 256;        // tokens up to which one launch does all,
+constexpr int EMB_ONE = 1024, EMB_ONE_WGS = 4096;  // tokens, and slices of them, up to which one launch does all,
 constexpr int64_t EMB_ONE_TABLE = (int64_t)1 << 23;  // with a table to be overwritten of up to so many elements
 constexpr int EMB_FILL_ROWS = 1024; // rows that a workgroup of that launch writes zeros to at most
 constexpr int EMB_FEW = 8192;       // tokens up to which ranks are counted in one launch

@@ -423,29 +423,41 @@ template <typename TT, int E, int NW> __global__ __launch_bounds__(NW * 64) void
 }
 
 // ------------------------------------------------------------------ few tokens
-// Up to EMB_ONE tokens in one launch, without sorting: a wave takes a token and 64
-// pieces of columns, and if no earlier token has the same id adds the rows of all
-// that do, 8 at a time, in order.  Without `accumulate` the workgroups behind those
-// write zeros to the rows that no token has.  (Three launches take 13 us from the
-// host, this one 7.)
+// Up to EMB_ONE tokens in one launch, without sorting: a workgroup takes a token
+// and 64 pieces of columns, and if no earlier token has the same id adds the rows of
+// all that do: each of its 4 waves every 4th, 8 at a time, in order, and their sums in
+// order.  Without ADD the workgroups behind those write zeros to the rows that no
+// token has.  (Sorting, sums and join take 13 us of three launches, this one 7.)
 template <typename ID, typename TD, typename TT, int E, bool ADD>
 __global__ __launch_bounds__(256) void emb_one_kernel(EmbArgs p, int slices, int wgs)
 {
-    constexpr int B = 8;
-    __shared__ int keys[EMB_ONE];
-    __shared__ uint64_t there[EMB_FILL_ROWS / 64];
-    const int tid = threadIdx.x, lane = tid & 63;
-    keys[tid] = tid < p.T ? token_key((const ID *)p.ids, tid, p.V) : p.V;
-    static_assert(EMB_ONE == 256, "a thread a token");
-    if ((int)blockIdx.x >= wgs) {
+    constexpr int B = 8, NW = 4, GROUPS = EMB_ONE / 64, MINE = EMB_ONE / 256;
+    __shared__ uint64_t same[GROUPS], there[EMB_FILL_ROWS / 64];
+    __shared__ int list[EMB_ONE];
+    __shared__ float all[NW][E][64];
+    const int tid = threadIdx.x, lane = tid & 63, wave = tid >> 6;
+    const bool fills = (int)blockIdx.x >= wgs;
+    const int t = fills ? 0 : blockIdx.x / slices, piece = (blockIdx.x - t * slices) * 64 + lane;
+    const int key = p.T > 0 ? token_key((const ID *)p.ids, t, p.V) : p.V;
+    int own[MINE];  // of tokens tid, tid + 256, ...
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        const int at = i * 256 + tid;
+        own[i] = i * 256 < p.T ? token_key((const ID *)p.ids, at < p.T ? at : p.T - 1, p.V) : p.V;
+        own[i] = at < p.T ? own[i] : p.V;
+    }
+    if (fills) {
         const int64_t per = emb_fill_rows(p.d), r0 = ((int64_t)blockIdx.x - wgs) * per;
         const int rows = (int)(r0 + per < p.V ? per : p.V - r0);
         if (tid < EMB_FILL_ROWS / 64)
             there[tid] = 0;
         __syncthreads();
-        const int64_t r = keys[tid] - r0;
-        if (keys[tid] < p.V && r >= 0 && r < rows)
-            atomicOr((unsigned long long *)&there[r >> 6], 1ull << (r & 63));
+#pragma unroll
+        for (int i = 0; i < MINE; ++i) {
+            const int64_t r = own[i] - r0;
+            if (own[i] < p.V && r >= 0 && r < rows)
+                atomicOr((unsigned long long *)&there[r >> 6], 1ull << (r & 63));
+        }
         __syncthreads();
         const int pieces = (p.d + E - 1) / E;
         const float zero[E] = {};
@@ -459,52 +471,63 @@ __global__ __launch_bounds__(256) void emb_one_kernel(EmbArgs p, int slices, int
         }
         return;
     }
-    __syncthreads();
-    const int unit = __builtin_amdgcn_readfirstlane(blockIdx.x * 4 + (tid >> 6));
-    const int t = unit / slices, piece = (unit - t * slices) * 64 + lane;
-    if (t >= p.T)
-        return;
-    const int key = __builtin_amdgcn_readfirstlane(keys[t]);
     if (key >= p.V)
         return;
-    uint64_t same[EMB_ONE / 64];
+    int earlier = 0;
 #pragma unroll
-    for (int g = 0; g < EMB_ONE / 64; ++g)
-        same[g] = __ballot(keys[g * 64 + lane] == key);
-    bool first = true;
-#pragma unroll
-    for (int g = 0; g < EMB_ONE / 64; ++g)
-        first = first && (same[g] & (g * 64 + 64 <= t ? ~0ull : g * 64 <= t ? (1ull << (t - g * 64)) - 1 : 0ull)) == 0;
-    if (!first || piece >= (p.d + E - 1) / E)
+    for (int i = 0; i < MINE; ++i)
+        earlier |= own[i] == key && i * 256 + tid < t;
+    if (__syncthreads_or(earlier))
         return;
-    int from;
-    const int c = rows_column<E>(piece, p.d, from);
+#pragma unroll
+    for (int i = 0; i < MINE; ++i) {
+        const uint64_t m = __ballot(own[i] == key);
+        if (lane == 0)
+            same[i * 4 + wave] = m;  // token i 256 + tid is lane `lane` of group 4 i + wave
+    }
+    __syncthreads();
+    int n = 0;
+    for (int g = 0; g < GROUPS && g * 64 < p.T; ++g) {
+        const uint64_t m = same[g];
+        if (g % 4 == wave && (m >> lane & 1))
+            list[n + __popcll(m & ((1ull << lane) - 1))] = g * 64 + lane;
+        n += __popcll(m);
+    }
+    int from = 0;
+    const bool on = piece < (p.d + E - 1) / E;
+    const int c = on ? rows_column<E>(piece, p.d, from) : 0;  // (lanes past the columns read the first ones)
     RowPiece<TT, E> old;
     if constexpr (ADD)
         old.load((const TT *)p.out + (int64_t)key * p.d + c);
+    __syncthreads();
     float sum[E];
 #pragma unroll
     for (int e = 0; e < E; ++e)
         sum[e] = 0.f;
+    for (int i0 = wave; i0 < n; i0 += NW * B) {
+        RowPiece<TD, E> v[B];
 #pragma unroll
-    for (int g = 0; g < EMB_ONE / 64; ++g)
-        while (same[g]) {
-            RowPiece<TD, E> v[B];
-            const int n = __popcll(same[g]);
+        for (int b = 0; b < B; ++b)
+            v[b].load((const TD *)p.in + (int64_t)list[i0 + b * NW < n ? i0 + b * NW : i0] * p.d + c);
 #pragma unroll
-            for (int b = 0; b < B; ++b) {
-                const int at = g * 64 + (same[g] ? __builtin_ctzll(same[g]) : t - g * 64);
-                same[g] &= same[g] - 1;
-                v[b].load((const TD *)p.in + (int64_t)at * p.d + c);
-            }
+        for (int b = 0; b < B; ++b)
+            if (i0 + b * NW < n)
 #pragma unroll
-            for (int b = 0; b < B; ++b)
-                if (b < n)
+                for (int e = 0; e < E; ++e)
+                    sum[e] += v[b].at(e);
+    }
+    if (n > 1) {
 #pragma unroll
-                    for (int e = 0; e < E; ++e)
-                        sum[e] += v[b].at(e);
-        }
-    emb_write<TT, E, ADD>(p, key, c, from, sum, old);
+        for (int e = 0; e < E; ++e)
+            all[wave][e][lane] = sum[e];
+        __syncthreads();
+        for (int k = 1; k < NW && k < n; ++k)
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                sum[e] += all[k][e][lane];
+    }
+    if (wave == 0 && on)
+        emb_write<TT, E, ADD>(p, key, c, from, sum, old);
 }
 
 // ------------------------------------------------------------------ host
@@ -609,9 +632,11 @@ template <typename TD, typename TT, int E, int W> static hipError_t run_sums(con
     return hipGetLastError();
 }
 
+static int64_t slices_of(int d) { return ceil_div(ceil_div(d, d >= 4 ? 4 : 1), 64); }
+
 template <typename ID, typename TD, typename TT, int E> static hipError_t run_one(const EmbArgs &p, hipStream_t s)
 {
-    const int64_t slices = ceil_div(ceil_div(p.d, E), 64), wgs = ceil_div(p.T * slices, 4);
+    const int64_t slices = slices_of(p.d), wgs = p.T * slices;
     const int64_t fill = p.accumulate ? 0 : ceil_div(p.V, emb_fill_rows(p.d));
     const dim3 grid((unsigned)(wgs + fill)), block(256);
     if (p.accumulate)
@@ -626,7 +651,8 @@ hipError_t launch_embed_backward(const EmbArgs &args, hipStream_t s)
     EmbArgs p = args;
     if (p.T == 0 && p.accumulate)
         return hipSuccess;
-    const bool one = p.T <= EMB_ONE && (p.accumulate || (int64_t)p.V * p.d <= EMB_ONE_TABLE);
+    const bool one = p.T <= EMB_ONE && p.T * slices_of(p.d) <= EMB_ONE_WGS &&
+                     (p.accumulate || (int64_t)p.V * p.d <= EMB_ONE_TABLE);
     if (!one) {
         const hipError_t e = p.id64 ? run_sort<int64_t>(p, s) : run_sort<int32_t>(p, s);
         if (e != hipSuccess || p.T == 0)
