@@ -107,7 +107,7 @@ __device__ __forceinline__ void lp_finish(const LpArgs &p, int64_t t, const LpSt
 
 constexpr int LP_THREADS = 256, LP_CAND = 1024;
 constexpr int LP_MANY = 192;  // logits that reach a bound, from which on equal ones are told apart first
-constexpr int LP_SEG = 4096, LP_MOST_SEGS = 64;
+constexpr int LP_SEG = 4096, LP_MOST_SEGS = 64, LP_ONCE = 4;
 
 // Workgroup-wide scratch of the alternatives.
 struct LpTop {
@@ -119,34 +119,18 @@ struct LpTop {
     uint64_t win;
 };
 
-// The largest of the wave's values (DPP row shifts and row broadcasts).
-__device__ __forceinline__ uint32_t lp_wave_max(uint32_t v)
+// The r-th largest (r from 1 to 64) of the wave's values, bit by bit: the largest
+// number that r of them reach.  (Taking the largest out r - 1 times costs as much at
+// r = 4, three times as much at 16.)
+__device__ __forceinline__ uint32_t lp_nth(uint32_t v, int r)
 {
-    auto step = [&](auto ctrl, auto rows) {
-        const uint32_t o = (uint32_t)__builtin_amdgcn_update_dpp(0, (int)v, decltype(ctrl)::value, decltype(rows)::value,
-                                                                 0xf, false);
-        v = o > v ? o : v;
-    };
-    using std::integral_constant;
-    step(integral_constant<int, 0x111>{}, integral_constant<int, 0xf>{});  // row_shr:1
-    step(integral_constant<int, 0x112>{}, integral_constant<int, 0xf>{});  // row_shr:2
-    step(integral_constant<int, 0x114>{}, integral_constant<int, 0xf>{});  // row_shr:4
-    step(integral_constant<int, 0x118>{}, integral_constant<int, 0xf>{});  // row_shr:8
-    step(integral_constant<int, 0x142>{}, integral_constant<int, 0xa>{});  // row_bcast:15
-    step(integral_constant<int, 0x143>{}, integral_constant<int, 0xc>{});  // row_bcast:31
-    return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
-}
-
-// The r-th largest (r from 1 to 64) of the wave's values: the largest is taken out
-// r - 1 times.  (Counting the larger ones of each costs as much at r = 16.)
-__device__ __forceinline__ uint32_t lp_nth(uint32_t v, int r, int lane)
-{
-    uint32_t top = lp_wave_max(v);
-    for (int i = 1; i < r; ++i) {
-        v = lane == __builtin_ctzll(__ballot(v == top)) ? 0u : v;
-        top = lp_wave_max(v);
+    uint32_t at = 0;
+#pragma unroll
+    for (int bit = 31; bit >= 0; --bit) {
+        const uint32_t up = at | 1u << bit;
+        at = __popcll(__ballot(v >= up)) >= r ? up : at;
     }
-    return top;
+    return at;
 }
 
 // The k best keys of cand[0 .. n), best first, to emit(rank, key).
@@ -170,11 +154,57 @@ __device__ __forceinline__ void lp_offer(LpTop &sh, float x, int v)
         sh.cand[at] = lp_key(x, v);
 }
 
+// Lists the logits of a segment that reach the order `least`.  The pieces of the few
+// threads that have any, a few kilobytes that the caches hold, are read again by all
+// (from the registers that they are in: 32 comparisons by every wave, 16000 x 5080
+// bf16 109 us in the place of 65), and a lane takes its places in the list at once.
+template <typename TI, int E>
+__device__ __forceinline__ void lp_list(const TI *z, int v0, int n, uint32_t head, uint32_t least, LpTop &sh, int tid)
+{
+    const int whole = n / E, rest = n - whole * E, each = (whole + LP_THREADS - 1) / LP_THREADS;
+    if (head >= least)
+        sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
+    __syncthreads();
+    const int nt = sh.n_threads;
+    if (nt > LP_MANY) {  // at least so many logits reach it
+        if (tid == 0)
+            sh.count = nt;
+        return;
+    }
+    for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
+        const int of = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
+        if (j < each) {
+            const int at = (j * LP_THREADS + of) * E;
+            if (at + E > n)
+                continue;
+            RowPiece<TI, E> x;
+            x.load(z + at);
+            int hits = 0;
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                hits += lp_order(x.at(e)) >= least;
+            if (hits) {
+                int to = atomicAdd(&sh.count, hits);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    if (lp_order(x.at(e)) >= least) {
+                        if (to < LP_CAND)
+                            sh.cand[to] = lp_key(x.at(e), v0 + at + e);
+                        ++to;
+                    }
+            }
+        } else if (of < rest) {
+            const float x = (float)z[whole * E + of];
+            if (lp_order(x) >= least)
+                lp_offer(sh, x, v0 + whole * E + of);
+        }
+    }
+}
+
 // The k best logits of the segment [v0, v0 + n) of a row, best first, to
 // emit(rank, key); emit(rank, 0) where there are fewer.  `largest`: the largest of
 // those that this thread has read: pieces tid, tid + 256, ... of E elements, and
-// element tid of the rest; own(f) calls f(logit, index) for each of them, and
-// list(order) adds the keys of all that reach an order to the list.  In each
+// element tid of the rest; own(f) calls f(logit, index) for each of them.  In each
 // of the 4 waves k / 4 threads have a largest that reaches the (k / 4)-th largest of
 // the wave's: the lowest of these four values is a bound that k logits reach.  Only
 // threads whose largest reaches it have any that do; the logits that reach it are
@@ -183,12 +213,12 @@ __device__ __forceinline__ void lp_offer(LpTop &sh, float x, int v)
 // lowest indices first.  If even those above the bound are more than the list holds
 // (all in few threads), the best is taken k times: a tournament of the threads' best
 // remaining.
-template <typename TI, int E, typename O, typename L, typename F>
-__device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, O own, L list, LpTop &sh, int tid, F emit)
+template <typename TI, int E, typename O, typename F>
+__device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int k, float largest, O own, LpTop &sh, int tid, F emit)
 {
     const int whole = n / E, rest = n - whole * E, lane = tid & 63, each = (whole + LP_THREADS - 1) / LP_THREADS;
     const uint32_t head = lp_order(largest);
-    uint32_t tau = lp_nth(head, (k + LP_THREADS / 64 - 1) / (LP_THREADS / 64), lane);
+    uint32_t tau = lp_nth(head, (k + LP_THREADS / 64 - 1) / (LP_THREADS / 64));
     if (lane == 0)
         sh.tau[tid >> 6] = tau;
     if (tid == 0) {
@@ -199,7 +229,7 @@ __device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int 
 #pragma unroll
     for (int w = 0; w < LP_THREADS / 64; ++w)
         tau = sh.tau[w] < tau ? sh.tau[w] : tau;
-    list(head, tau);
+    lp_list<TI, E>(z, v0, n, head, tau, sh, tid);
     __syncthreads();
     int found = sh.count;
     if (found > LP_MANY) {
@@ -404,55 +434,26 @@ template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THRE
             if (tid < rest)
                 f((float)z[whole * E + tid], v0 + whole * E + tid);
         };
-        // the pieces of the few threads that have any, a few kilobytes that the caches hold, are read again by all
-        auto list = [&](uint32_t head, uint32_t least) {
-            if (head >= least)
-                sh.cand_threads[atomicAdd(&sh.n_threads, 1)] = tid;
-            __syncthreads();
-            const int each = (whole + LP_THREADS - 1) / LP_THREADS, nt = sh.n_threads;
-            if (nt > LP_MANY) {  // at least so many logits reach it
-                if (tid == 0)
-                    sh.count = nt;
-                return;
-            }
-            for (int i = tid; i < nt * (each + 1); i += LP_THREADS) {
-                const int of = sh.cand_threads[i / (each + 1)], j = i % (each + 1);
-                if (j < each) {
-                    const int at = (j * LP_THREADS + of) * E;
-                    if (at + E <= n) {
-                        RowPiece<TI, E> x;
-                        x.load(z + at);
-#pragma unroll
-                        for (int e = 0; e < E; ++e)
-                            if (lp_order(x.at(e)) >= least)
-                                lp_offer(sh, x.at(e), v0 + at + e);
-                    }
-                } else if (of < rest) {
-                    const float x = (float)z[whole * E + of];
-                    if (lp_order(x) >= least)
-                        lp_offer(sh, x, v0 + whole * E + of);
-                }
-            }
-        };
         if (p.segs == 1) {
             const LpRow row(st);
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) {
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
                 p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
                 p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
             });
         } else {
             uint64_t *keys = p.keys + (t * p.segs + s) * p.k;
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
         }
     }
 }
 
-// One workgroup a segment of at most LP_SEG logits: few rows, where the time is that
-// of one trip to memory and what follows.  The pieces are all requested at once; the
-// segment's maximum comes before its exponentials, so that no sum is scaled.
+// One workgroup a row or a segment of at most LP_ONCE pieces a thread: short rows,
+// and few rows, where the time is that of one trip to memory and what follows.  The
+// pieces are all requested at once; the segment's maximum comes before its
+// exponentials, so that no sum is scaled.
 template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_segment_kernel(LpArgs p)
 {
-    constexpr int E = Elt<TI>::PER_CHUNK, U = LP_SEG / LP_THREADS / E, NW = LP_THREADS / 64;
+    constexpr int E = Elt<TI>::PER_CHUNK, U = LP_ONCE, NW = LP_THREADS / 64;
     __shared__ float tops[NW];
     __shared__ LpState waves[NW];
     __shared__ __attribute__((aligned(16))) char top_mem[TOP ? sizeof(LpTop) : 16];
@@ -522,46 +523,15 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
             if (tid < rest)
                 f(last, v0 + whole * E + tid);
         };
-        // they are in registers: a wave counts them, takes places for them, and writes them (an atomic a logit: 2 us)
-        auto list = [&](uint32_t, uint32_t least) {
-            const float x0 = lp_key_value((uint64_t)least << 32);
-            int count = 0;
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    count += __popcll(__ballot(tid + u * LP_THREADS < whole && v[u].at(e) >= x0));
-            const uint64_t end = __ballot(tid < rest && last >= x0);
-            count += __popcll(end);
-            int at = 0;
-            if (lane == 0)
-                at = atomicAdd(&sh.count, count);
-            at = __builtin_amdgcn_readfirstlane(at);
-            auto place = [&](uint64_t hits, float x, int index) {
-                if (hits == 0)
-                    return;
-                const int to = at + __builtin_amdgcn_mbcnt_hi((uint32_t)(hits >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)hits, 0));
-                if ((hits >> lane & 1) && to < LP_CAND)
-                    sh.cand[to] = lp_key(x, index);
-                at += __popcll(hits);
-            };
-#pragma unroll
-            for (int u = 0; u < U; ++u)
-#pragma unroll
-                for (int e = 0; e < E; ++e)
-                    place(__ballot(tid + u * LP_THREADS < whole && v[u].at(e) >= x0), v[u].at(e),
-                          v0 + (tid + u * LP_THREADS) * E + e);
-            place(end, last, v0 + whole * E + tid);
-        };
         if (p.segs == 1) {
             const LpRow row(st);
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) {
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
                 p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
                 p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
             });
         } else {
             uint64_t *keys = p.keys + (t * p.segs + s) * p.k;
-            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, list, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
+            lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) { keys[r] = key; });
         }
     }
 }
@@ -622,7 +592,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
         }
         const uint32_t entry = (uint32_t)(entry_key >> 32);
         // (an order of 0 is no key's: one below all of them where a list is shorter than j)
-        const uint64_t bound = (uint64_t)lp_nth(entry, r, lane) << 32 | 1;
+        const uint64_t bound = (uint64_t)lp_nth(entry, r) << 32 | 1;
         __syncthreads();
         auto list = [&](uint64_t least) {
             auto offer = [&](uint64_t key) {
@@ -641,7 +611,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
             const uint32_t order = (uint32_t)(bound >> 32);
             const int above = __popcll(__ballot(on && entry > order));
             const uint32_t low = on && entry == order ? (uint32_t)entry_key : 0;
-            const uint64_t exact = (uint64_t)order << 32 | lp_nth(low, r - above, lane);
+            const uint64_t exact = (uint64_t)order << 32 | lp_nth(low, r - above);
             __syncthreads();
             if (tid == 0)
                 count = 0;
@@ -771,7 +741,7 @@ hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
     auto run = [&](auto type, auto top) {
         using TI = decltype(type);
         constexpr bool TOP = decltype(top)::value;
-        if (p.seg <= LP_SEG)
+        if (p.seg <= LP_THREADS * LP_ONCE * Elt<TI>::PER_CHUNK)
             logprob_segment_kernel<TI, TOP><<<grid, block, 0, s>>>(p);
         else if (!TOP && (int64_t)p.T * p.V * (int64_t)sizeof(TI) > ((int64_t)256 << 20))
             logprob_kernel<TI, TOP, true><<<grid, block, 0, s>>>(p);
