@@ -79,7 +79,7 @@ def _check_backward(tw, z, targets, scale=1.0, entropy=True, logp=True, in_place
 
 
 # widths around the pieces of 4 and 8, the workgroup's 256 threads, segments of 4096 and rows of 48 KB, which few rows are not cut below
-WIDTHS = [1, 2, 3, 4, 5, 7, 8, 9, 63, 255, 257, 1000, 2047, 2048, 2049, 4096, 4097, 8191, 8200, 12288, 12289, 20001, 24576, 24577, 50001]
+WIDTHS = [1, 2, 3, 4, 5, 7, 8, 9, 63, 255, 257, 500, 537, 944, 1000, 2047, 2048, 2049, 4096, 4097, 8191, 8200, 12288, 12289, 20001, 24576, 24577, 50001]
 
 
 @pytest.mark.parametrize("V", WIDTHS)

@@ -205,8 +205,10 @@ __device__ __forceinline__ void lp_list(const TI *z, int v0, int n, uint32_t hea
 // emit(rank, key); emit(rank, 0) where there are fewer.  `largest`: the largest of
 // those that this thread has read: pieces tid, tid + 256, ... of E elements, and
 // element tid of the rest; own(f) calls f(logit, index) for each of them.  In each
-// of the 4 waves k / 4 threads have a largest that reaches the (k / 4)-th largest of
-// the wave's: the lowest of these four values is a bound that k logits reach.  Only
+// of the N waves whose threads all have logits, k / N threads have a largest that
+// reaches the (k / N)-th largest of the wave's: the lowest of these values is a bound
+// that k logits reach (a row too short for one such wave has its first wave's k-th,
+// or none).  Only
 // threads whose largest reaches it have any that do; the logits that reach it are
 // ranked by comparing each with each.  Where many do (equal logits in bulk), those
 // above the bound are listed, and then as many of the equal ones as are wanted, the
@@ -218,7 +220,12 @@ __device__ __forceinline__ void lp_alternatives(const TI *z, int v0, int n, int 
 {
     const int whole = n / E, rest = n - whole * E, lane = tid & 63, each = (whole + LP_THREADS - 1) / LP_THREADS;
     const uint32_t head = lp_order(largest);
-    uint32_t tau = lp_nth(head, (k + LP_THREADS / 64 - 1) / (LP_THREADS / 64));
+    const int have = whole > rest ? whole : rest, full = have < LP_THREADS ? have / 64 : LP_THREADS / 64;
+    uint32_t tau = 0xFFFFFFFFu;
+    if ((tid >> 6) < full)
+        tau = lp_nth(head, (k + full - 1) / full);
+    else if (full == 0 && tid < 64)
+        tau = k <= have ? lp_nth(head, k) : lp_order(-INFINITY);
     if (lane == 0)
         sh.tau[tid >> 6] = tau;
     if (tid == 0) {
@@ -611,7 +618,12 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
             const uint32_t order = (uint32_t)(bound >> 32);
             const int above = __popcll(__ballot(on && entry > order));
             const uint32_t low = on && entry == order ? (uint32_t)entry_key : 0;
-            const uint64_t exact = (uint64_t)order << 32 | lp_nth(low, r - above);
+            uint64_t exact = (uint64_t)order << 32 | lp_nth(low, r - above);
+            // and a list's last entry is a bound that it reaches by itself
+            const uint64_t end = on ? keys[lane * p.k + p.k - 1] : 0;
+            const uint32_t high = lp_nth((uint32_t)(end >> 32), 1);
+            const uint64_t last = (uint64_t)high << 32 | lp_nth((uint32_t)(end >> 32) == high ? (uint32_t)end : 0, 1);
+            exact = last > exact ? last : exact;
             __syncthreads();
             if (tid == 0)
                 count = 0;
