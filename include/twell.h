@@ -463,10 +463,16 @@ TWELL_API int twell_act_unpack(const twell_packed_t *from, int32_t T, int32_t d,
 /* twell_glu_forward in bf16 (same sizes and types) that keeps g and u, before
  * they are rounded to bf16, in 8 bits ([T][F], codes 16-byte aligned); h is the
  * same.  An fp32 layer packs what twell_glu_forward stores.
+ * keep_sign 1 : values of g above 0 keep at least code 1 (off by up to a step in
+ * the place of half of one).  For TWELL_ACT_RELU, whose slope is that of the sign:
+ * a g below half a step reads back as 0 otherwise, and its gradient is lost (of a
+ * Gaussian g's 2-norm 6 to 9%; the smooth activations' gradients move by 0.7%
+ * either way, ReLU's with it too).
  * workspace : >= twell_glu_packed_workspace_bytes(T, d, F), otherwise as there. */
 TWELL_API int twell_glu_forward_packed(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d,
                                        int32_t F, int32_t act, void *h, const twell_packed_t *g,
-                                       const twell_packed_t *u, void *workspace, size_t workspace_bytes, void *stream);
+                                       const twell_packed_t *u, int32_t keep_sign, void *workspace,
+                                       size_t workspace_bytes, void *stream);
 TWELL_API size_t twell_glu_packed_workspace_bytes(int32_t T, int32_t d, int32_t F);
 
 /* twell_glu_backward in bf16 from the values that g's and u's codes stand for.

@@ -137,7 +137,7 @@ def test_glu_packed():
     assert big > 0
 
     def f(x=GOOD, wg=GOOD, wu=GOOD, T=128, d=4096, F=64, act=1, h=GOOD, g=_pk(), u=_pk(), ws=GOOD, n=big):
-        return lib.twell_glu_forward_packed(x, wg, wu, T, d, F, act, h, g, u, ws, n, None)
+        return lib.twell_glu_forward_packed(x, wg, wu, T, d, F, act, h, g, u, 1, ws, n, None)
 
     for k in ("x", "wg", "wu", "h"):
         assert f(**{k: None}) == NULL and f(**{k: GOOD + 8}) == ALIGN, k

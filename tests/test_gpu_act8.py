@@ -193,6 +193,33 @@ def test_h_is_the_gated_product_s(gpu_lib, T, d, F):
     assert torch.equal(_forward(gpu_lib, x, wg, wu, "gelu")[0], h)
 
 
+@pytest.mark.parametrize("T,d,F", [(100, 128, 192), (300, 256, 512), (128, 4096, 512), (1003, 1024, 4096), (8192, 512, 1024)])
+def test_glu_packed_keeps_the_sign(gpu_lib, T, d, F):
+    """keep_sign: the codes of g that are 0 for a g above 0 are 1, all others, u and h as without; and ReLU's gradients
+    are as far from those of the exact g and u as the others' roundings: half a step is 2^-8 of a block's largest, about
+    2^-6.5 of its typical value, and bf16's 2^-8 enter twice: 2% of the 2-norm are allowed."""
+    import torch
+    say(f"case glu packed keep_sign {T} {d} {F}")
+    x, wg, wu = _inputs(T, d, F)
+    plain = _forward(gpu_lib, x, wg, wu, "relu")
+    h, (g, *_), (u, *_) = _nan(T, F), _packed(gpu_lib, T, F), _packed(gpu_lib, T, F)
+    gpu_lib.twell_glu_forward_packed(x, wg, wu, "relu", h, g, u, gpu_lib.glu_packed_workspace(T, d, F), keep_sign=True)
+    for a, b in ((h, plain[0]), (u.code, plain[2].code), (u.scale, plain[2].scale), (g.scale, plain[1].scale)):
+        assert torch.equal(a, b)
+    exact, bound = dense_ref.glu_forward(x, wg, wu, "relu")["g"]
+    sure = exact.abs() > bound
+    raised = (plain[1].code == 0) & (exact > 0)
+    want = torch.where(raised, torch.ones_like(g.code), plain[1].code)
+    assert torch.equal(g.code[sure], want[sure]) and raised.any()
+    dh = _rnd(T, F, seed=3)
+    got = _nan(T, d), _nan(F, d), _nan(F, d)
+    gpu_lib.twell_glu_backward_packed(x, wg, wu, g, u, dh, "relu", *got, gpu_lib.glu_backward_workspace(T, d, F, torch.bfloat16))
+    uv, xd = x.double() @ wu.double().T, x.double()
+    dg, du = dh.double() * uv * (exact > 0), dh.double() * exact.clamp_min(0)
+    for a, b in zip(got, (dg @ wg.double() + du @ wu.double(), dg.T @ xd, du.T @ xd)):
+        assert float((a.double() - b).norm() / b.norm()) < 0.02
+
+
 def test_glu_packed_bad_rows(gpu_lib):
     """NaN and infinities in x spoil the kept values of their own rows only."""
     import torch

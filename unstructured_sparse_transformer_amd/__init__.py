@@ -154,7 +154,7 @@ def load(path: str = LIB_PATH):
     F32, I64, SIZE, PK = ctypes.c_float, ctypes.c_int64, ctypes.c_size_t, ctypes.POINTER(TwellPackedT)
     lib.twell_act_pack.argtypes = [P, I32, I32, I32, PK, P]
     lib.twell_act_unpack.argtypes = [PK, I32, I32, I32, P, P]
-    lib.twell_glu_forward_packed.argtypes = [P, P, P, I32, I32, I32, I32, P, PK, PK, P, SIZE, P]
+    lib.twell_glu_forward_packed.argtypes = [P, P, P, I32, I32, I32, I32, P, PK, PK, I32, P, SIZE, P]
     lib.twell_glu_backward_packed.argtypes = [P, P, P, PK, PK, P, I32, I32, I32, I32, P, P, P, P, P, SIZE, P]
     lib.twell_embed_forward.argtypes = [P, I32, I32, P, I32, I32, I32, F32, P, I32, P]
     lib.twell_embed_backward.argtypes = [P, I32, I32, P, I32, I32, I32, F32, I32, P, I32, P, SIZE, P]
@@ -631,15 +631,17 @@ def glu_packed_workspace(T: int, d: int, F: int, device="cuda"):
     return torch.empty(n, dtype=torch.uint8, device=device) if n else None
 
 
-def twell_glu_forward_packed(x, wg_t, wu_t, act: str, h, g: PackedAct, u: PackedAct, workspace=None, stream=None):
-    """twell_glu_forward in bfloat16, with g and u kept in 8 bits."""
+def twell_glu_forward_packed(x, wg_t, wu_t, act: str, h, g: PackedAct, u: PackedAct, workspace=None, keep_sign: bool = False,
+                             stream=None):
+    """twell_glu_forward in bfloat16, with g and u kept in 8 bits; keep_sign: positive values of g keep at least code 1,
+    for relu, whose gradient where g is small is lost otherwise (see include/twell.h)."""
     import torch
     fn = "twell_glu_forward_packed"
     dev, (T, d), F = _device(fn, x), x.shape, wg_t.shape[0]
     p = [_tensor(fn, k, t, s, dev, torch.bfloat16) for k, t, s in (("x", x, (T, d)), ("wg_t", wg_t, (F, d)),
                                                                    ("wu_t", wu_t, (F, d)), ("h", h, (T, F)))]
     kept = [_packed(fn, k, t, (T, F), dev) for k, t in (("g", g), ("u", u))]
-    _check(fn, load().twell_glu_forward_packed(*p[:3], _i32(T), _i32(d), _i32(F), _act(fn, act), p[3], *kept,
+    _check(fn, load().twell_glu_forward_packed(*p[:3], _i32(T), _i32(d), _i32(F), _act(fn, act), p[3], *kept, int(bool(keep_sign)),
                                                *_workspace(fn, workspace, dev), _stream(stream, dev)))
 
 

@@ -48,19 +48,27 @@ struct A8Scale {
     }
 };
 
-// The codes of 4 values, one a byte: round to nearest even, by an addition whose
-// result has the whole number in its lowest bits.  The product is rounded by itself
-// first, so that a code does not depend on whether a compiler fuses the two; FUSED:
-// in one operation (values that no other operation has in these 32 bits).
-template <bool FUSED = false> __device__ __forceinline__ uint32_t a8_whole(float v, float inv)
+// How a value becomes a code: the product with 1 / step rounded by itself first, so
+// that a code does not depend on whether a compiler fuses the two; in one operation
+// (values that no other operation has in these 32 bits); or so, and values above 0 at
+// least 1.
+enum A8Round { A8_TWICE, A8_FUSED, A8_SIGN };
+
+// A value's code in the lowest byte: round to nearest even, by an addition whose
+// result has the whole number in its lowest bits.
+template <A8Round R> __device__ __forceinline__ uint32_t a8_whole(float v, float inv)
 {
 #pragma clang fp contract(off)
     constexpr float WHOLE = 12582912.f;  // 1.5 2^23
-    return __float_as_uint(FUSED ? __builtin_fmaf(v, inv, WHOLE) : v * inv + WHOLE);
+    const float w = R == A8_TWICE ? v * inv + WHOLE : __builtin_fmaf(v, inv, WHOLE);
+    const float up = R == A8_SIGN && v > 0.f ? WHOLE + 1.f : w;
+    return __float_as_uint(w > up ? w : up);
 }
-template <bool FUSED = false> __device__ __forceinline__ uint32_t a8_codes(float a, float b, float c, float d, float inv)
+
+// The codes of 4 values, one a byte.
+template <A8Round R = A8_TWICE> __device__ __forceinline__ uint32_t a8_codes(float a, float b, float c, float d, float inv)
 {
-    const uint32_t x = a8_whole<FUSED>(a, inv), y = a8_whole<FUSED>(b, inv), z = a8_whole<FUSED>(c, inv), w = a8_whole<FUSED>(d, inv);
+    const uint32_t x = a8_whole<R>(a, inv), y = a8_whole<R>(b, inv), z = a8_whole<R>(c, inv), w = a8_whole<R>(d, inv);
     return __builtin_amdgcn_perm(__builtin_amdgcn_perm(w, z, 0x0C0C0400u), __builtin_amdgcn_perm(y, x, 0x0C0C0400u), 0x05040100u);
 }
 

@@ -4,7 +4,8 @@
 //   scale = max |x| / 127 over 32 consecutive elements of a row, in bf16, rounded up
 //   code = round(x / scale) in 8 bits,  value = code * scale
 // Linear codes: what a gradient needs of an activation is its absolute error (act
-// and act' are smooth), which is at most half a step, 0.4% of the block's largest;
+// and act' are smooth; ReLU's slope needs its sign, see glu.hip), which is at most
+// half a step, 0.4% of the block's largest;
 // a floating 8-bit code of 3 bits of mantissa is off by up to 6% of the value
 // itself.  Bound by memory: 3.06 bytes an element of bf16 either way
 // (8192 x 8192: packed in 39 us, 5.3 TB/s; unpacked, from caches in part, in 31 us).

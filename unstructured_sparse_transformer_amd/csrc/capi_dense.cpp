@@ -219,8 +219,8 @@ size_t twell_glu_packed_workspace_bytes(int32_t T, int32_t d, int32_t F)
 }
 
 int twell_glu_forward_packed(const void *x, const void *wg_t, const void *wu_t, int32_t T, int32_t d, int32_t F,
-                             int32_t act, void *h, const twell_packed_t *g, const twell_packed_t *u, void *workspace,
-                             size_t workspace_bytes, void *stream)
+                             int32_t act, void *h, const twell_packed_t *g, const twell_packed_t *u, int32_t keep_sign,
+                             void *workspace, size_t workspace_bytes, void *stream)
 {
     TWELL_TRY(check_glu(T, d, F, TWELL_BF16, act));
     if (T == 0)
@@ -241,6 +241,7 @@ int twell_glu_forward_packed(const void *x, const void *wg_t, const void *wu_t, 
     a.h = h;
     a.g8 = packed8(g);
     a.u8 = packed8(u);
+    a.keep_sign = keep_sign != 0;
     a.part = static_cast<float *>(workspace);
     return hip_status(twell::launch_glu(TWELL_BF16, a, static_cast<hipStream_t>(stream)));
 }

@@ -20,6 +20,7 @@ struct GluFwd {
     const void *x, *wg, *wu;
     void *h, *g, *u;  // g, u may be NULL
     Packed8 g8, u8;   // g and u in 8 bits instead (code NULL: not wanted), bf16 only
+    int keep_sign;    // g's positive values keep at least code 1
     float *part;      // [splits][g | u][T][F] partial sums
     int splits;       // of K, when the tiles alone leave CUs idle
 };

@@ -375,10 +375,10 @@ template <typename TI> __device__ __forceinline__ bool lp_target(const LpArgs &p
 }
 
 // One workgroup a row, or a segment of a row that is longer than LP_SEG.
-// Bound by memory: 4096 x 131072 bf16 take 185 us (5.8 TB/s), with or without the
+// Bound by memory: 4096 x 131072 bf16 take 168 us (6.4 TB/s), with or without the
 // entropy's operations.  ONCE: more than the caches behind the L2s hold, read past
 // them (190 us through them; workgroups that start at different places of their
-// rows 195 us, segments of 4096 222 us).
+// rows 3% more, segments of 4096 a sixth more).
 template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THREADS) void logprob_kernel(LpArgs p)
 {
     constexpr int E = Elt<TI>::PER_CHUNK, U = 4;
@@ -457,7 +457,8 @@ template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THRE
 // One workgroup a row or a segment of at most LP_ONCE pieces a thread: short rows,
 // and few rows, where the time is that of one trip to memory and what follows.  The
 // pieces are all requested at once; the segment's maximum comes before its
-// exponentials, so that no sum is scaled.
+// exponentials, so that no sum is scaled.  32 segments of 4096 bf16 take 3 us, with
+// 20 alternatives 7: the bound, the candidates' second read and their ranks.
 template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_segment_kernel(LpArgs p)
 {
     constexpr int E = Elt<TI>::PER_CHUNK, U = LP_ONCE, NW = LP_THREADS / 64;
@@ -546,7 +547,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
 // The segments of a row joined: a lane a segment, in every wave.  The k best of
 // their sorted lists: where r lists' entries number j reach a bound, r j keys do; the
 // r-th largest of these entries, with r j >= k, is one, and the few keys that reach
-// it are ranked.
+// it are ranked.  2 us, with 20 alternatives 4.
 template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_join_kernel(LpArgs p)
 {
     constexpr int MOST = LP_MOST_TOP * LP_MOST_SEGS;
@@ -639,7 +640,8 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
 
 // ------------------------------------------------------------------ backward
 // One workgroup a chunk of a row.  Every thread has read all of its elements
-// before it writes them: dlogits may be logits.
+// before it writes them: dlogits may be logits.  Bound by memory: 4096 x 131072 bf16
+// with the entropy's gradient 360 us (5.9 TB/s).
 constexpr int LP_BACK_U = 4;
 template <typename TI> __global__ __launch_bounds__(LP_THREADS) void logprob_backward_kernel(LpArgs p)
 {
