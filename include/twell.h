@@ -454,7 +454,7 @@ typedef struct twell_packed_t {
 } twell_packed_t;
 
 /* x, out : device [T][d] vdtype, aligned as their elements; T <= 2^30,
- * d <= 2^20. */
+ * d <= 2^20, and T ceil(d / 32) below 2^31 - 2^7 (TWELL_F32: 2^30 - 2^6). */
 TWELL_API int twell_act_pack(const void *x, int32_t T, int32_t d, int32_t vdtype, const twell_packed_t *to,
                              void *stream);
 TWELL_API int twell_act_unpack(const twell_packed_t *from, int32_t T, int32_t d, int32_t vdtype, void *out,
@@ -544,7 +544,8 @@ TWELL_API int twell_block_norm_backward(const twell_block_norm_t *bn, const void
  * ids : device [T] of int32 or int64 (id_bits 32 or 64).  An id outside 0 .. V-1
  * (padding) gives a row of zeros, and adds to no gradient.
  * table [V][d] vdtype, out [T][d] odtype: TWELL_BF16 or TWELL_F32 each, aligned as
- * their elements.  T, V <= 2^30, d <= 2^20, T d < 2^41. */
+ * their elements.  T, V <= 2^30, d <= 2^20, and T ceil(d / 4) (d < 4: T d) below
+ * 2^34 - 2^10. */
 TWELL_API int twell_embed_forward(const void *ids, int32_t id_bits, int32_t T, const void *table, int32_t V, int32_t d,
                                   int32_t vdtype, float scale, void *out, int32_t odtype, void *stream);
 
@@ -562,7 +563,7 @@ TWELL_API size_t twell_embed_workspace_bytes(int32_t T, int32_t V, int32_t d);
 
 /* ---- Log probabilities -----------------------------------------------------
  * From logits z [T][V] (vdtype, rows `ld` >= V elements apart, aligned as their
- * elements) times scale > 0 (an inverse temperature), for each row:
+ * elements; T, V <= 2^30, T ceil(V / 2048) < 2^31) times scale > 0 (an inverse temperature), for each row:
  *   norm     [T][2] float: m = the largest logit, and L = log sum exp(scale (z - m))
  *   logp     [T] float: of the token targets[t], scale (z - m) - L.  targets :
  *            device int32 or int64 [T] (id_bits); one outside 0 .. V-1 has logp 0

@@ -129,6 +129,17 @@ def test_act_pack():
             assert f(**kw) == SHAPE, kw
 
 
+def test_threads_of_a_launch():
+    """Sizes whose threads pass what a launch counts in 32 bits are refused on the host."""
+    lib = tw.load()
+    for T, d in ((BIG, 64), (BIG, 61), (1 << 24, 1 << 12)):
+        assert lib.twell_embed_forward(GOOD, 64, T, GOOD, 10, d, 1, 1.0, GOOD, 1, None) == SHAPE, (T, d)
+        assert lib.twell_embed_workspace_bytes(T, 10, d) == 0, (T, d)
+    for T, d, vd in ((BIG, 1, 0), (BIG, 33, 1), (1 << 20, 1 << 15, 0), (1 << 20, 1 << 16, 1)):
+        assert lib.twell_act_pack(GOOD, T, d, vd, _pk(), None) == SHAPE, (T, d, vd)
+        assert lib.twell_act_unpack(_pk(), T, d, vd, GOOD, None) == SHAPE, (T, d, vd)
+
+
 def test_glu_packed():
     lib = tw.load()
     size = lib.twell_glu_packed_workspace_bytes

@@ -289,6 +289,30 @@ def test_rows_past_32_bits(gpu_lib):
     assert float(z[T - 1, V - 9]) < -0.2 and float(z[T - 1, V - 5]) > 0.2
 
 
+@pytest.mark.parametrize("dtype,bits", [("bfloat16", "int32"), ("float32", "int64")])
+def test_more_rows_than_a_launch_has(gpu_lib, dtype, bits):
+    """2^24 + 3 short rows: a workgroup of 256 threads each passes what a launch counts in 32 bits."""
+    import torch
+    T, V = (1 << 24) + 3, 3
+    say(f"case logprob, {T} rows of {V} {dtype}")
+    z, t = _logits(T, V, dtype, ld=4), _targets(T, V, bits)
+    got, idx = _forward(gpu_lib, z, t, 0.5, 2)
+    dz = torch.full((T, V), NAN, dtype=z.dtype, device="cuda")
+    gpu_lib.twell_logprob_backward(z, t, got["norm"], got["logp"], dz, scale=0.5, entropy=got["entropy"],
+                                   dentropy=got["entropy"])
+    for some in (slice(0, 1000), slice(T - 1003, T)):
+        want, order = tokens_ref.logprob_forward(z[some], t[some], 0.5, 2)
+        for name in got:
+            tokens_ref.check(got[name][some], *want[name], name)
+        assert torch.equal(idx[some].long(), order), "top_idx"
+        one = {name: x[some].contiguous() for name, x in got.items()}
+        part = torch.empty_like(dz[some])
+        gpu_lib.twell_logprob_backward(z[some], t[some].contiguous(), one["norm"], one["logp"], part, scale=0.5,
+                                       entropy=one["entropy"], dentropy=one["entropy"])
+        assert torch.equal(dz[some], part), "dlogits"
+    assert bool((got["entropy"] < 1.1).all()) and not bool(dz.isnan().any())  # (ln 3 at most): every row is written
+
+
 @pytest.mark.parametrize("T,V", [(1, 40000), (60, 9000), (1200, 3001)])
 def test_same_bits_graph_and_streams(gpu_lib, T, V):
     """Repeated calls, a workspace for more rows, another stream and a captured graph's replays, the gradient in place

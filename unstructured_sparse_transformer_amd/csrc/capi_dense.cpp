@@ -39,14 +39,15 @@ int check_packed(const twell_packed_t *p, size_t code_align)
 
 twell::Packed8 packed8(const twell_packed_t *p) { return twell::Packed8{p->code, static_cast<uint16_t *>(p->scale)}; }
 
-// Sizes of rows that are packed: a launch's workgroups of 256 pieces of 4 elements fit a grid.
+// Sizes of rows that are packed: the threads, of 2 pieces of 16 bytes each, are counted in 32 bits.
 int check_act(int32_t T, int32_t d, int32_t vdtype)
 {
     if (!known_dtype(vdtype))
         return TWELL_E_UNSUPPORTED;
     if (T < 0 || T > MOST_ROWS || d < 1 || d > (1 << 20))
         return TWELL_E_SHAPE;
-    return (int64_t)T * twell::a8_blocks(d) * 8 / 256 < ((int64_t)1 << 31) - 1 ? TWELL_OK : TWELL_E_SHAPE;
+    const int64_t pieces = T * twell::a8_blocks(d) * (vdtype == TWELL_BF16 ? 4 : 8);
+    return pieces <= (((int64_t)1 << 24) - 1) * 512 ? TWELL_OK : TWELL_E_SHAPE;
 }
 
 // The descriptor of the block norms, and with `gated` its gate pointer.

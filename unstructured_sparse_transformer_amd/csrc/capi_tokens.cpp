@@ -17,15 +17,16 @@ constexpr int32_t MOST_TOKENS = 1 << 30;  // of a vocabulary: keys up to V, and 
 
 int check_ids(const void *ids, int32_t id_bits) { return check_vec(ids, id_bits / 8); }
 
-// Sizes of the embedding calls: a launch's workgroups of 256 pieces of 4 columns (below 4: of one) fit a grid.
+// Sizes of the embedding calls: the lookup's threads, of 4 pieces of 4 columns each (below 4: of one), are counted in 32
+// bits.
 int check_embed(int32_t T, int32_t V, int32_t d)
 {
     if (T < 0 || T > MOST_ROWS || V < 1 || V > MOST_TOKENS || d < 1 || d > (1 << 20))
         return TWELL_E_SHAPE;
-    return (int64_t)T * (d < 4 ? d : (d + 3) / 4) / 256 < ((int64_t)1 << 31) - 1 ? TWELL_OK : TWELL_E_SHAPE;
+    return (int64_t)T * (d < 4 ? d : (d + 3) / 4) <= (((int64_t)1 << 24) - 1) * 1024 ? TWELL_OK : TWELL_E_SHAPE;
 }
 
-// Sizes of the log probabilities: a launch's workgroups of 2048 logits fit a grid.
+// Sizes of the log probabilities: rows times pieces of 2048 logits stay below 2^31.
 int check_logprob(int32_t T, int32_t V, int32_t k)
 {
     if (T < 0 || T > MOST_ROWS || V < 1 || V > MOST_TOKENS || k < 0 || k > V)

@@ -742,11 +742,40 @@ size_t lp_most_workspace(int T, int V, int k)
     return bytes_of(a < b ? a : b, k);
 }
 
-hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
+// A launch's threads are counted in 32 bits: workgroups that it has at most.  More rows take further launches.
+constexpr int64_t LP_GRID = ((int64_t)1 << 32) / LP_THREADS - 1;
+
+// The call's rows from t0 on, at most `most`.
+static LpArgs lp_rows(const LpArgs &a, int64_t t0, int64_t most)
 {
-    LpArgs p = args;
-    p.scale2 = p.scale * LP_LOG2E;
-    lp_segments(p.T, p.V, p.bf16, p.segs, p.seg);
+    const int es = a.bf16 ? 2 : 4;
+    LpArgs p = a;
+    auto on = [&](auto &q, int64_t step) {
+        if (q)
+            q += t0 * step;
+    };
+    auto bytes_on = [&](auto &q, int64_t step) {
+        if (q)
+            q = (std::remove_reference_t<decltype(q)>)((uintptr_t)q + t0 * step);
+    };
+    p.T = (int)(a.T - t0 < most ? a.T - t0 : most);
+    bytes_on(p.logits, a.ld * es);
+    bytes_on(p.dlogits, a.ldd * es);
+    bytes_on(p.targets, a.id64 ? 8 : 4);
+    on(p.logp, 1);
+    on(p.norm, 2);
+    on(p.entropy, 1);
+    on(p.top_logp, a.k);
+    on(p.top_idx, a.k);
+    on(p.norm_in, 2);
+    on(p.entropy_in, 1);
+    on(p.dlogp, 1);
+    on(p.dentropy, 1);
+    return p;
+}
+
+static hipError_t run_logprob(LpArgs p, void *ws, hipStream_t s)
+{
     if (p.segs > 1) {
         p.keys = (uint64_t *)ws;
         p.part = (LpState *)(p.keys + (int64_t)p.T * p.segs * p.k);
@@ -779,18 +808,38 @@ hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
     return hipGetLastError();
 }
 
-hipError_t launch_logprob_backward(const LpArgs &args, hipStream_t s)
+hipError_t launch_logprob(const LpArgs &args, void *ws, hipStream_t s)
 {
     LpArgs p = args;
     p.scale2 = p.scale * LP_LOG2E;
-    p.seg = LP_THREADS * LP_BACK_U * (p.bf16 ? 8 : 4);
-    p.segs = (int)ceil_div(p.V, p.seg);
-    const dim3 grid((unsigned)((int64_t)p.T * p.segs)), block(LP_THREADS);
-    if (p.bf16)
-        logprob_backward_kernel<__bf16><<<grid, block, 0, s>>>(p);
-    else
-        logprob_backward_kernel<float><<<grid, block, 0, s>>>(p);
-    return hipGetLastError();
+    lp_segments(p.T, p.V, p.bf16, p.segs, p.seg);
+    for (int64_t t0 = 0; t0 < p.T; t0 += LP_GRID) {  // (rows in segments are fewer than LP_WGS)
+        const hipError_t e = run_logprob(lp_rows(p, t0, LP_GRID), ws, s);
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
+}
+
+hipError_t launch_logprob_backward(const LpArgs &args, hipStream_t s)
+{
+    LpArgs all = args;
+    all.scale2 = all.scale * LP_LOG2E;
+    all.seg = LP_THREADS * LP_BACK_U * (all.bf16 ? 8 : 4);
+    all.segs = (int)ceil_div(all.V, all.seg);
+    const int64_t most = LP_GRID / all.segs;
+    for (int64_t t0 = 0; t0 < all.T; t0 += most) {
+        const LpArgs p = lp_rows(all, t0, most);
+        const dim3 grid((unsigned)((int64_t)p.T * p.segs)), block(LP_THREADS);
+        if (p.bf16)
+            logprob_backward_kernel<__bf16><<<grid, block, 0, s>>>(p);
+        else
+            logprob_backward_kernel<float><<<grid, block, 0, s>>>(p);
+        const hipError_t e = hipGetLastError();
+        if (e != hipSuccess)
+            return e;
+    }
+    return hipSuccess;
 }
 
 }  // namespace twell
