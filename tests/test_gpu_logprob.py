@@ -182,6 +182,74 @@ def test_all_in_few_threads(gpu_lib, T, dtype):
         _check_forward(gpu_lib, x, t, 1.0, k)
 
 
+SHORT = [(5, 1), (5, 9), (3, 511), (6, 517), (7, 1027), (5, 1028), (5, 2047), (5, 2055), (5, 2056), (2049, 2050), (2051, 4103), (2050, 4104)]
+
+
+@pytest.mark.parametrize("T,V", SHORT)
+@pytest.mark.parametrize("dtype", TYPES)
+def test_short_rows(gpu_lib, T, V, dtype):
+    """Rows that a wave holds in registers, up to the widths from which on a workgroup takes one; as they are,
+    of few values, masked, and with the largest logits in few lanes."""
+    import torch
+    say(f"case logprob short rows T={T} V={V} {dtype}")
+    E = 8 if dtype == "bfloat16" else 4
+    z, t = _logits(T, V, dtype, seed=V, ld=V + 3), _targets(T, V)
+    lane = torch.arange(V, device="cuda") // E % 64
+    gen = torch.Generator(device="cuda").manual_seed(V)
+    few = torch.randint(0, 3, (T, V), generator=gen, device="cuda").to(z.dtype)
+    some = torch.where(torch.rand((T, V), generator=gen, device="cuda") < 0.98, -INF, z)
+    none = some.clone()
+    none[T // 2] = -INF
+    for k in sorted({0, 1, min(V, 20), min(V, 24), min(V, 25), min(V, 64)}):
+        _check_forward(gpu_lib, z, t, 0.7, k)
+        if k:
+            _check_forward(gpu_lib, few, t, 1.0, k)
+            _check_forward(gpu_lib, torch.full_like(few, -2), t, 1.0, k)
+            _check_forward(gpu_lib, some, t, 1.0, k)
+            _check_forward(gpu_lib, none, t, 1.0, k)
+            for lanes in (1, 5, 18):
+                _check_forward(gpu_lib, torch.where(lane < lanes, z * 0.25 + 40, z), t, 1.0, k)
+                _check_forward(gpu_lib, torch.where(lane < lanes, torch.round(z) + 40, few), t, 1.0, k)
+    _check_backward(gpu_lib, z, t, 0.7)
+
+
+@pytest.mark.parametrize("bad", [NAN, -NAN, INF])
+@pytest.mark.parametrize("T,V", [(6, 700), (2049, 4099)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_nan_in_short_rows(gpu_lib, bad, T, V, dtype):
+    """They spoil their own row, and no other that the same workgroup has."""
+    import torch
+    k = 6
+    say(f"case logprob bad {bad} T={T} V={V} {dtype}")
+    z, t = _logits(T, V, dtype), _targets(T, V).clamp(0, V - 1)
+    clean, order = _forward(gpu_lib, z, t, 1.0, k)
+    for where in (0, V // 2, V - 1):
+        x = z.clone()
+        x[1, where] = bad
+        got, idx = _forward(gpu_lib, x, t, 1.0, k)
+        rest = torch.arange(T, device="cuda") != 1
+        for name, v in got.items():
+            assert torch.isnan(v[1]).all(), name
+            assert torch.equal(v[rest], clean[name][rest]), name
+        assert idx[1].tolist() == list(range(k)) and torch.equal(idx[rest], order[rest])
+
+
+@pytest.mark.parametrize("T,V", [(5, 700), (5, 2055), (2049, 3001), (2047, 3001)])
+@pytest.mark.parametrize("dtype", TYPES)
+def test_same_bits_with_any_alternatives(gpu_lib, T, V, dtype):
+    """A row's sums do not depend on how many alternatives are asked for, nor on the run."""
+    import torch
+    say(f"case logprob bits T={T} V={V} {dtype}")
+    z, t = _logits(T, V, dtype), _targets(T, V)
+    one, _ = _forward(gpu_lib, z, t, 1.0, 0)
+    for k in (0, 1, 20, 64, 64):
+        got, idx = _forward(gpu_lib, z, t, 1.0, k)
+        for name in ("norm", "entropy", "logp"):
+            assert torch.equal(got[name], one[name]), (name, k)
+    again, order = _forward(gpu_lib, z, t, 1.0, 64)
+    assert torch.equal(again["top_logp"], got["top_logp"]) and torch.equal(order, idx)
+
+
 @pytest.mark.parametrize("T,V", [(3, 8209), (3, 30011), (1100, 8209)])
 @pytest.mark.parametrize("dtype", TYPES)
 def test_masked_logits(gpu_lib, T, V, dtype):

@@ -66,11 +66,11 @@ __device__ __forceinline__ uint32_t lp_order(float z)
     return b ^ (b >> 31 ? 0xFFFFFFFFu : 0x80000000u);
 }
 __device__ __forceinline__ uint64_t lp_key(float z, int v) { return (uint64_t)lp_order(z) << 32 | (0xFFFFFFFFu - (uint32_t)v); }
-__device__ __forceinline__ float lp_key_value(uint64_t key)
+__device__ __forceinline__ float lp_value(uint32_t order)
 {
-    const uint32_t o = (uint32_t)(key >> 32);
-    return __uint_as_float(o ^ (o >> 31 ? 0x80000000u : 0xFFFFFFFFu));
+    return __uint_as_float(order ^ (order >> 31 ? 0x80000000u : 0xFFFFFFFFu));
 }
+__device__ __forceinline__ float lp_key_value(uint64_t key) { return lp_value((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int lp_key_index(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
 // The value of a row's results from its whole sums.
@@ -544,6 +544,239 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
     }
 }
 
+// A wave's row of at most U pieces a lane, in registers: f(x, index, there) for every
+// lane's elements, whether the row has them or not, a piece of every lane after another.
+template <typename TI, int E, int U> struct LpLanes {
+    RowPiece<TI, E> v[U];
+    float last;
+    int whole, rest, lane;
+    __device__ __forceinline__ LpLanes(const TI *z, int n, int lane) : last(-INFINITY), whole(n / E), rest(n % E), lane(lane)
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (lane + u * 64 < whole)
+                v[u].load(z + (lane + u * 64) * E);
+        if (lane < rest)
+            last = (float)z[whole * E + lane];
+    }
+    template <typename F> __device__ __forceinline__ void each(F f) const
+    {
+#pragma unroll
+        for (int u = 0; u < U; ++u)
+            if (u * 64 < whole) {
+                const bool there = lane + u * 64 < whole;
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    f(there ? v[u].at(e) : -INFINITY, (lane + u * 64) * E + e, there);
+            }
+        if (rest)
+            f(last, whole * E + lane, lane < rest);
+    }
+    // How many elements pass a test, and the keys of the first `most` of them to a list.
+    template <typename F> __device__ __forceinline__ int count(F test) const
+    {
+        int n = 0;
+        each([&](float x, int, bool there) { n += __popcll(__ballot(there && test(x))); });
+        return n;
+    }
+    template <typename F> __device__ __forceinline__ int list(uint64_t *to, int most, F test) const
+    {
+        int n = 0;
+        each([&](float x, int v, bool there) {
+            const bool hit = there && test(x);
+            const uint64_t hits = __ballot(hit);
+            if (hits) {
+                const int at = n + __popcll(hits & ((1ull << lane) - 1));
+                if (hit && at < most)
+                    to[at] = lp_key(x, v);
+                n += __popcll(hits);
+            }
+        });
+        return n;
+    }
+};
+
+// Orders the wave's writes to LDS and its reads of them.
+__device__ __forceinline__ void lp_wave_fence()
+{
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+}
+
+// The k best of a wave's row to emit(rank, key), best first; `largest`: of a lane's
+// elements.  Of these, or where k is more than LP_WAVE_HEADS of the lanes' pieces, k have a
+// largest that reaches the k-th largest: a bound that k logits reach (of 64 lanes the
+// 64th lets 250 of 2048 pass, of their 256 pieces 80).  What reaches the bound is listed
+// (masked logits only if there are too few others), and each compared with each.  Where
+// that is much more than k (equal logits in bulk, all in few lanes), the k-th largest of
+// all is found: it is the least that reaches the bound, unless k are above that; those
+// are listed in their turn, and if they too are many the k-th is found bit by bit, from the
+// list, or from the row where that is too short.  What is above it is listed, and as many
+// equal to it as are wanted, the lowest indices first.
+constexpr int LP_WAVE_CAND = 512, LP_WAVE_FEW = 96, LP_WAVE_HEADS = 24;
+template <typename TI, int E, int U, typename F>
+__device__ __forceinline__ void lp_wave_alternatives(const LpLanes<TI, E, U> &z, int k, float largest, uint64_t *list, F emit)
+{
+    constexpr int MINE = LP_WAVE_CAND / 64;
+    const int lane = z.lane;
+    const uint32_t lowest = lp_order(-INFINITY);
+    // the largest order that k of many reach, or one below it, down to bit `last`: reach(order) counts them
+    auto nth = [&](int last, auto reach) {
+        uint32_t at = 0;
+        for (int bit = 31; bit >= last; --bit) {
+            const uint32_t up = at | 1u << bit;
+            at = reach(up) >= k ? up : at;
+        }
+        return at < lowest ? lowest : at;
+    };
+    float bound = -INFINITY;
+    if (k <= LP_WAVE_HEADS) {
+        if (k <= (z.whole > z.rest ? z.whole : z.rest))
+            bound = lp_value(lp_nth(lp_order(largest), k));
+    } else if (k <= z.whole) {
+        uint32_t head[U];
+#pragma unroll
+        for (int u = 0; u < U; ++u) {
+            float top = z.v[u].at(0);
+#pragma unroll
+            for (int e = 1; e < E; ++e)
+                top = lp_max(top, z.v[u].at(e));
+            head[u] = lane + u * 64 < z.whole ? lp_order(top) : 0;
+        }
+        bound = lp_value(nth(12, [&](uint32_t least) {
+            int n = 0;
+#pragma unroll
+            for (int u = 0; u < U; ++u)
+                if (u * 64 < z.whole)
+                    n += __popcll(__ballot(head[u] >= least));
+            return n;
+        }));
+    }
+    bound = fmaxf(bound, -__FLT_MAX__);  // (masked ones only if there are no others)
+    int n = z.list(list, LP_WAVE_CAND, [&](float x) { return x >= bound; });
+    lp_wave_fence();
+    float least = -INFINITY;
+    bool exact = n > LP_WAVE_FEW;
+    if (exact) {
+        least = INFINITY;
+        z.each([&](float x, int, bool there) { least = there && x >= bound && x < least ? x : least; });
+#pragma unroll
+        for (int o = 32; o > 0; o >>= 1)
+            least = fminf(least, __shfl_xor(least, o, 64));
+        if (z.count([&](float x) { return x > least; }) >= k) {
+            n = z.list(list, LP_WAVE_CAND, [&](float x) { return x > least; });
+            lp_wave_fence();
+            exact = n > LP_WAVE_FEW;
+            if (n > LP_WAVE_CAND) {
+                least = lp_value(nth(0, [&](uint32_t order) {
+                    const float from = lp_value(order < lowest ? lowest : order);
+                    return z.count([&](float x) { return x >= from; });
+                }));
+            } else if (exact) {
+                uint32_t mine[MINE];
+#pragma unroll
+                for (int q = 0; q < MINE; ++q)
+                    mine[q] = q * 64 + lane < n ? (uint32_t)(list[q * 64 + lane] >> 32) : 0;
+                least = lp_value(nth(0, [&](uint32_t order) {
+                    int reach = 0;
+#pragma unroll
+                    for (int q = 0; q < MINE; ++q)
+                        if (q * 64 < n)
+                            reach += __popcll(__ballot(mine[q] >= order));
+                    return reach;
+                }));
+            }
+        }
+    }
+    if (exact)
+        n = z.list(list, LP_WAVE_CAND, [&](float x) { return x > least; });
+    if (n < k) {
+#pragma unroll
+        for (int u = 0; u <= U; ++u) {
+            if (n >= k)
+                continue;
+            uint32_t same = 0;
+            if (u < U && lane + u * 64 < z.whole)
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    same |= (uint32_t)(z.v[u < U ? u : 0].at(e) == least) << e;
+            if (u == U && lane < z.rest)
+                same = z.last == least;
+            if (!__ballot(same != 0))
+                continue;
+            int total;
+            int to = n + wave_excl_scan(__popc(same), lane, total);
+#pragma unroll
+            for (int e = 0; e < E; ++e)
+                if (same >> e & 1 && to < k)
+                    list[to++] = lp_key(least, (u < U ? (lane + u * 64) * E : z.whole * E + lane) + e);
+            n = n + total < k ? n + total : k;
+        }
+    }
+    lp_wave_fence();
+    static_assert(LP_WAVE_FEW <= 128, "two keys a lane");
+    const uint64_t a = lane < n ? list[lane] : 0, b = 64 + lane < n ? list[64 + lane] : 0;
+    int above_a = a ? 0 : k, above_b = b ? 0 : k;
+    if (n <= 64) {
+#pragma unroll 16
+        for (int j = 0; j < n; ++j)
+            above_a += list[j] > a;
+    } else {
+#pragma unroll 16
+        for (int j = 0; j < n; ++j) {
+            const uint64_t other = list[j];
+            above_a += other > a;
+            above_b += other > b;
+        }
+    }
+    if (above_a < k)
+        emit(above_a, a);
+    if (above_b < k)
+        emit(above_b, b);
+}
+
+// One wave a row that it holds in registers: no barriers, and no sum is scaled.  16000 x
+// 1404 bf16 take 13 us (3.4 TB/s), with 5 alternatives 20, with 64 42: a row's reductions,
+// bounds and ranks take longer than its bytes.
+template <typename TI, int U, bool TOP> __global__ __launch_bounds__(LP_THREADS) void logprob_wave_kernel(LpArgs p)
+{
+    constexpr int E = Elt<TI>::PER_CHUNK, NW = LP_THREADS / 64;
+    __shared__ uint64_t lists[TOP ? NW : 1][TOP ? LP_WAVE_CAND : 1];
+    const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int64_t t = (int64_t)blockIdx.x * NW + wave;
+    if (t >= p.T)
+        return;
+    const float c = p.scale2;
+    float target = 0.f;
+    const bool given = lane == 0 && lp_target<TI>(p, t, target);
+    const LpLanes<TI, E, U> z((const TI *)p.logits + t * p.ld, p.V, lane);
+    float largest = -INFINITY;
+    z.each([&](float x, int, bool) { largest = lp_max(largest, x); });
+    float top = largest;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1)
+        top = lp_max(top, __shfl_xor(top, o, 64));
+    LpState st{top, 0.f, 0.f};
+    z.each([&](float x, int, bool) { st.add(x, c); });
+    st.s = wave_sum(st.s);
+    st.w = wave_sum(st.w);
+    if (lane == 0)
+        lp_finish(p, t, st, given, target);
+    if constexpr (TOP) {
+        const LpRow row(st);
+        auto emit = [&](int r, uint64_t key) {
+            p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
+            p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
+        };
+        if (row.bad) {
+            if (lane < p.k)
+                emit(lane, 0);
+        } else {
+            lp_wave_alternatives<TI, E, U>(z, p.k, largest, lists[wave], emit);
+        }
+    }
+}
+
 // The segments of a row joined: a lane a segment, in every wave.  The k best of
 // their sorted lists: where r lists' entries number j reach a bound, r j keys do; the
 // r-th largest of these entries, with r j >= k, is one, and the few keys that reach
@@ -708,6 +941,14 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 // us).
 constexpr int LP_WGS = 1024, LP_WHOLE = 48 << 10;
 
+// Rows that one wave takes: of up to LP_WAVE_SMALL pieces a lane at any number (64 x 536
+// fp32 with 5 alternatives 4.9 us, a workgroup a row 5.6; 16000 x 1404 bf16 20 and 51,
+// with 64 alternatives 42 and 85; slower for few rows with 64, 64 x 1404 10.0 and 8.8: a
+// row's sums are not to depend on how many are asked for), of up to LP_WAVE_MORE from
+// LP_WAVE_ROWS on (5: 1024 x 4096 bf16 8.2 and 8.0 us, 2048 11.7 and 13.3, 16000 39 and 62).
+// Twice as many pieces are slower at any number (16000 x 8000 bf16 109 and 73 us).
+constexpr int LP_WAVE_ROWS = 2048, LP_WAVE_SMALL = 4, LP_WAVE_MORE = 8;
+
 static int most_segments(int V)
 {
     const int64_t n = ceil_div(V, LP_SEG);
@@ -784,7 +1025,13 @@ static hipError_t run_logprob(LpArgs p, void *ws, hipStream_t s)
     auto run = [&](auto type, auto top) {
         using TI = decltype(type);
         constexpr bool TOP = decltype(top)::value;
-        if (p.seg <= LP_THREADS * LP_ONCE * Elt<TI>::PER_CHUNK)
+        const dim3 waves((unsigned)ceil_div(p.T, LP_THREADS / 64));
+        const int pieces = p.V / Elt<TI>::PER_CHUNK;
+        if (pieces <= 64 * LP_WAVE_SMALL)
+            logprob_wave_kernel<TI, LP_WAVE_SMALL, TOP><<<waves, block, 0, s>>>(p);
+        else if (pieces <= 64 * LP_WAVE_MORE && p.T >= LP_WAVE_ROWS)
+            logprob_wave_kernel<TI, LP_WAVE_MORE, TOP><<<waves, block, 0, s>>>(p);
+        else if (p.seg <= LP_THREADS * LP_ONCE * Elt<TI>::PER_CHUNK)
             logprob_segment_kernel<TI, TOP><<<grid, block, 0, s>>>(p);
         else if (!TOP && (int64_t)p.T * p.V * (int64_t)sizeof(TI) > ((int64_t)256 << 20))
             logprob_kernel<TI, TOP, true><<<grid, block, 0, s>>>(p);
