@@ -567,8 +567,13 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct MulTile {
     int bm, bn;
     double stage, rest, alone;
+    double end = 0;  // more where K is not split
 };
 constexpr MulTile MUL_TILES[] = {{256, 256, 1.5, 4, 1}, {256, 128, 0.8, 5.5, 1}, {128, 128, 0.6, 5, 1}, {128, 64, 0.41, 6, 1}};
+// The forward product that leaves g and u in 8 bits: a tile's end takes longer, a large
+// one's most, whose CU has no other (1 x 64 x 5440 13.4 us without that, 5.9 with it, 4096 x 64 x
+// 1024 16.7 and 11.1, 8192 x 2048 x 8192 the same tile).
+constexpr MulTile FWD_TILES_PACKED[] = {{256, 256, 1.5, 4, 1, 11.5}, {256, 128, 0.8, 5.5, 1, 3.5}, {128, 128, 0.6, 5, 1, 0.8}, {128, 64, 0.41, 6, 1}};
 constexpr MulTile FWD_TILES_F32[] = {{128, 128, 3.7, 4, 1.05}, {64, 128, 1.9, 2, 1.1}};
 constexpr MulTile MUL_TILES_F32[] = {{128, 128, 3.8, 4, 1.05}, {64, 64, 1.0, 1.5, 1.3}};
 constexpr double MUL_JOIN_US = 4, MUL_SPLIT_US = 0.45, MUL_PART_BYTES_PER_US = 5e6;
@@ -583,7 +588,7 @@ static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, in
     for (int t = 0; t < tiles; ++t)
         for (int splits = 1; splits <= MUL_MOST_SPLITS && (splits == 1 || splits <= stages); splits *= 2) {
             const int64_t wgs = ceil_div(M, tile[t].bm) * ceil_div(N, tile[t].bn) * splits;
-            double us = (double)ceil_div(ceil_div(wgs, 8), CUS / 8) * ((double)ceil_div(stages, splits) * tile[t].stage + tile[t].rest);
+            double us = (double)ceil_div(ceil_div(wgs, 8), CUS / 8) * ((double)ceil_div(stages, splits) * tile[t].stage + tile[t].rest + (splits == 1 ? tile[t].end : 0));
             if (wgs <= CUS)
                 us *= tile[t].alone;
             if (splits > 1)
@@ -600,7 +605,9 @@ static MulPlan forward_plan(int vdtype, int T, int d, int F, bool packed)
 {
     if (T <= GLU_FEW && !packed)  // (the streaming kernel's workgroups hold less than a block of 8-bit codes)
         return {0, 1};
-    return vdtype == 1 ? mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d) : mul_plan(FWD_TILES_F32, 2, T, 2 * (int64_t)F, d);
+    if (vdtype == 1)
+        return mul_plan(packed ? FWD_TILES_PACKED : MUL_TILES, 4, T, 2 * (int64_t)F, d);
+    return mul_plan(FWD_TILES_F32, 2, T, 2 * (int64_t)F, d);
 }
 
 // The most bytes that a call with up to T rows needs; need(t) is a call's with t
