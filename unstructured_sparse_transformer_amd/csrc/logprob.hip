@@ -454,7 +454,7 @@ template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THRE
     }
 }
 
-// One workgroup a row or a segment of at most LP_ONCE pieces a thread: short rows,
+// One workgroup a row or a segment of at most LP_ONCE pieces a thread: rows too long for a wave,
 // and few rows, where the time is that of one trip to memory and what follows.  The
 // pieces are all requested at once; the segment's maximum comes before its
 // exponentials, so that no sum is scaled.  32 segments of 4096 bf16 take 3 us, with
