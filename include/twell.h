@@ -461,8 +461,10 @@ TWELL_API int twell_act_unpack(const twell_packed_t *from, int32_t T, int32_t d,
                                void *stream);
 
 /* twell_glu_forward in bf16 (same sizes and types) that keeps g and u, before
- * they are rounded to bf16, in 8 bits ([T][F], codes 16-byte aligned); h is the
- * same.  An fp32 layer packs what twell_glu_forward stores.
+ * they are rounded to bf16, in 8 bits ([T][F], codes 16-byte aligned).  h has the
+ * same bits from 65 rows on; up to 64, where the two add up in other orders, it may
+ * differ by the rounding of its sums.  An fp32 layer packs what twell_glu_forward
+ * stores.
  * keep_sign 1 : values of g above 0 keep at least code 1 (off by up to a step in
  * the place of half of one).  For TWELL_ACT_RELU, whose slope is that of the sign:
  * a g below half a step reads back as 0 otherwise, and its gradient is lost (of a

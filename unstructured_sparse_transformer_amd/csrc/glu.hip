@@ -579,14 +579,16 @@ constexpr MulTile MUL_TILES_F32[] = {{128, 128, 3.8, 4, 1.05}, {64, 64, 1.0, 1.5
 constexpr double MUL_JOIN_US = 4, MUL_SPLIT_US = 0.45, MUL_PART_BYTES_PER_US = 5e6;
 constexpr int CUS = 256, MUL_MOST_SPLITS = 16;
 
-// The tile and the number of K splits with the least estimated time.
-static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, int64_t K)
+// The tile and the number of K splits (`only`, unless that is 0) with the least estimated time.
+static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, int64_t K, int only = 0)
 {
-    MulPlan best{0, 1};
+    MulPlan best{0, only ? only : 1};
     double best_us = 1e300;
     const int64_t stages = ceil_div(K, 64);
     for (int t = 0; t < tiles; ++t)
         for (int splits = 1; splits <= MUL_MOST_SPLITS && (splits == 1 || splits <= stages); splits *= 2) {
+            if (only && splits != only)
+                continue;
             const int64_t wgs = ceil_div(M, tile[t].bm) * ceil_div(N, tile[t].bn) * splits;
             double us = (double)ceil_div(ceil_div(wgs, 8), CUS / 8) * ((double)ceil_div(stages, splits) * tile[t].stage + tile[t].rest + (splits == 1 ? tile[t].end : 0));
             if (wgs <= CUS)
@@ -601,12 +603,16 @@ static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, in
     return best;
 }
 
+// The product that leaves g and u in 8 bits takes its own tiles, but splits K as the other one does, whose h it has to the
+// last bit (by the estimates that costs 1 in 1500 sizes up to 2%, less than 1 us).
 static MulPlan forward_plan(int vdtype, int T, int d, int F, bool packed)
 {
-    if (T <= GLU_FEW && !packed)  // (the streaming kernel's workgroups hold less than a block of 8-bit codes)
+    if (packed)  // (the streaming kernel's workgroups hold less than a block of 8-bit codes)
+        return mul_plan(FWD_TILES_PACKED, 4, T, 2 * (int64_t)F, d, T > GLU_FEW ? forward_plan(vdtype, T, d, F, false).splits : 0);
+    if (T <= GLU_FEW)
         return {0, 1};
     if (vdtype == 1)
-        return mul_plan(packed ? FWD_TILES_PACKED : MUL_TILES, 4, T, 2 * (int64_t)F, d);
+        return mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d);
     return mul_plan(FWD_TILES_F32, 2, T, 2 * (int64_t)F, d);
 }
 
@@ -651,8 +657,9 @@ size_t glu_forward_most_ws(int T, int d, int F, int vdtype, bool packed)
         MulPlan plan;
         size_t bytes;
     };
+    // (beyond GLU_FEW rows the packed product's splits are those of the other's plan, which has the bytes' estimate)
     return most_bytes_to(T, [&](int t) {
-        const MulPlan plan = forward_plan(vdtype, t, d, F, packed);
+        const MulPlan plan = forward_plan(vdtype, t, d, F, packed && t <= GLU_FEW);
         return Need{plan, forward_bytes(plan, t, F)};
     });
 }
