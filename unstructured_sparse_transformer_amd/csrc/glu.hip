@@ -567,20 +567,19 @@ static int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 struct MulTile {
     int bm, bn;
     double stage, rest, alone;
-    double end = 0;  // more where K is not split
+    double end8 = 0;  // more where K is not split and g and u leave in 8 bits
 };
-constexpr MulTile MUL_TILES[] = {{256, 256, 1.5, 4, 1}, {256, 128, 0.8, 5.5, 1}, {128, 128, 0.6, 5, 1}, {128, 64, 0.41, 6, 1}};
-// The forward product that leaves g and u in 8 bits: a tile's end takes longer, a large
-// one's most, whose CU has no other (1 x 64 x 5440 13.4 us without that, 5.9 with it, 4096 x 64 x
-// 1024 16.7 and 11.1, 8192 x 2048 x 8192 the same tile).
-constexpr MulTile FWD_TILES_PACKED[] = {{256, 256, 1.5, 4, 1, 11.5}, {256, 128, 0.8, 5.5, 1, 3.5}, {128, 128, 0.6, 5, 1, 0.8}, {128, 64, 0.41, 6, 1}};
+// A tile whose g and u leave in 8 bits takes longer to end, a large one most, whose CU has no other (1 x 64 x 5440 13.4 us
+// without `end8`, 5.9 with it, 4096 x 64 x 1024 16.7 and 11.1, 8192 x 2048 x 8192 the same tile).
+constexpr MulTile MUL_TILES[] = {{256, 256, 1.5, 4, 1, 11.5}, {256, 128, 0.8, 5.5, 1, 3.5}, {128, 128, 0.6, 5, 1, 0.8}, {128, 64, 0.41, 6, 1}};
 constexpr MulTile FWD_TILES_F32[] = {{128, 128, 3.7, 4, 1.05}, {64, 128, 1.9, 2, 1.1}};
 constexpr MulTile MUL_TILES_F32[] = {{128, 128, 3.8, 4, 1.05}, {64, 64, 1.0, 1.5, 1.3}};
 constexpr double MUL_JOIN_US = 4, MUL_SPLIT_US = 0.45, MUL_PART_BYTES_PER_US = 5e6;
 constexpr int CUS = 256, MUL_MOST_SPLITS = 16;
 
-// The tile and the number of K splits (`only`, unless that is 0) with the least estimated time.
-static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, int64_t K, int only = 0)
+// The tile and the number of K splits (`only`, unless that is 0) with the least estimated time; packed: g and u leave in
+// 8 bits.
+static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, int64_t K, bool packed = false, int only = 0)
 {
     MulPlan best{0, only ? only : 1};
     double best_us = 1e300;
@@ -590,7 +589,7 @@ static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, in
             if (only && splits != only)
                 continue;
             const int64_t wgs = ceil_div(M, tile[t].bm) * ceil_div(N, tile[t].bn) * splits;
-            double us = (double)ceil_div(ceil_div(wgs, 8), CUS / 8) * ((double)ceil_div(stages, splits) * tile[t].stage + tile[t].rest + (splits == 1 ? tile[t].end : 0));
+            double us = (double)ceil_div(ceil_div(wgs, 8), CUS / 8) * ((double)ceil_div(stages, splits) * tile[t].stage + tile[t].rest + (packed && splits == 1 ? tile[t].end8 : 0));
             if (wgs <= CUS)
                 us *= tile[t].alone;
             if (splits > 1)
@@ -608,7 +607,7 @@ static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, in
 static MulPlan forward_plan(int vdtype, int T, int d, int F, bool packed)
 {
     if (packed)  // (the streaming kernel's workgroups hold less than a block of 8-bit codes)
-        return mul_plan(FWD_TILES_PACKED, 4, T, 2 * (int64_t)F, d, T > GLU_FEW ? forward_plan(vdtype, T, d, F, false).splits : 0);
+        return mul_plan(MUL_TILES, 4, T, 2 * (int64_t)F, d, true, T > GLU_FEW ? forward_plan(vdtype, T, d, F, false).splits : 0);
     if (T <= GLU_FEW)
         return {0, 1};
     if (vdtype == 1)
@@ -670,20 +669,22 @@ static dim3 join_grid(int64_t n)
     return dim3((unsigned)(wgs < 4096 ? wgs : 4096));
 }
 
+// The bf16 kernel of a tile of MUL_TILES.
 template <GluPack PACK> static void launch_glu_tiles(int tile, dim3 grid, const GluFwd &p, hipStream_t s)
 {
+    constexpr const MulTile *t = MUL_TILES;
     switch (tile) {
     case 0:
-        glu_kernel<__bf16, 256, 256, 64, 128, 2, PACK><<<grid, dim3(512), 0, s>>>(p);
+        glu_kernel<__bf16, t[0].bm, t[0].bn, 64, 128, 2, PACK><<<grid, dim3(512), 0, s>>>(p);
         break;
     case 1:
-        glu_kernel<__bf16, 256, 128, 64, 64, 3, PACK><<<grid, dim3(512), 0, s>>>(p);
+        glu_kernel<__bf16, t[1].bm, t[1].bn, 64, 64, 3, PACK><<<grid, dim3(512), 0, s>>>(p);
         break;
     case 2:
-        glu_kernel<__bf16, 128, 128, 32, 64, 4, PACK><<<grid, dim3(512), 0, s>>>(p);
+        glu_kernel<__bf16, t[2].bm, t[2].bn, 32, 64, 4, PACK><<<grid, dim3(512), 0, s>>>(p);
         break;
     default:
-        glu_kernel<__bf16, 128, 64, 32, 64, 3, PACK><<<grid, dim3(256), 0, s>>>(p);
+        glu_kernel<__bf16, t[3].bm, t[3].bn, 32, 64, 3, PACK><<<grid, dim3(256), 0, s>>>(p);
         break;
     }
 }
