@@ -546,8 +546,8 @@ TWELL_API int twell_block_norm_backward(const twell_block_norm_t *bn, const void
  * ids : device [T] of int32 or int64 (id_bits 32 or 64).  An id outside 0 .. V-1
  * (padding) gives a row of zeros, and adds to no gradient.
  * table [V][d] vdtype, out [T][d] odtype: TWELL_BF16 or TWELL_F32 each, aligned as
- * their elements.  T, V <= 2^30, d <= 2^20, and T ceil(d / 4) (d < 4: T d) below
- * 2^34 - 2^10. */
+ * their elements; out overlaps neither table nor ids.  T, V <= 2^30, d <= 2^20, and
+ * T ceil(d / 4) (d < 4: T d) below 2^34 - 2^10. */
 TWELL_API int twell_embed_forward(const void *ids, int32_t id_bits, int32_t T, const void *table, int32_t V, int32_t d,
                                   int32_t vdtype, float scale, void *out, int32_t odtype, void *stream);
 
@@ -556,6 +556,7 @@ TWELL_API int twell_embed_forward(const void *ids, int32_t id_bits, int32_t T, c
  *   accumulate 0 : dtable [V][d] vdtype is overwritten (rows without tokens: 0);
  *              1 : the sums are added to what is there (a table that the head
  *                  shares), and rows without tokens are not touched.
+ * dtable overlaps neither dout nor ids.
  * workspace : device, >= twell_embed_workspace_bytes(T, V, d) (never shrinking as
  * T grows), 256-byte aligned, content ignored on entry. */
 TWELL_API int twell_embed_backward(const void *ids, int32_t id_bits, int32_t T, const void *dout, int32_t dodtype,

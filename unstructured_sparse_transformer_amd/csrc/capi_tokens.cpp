@@ -68,6 +68,9 @@ int twell_embed_forward(const void *ids, int32_t id_bits, int32_t T, const void 
     TWELL_TRY(check_ids(ids, id_bits));
     TWELL_TRY(check_vec(table, elem_size(vdtype)));
     TWELL_TRY(check_vec(out, elem_size(odtype)));
+    const int64_t written = (int64_t)T * d * elem_size(odtype);
+    if (overlap(out, written, table, (int64_t)V * d * elem_size(vdtype)) || overlap(out, written, ids, (int64_t)T * (id_bits / 8)))
+        return TWELL_E_SHAPE;
     twell::EmbArgs a{};
     a.T = T;
     a.V = V;
@@ -118,6 +121,10 @@ int twell_embed_backward(const void *ids, int32_t id_bits, int32_t T, const void
     a.in = dout;
     a.out = dtable;
     TWELL_TRY(check_ws(workspace, workspace_bytes, twell::emb_layout(a, workspace)));
+    const int64_t written = (int64_t)V * d * elem_size(vdtype);
+    if (overlap(dtable, written, dout, (int64_t)T * d * elem_size(dodtype)) ||
+        overlap(dtable, written, ids, (int64_t)T * (id_bits / 8)))
+        return TWELL_E_SHAPE;
     return hip_status(twell::launch_embed_backward(a, static_cast<hipStream_t>(stream)));
 }
 

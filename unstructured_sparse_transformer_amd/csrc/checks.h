@@ -42,6 +42,13 @@ inline int check_vec(const void *p, size_t es)
     return aligned_to(p, es) ? TWELL_OK : TWELL_E_ALIGN;
 }
 
+// Whether na bytes at a and nb bytes at b share any.
+inline bool overlap(const void *a, int64_t na, const void *b, int64_t nb)
+{
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return na > 0 && nb > 0 && x < y + (uintptr_t)nb && y < x + (uintptr_t)na;
+}
+
 inline size_t up256(size_t b) { return (b + 255) & ~(size_t)255; }
 
 // The workspace argument against a layout's size.
