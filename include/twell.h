@@ -453,8 +453,9 @@ typedef struct twell_packed_t {
     void *scale;  /* device [T][ceil(d / 32)] bf16 */
 } twell_packed_t;
 
-/* x, out : device [T][d] vdtype, aligned as their elements; T <= 2^30,
- * d <= 2^20, and T ceil(d / 32) below 2^31 - 2^7 (TWELL_F32: 2^30 - 2^6). */
+/* x, out : device [T][d] vdtype, aligned as their elements, apart from the codes and
+ * the scales; T <= 2^30, d <= 2^20, and T ceil(d / 32) below 2^31 - 2^7 (TWELL_F32:
+ * 2^30 - 2^6). */
 TWELL_API int twell_act_pack(const void *x, int32_t T, int32_t d, int32_t vdtype, const twell_packed_t *to,
                              void *stream);
 TWELL_API int twell_act_unpack(const twell_packed_t *from, int32_t T, int32_t d, int32_t vdtype, void *out,

@@ -1,4 +1,7 @@
-"""Calls of the token operators whose result lies in part in what they read are refused on the host (no GPU needed)."""
+"""Calls of the token operators and of the 8-bit activations whose result lies in part in what they read are refused on the
+host (no GPU needed)."""
+
+import ctypes
 
 import pytest
 
@@ -35,6 +38,20 @@ def test_embed_backward(T, V, d, add):
         assert call(AT * 64, AT, AT + off) == SHAPE, off
     for off in _places(dtable, ids):
         assert call(AT, AT * 64, AT + off) == SHAPE, off
+
+
+@pytest.mark.parametrize("T,d", [(8, 32), (1, 1), (5, 1001)])
+@pytest.mark.parametrize("vd", [0, 1])
+def test_act_pack(T, d, vd):
+    lib = tw.load()
+    es, scales = (4, 2)[vd], T * -(-d // 32) * 2
+    pack = lambda x, c, s: lib.twell_act_pack(x, T, d, vd, ctypes.byref(tw.TwellPackedT(c, s)), None)  # noqa: E731
+    unpack = lambda x, c, s: lib.twell_act_unpack(ctypes.byref(tw.TwellPackedT(c, s)), T, d, vd, x, None)  # noqa: E731
+    for f in (pack, unpack):
+        for off in _places(T * d, T * d * es):
+            assert f(AT, AT + off, AT * 64) == SHAPE, off
+        for off in _places(scales, T * d * es):
+            assert f(AT, AT * 64, AT + off) == SHAPE, off
 
 
 @pytest.mark.gpu

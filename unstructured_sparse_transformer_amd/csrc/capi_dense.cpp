@@ -39,6 +39,13 @@ int check_packed(const twell_packed_t *p, size_t code_align)
 
 twell::Packed8 packed8(const twell_packed_t *p) { return twell::Packed8{p->code, static_cast<uint16_t *>(p->scale)}; }
 
+// Whether T rows of d codes, or their scales, lie in part in `rows` of elements of that type.
+bool packed_overlaps(const twell_packed_t *p, const void *rows, int32_t T, int32_t d, int32_t vdtype)
+{
+    const int64_t bytes = (int64_t)T * d * elem_size(vdtype), scales = T * twell::a8_blocks(d) * 2;
+    return overlap(p->code, (int64_t)T * d, rows, bytes) || overlap(p->scale, scales, rows, bytes);
+}
+
 // Sizes of rows that are packed: the threads, of 2 pieces of 16 bytes each, are counted in 32 bits.
 int check_act(int32_t T, int32_t d, int32_t vdtype)
 {
@@ -296,6 +303,8 @@ int twell_act_pack(const void *x, int32_t T, int32_t d, int32_t vdtype, const tw
         return TWELL_OK;
     TWELL_TRY(check_vec(x, elem_size(vdtype)));
     TWELL_TRY(check_packed(to, 1));
+    if (packed_overlaps(to, x, T, d, vdtype))
+        return TWELL_E_SHAPE;
     return hip_status(twell::launch_act_pack(vdtype, x, T, d, packed8(to), static_cast<hipStream_t>(stream)));
 }
 
@@ -306,6 +315,8 @@ int twell_act_unpack(const twell_packed_t *from, int32_t T, int32_t d, int32_t v
         return TWELL_OK;
     TWELL_TRY(check_packed(from, 1));
     TWELL_TRY(check_vec(out, elem_size(vdtype)));
+    if (packed_overlaps(from, out, T, d, vdtype))
+        return TWELL_E_SHAPE;
     return hip_status(twell::launch_act_unpack(vdtype, packed8(from), T, d, out, static_cast<hipStream_t>(stream)));
 }
 
