@@ -6,7 +6,7 @@ A layer adds alpha * gate * norm(FFN(norm(stream))) to a 32-bit residual stream.
 sum and the norm before the next FFN are one call.  The FFN is the dense gated product followed by a plain matrix
 product of torch's (``gated``; its backward pass takes two more), or the ReLU-sparse one on its hybrid activations
 (``sparse``).  With ``--keep 8`` the gated FFN keeps its two products for the backward pass in 8 bits, and its hidden
-activation not at all.  The weights are 32-bit masters with 16-bit copies for the layers; one call updates all of them.
+activation not at all: all layers use one buffer for it.  The weights are 32-bit masters with 16-bit copies for the layers; one call updates all of them.
 
 The layers learn a function of vectors, or with ``--vocab`` the token after each token: an embedding in front of them,
 log probabilities behind them, and one table for both.
@@ -26,11 +26,11 @@ BF16, F32 = torch.bfloat16, torch.float32
 
 
 class Gated:
-    """h = silu(n W_g) * (n W_u), y = h W_d."""
+    """h = silu(n W_g) * (n W_u), y = h W_d.  first: the stack's first layer (None for that one itself)."""
 
     y_type = dx_type = BF16
 
-    def __init__(self, T, d, F, weights):
+    def __init__(self, T, d, F, weights, first=None):
         self.wg, self.wu, self.wd = weights
         new = lambda *s: torch.empty(s, dtype=BF16, device="cuda")  # noqa: E731
         self.h, self.g, self.u, self.y = new(T, F), new(T, F), new(T, F), new(T, d)
@@ -52,12 +52,19 @@ class Gated:
 
 
 class GatedKept8(Gated):
-    """The same with g and u kept in 8 bits, and h taken from these again."""
+    """The same with g and u kept in 8 bits, and h taken from these again: what a layer keeps from its forward to its
+    backward pass is these and y, and the layers of a stack share the buffers of h and dh and the workspaces."""
 
-    def __init__(self, T, d, F, weights):
-        super().__init__(T, d, F, weights)
+    def __init__(self, T, d, F, weights, first=None):
+        self.wg, self.wu, self.wd = weights
+        new = lambda *s: torch.empty(s, dtype=BF16, device="cuda")  # noqa: E731
         self.g, self.u = (tw.PackedAct.empty(T, F) for _ in range(2))
-        self.ws = tw.glu_packed_workspace(T, d, F)
+        self.y, self.dx, self.grads = new(T, d), new(T, d), [new(F, d) for _ in range(3)]
+        if first is None:
+            self.h, self.dh = new(T, F), new(T, F)
+            self.ws, self.ws_backward = tw.glu_packed_workspace(T, d, F), tw.glu_backward_workspace(T, d, F, BF16)
+        else:
+            self.h, self.dh, self.ws, self.ws_backward = first.h, first.dh, first.ws, first.ws_backward
 
     def forward(self, n):
         self.n = n
@@ -77,7 +84,7 @@ class Sparse:
 
     y_type = dx_type = F32
 
-    def __init__(self, T, d, F, weights):
+    def __init__(self, T, d, F, weights, first=None):
         self.wg, self.wu, self.wd = weights
         self.hy = tw.Hybrid.empty(T, F, 128, 32, BF16, T)
         self.y, self.dx = (torch.empty((T, d), dtype=F32, device="cuda") for _ in range(2))
@@ -111,7 +118,9 @@ class Stack:
         self.w_pre = [ones() for _ in range(layers + 1)]   # the norm before each FFN, and the last one
         self.w_post = [ones() for _ in range(layers)]      # the norm after each FFN
         self.gate = [ones().view(1, d) for _ in range(layers)]
-        self.ffn = [ffn(T, d, F, c) for c in self.copies]
+        self.ffn = []
+        for c in self.copies:
+            self.ffn.append(ffn(T, d, F, c, *self.ffn[:1]))
         self.first = tw.BlockNorm(w_pre=self.w_pre[0])
         self.norms = [tw.BlockNorm(alpha=alpha, post=True, w_post=self.w_post[k], w_pre=self.w_pre[k + 1])
                       for k in range(layers)]
