@@ -579,7 +579,9 @@ TWELL_API size_t twell_embed_workspace_bytes(int32_t T, int32_t V, int32_t d);
  * Each of logp (then targets too), norm and entropy may be NULL, k may be 0; not
  * all of them.  A logit of -inf is a masked token: p = 0, logp = -inf.  A row of
  * nothing else has m = logp = -inf, L = entropy = 0.  A NaN or +inf in a row makes
- * its results NaN, and its top_idx 0 .. k-1.  Sums are fp32 in a fixed order.
+ * its results NaN, and its top_idx 0 .. k-1.  Sums are fp32 in a fixed order; where one
+ * token has nearly all of the probability, L, its logp and the entropy are right
+ * relative to themselves, as its 1 - p in the gradient is.
  * workspace : device, >= twell_logprob_workspace_bytes(T, V, k) (where that is 0 it
  * may be NULL; never shrinking as T grows), 256-byte aligned, content ignored on
  * entry. */

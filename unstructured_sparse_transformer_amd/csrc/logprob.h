@@ -10,7 +10,7 @@ namespace twell {
 
 constexpr int LP_MOST_TOP = 64;  // alternatives of a row
 
-struct LpState;  // what is known of a part of a row
+struct LpSum;  // the sums of a part of a row
 
 struct LpArgs {
     int T, V, k;
@@ -22,7 +22,7 @@ struct LpArgs {
     float *logp, *norm, *entropy, *top_logp;
     int32_t *top_idx;
     int segs, seg;        // segments of a row, and elements of one
-    LpState *part;        // [T][segs]
+    LpSum *part;          // [T][segs]
     uint64_t *keys;       // [T][segs][k]
     // backward
     const float *norm_in, *entropy_in, *dlogp, *dentropy;

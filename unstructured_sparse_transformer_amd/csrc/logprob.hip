@@ -6,11 +6,13 @@
 //   S = sum exp(c (z - m)),  W = sum c (z - m) exp(c (z - m)),  L = log S
 //   logp[v] = c (z[v] - m) - L,   entropy H = L - W / S
 //   dz[v] = c (dlogp (1[v = target] - p[v]) - dH p[v] (logp[v] + H))
-// Everything is relative to m, so nothing of size c m cancels: H is a sum of two
-// terms of one sign, and a likely token's logp keeps its digits.  A row is read
-// once, with the running maximum and sums of each thread (a larger maximum scales
-// the sums before it); a logit of -inf has p = 0, and its term of W is 0.
-// Exponentials are in base 2, as the hardware has them.
+// Everything is relative to m, so nothing of size c m cancels, and H is a sum of two
+// terms of one sign.  Below S = 2 one logit is above all others, whose sum would lose
+// its digits next to that one's 1: it is taken apart from it (lp_others), so that a
+// confident row's L = log(1 + (S - 1)), H and 1 - p are right relative to themselves.
+// A row is read once, with the running maximum and sums of each thread (a larger
+// maximum scales the sums before it); a logit of -inf has p = 0, and its term of W is
+// 0.  Exponentials are in base 2, as the hardware has them.
 #include "logprob.h"
 #include "rows.h"
 #include "wave_ops.h"
@@ -73,14 +75,21 @@ __device__ __forceinline__ float lp_value(uint32_t order)
 __device__ __forceinline__ float lp_key_value(uint64_t key) { return lp_value((uint32_t)(key >> 32)); }
 __device__ __forceinline__ int lp_key_index(uint64_t key) { return (int)(0xFFFFFFFFu - (uint32_t)key); }
 
+// The whole sums of a row or of a segment of one: more = S - 1, of nothing but masked
+// logits -1.
+struct LpSum {
+    float m, more, w;
+};
+
 // The value of a row's results from its whole sums.
 struct LpRow {
     float m, size2, entropy;  // size2 = log2 S
     bool bad, empty;
-    __device__ __forceinline__ LpRow(const LpState &t) : m(t.m), bad(!(t.m < INFINITY)), empty(t.m == -INFINITY)
+    __device__ __forceinline__ LpRow(const LpSum &t) : m(t.m), bad(!(t.m < INFINITY)), empty(t.m == -INFINITY)
     {
-        size2 = empty ? 0.f : __builtin_amdgcn_logf(t.s);
-        entropy = empty ? 0.f : LP_LN2 * (size2 - t.w / t.s);
+        const float s = 1.f + t.more;
+        size2 = empty ? 0.f : s < 2.f ? LP_LOG2E * log1pf(t.more) : __builtin_amdgcn_logf(s);
+        entropy = empty ? 0.f : LP_LN2 * (size2 - t.w / s);
     }
     __device__ __forceinline__ float logp(float z, float scale) const
     {
@@ -91,7 +100,7 @@ struct LpRow {
 };
 
 // A row's results; `given`: its token's logit is z.
-__device__ __forceinline__ void lp_finish(const LpArgs &p, int64_t t, const LpState &sum, bool given, float z)
+__device__ __forceinline__ void lp_finish(const LpArgs &p, int64_t t, const LpSum &sum, bool given, float z)
 {
     const LpRow row(sum);
     const float nan = __uint_as_float(0x7FC00000u);
@@ -362,6 +371,49 @@ __device__ __forceinline__ LpState lp_sum(LpState t, float c, LpState *waves, in
     return all;
 }
 
+// Whether one logit is above all others: its exponential is 1 itself.
+__device__ __forceinline__ bool lp_confident(float s) { return s >= 1.f && s < 2.f; }
+
+struct LpOthers {
+    int who;
+    float waves[LP_THREADS / 64];
+};
+
+// S - 1 of such a segment, in every thread: the threads' own sums relative to m, but
+// for the thread `has`, whose logits (pieces tid, tid + 256, ... and one of the rest)
+// all read again, without the largest.  Only such rows pay for it: 4096 x 131072 bf16
+// of them take 169 us, others 166; 16000 x 1404, a wave each, 17.6 and 13.4.  (Counting
+// the largest logits apart in every row's sums: 183 us and 17.4.)
+template <typename TI, int E>
+__device__ __forceinline__ float lp_others(const TI *z, int n, float m, float c, float own, bool has, LpOthers &sh, int tid)
+{
+    const int whole = n / E, rest = n - whole * E;
+    if (has)
+        sh.who = tid;
+    __syncthreads();
+    const int who = sh.who;
+    float s = has ? 0.f : own;
+    auto add = [&](float x) { s += x < m ? lp_exp2(lp_arg(x, m, c)) : 0.f; };
+    for (int i = tid * LP_THREADS + who; i < whole; i += LP_THREADS * LP_THREADS) {
+        RowPiece<TI, E> v;
+        v.load(z + (int64_t)i * E);
+#pragma unroll
+        for (int e = 0; e < E; ++e)
+            add(v.at(e));
+    }
+    if (tid == 0 && who < rest)
+        add((float)z[whole * E + who]);
+    s = wave_sum(s);
+    if ((tid & 63) == 0)
+        sh.waves[tid >> 6] = s;
+    __syncthreads();
+    s = sh.waves[0];
+#pragma unroll
+    for (int w = 1; w < LP_THREADS / 64; ++w)
+        s += sh.waves[w];
+    return s;
+}
+
 // ------------------------------------------------------------------ forward
 // The token's logit of a row, and whether there is one: asked for before the row is
 // read, used after.
@@ -383,6 +435,7 @@ template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THRE
 {
     constexpr int E = Elt<TI>::PER_CHUNK, U = 4;
     __shared__ LpState waves[LP_THREADS / 64];
+    __shared__ LpOthers others;
     __shared__ __attribute__((aligned(16))) char top_mem[TOP ? sizeof(LpTop) : 16];
     const int tid = threadIdx.x;
     const int64_t t = blockIdx.x / p.segs;
@@ -420,13 +473,16 @@ template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THRE
             st.raise(lp_max(x, st.m), c);
         st.add(x, c);
     }
-    const float largest = st.m;
+    const float largest = st.m, own = st.s;
     st = lp_sum(st, c, waves, tid);
+    LpSum sum{st.m, st.s - 1.f, st.w};
+    if (lp_confident(st.s))
+        sum.more = lp_others<TI, E>(z, n, st.m, c, own * lp_exp2(lp_arg(largest, st.m, c)), largest == st.m, others, tid);
     if (tid == 0) {
         if (p.segs == 1)
-            lp_finish(p, t, st, given, target);
+            lp_finish(p, t, sum, given, target);
         else
-            p.part[t * p.segs + s] = st;
+            p.part[t * p.segs + s] = sum;
     }
     if constexpr (TOP) {
         LpTop &sh = *reinterpret_cast<LpTop *>(top_mem);
@@ -442,7 +498,7 @@ template <typename TI, bool TOP, bool ONCE> __global__ __launch_bounds__(LP_THRE
                 f((float)z[whole * E + tid], v0 + whole * E + tid);
         };
         if (p.segs == 1) {
-            const LpRow row(st);
+            const LpRow row(sum);
             lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
                 p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
                 p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
@@ -464,6 +520,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
     constexpr int E = Elt<TI>::PER_CHUNK, U = LP_ONCE, NW = LP_THREADS / 64;
     __shared__ float tops[NW];
     __shared__ LpState waves[NW];
+    __shared__ LpOthers others;
     __shared__ __attribute__((aligned(16))) char top_mem[TOP ? sizeof(LpTop) : 16];
     const int tid = threadIdx.x, lane = tid & 63;
     const int64_t t = blockIdx.x / p.segs;
@@ -506,18 +563,21 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
                 st.add(v[u].at(e), c);
     if (tid < rest)
         st.add(last, c);
+    const float own = st.s;
     st.s = wave_sum(st.s);
     st.w = wave_sum(st.w);
     if (lane == 0)
         waves[tid >> 6] = st;
     __syncthreads();
     st.s = waves[0].s + waves[1].s + waves[2].s + waves[3].s;
-    st.w = waves[0].w + waves[1].w + waves[2].w + waves[3].w;
+    LpSum sum{st.m, st.s - 1.f, waves[0].w + waves[1].w + waves[2].w + waves[3].w};
+    if (lp_confident(st.s))
+        sum.more = lp_others<TI, E>(z, n, st.m, c, own, largest == st.m, others, tid);
     if (tid == 0) {
         if (p.segs == 1)
-            lp_finish(p, t, st, given, target);
+            lp_finish(p, t, sum, given, target);
         else
-            p.part[t * p.segs + s] = st;
+            p.part[t * p.segs + s] = sum;
     }
     if constexpr (TOP) {
         LpTop &sh = *reinterpret_cast<LpTop *>(top_mem);
@@ -532,7 +592,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
                 f(last, v0 + whole * E + tid);
         };
         if (p.segs == 1) {
-            const LpRow row(st);
+            const LpRow row(sum);
             lp_alternatives<TI, E>(z, v0, n, p.k, largest, own, sh, tid, [&](int r, uint64_t key) {
                 p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
                 p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
@@ -571,6 +631,18 @@ template <typename TI, int E, int U> struct LpLanes {
             }
         if (rest)
             f(last, whole * E + lane, lane < rest);
+    }
+    // lp_others of the wave's row: the lane `has` has U E elements and one of the rest, read again by as many lanes.
+    __device__ __forceinline__ float others(const TI *z, float m, float c, float own, bool has) const
+    {
+        static_assert(U * E <= 64, "an element a lane");
+        const int i = __builtin_ctzll(__ballot(has)) + lane / E * 64;
+        float s = has ? (last < m ? lp_exp2(lp_arg(last, m, c)) : 0.f) : own;
+        if (lane < U * E && i < whole) {
+            const float x = (float)z[i * E + lane % E];
+            s += x < m ? lp_exp2(lp_arg(x, m, c)) : 0.f;
+        }
+        return wave_sum(s);
     }
     // How many elements pass a test, and the keys of the first `most` of them to a list.
     template <typename F> __device__ __forceinline__ int count(F test) const
@@ -758,12 +830,14 @@ template <typename TI, int U, bool TOP> __global__ __launch_bounds__(LP_THREADS)
         top = lp_max(top, __shfl_xor(top, o, 64));
     LpState st{top, 0.f, 0.f};
     z.each([&](float x, int, bool) { st.add(x, c); });
-    st.s = wave_sum(st.s);
-    st.w = wave_sum(st.w);
+    const float all = wave_sum(st.s);
+    LpSum sum{top, all - 1.f, wave_sum(st.w)};
+    if (lp_confident(all))
+        sum.more = z.others((const TI *)p.logits + t * p.ld, top, c, st.s, largest == top);
     if (lane == 0)
-        lp_finish(p, t, st, given, target);
+        lp_finish(p, t, sum, given, target);
     if constexpr (TOP) {
-        const LpRow row(st);
+        const LpRow row(sum);
         auto emit = [&](int r, uint64_t key) {
             p.top_idx[t * p.k + r] = row.bad ? r : lp_key_index(key);
             p.top_logp[t * p.k + r] = row.logp(lp_key_value(key), p.scale);
@@ -792,7 +866,7 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
     const bool on = lane < p.segs;
     float target = 0.f;
     const bool given = tid == 0 && lp_target<TI>(p, t, target);
-    LpState st = p.part[t * p.segs + (on ? lane : 0)];
+    LpSum sum = p.part[t * p.segs + (on ? lane : 0)];
     constexpr int EARLY = 4;  // keys a thread asks for before the bound is known
     const uint64_t *keys = nullptr;
     uint64_t early[EARLY];
@@ -811,19 +885,22 @@ template <typename TI, bool TOP> __global__ __launch_bounds__(LP_THREADS) void l
         if (tid == 0)
             count = 0;
     }
-    if (!on)
-        st = LpState{-INFINITY, 0.f, 0.f};
+    LpState st{on ? sum.m : -INFINITY, on ? 1.f + sum.more : 0.f, on ? sum.w : 0.f};
     float top = st.m;
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1)
         top = lp_max(top, __shfl_xor(top, o, 64));
+    const bool largest = st.m == top;
+    const float more = sum.more;
     st.raise(top, c);
-    st.s = wave_sum(st.s);
-    st.w = wave_sum(st.w);
+    const float all = wave_sum(st.s);
+    sum = LpSum{top, all - 1.f, wave_sum(st.w)};
+    if (lp_confident(all))  // the segment that has the largest logit, without it, and the others
+        sum.more = wave_sum(largest ? more : st.s);
     if (tid == 0)
-        lp_finish(p, t, st, given, target);
+        lp_finish(p, t, sum, given, target);
     if constexpr (TOP) {
-        const LpRow row(st);
+        const LpRow row(sum);
         if (row.bad) {
             for (int i = tid; i < p.k; i += LP_THREADS) {
                 p.top_idx[t * p.k + i] = i;
@@ -890,18 +967,22 @@ template <typename TI> __global__ __launch_bounds__(LP_THREADS) void logprob_bac
     int at = p.V;
     if (p.dlogp)
         at = p.id64 ? token_key((const int64_t *)p.targets, t, p.V) : token_key((const int32_t *)p.targets, t, p.V);
-    // dz = p (a - b logp) [+ -a at the target], in base 2
+    // dz = p (a + b log2 p), at the target p (a0 + b log2 p) + d (1 - p)
     const float h = p.dentropy ? p.dentropy[t] * p.scale : 0.f;
     const float d = at < p.V && !empty ? p.dlogp[t] * p.scale : 0.f;
-    float a = -d - (p.dentropy ? h * p.entropy_in[t] : 0.f), b = -h * LP_LN2;
-    if (empty)
-        a = b = 0.f;
+    float a0 = p.dentropy && !empty ? -h * p.entropy_in[t] : 0.f;
+    const float b = empty ? 0.f : -h * LP_LN2;
     if (size != size)
-        a = size;
+        a0 = size;
+    const float a = a0 - d;
     const float base = empty ? 0.f : m, size2 = size * LP_LOG2E;
     auto grad = [&](float x) {
         const float l = fmaxf(fmaf(x - base, p.scale2, -size2), LP_LEAST);
         return lp_exp2(l) * fmaf(b, l, a);
+    };
+    auto grad_target = [&](float x) {  // (1 - p of a likely token would lose its digits)
+        const float l = fmaxf(fmaf(x - base, p.scale2, -size2), LP_LEAST);
+        return fmaf(-d, expm1f(l * LP_LN2), lp_exp2(l) * fmaf(b, l, a0));
     };
     const int whole = n / E, rest = n - whole * E;
     at -= v0;
@@ -921,15 +1002,21 @@ template <typename TI> __global__ __launch_bounds__(LP_THREADS) void logprob_bac
 #pragma unroll
             for (int e = 0; e < E; ++e)
                 g[e] = grad(v[u].at(e));
-            if (at >= i && at < i + E)
+            if (at >= i && at < i + E) {
+                float x = 0.f;
 #pragma unroll
                 for (int e = 0; e < E; ++e)
-                    g[e] += at == i + e ? d : 0.f;
+                    x = at == i + e ? v[u].at(e) : x;
+                x = grad_target(x);
+#pragma unroll
+                for (int e = 0; e < E; ++e)
+                    g[e] = at == i + e ? x : g[e];
+            }
             rows_store<E>(o + i, g, 0);
         }
     }
     if (tid < rest)
-        o[whole * E + tid] = (TI)(grad((float)last) + (at == whole * E + tid ? d : 0.f));
+        o[whole * E + tid] = (TI)(at == whole * E + tid ? grad_target((float)last) : grad((float)last));
 }
 
 // ------------------------------------------------------------------ host
@@ -964,7 +1051,7 @@ void lp_segments(int T, int V, int bf16, int &segs, int &seg)
     segs = (int)ceil_div(V, seg);
 }
 
-static size_t bytes_of(int64_t parts, int k) { return (size_t)parts * (sizeof(LpState) + (size_t)k * 8); }
+static size_t bytes_of(int64_t parts, int k) { return (size_t)parts * (sizeof(LpSum) + (size_t)k * 8); }
 
 size_t lp_workspace(int T, int V, int bf16, int k)
 {
@@ -1019,7 +1106,7 @@ static hipError_t run_logprob(LpArgs p, void *ws, hipStream_t s)
 {
     if (p.segs > 1) {
         p.keys = (uint64_t *)ws;
-        p.part = (LpState *)(p.keys + (int64_t)p.T * p.segs * p.k);
+        p.part = (LpSum *)(p.keys + (int64_t)p.T * p.segs * p.k);
     }
     const dim3 grid((unsigned)((int64_t)p.T * p.segs)), block(LP_THREADS);
     auto run = [&](auto type, auto top) {
