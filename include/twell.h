@@ -480,7 +480,8 @@ TWELL_API size_t twell_glu_packed_workspace_bytes(int32_t T, int32_t d, int32_t 
 
 /* twell_glu_backward in bf16 from the values that g's and u's codes stand for.
  * h (device [T][F] bf16, or NULL) receives act(g) * u of those values, for the
- * gradient of the product after it: the forward's h need not be kept.  Any of h,
+ * gradient of the product after it: the forward's h need not be kept (8192 x 8192:
+ * 29 us more).  Any of h,
  * dx, and dwg with dwu may be NULL, not all.
  * workspace : >= twell_glu_backward_workspace_bytes(T, d, F, TWELL_BF16). */
 TWELL_API int twell_glu_backward_packed(const void *x, const void *wg_t, const void *wu_t, const twell_packed_t *g,
@@ -579,8 +580,10 @@ TWELL_API size_t twell_embed_workspace_bytes(int32_t T, int32_t V, int32_t d);
  * Each of logp (then targets too), norm and entropy may be NULL, k may be 0; not
  * all of them.  A logit of -inf is a masked token: p = 0, logp = -inf.  A row of
  * nothing else has m = logp = -inf, L = entropy = 0.  A NaN or +inf in a row makes
- * its results NaN, and its top_idx 0 .. k-1.  Sums are fp32 in a fixed order; where one
- * token has nearly all of the probability, L, its logp and the entropy are right
+ * its results NaN, and its top_idx 0 .. k-1.  Sums are fp32 in a fixed order, which
+ * depends on T, V and vdtype (few long rows are cut into segments): the same row among
+ * other numbers of rows may differ in its last bits, with another k it does not.  Where
+ * one token has nearly all of the probability, L, its logp and the entropy are right
  * relative to themselves, as its 1 - p in the gradient is.
  * workspace : device, >= twell_logprob_workspace_bytes(T, V, k) (where that is 0 it
  * may be NULL; never shrinking as T grows), 256-byte aligned, content ignored on

@@ -29,7 +29,7 @@ __device__ __forceinline__ float a8_max(float a, float x) { return __builtin_ele
 // as a whole.
 //
 // Both quotients are those of a correctly rounded division, in a third of its
-// operations (a tile of the gated product has 256 scales a lane): an estimate and
+// operations (of the gated product's largest tile a lane makes 8 scales): an estimate and
 // one exact remainder.  A quotient by 127, or of 1 by a step of 8 bits of mantissa,
 // is at least 1 / 512 of a unit in the last place away from where rounding turns, and
 // the corrected estimate within 2^-20 of one.

@@ -8,7 +8,7 @@
 // half a step, 0.4% of the block's largest;
 // a floating 8-bit code of 3 bits of mantissa is off by up to 6% of the value
 // itself.  Bound by memory: 3.06 bytes an element of bf16 either way
-// (8192 x 8192: packed in 39 us, 5.3 TB/s; unpacked, from caches in part, in 31 us).
+// (8192 x 8192: packed in 35.5 us, 5.8 TB/s; unpacked, from caches in part, in 30 us).
 #include "act8.h"
 #include "rows.h"
 
@@ -135,8 +135,9 @@ template <typename TO, int A8_U> __global__ __launch_bounds__(256) void act_unpa
 
 // ------------------------------------------------------------------ host
 // From A8_LARGE elements on (more than the L2s hold) two items a thread, past the
-// caches: 8192 x 8192 bf16 39 and 31 us, 46 and 32 us with one through them; 64 x 1001
-// fp32 3.8 us with two, 2.9 us with one.
+// caches: calls of 8192 x 8192 fp32 59.7 and 64.1 us, 63.5 and 70.1 with one through
+// them; bf16 35.2 and 30.3, with one 34.7 and 31.6; the kernels of 64 x 1001 fp32 3.8 us
+// with two, 2.8 with one.
 constexpr int64_t A8_LARGE = (int64_t)1 << 24;
 
 static dim3 a8_grid(int64_t items, int each) { return dim3((unsigned)((items + 256 * each - 1) / (256 * each))); }

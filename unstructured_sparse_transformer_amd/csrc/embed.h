@@ -9,10 +9,20 @@
 namespace twell {
 
 constexpr int EMB_WINDOW = 32, EMB_WINDOW_SHORT = 8;  // sorted tokens that one sum takes at most
-constexpr int EMB_ONE = 1024, EMB_ONE_WGS = 4096;  // tokens, and slices of them, up to which one launch does all,
-constexpr int64_t EMB_ONE_TABLE = (int64_t)1 << 23;  // with a table to be overwritten of up to so many elements
+// Tokens, and slices of 256 columns of them, up to which one launch does all, with a
+// table to be overwritten of up to so many elements.  (us in one launch and by sorting,
+// tables of 1024 rows: 1024 tokens of 256 6.8 and 12, of 1024 9.9 and 12.3, of 2048, 8192
+// slices, 15.2 and 12.3; 512 of 2048 9.9 and 12.2, of 4096, 8192 slices, 15.0 and 12.1.
+// Larger tables, 2^25 elements: 256 tokens 20 and 27, 1024 26 and 29; 2^23 and 1024
+// tokens 15.0 and 12.9.)
+constexpr int EMB_ONE = 1024, EMB_ONE_WGS = 4096;
+constexpr int64_t EMB_ONE_TABLE = (int64_t)1 << 23;
 constexpr int EMB_FILL_ROWS = 1024; // rows that a workgroup of that launch writes zeros to at most
-constexpr int EMB_FEW = 8192;       // tokens up to which ranks are counted in one launch
+// Tokens up to which ranks are counted in one launch, whose LDS holds their keys (the
+// whole call, added to a table, and with sorting passes instead: 2048 x 64 12.5 and 20.6
+// us, 4096 x 64 15.1 and 21.8, 8192 x 64 21.4 and 22.4, 4096 x 2048 23.0 and 28.5, 8192 x
+// 2048 39.0 and 39.1).
+constexpr int EMB_FEW = 8192;
 constexpr int EMB_DIGIT_BITS = 9;   // of a sorting pass
 constexpr int EMB_MOST_BLOCKS = 256;  // workgroups of a sorting pass
 
@@ -32,7 +42,9 @@ struct EmbArgs {
 };
 
 // Tokens up to which the short windows are taken: where they are too few, or their
-// rows too narrow, for the others to give every CU a few waves.
+// rows too narrow, for the others to give every CU a few waves (short and long, added to
+// a table: 2048 x 2048 15.2 and 17.5 us, 4096 x 2048 29.2 and 22.9, 4096 x 1024 19.0 and
+// 20.0, 4096 x 512 16.1 and 19.6, 8192 x 256 22.4 and 25.3, 16384 x 256 29.5 and 28.9).
 inline int emb_short(int d) { return d <= 256 ? 8192 : 2048; }
 
 // The most windows of any call with up to T tokens.

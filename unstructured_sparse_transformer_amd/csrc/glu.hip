@@ -81,11 +81,12 @@ enum GluPack { GLU_PLAIN, GLU_PACK, GLU_PACK_SIGN };
 // (value(fn, i)) to memory.  32 columns of a row, a block of the codes, are 16
 // values of a lane and 16 of the lane 32 further: one exchange gives both the
 // largest.  Two swaps of the lanes' halves turn their pieces of 4 columns into 16
-// consecutive ones a lane.  8192 x 2048 x 8192 forward takes 505 us with them where it
-// takes 487 with g and u in bf16: 60 operations a block and lane stand against half
-// of the bytes, which leave between other tiles' products anyway; the backward pass
-// gets 20 us of its 115 for dg and du back.  Past the caches the codes' stores, 32
-// bytes of a row each, take 30 us more.
+// consecutive ones a lane.  8192 x 2048 x 8192 forward takes 491 us with them where it
+// takes 480 with g and u in bf16 (495 where the sign is kept; in turn, on three sets of
+// inputs): 60 operations a block and lane stand against half of the bytes, which leave
+// between other tiles' products anyway; the backward pass gets 20 us of its 115 for dg
+// and du back.  Past the caches the codes' stores, 32 bytes of a row each, take 30 us
+// more.
 template <int NB, A8Round R, typename V>
 __device__ __forceinline__ void glu_pack_rows(int lane, V value, const Packed8 &to, int64_t ld, int m0, int n0, int M, int N)
 {
@@ -403,8 +404,8 @@ template <typename TI, bool ONCE> __global__ __launch_bounds__(256) void glu_dac
     }
 }
 
-// The same from 8-bit codes: 8 bytes an element, and 2 more for h (93 us, 5.8 TB/s,
-// at 8192 x 8192).
+// The same from 8-bit codes: 8 bytes an element, and 2 more for h (8192 x 8192: 96 us,
+// 5.7 TB/s, with h 119).
 template <bool ONCE> __global__ __launch_bounds__(256) void glu_dact8_kernel(GluBwd p, int rows)
 {
     const int per_row = p.F / 8;
@@ -569,8 +570,9 @@ struct MulTile {
     double stage, rest, alone;
     double end8 = 0;  // more where K is not split and g and u leave in 8 bits
 };
-// A tile whose g and u leave in 8 bits takes longer to end, a large one most, whose CU has no other (1 x 64 x 5440 13.4 us
-// without `end8`, 5.9 with it, 4096 x 64 x 1024 16.7 and 11.1, 8192 x 2048 x 8192 the same tile).
+// A tile whose g and u leave in 8 bits takes longer to end, a large one most, whose CU has no other (1 x 64 x 5440 13.8 us
+// without `end8`, with it 8.5, the host's call; 4096 x 64 x 1024 17.0 and 11.4, 547 x 192 x 6272 19.1 and 15.4, 300 x 512 x
+// 512 8.8 and 9.0; with it the choice is the best of the four tiles or at most 1 us off at 15 sizes of 1 to 8192 rows).
 constexpr MulTile MUL_TILES[] = {{256, 256, 1.5, 4, 1, 11.5}, {256, 128, 0.8, 5.5, 1, 3.5}, {128, 128, 0.6, 5, 1, 0.8}, {128, 64, 0.41, 6, 1}};
 constexpr MulTile FWD_TILES_F32[] = {{128, 128, 3.7, 4, 1.05}, {64, 128, 1.9, 2, 1.1}};
 constexpr MulTile MUL_TILES_F32[] = {{128, 128, 3.8, 4, 1.05}, {64, 64, 1.0, 1.5, 1.3}};
@@ -603,7 +605,8 @@ static MulPlan mul_plan(const MulTile *tile, int tiles, int64_t M, int64_t N, in
 }
 
 // The product that leaves g and u in 8 bits takes its own tiles, but splits K as the other one does, whose h it has to the
-// last bit (by the estimates that costs 1 in 1500 sizes up to 2%, less than 1 us).
+// last bit.  (1 in 1500 sizes would split differently by the estimates, for up to 2%; such are faster as they are: 293 x
+// 3712 x 3584 31.3 us, in 2 splits 36.3, 1249 x 4032 x 896 33.7 and 37.0, 129 x 3904 x 7936 38.1 and 38.7.)
 static MulPlan forward_plan(int vdtype, int T, int d, int F, bool packed)
 {
     if (packed)  // (the streaming kernel's workgroups hold less than a block of 8-bit codes)

@@ -442,7 +442,7 @@ template <typename TI> __device__ __forceinline__ bool lp_target(const LpArgs &p
 }
 
 // One workgroup a row, or a segment of a row that is longer than LP_SEG.
-// Bound by memory: 4096 x 131072 bf16 take 168 us (6.4 TB/s), with or without the
+// Bound by memory: 4096 x 131072 bf16 take 166 us (6.5 TB/s), with or without the
 // entropy's operations.  ONCE: more than the caches behind the L2s hold, read past
 // them (190 us through them; workgroups that start at different places of their
 // rows 3% more, segments of 4096 a sixth more).
