@@ -568,7 +568,8 @@ TWELL_API size_t twell_embed_workspace_bytes(int32_t T, int32_t V, int32_t d);
 
 /* ---- Log probabilities -----------------------------------------------------
  * From logits z [T][V] (vdtype, rows `ld` >= V elements apart, aligned as their
- * elements; T, V <= 2^30, T ceil(V / 2048) < 2^31) times scale > 0 (an inverse temperature), for each row:
+ * elements; T, V <= 2^30, T ceil(V / 2048) < 2^31) times scale (an inverse temperature,
+ * above 0 and at most 2.3e38), for each row:
  *   norm     [T][2] float: m = the largest logit, and L = log sum exp(scale (z - m))
  *   logp     [T] float: of the token targets[t], scale (z - m) - L.  targets :
  *            device int32 or int64 [T] (id_bits); one outside 0 .. V-1 has logp 0

@@ -50,7 +50,8 @@ bool apart(const void *a, int64_t ld, const void *b, int64_t ldd, int64_t T, int
     return off >= (uintptr_t)row && off + (uintptr_t)row <= (uintptr_t)ld;
 }
 
-bool good_scale(float scale) { return scale > 0 && std::isfinite(scale); }
+// The kernels take the scale times log2(e): infinite, it would make the largest logit's exponential that of no number.
+bool good_scale(float scale) { return scale > 0 && std::isfinite(scale * 1.44269504f); }
 bool known_ids(int32_t id_bits) { return id_bits == 32 || id_bits == 64; }
 
 }  // namespace
